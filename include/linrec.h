@@ -503,6 +503,77 @@ int wkv4_forward_noalloc(int64_t B, int64_t T, int64_t C,
                          const float *w, const float *u, const float *k, const float *v,
                          float *y, void *stream);
 
+/* Element types of the operators below (their tensors' type; states, and the norm's
+ * parameters and their gradients, are always float32). */
+#define LINREC_F32 0
+#define LINREC_BF16 1
+
+/*
+ * Gated delta rule: a recurrence whose state S is a (Dk, Dv) matrix per batch row and value
+ * head.  With a_t = e^{g_t}, and value head h reading key head h / (Hv / Hk):
+ *
+ *   x_t = v_t - (a_t S_{t-1})^T k_t        what the state does not predict of v_t yet
+ *   S_t = a_t S_{t-1} + beta_t k_t x_t^T
+ *   o_t = scale * S_t^T q_t
+ *
+ *   q, k     (B,T,Hk,Dk), v (B,T,Hv,Dv), g, beta (B,T,Hv)  of type dtype; g <= 0 (-inf allowed:
+ *            it clears the state); Hv a multiple of Hk; 1 <= Dk <= 128, 1 <= Dv <= 256
+ *   lengths  (B) int32 or NULL: tokens t >= lengths[b] (clamped to 0..T) of row b are absent:
+ *            they leave the state alone, o is 0 there, and nothing of them is used
+ *   s_in     (B,Hv,Dk,Dv) float32 or NULL (zero)
+ *   o        (B,T,Hv,Dv) of type dtype
+ *   s_out    (B,Hv,Dk,Dv) float32 or NULL: the state after the last token (s_in with T = 0).
+ *            It may be s_in itself, here and in gated_delta_decode_step.
+ *
+ * Long sequences are taken in chunks of 64 tokens; a value that is not finite then reaches
+ * the outputs of its own chunk, earlier tokens among them.  The states are float32 throughout.
+ * Any of B, T, Hk, Hv equal to 0 enqueues nothing but s_out.
+ */
+int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                        const void *q, const void *k, const void *v, const void *g, const void *beta,
+                        const int32_t *lengths, const float *s_in, float scale, void *o, float *s_out,
+                        void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace of gated_delta_forward and gated_delta_forward_ckpt (backward = 0) or of
+ * gated_delta_backward (backward = 1, with or without a checkpoint). */
+size_t gated_delta_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                                  int backward);
+
+/* One token (q, k (B,Hk,Dk), v, o (B,Hv,Dv), g, beta (B,Hv)) in recurrent form, for decoding.
+ * s_in may be NULL (zero); s_out may be s_in (updated in place).  No workspace. */
+int gated_delta_decode_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype, const void *q,
+                            const void *k, const void *v, const void *g, const void *beta, const float *s_in,
+                            float scale, void *o, float *s_out, void *stream);
+
+/*
+ * Group norm of each token's channels with an activation or a gate; x (N,C) has the channels
+ * last, in G groups of D = C/G (N is every leading size multiplied out, e.g. B*T).  Nothing is
+ * summed over tokens, so a causal model may use it.
+ *
+ *   n = (x - mean) / sqrt(var + eps)   over the D channels of one token's group (biased var)
+ *   y = n * weight + bias
+ *   out = act(y) without gate;  y * act(gate) with it
+ *
+ *   x, gate, out (N,C) of type dtype (gate may be NULL); weight, bias (C) float32
+ *   act  LINREC_ACT_NONE or LINREC_ACT_SILU (t * sigmoid(t));  eps >= 0
+ *   G divides C; C/G <= 8192
+ */
+#define LINREC_ACT_NONE 0
+#define LINREC_ACT_SILU 1
+
+int group_norm_act(int64_t N, int64_t C, int64_t G, int dtype, const void *x, const float *weight, const float *bias,
+                   const void *gate, float eps, int act, void *out, void *stream);
+
+/* Its gradients for the upstream gradient gout (N,C): gx, ggate (N,C) of type dtype (ggate
+ * NULL exactly when gate is), gweight, gbias (C) float32, summed over the N tokens in a fixed
+ * order (zero for N = 0). */
+int group_norm_act_backward(int64_t N, int64_t C, int64_t G, int dtype, const void *x, const float *weight,
+                            const float *bias, const void *gate, const void *gout, float eps, int act, void *gx,
+                            float *gweight, float *gbias, void *ggate, void *workspace, size_t ws_bytes,
+                            void *stream);
+
+size_t group_norm_act_backward_workspace_size(int64_t N, int64_t C, int64_t G);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,11 +10,14 @@ __all__ = ["wkv4_forward", "wkv4_forward_noalloc", "wkv4_forward_ex", "wkv4_deco
            "wkv4_forward_ckpt", "wkv4_backward_ckpt", "wkv4_forward_ckpt_ex", "wkv4_backward_ckpt_ex", "wkv4_checkpoint_size", "scan_real", "scan_complex", "scan_real_backward",
            "scan_complex_backward", "scan_mingru", "scan_minlstm", "scan_real_decay",
            "scan_complex_normalized", "scan_mingru_backward", "scan_minlstm_backward",
-           "scan_real_decay_backward", "scan_complex_normalized_backward", "workspace_size", "LinrecError"]
+           "scan_real_decay_backward", "scan_complex_normalized_backward", "workspace_size", "LinrecError",
+           "gated_delta_forward", "gated_delta_decode_step", "gated_delta_workspace_size",
+           "group_norm_act", "group_norm_act_backward", "group_norm_act_workspace_size"]
 
 
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)
+        return value
     raise AttributeError(name)

@@ -100,6 +100,19 @@ def load(path: str | None = None):
                         ("linrec_scan_real_decay_backward", 7), ("linrec_scan_complex_normalized_backward", 8)):
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = [_I64, _I64, _I64] + [_VP] * n + [_VP, _SZ, _VP]
+        _F, _INT = ctypes.c_float, ctypes.c_int
+        lib.gated_delta_workspace_size.restype = _SZ
+        lib.gated_delta_workspace_size.argtypes = [_I64] * 6 + [_INT, _INT]
+        lib.gated_delta_forward.restype = _INT
+        lib.gated_delta_forward.argtypes = [_I64] * 6 + [_INT] + [_VP] * 7 + [_F, _VP, _VP, _VP, _SZ, _VP]
+        lib.gated_delta_decode_step.restype = _INT
+        lib.gated_delta_decode_step.argtypes = [_I64] * 5 + [_INT] + [_VP] * 6 + [_F] + [_VP] * 3
+        lib.group_norm_act.restype = _INT
+        lib.group_norm_act.argtypes = [_I64] * 3 + [_INT] + [_VP] * 4 + [_F, _INT, _VP, _VP]
+        lib.group_norm_act_backward_workspace_size.restype = _SZ
+        lib.group_norm_act_backward_workspace_size.argtypes = [_I64] * 3
+        lib.group_norm_act_backward.restype = _INT
+        lib.group_norm_act_backward.argtypes = ([_I64] * 3 + [_INT] + [_VP] * 5 + [_F, _INT] + [_VP] * 5 + [_SZ, _VP])
         if path is None:
             _lib = lib
         return lib
@@ -695,3 +708,183 @@ def scan_complex_normalized_backward(lam, u, x, gx, x0=None, want_gx0=None, work
                                                        _ptr(glam), _ptr(gu), _ptr(gx0), _ptr(ws), nws, _stream(dev)),
            "linrec_scan_complex_normalized_backward")
     return glam, gu, gx0
+
+
+# ---- gated delta rule and group norm: float32 or bfloat16 tensors ------------------------------
+# These run once per decoded token, so their checks are one comparison each where all is well.
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}  # LINREC_F32, LINREC_BF16
+_ACTS = {"none": 0, "silu": 1}
+
+
+def _dtype_code(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    return code
+
+
+def _need(t, name, dtype, shape, device):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and
+            t.is_contiguous()):
+        _expect(t, name, dtype, shape, device)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _delta_shape(q, k, v, g, beta, lead):
+    """Sizes of the gated delta rule's inputs (``lead`` leading axes), checked against each other."""
+    code = _dtype_code(q, "q")
+    if q.dim() != lead + 2 or not isinstance(v, torch.Tensor) or v.dim() != lead + 2:
+        raise ValueError("q, k and v must have %d axes" % (lead + 2))
+    front, (Hk, Dk), (Hv, Dv) = tuple(q.shape[:lead]), q.shape[lead:], v.shape[lead:]
+    dt, dev = q.dtype, q.device
+    _need(q, "q", dt, front + (Hk, Dk), dev)
+    _need(k, "k", dt, front + (Hk, Dk), dev)
+    _need(v, "v", dt, front + (Hv, Dv), dev)
+    _need(g, "g", dt, front + (Hv,), dev)
+    _need(beta, "beta", dt, front + (Hv,), dev)
+    return code, front, Hk, Hv, Dk, Dv
+
+
+def _scratch(nbytes, device, workspace):
+    if nbytes == 0:
+        return None
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _workspace(nbytes, device, workspace)[0]
+
+
+def gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, dtype=torch.float32, backward=False) -> int:
+    """Bytes of workspace of gated_delta_forward (and _ckpt), or of gated_delta_backward."""
+    return int(load().gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, _DTYPES[dtype], int(backward)))
+
+
+def gated_delta_forward(q, k, v, g, beta, state=None, lengths=None, scale=None, want_state=True, out=None,
+                        workspace=None):
+    """(o, state_out) of the gated delta rule: with S (Dk,Dv) per batch row and value head and
+    a = e^g, x = v - (a S)^T k, S' = a S + beta k x^T, o = scale S'^T q.
+
+    q, k (B,T,Hk,Dk), v (B,T,Hv,Dv), g, beta (B,T,Hv), all float32 or all bfloat16; Hv a
+    multiple of Hk, value head h reading key head h // (Hv // Hk).  ``state`` (B,Hv,Dk,Dv)
+    float32 or None (zero); ``lengths`` (B,) int32 on the device: tokens at or beyond a row's
+    length are absent (o is 0 there); ``scale`` defaults to Dk ** -0.5.  state_out is None
+    unless ``want_state``; ``out`` = (o, state_out) buffers."""
+    lib = load()
+    code, (B, T), Hk, Hv, Dk, Dv = _delta_shape(q, k, v, g, beta, 2)
+    dev = q.device
+    if state is not None:
+        _need(state, "state", torch.float32, (B, Hv, Dk, Dv), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+    if out is None:
+        o = torch.empty_like(v)
+        s_out = torch.empty((B, Hv, Dk, Dv), dtype=torch.float32, device=dev) if want_state else None
+    else:
+        o, s_out = out
+        _need(o, "out[0]", q.dtype, (B, T, Hv, Dv), dev)
+        if s_out is not None:
+            _need(s_out, "out[1]", torch.float32, (B, Hv, Dk, Dv), dev)
+    nws = lib.gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, code, 0)
+    ws = _scratch(nws, dev, workspace)
+    _check(lib.gated_delta_forward(B, T, Hk, Hv, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                   beta.data_ptr(), _addr(lengths), _addr(state),
+                                   Dk ** -0.5 if scale is None else scale, o.data_ptr(), _addr(s_out), _addr(ws), nws,
+                                   _raw_stream(dev)), "gated_delta_forward")
+    return o, s_out
+
+
+def gated_delta_decode_step(q, k, v, g, beta, state, scale=None, state_out=None, out=None):
+    """One token of the gated delta rule in recurrent form: q, k (B,Hk,Dk), v (B,Hv,Dv), g, beta
+    (B,Hv), all float32 or all bfloat16; ``state`` (B,Hv,Dk,Dv) float32, updated IN PLACE unless
+    ``state_out`` is given.  Returns o (B,Hv,Dv)."""
+    lib = load()
+    code, (B,), Hk, Hv, Dk, Dv = _delta_shape(q, k, v, g, beta, 1)
+    dev = q.device
+    _need(state, "state", torch.float32, (B, Hv, Dk, Dv), dev)
+    if state_out is None:
+        state_out = state
+    else:
+        _need(state_out, "state_out", torch.float32, (B, Hv, Dk, Dv), dev)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need(out, "out", q.dtype, (B, Hv, Dv), dev)
+    _check(lib.gated_delta_decode_step(B, Hk, Hv, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                       beta.data_ptr(), state.data_ptr(), Dk ** -0.5 if scale is None else scale,
+                                       out.data_ptr(), state_out.data_ptr(), _raw_stream(dev)),
+           "gated_delta_decode_step")
+    return out
+
+
+def _norm_shape(x, groups, weight, bias, gate, act):
+    code = _dtype_code(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have a channel axis")
+    shape, C, dev = x.shape, x.shape[-1], x.device
+    _need(x, "x", x.dtype, shape, dev)
+    _need(weight, "weight", torch.float32, (C,), dev)
+    _need(bias, "bias", torch.float32, (C,), dev)
+    if gate is not None:
+        _need(gate, "gate", x.dtype, shape, dev)
+    if act not in _ACTS:
+        raise ValueError("act must be one of %s, got %r" % (sorted(_ACTS), act))
+    N = 1
+    for n in shape[:-1]:
+        N *= n
+    return code, N, C, dev
+
+
+def group_norm_act(x, groups, weight, bias, gate=None, act="silu", eps=1e-5, out=None):
+    """Group norm of each token's channels, then an activation: x (..., C) float32 or bfloat16 in
+    ``groups`` groups of C/groups channels, y = n * weight + bias with n normalised over one
+    token's group; returns act(y), or y * act(gate) with ``gate`` (..., C).  weight, bias (C,)
+    float32; act 'silu' or 'none'."""
+    lib = load()
+    code, N, C, dev = _norm_shape(x, groups, weight, bias, gate, act)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", x.dtype, x.shape, dev)
+    _check(lib.group_norm_act(N, C, groups, code, x.data_ptr(), weight.data_ptr(), bias.data_ptr(), _addr(gate), eps,
+                              _ACTS[act], out.data_ptr(), _raw_stream(dev)), "group_norm_act")
+    return out
+
+
+def group_norm_act_workspace_size(N, C, groups) -> int:
+    """Bytes of workspace of group_norm_act_backward over N tokens."""
+    return int(load().group_norm_act_backward_workspace_size(N, C, groups))
+
+
+def group_norm_act_backward(x, groups, weight, bias, gout, gate=None, act="silu", eps=1e-5, out=None, workspace=None):
+    """(gx, gweight, gbias, ggate) of group_norm_act for the upstream gradient ``gout``; ggate is
+    None without ``gate``.  ``out`` gives the four buffers."""
+    lib = load()
+    code, N, C, dev = _norm_shape(x, groups, weight, bias, gate, act)
+    _need(gout, "gout", x.dtype, x.shape, dev)
+    if out is None:
+        gx = torch.empty_like(x)
+        gw, gb = torch.empty((2, C), dtype=torch.float32, device=dev)
+        gg = torch.empty_like(x) if gate is not None else None
+    else:
+        gx, gw, gb, gg = out
+        _need(gx, "out[0]", x.dtype, x.shape, dev)
+        _need(gw, "out[1]", torch.float32, (C,), dev)
+        _need(gb, "out[2]", torch.float32, (C,), dev)
+        if gate is not None:
+            _need(gg, "out[3]", x.dtype, x.shape, dev)
+    nws = lib.group_norm_act_backward_workspace_size(N, C, groups)
+    ws = _scratch(nws, dev, workspace)
+    _check(lib.group_norm_act_backward(N, C, groups, code, x.data_ptr(), weight.data_ptr(), bias.data_ptr(),
+                                       _addr(gate), gout.data_ptr(), eps, _ACTS[act], gx.data_ptr(), gw.data_ptr(),
+                                       gb.data_ptr(), _addr(gg), _addr(ws), nws, _raw_stream(dev)),
+           "group_norm_act_backward")
+    return gx, gw, gb, gg

@@ -15,6 +15,8 @@
 #include "wkv_backward.hpp"
 #include "wkv_decode.hpp"
 #include "token_shift.hpp"
+#include "gated_delta.hpp"
+#include "group_norm.hpp"
 
 #define LINREC_API extern "C" __attribute__((visibility("default")))
 
@@ -874,4 +876,164 @@ LINREC_API int wkv4_forward_noalloc(int64_t B, int64_t T, int64_t C, const float
     const linrec::WkvArgs A{w, u, k, v, y, env_int("LINREC_WKV_EXACT", 0) > 0 ? 1 : 0, nullptr, nullptr, nullptr};
     return hip_status(linrec::run_wkv_forward(A, geom_of(linrec::kKindWkv, p, B, T, C, ws), p, (hipStream_t)stream),
                       "wkv4_forward_noalloc launch");
+}
+
+namespace {
+
+int64_t elem_bytes(int dtype) { return dtype == LINREC_BF16 ? 2 : 4; }
+
+int check_dtype(int dtype) {
+    if (dtype != LINREC_F32 && dtype != LINREC_BF16)
+        return fail(LINREC_ERR_INVALID_ARG, "dtype %d is neither LINREC_F32 nor LINREC_BF16", dtype);
+    return LINREC_OK;
+}
+
+// Sizes of the gated delta rule: head counts and widths the kernels take, tensors addressable.
+int check_delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype) {
+    int st = check_dtype(dtype);
+    if (st) return st;
+    if (B < 0 || T < 0 || Hk < 0 || Hv < 0)
+        return fail(LINREC_ERR_INVALID_ARG, "negative size: B=%lld T=%lld Hk=%lld Hv=%lld", (long long)B,
+                    (long long)T, (long long)Hk, (long long)Hv);
+    if (Dk < 1 || Dk > linrec::kDeltaMaxDk || Dv < 1 || Dv > linrec::kDeltaMaxDv)
+        return fail(LINREC_ERR_INVALID_ARG, "head widths Dk=%lld Dv=%lld outside 1..%d and 1..%d", (long long)Dk,
+                    (long long)Dv, linrec::kDeltaMaxDk, linrec::kDeltaMaxDv);
+    if (Hk > 0 && Hv % Hk != 0)
+        return fail(LINREC_ERR_INVALID_ARG, "Hv=%lld is no multiple of Hk=%lld", (long long)Hv, (long long)Hk);
+    if (Hk == 0 && Hv > 0) return fail(LINREC_ERR_INVALID_ARG, "Hk=0 with Hv=%lld", (long long)Hv);
+    int64_t bt = 0, bh = 0;
+    if (__builtin_mul_overflow(B, T, &bt) || __builtin_mul_overflow(B, Hv, &bh))
+        return fail(LINREC_ERR_INVALID_ARG, "B*T or B*Hv overflows int64");
+    // Row counts a grid can hold.
+    if (bh > (int64_t)0x7fffffff / 64) return fail(LINREC_ERR_UNSUPPORTED, "B*Hv=%lld is too large", (long long)bh);
+    if (Hv > 0x7fffffff || Hk > 0x7fffffff) return fail(LINREC_ERR_UNSUPPORTED, "too many heads");
+    if ((st = check_shape(bt, Hk, Dk, 4)) || (st = check_shape(bt, Hv, Dv, 4)) || (st = check_shape(bh, Dk, Dv, 4)))
+        return st;
+    return LINREC_OK;
+}
+
+// Required pointers: not NULL, aligned to the element.
+int check_ptrs(std::initializer_list<const void*> need, int64_t elem) {
+    for (const void* p : need)
+        if (!p) return fail(LINREC_ERR_INVALID_ARG, "a required pointer is NULL");
+    for (const void* p : need)
+        if (!aligned(p, elem)) return fail(LINREC_ERR_UNSUPPORTED, "pointer not %lld-byte aligned", (long long)elem);
+    return LINREC_OK;
+}
+
+int check_f32_ptrs(std::initializer_list<const void*> optional) {
+    for (const void* p : optional)
+        if (p && !aligned(p, 4)) return fail(LINREC_ERR_UNSUPPORTED, "pointer not 4-byte aligned");
+    return LINREC_OK;
+}
+
+linrec::DeltaShape delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                               const int32_t* lengths, float scale) {
+    return {B, T, (int)Hk, (int)Hv, (int)Dk, (int)Dv, dtype, lengths, scale};
+}
+
+// out = in (zero without it) over n floats; nothing where they are one buffer.
+hipError_t pass_state(float* out, const float* in, int64_t n, hipStream_t st) {
+    if (!out || n == 0 || out == in) return hipSuccess;
+    return in ? linrec::run_copy(out, in, n, st) : linrec::run_fill_zero(out, n, st);
+}
+
+}  // namespace
+
+LINREC_API size_t gated_delta_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                             int dtype, int backward) {
+    (void)backward;
+    if (check_delta_shape(B, T, Hk, Hv, Dk, Dv, dtype) || B == 0 || T == 0 || Hv == 0) return 0;
+    return 0;
+}
+
+LINREC_API int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                                   const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                   const int32_t* lengths, const float* s_in, float scale, void* o, float* s_out,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_delta_shape(B, T, Hk, Hv, Dk, Dv, dtype);
+    if (st) return st;
+    if (B == 0 || Hv == 0) return ok();
+    if ((st = check_f32_ptrs({lengths, s_in, s_out}))) return st;
+    if (T == 0)
+        return hip_status(pass_state(s_out, s_in, B * Hv * Dk * Dv, (hipStream_t)stream), "gated_delta_forward state");
+    if ((st = check_ptrs({q, k, v, g, beta, o}, elem_bytes(dtype)))) return st;
+    if ((st = check_ws(workspace, ws_bytes, gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, dtype, 0)))) return st;
+    const linrec::DeltaShape s = delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, lengths, scale);
+    const linrec::DeltaFwdArgs A{q, k, v, g, beta, s_in, o, s_out};
+    return hip_status(linrec::run_delta_recurrent(s, A, (hipStream_t)stream), "gated_delta_forward launch");
+}
+
+LINREC_API int gated_delta_decode_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                                       const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                       const float* s_in, float scale, void* o, float* s_out, void* stream) {
+    int st = check_delta_shape(B, 1, Hk, Hv, Dk, Dv, dtype);
+    if (st) return st;
+    if (B == 0 || Hv == 0) return ok();
+    if ((st = check_ptrs({q, k, v, g, beta, o}, elem_bytes(dtype))) || (st = check_ptrs({s_out}, 4)) ||
+        (st = check_f32_ptrs({s_in})))
+        return st;
+    const linrec::DeltaShape s = delta_shape(B, 1, Hk, Hv, Dk, Dv, dtype, nullptr, scale);
+    const linrec::DeltaFwdArgs A{q, k, v, g, beta, s_in, o, s_out};
+    return hip_status(linrec::run_delta_recurrent(s, A, (hipStream_t)stream), "gated_delta_decode_step launch");
+}
+
+namespace {
+
+int check_norm(int64_t N, int64_t C, int64_t G, int dtype, float eps, int act) {
+    int st = check_dtype(dtype);
+    if (st) return st;
+    if ((st = check_shape(1, N, C, 4))) return st;
+    if (G < 1 || C % G != 0) return fail(LINREC_ERR_INVALID_ARG, "G=%lld does not divide C=%lld", (long long)G, (long long)C);
+    if (C / G > linrec::kNormMaxGroup)
+        return fail(LINREC_ERR_UNSUPPORTED, "groups of %lld channels; at most %d", (long long)(C / G), linrec::kNormMaxGroup);
+    if (C > 0x7fffffff) return fail(LINREC_ERR_UNSUPPORTED, "C=%lld is too large", (long long)C);
+    if (act != LINREC_ACT_NONE && act != LINREC_ACT_SILU) return fail(LINREC_ERR_INVALID_ARG, "unknown act %d", act);
+    if (!(eps >= 0.f)) return fail(LINREC_ERR_INVALID_ARG, "eps must be >= 0");
+    return LINREC_OK;
+}
+
+}  // namespace
+
+LINREC_API int group_norm_act(int64_t N, int64_t C, int64_t G, int dtype, const void* x, const float* weight,
+                              const float* bias, const void* gate, float eps, int act, void* out, void* stream) {
+    int st = check_norm(N, C, G, dtype, eps, act);
+    if (st) return st;
+    if (N == 0 || C == 0) return ok();
+    if ((st = check_ptrs({x, out}, elem_bytes(dtype))) || (st = check_ptrs({weight, bias}, 4))) return st;
+    if (gate && (st = check_ptrs({gate}, elem_bytes(dtype)))) return st;
+    linrec::NormArgs A{};
+    A.x = x, A.gate = gate, A.weight = weight, A.bias = bias, A.y = out;
+    A.N = N, A.C = C, A.G = (int)G, A.D = (int)(C / G), A.eps = eps, A.act = act, A.dtype = dtype;
+    return hip_status(linrec::run_group_norm(A, (hipStream_t)stream), "group_norm_act launch");
+}
+
+LINREC_API size_t group_norm_act_backward_workspace_size(int64_t N, int64_t C, int64_t G) {
+    if (check_norm(N, C, G, LINREC_F32, 0.f, 0) || N == 0 || C == 0) return 0;
+    return align256(linrec::group_norm_backward_ws_bytes(N, C, (int)G));
+}
+
+LINREC_API int group_norm_act_backward(int64_t N, int64_t C, int64_t G, int dtype, const void* x, const float* weight,
+                                       const float* bias, const void* gate, const void* gout, float eps, int act,
+                                       void* gx, float* gweight, float* gbias, void* ggate, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+    int st = check_norm(N, C, G, dtype, eps, act);
+    if (st) return st;
+    if (C == 0) return ok();
+    if ((st = check_ptrs({gweight, gbias}, 4))) return st;
+    if (N == 0) {
+        hipError_t e = linrec::run_fill_zero(gweight, C, (hipStream_t)stream);
+        if (e == hipSuccess) e = linrec::run_fill_zero(gbias, C, (hipStream_t)stream);
+        return hip_status(e, "group_norm_act_backward zero fill");
+    }
+    if ((gate == nullptr) != (ggate == nullptr))
+        return fail(LINREC_ERR_INVALID_ARG, "gate and ggate must be given together");
+    if ((st = check_ptrs({x, gout, gx}, elem_bytes(dtype))) || (st = check_ptrs({weight, bias}, 4))) return st;
+    if (gate && (st = check_ptrs({gate, ggate}, elem_bytes(dtype)))) return st;
+    if ((st = check_ws(workspace, ws_bytes, group_norm_act_backward_workspace_size(N, C, G)))) return st;
+    linrec::NormArgs A{};
+    A.x = x, A.gate = gate, A.weight = weight, A.bias = bias, A.gy = gout, A.gx = gx, A.ggate = ggate;
+    A.gweight = gweight, A.gbias = gbias, A.part = (float*)workspace;
+    A.N = N, A.C = C, A.G = (int)G, A.D = (int)(C / G), A.eps = eps, A.act = act, A.dtype = dtype;
+    return hip_status(linrec::run_group_norm_backward(A, (hipStream_t)stream), "group_norm_act_backward launch");
 }
