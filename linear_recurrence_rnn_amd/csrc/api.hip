@@ -904,9 +904,11 @@ int check_delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, 
     int64_t bt = 0, bh = 0;
     if (__builtin_mul_overflow(B, T, &bt) || __builtin_mul_overflow(B, Hv, &bh))
         return fail(LINREC_ERR_INVALID_ARG, "B*T or B*Hv overflows int64");
-    // Row counts a grid can hold.
-    if (bh > (int64_t)0x7fffffff / 64) return fail(LINREC_ERR_UNSUPPORTED, "B*Hv=%lld is too large", (long long)bh);
-    if (Hv > 0x7fffffff || Hk > 0x7fffffff) return fail(LINREC_ERR_UNSUPPORTED, "too many heads");
+    // What a grid can hold: fewer than 2^32 lanes, at most 8 column tiles of 256 lanes a head
+    // and 64 lanes a chunk.
+    if (bh > (1 << 20)) return fail(LINREC_ERR_UNSUPPORTED, "B*Hv=%lld is above 2^20", (long long)bh);
+    if (T > (1 << 30) || bh * ceil_div(T, 64) >= (1 << 26))
+        return fail(LINREC_ERR_UNSUPPORTED, "B*Hv*T/64 is above 2^26, or T above 2^30");
     if ((st = check_shape(bt, Hk, Dk, 4)) || (st = check_shape(bt, Hv, Dv, 4)) || (st = check_shape(bh, Dk, Dv, 4)))
         return st;
     return LINREC_OK;
@@ -932,6 +934,19 @@ linrec::DeltaShape delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int
     return {B, T, (int)Hk, (int)Hv, (int)Dk, (int)Dv, dtype, lengths, scale};
 }
 
+// Sequences of up to this many tokens are taken token by token.
+bool delta_is_short(int64_t T) { return T <= env_int("LINREC_DELTA_SHORT", 16); }
+
+size_t delta_chunks_bytes(const linrec::DeltaShape& s) {
+    const size_t n = (size_t)linrec::delta_chunks(s);
+    return align256(n * 64 * 64 * sizeof(float)) + align256(n * 64 * sizeof(double));
+}
+
+linrec::DeltaChunks delta_chunks_at(const linrec::DeltaShape& s, void* ws) {
+    const size_t n = (size_t)linrec::delta_chunks(s);
+    return {(float*)ws, (double*)((char*)ws + align256(n * 64 * 64 * sizeof(float)))};
+}
+
 // out = in (zero without it) over n floats; nothing where they are one buffer.
 hipError_t pass_state(float* out, const float* in, int64_t n, hipStream_t st) {
     if (!out || n == 0 || out == in) return hipSuccess;
@@ -944,7 +959,8 @@ LINREC_API size_t gated_delta_workspace_size(int64_t B, int64_t T, int64_t Hk, i
                                              int dtype, int backward) {
     (void)backward;
     if (check_delta_shape(B, T, Hk, Hv, Dk, Dv, dtype) || B == 0 || T == 0 || Hv == 0) return 0;
-    return 0;
+    if (delta_is_short(T)) return 0;
+    return delta_chunks_bytes(delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, nullptr, 0.f));
 }
 
 LINREC_API int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
@@ -961,7 +977,12 @@ LINREC_API int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv,
     if ((st = check_ws(workspace, ws_bytes, gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, dtype, 0)))) return st;
     const linrec::DeltaShape s = delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, lengths, scale);
     const linrec::DeltaFwdArgs A{q, k, v, g, beta, s_in, o, s_out};
-    return hip_status(linrec::run_delta_recurrent(s, A, (hipStream_t)stream), "gated_delta_forward launch");
+    if (delta_is_short(T))
+        return hip_status(linrec::run_delta_recurrent(s, A, (hipStream_t)stream), "gated_delta_forward launch");
+    const linrec::DeltaChunks W = delta_chunks_at(s, workspace);
+    hipError_t e = linrec::run_delta_prepare(s, A, W, (hipStream_t)stream);
+    if (e == hipSuccess) e = linrec::run_delta_forward(s, A, W, (hipStream_t)stream);
+    return hip_status(e, "gated_delta_forward launch");
 }
 
 LINREC_API int gated_delta_decode_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
@@ -987,7 +1008,7 @@ int check_norm(int64_t N, int64_t C, int64_t G, int dtype, float eps, int act) {
     if (G < 1 || C % G != 0) return fail(LINREC_ERR_INVALID_ARG, "G=%lld does not divide C=%lld", (long long)G, (long long)C);
     if (C / G > linrec::kNormMaxGroup)
         return fail(LINREC_ERR_UNSUPPORTED, "groups of %lld channels; at most %d", (long long)(C / G), linrec::kNormMaxGroup);
-    if (C > 0x7fffffff) return fail(LINREC_ERR_UNSUPPORTED, "C=%lld is too large", (long long)C);
+    if (C > (1 << 24)) return fail(LINREC_ERR_UNSUPPORTED, "C=%lld is above 2^24", (long long)C);
     if (act != LINREC_ACT_NONE && act != LINREC_ACT_SILU) return fail(LINREC_ERR_INVALID_ARG, "unknown act %d", act);
     if (!(eps >= 0.f)) return fail(LINREC_ERR_INVALID_ARG, "eps must be >= 0");
     return LINREC_OK;

@@ -30,6 +30,18 @@ struct DeltaFwdArgs {
     float* s_out;        // (B,Hv,Dk,Dv), or null; may be s_in
 };
 
+// What the chunked kernels keep of each chunk of 64 tokens, (B*Hv, chunks, ...):
+//   tinv  (64,64) float32   (I + strictly lower e^{gam_i - gam_j} (k_i.k_j) beta_j)^{-1}
+//   gam   (64) float64      decays cumulated within the chunk
+struct DeltaChunks {
+    float* tinv;
+    double* gam;
+};
+inline int64_t delta_chunks(const DeltaShape& s) { return s.B * s.Hv * ((s.T + 63) / 64); }
+
+hipError_t run_delta_prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st);
+hipError_t run_delta_forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st);
+
 // Token by token, the state in registers: decoding and the shortest sequences.
 hipError_t run_delta_recurrent(const DeltaShape& s, const DeltaFwdArgs& A, hipStream_t st);
 
