@@ -534,10 +534,37 @@ int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk
                         const int32_t *lengths, const float *s_in, float scale, void *o, float *s_out,
                         void *workspace, size_t ws_bytes, void *stream);
 
-/* Bytes of workspace of gated_delta_forward and gated_delta_forward_ckpt (backward = 0) or of
- * gated_delta_backward (backward = 1, with or without a checkpoint). */
+/* Bytes of workspace of gated_delta_forward (backward = 0) or of gated_delta_backward (backward
+ * = 1, with or without a checkpoint).  with_state: whether s_in is given. */
 size_t gated_delta_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
-                                  int backward);
+                                  int with_state, int backward);
+
+/*
+ * Training.  gated_delta_forward_ckpt is gated_delta_forward that also keeps, in `ckpt` (of
+ * gated_delta_checkpoint_size bytes, 16-byte aligned), what the backward starts from: each
+ * chunk's inverse, its x and the state before it.  gated_delta_backward takes that checkpoint
+ * (of a call with the same sizes and inputs), or NULL and forms it again in its workspace.  What
+ * is kept has the tensors' type, or float32 where a state is carried in (s_in).
+ *
+ *   go      (B,T,Hv,Dv) upstream gradient of o; gs_out (B,Hv,Dk,Dv) float32 that of s_out, or NULL
+ *   gq, gk, gv, gg, gbeta   gradients, in the shape and type of q, k, v, g, beta (gq and gk summed
+ *           over the value heads that share a key head, in head order); zero for absent tokens
+ *   gs_in   (B,Hv,Dk,Dv) float32 gradient of s_in, or NULL (as it must be without s_in); it may
+ *           be gs_out itself
+ */
+size_t gated_delta_checkpoint_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                                   int with_state);
+
+int gated_delta_forward_ckpt(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                             const void *q, const void *k, const void *v, const void *g, const void *beta,
+                             const int32_t *lengths, const float *s_in, float scale, void *o, float *s_out,
+                             void *ckpt, size_t ckpt_bytes, void *stream);
+
+int gated_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                         const void *q, const void *k, const void *v, const void *g, const void *beta,
+                         const int32_t *lengths, const float *s_in, float scale, const void *ckpt,
+                         size_t ckpt_bytes, const void *go, const float *gs_out, void *gq, void *gk, void *gv,
+                         void *gg, void *gbeta, float *gs_in, void *workspace, size_t ws_bytes, void *stream);
 
 /* One token (q, k (B,Hk,Dk), v, o (B,Hv,Dv), g, beta (B,Hv)) in recurrent form, for decoding.
  * s_in may be NULL (zero); s_out may be s_in (updated in place).  No workspace. */

@@ -11,7 +11,8 @@ __all__ = ["wkv4_forward", "wkv4_forward_noalloc", "wkv4_forward_ex", "wkv4_deco
            "scan_complex_backward", "scan_mingru", "scan_minlstm", "scan_real_decay",
            "scan_complex_normalized", "scan_mingru_backward", "scan_minlstm_backward",
            "scan_real_decay_backward", "scan_complex_normalized_backward", "workspace_size", "LinrecError",
-           "gated_delta_forward", "gated_delta_decode_step", "gated_delta_workspace_size",
+           "gated_delta_forward", "gated_delta_forward_ckpt", "gated_delta_backward", "gated_delta_checkpoint_size",
+           "gated_delta_decode_step", "gated_delta_workspace_size",
            "group_norm_act", "group_norm_act_backward", "group_norm_act_workspace_size"]
 
 

@@ -102,9 +102,16 @@ def load(path: str | None = None):
             getattr(lib, name).argtypes = [_I64, _I64, _I64] + [_VP] * n + [_VP, _SZ, _VP]
         _F, _INT = ctypes.c_float, ctypes.c_int
         lib.gated_delta_workspace_size.restype = _SZ
-        lib.gated_delta_workspace_size.argtypes = [_I64] * 6 + [_INT, _INT]
+        lib.gated_delta_workspace_size.argtypes = [_I64] * 6 + [_INT, _INT, _INT]
         lib.gated_delta_forward.restype = _INT
         lib.gated_delta_forward.argtypes = [_I64] * 6 + [_INT] + [_VP] * 7 + [_F, _VP, _VP, _VP, _SZ, _VP]
+        lib.gated_delta_checkpoint_size.restype = _SZ
+        lib.gated_delta_checkpoint_size.argtypes = [_I64] * 6 + [_INT, _INT]
+        lib.gated_delta_forward_ckpt.restype = _INT
+        lib.gated_delta_forward_ckpt.argtypes = [_I64] * 6 + [_INT] + [_VP] * 7 + [_F, _VP, _VP, _VP, _SZ, _VP]
+        lib.gated_delta_backward.restype = _INT
+        lib.gated_delta_backward.argtypes = ([_I64] * 6 + [_INT] + [_VP] * 7 + [_F, _VP, _SZ] + [_VP] * 8 +
+                                             [_VP, _SZ, _VP])
         lib.gated_delta_decode_step.restype = _INT
         lib.gated_delta_decode_step.argtypes = [_I64] * 5 + [_INT] + [_VP] * 6 + [_F] + [_VP] * 3
         lib.group_norm_act.restype = _INT
@@ -763,9 +770,10 @@ def _scratch(nbytes, device, workspace):
     return _workspace(nbytes, device, workspace)[0]
 
 
-def gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, dtype=torch.float32, backward=False) -> int:
-    """Bytes of workspace of gated_delta_forward (and _ckpt), or of gated_delta_backward."""
-    return int(load().gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, _DTYPES[dtype], int(backward)))
+def gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, dtype=torch.float32, backward=False, with_state=True) -> int:
+    """Bytes of workspace of gated_delta_forward, or of gated_delta_backward."""
+    return int(load().gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, _DTYPES[dtype], int(with_state),
+                                                 int(backward)))
 
 
 def gated_delta_forward(q, k, v, g, beta, state=None, lengths=None, scale=None, want_state=True, out=None,
@@ -793,13 +801,87 @@ def gated_delta_forward(q, k, v, g, beta, state=None, lengths=None, scale=None, 
         _need(o, "out[0]", q.dtype, (B, T, Hv, Dv), dev)
         if s_out is not None:
             _need(s_out, "out[1]", torch.float32, (B, Hv, Dk, Dv), dev)
-    nws = lib.gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, code, 0)
+    nws = lib.gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, code, state is not None, 0)
     ws = _scratch(nws, dev, workspace)
     _check(lib.gated_delta_forward(B, T, Hk, Hv, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
                                    beta.data_ptr(), _addr(lengths), _addr(state),
                                    Dk ** -0.5 if scale is None else scale, o.data_ptr(), _addr(s_out), _addr(ws), nws,
                                    _raw_stream(dev)), "gated_delta_forward")
     return o, s_out
+
+
+def gated_delta_checkpoint_size(B, T, Hk, Hv, Dk, Dv, dtype=torch.float32, with_state=True) -> int:
+    """Bytes of what gated_delta_forward_ckpt keeps for the backward."""
+    return int(load().gated_delta_checkpoint_size(B, T, Hk, Hv, Dk, Dv, _DTYPES[dtype], int(with_state)))
+
+
+def gated_delta_forward_ckpt(q, k, v, g, beta, state=None, lengths=None, scale=None, out=None):
+    """(o, state_out, ckpt): gated_delta_forward that also keeps what gated_delta_backward starts
+    from; ``out`` = (o, state_out, ckpt) buffers."""
+    lib = load()
+    code, (B, T), Hk, Hv, Dk, Dv = _delta_shape(q, k, v, g, beta, 2)
+    dev = q.device
+    if state is not None:
+        _need(state, "state", torch.float32, (B, Hv, Dk, Dv), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+    nck = lib.gated_delta_checkpoint_size(B, T, Hk, Hv, Dk, Dv, code, state is not None)
+    if out is None:
+        o = torch.empty_like(v)
+        s_out = torch.empty((B, Hv, Dk, Dv), dtype=torch.float32, device=dev)
+        ckpt = torch.empty(nck, dtype=torch.uint8, device=dev)
+    else:
+        o, s_out, ckpt = out
+        _need(o, "out[0]", q.dtype, (B, T, Hv, Dv), dev)
+        _need(s_out, "out[1]", torch.float32, (B, Hv, Dk, Dv), dev)
+        _need(ckpt, "out[2]", torch.uint8, (nck,), dev)
+    _check(lib.gated_delta_forward_ckpt(B, T, Hk, Hv, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                        g.data_ptr(), beta.data_ptr(), _addr(lengths), _addr(state),
+                                        Dk ** -0.5 if scale is None else scale, o.data_ptr(), s_out.data_ptr(),
+                                        ckpt.data_ptr(), nck, _raw_stream(dev)), "gated_delta_forward_ckpt")
+    return o, s_out, ckpt
+
+
+def gated_delta_backward(q, k, v, g, beta, go, state=None, gstate=None, lengths=None, scale=None, ckpt=None, out=None,
+                         workspace=None):
+    """(gq, gk, gv, gg, gbeta, gstate_in) of gated_delta_forward for the upstream gradients ``go``
+    of o and ``gstate`` (or None) of the final state; gstate_in is None without ``state``.
+    ``ckpt`` is what gated_delta_forward_ckpt kept of the same inputs (formed again if None);
+    ``out`` gives the six buffers."""
+    lib = load()
+    code, (B, T), Hk, Hv, Dk, Dv = _delta_shape(q, k, v, g, beta, 2)
+    dev, dt = q.device, q.dtype
+    _need(go, "go", dt, (B, T, Hv, Dv), dev)
+    if state is not None:
+        _need(state, "state", torch.float32, (B, Hv, Dk, Dv), dev)
+    if gstate is not None:
+        _need(gstate, "gstate", torch.float32, (B, Hv, Dk, Dv), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+    nck = lib.gated_delta_checkpoint_size(B, T, Hk, Hv, Dk, Dv, code, state is not None)
+    if ckpt is not None:
+        _need(ckpt, "ckpt", torch.uint8, (nck,), dev)
+    if out is None:
+        gq, gk, gv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        gg, gb = torch.empty_like(g), torch.empty_like(beta)
+        gs = torch.empty_like(state) if state is not None else None
+    else:
+        gq, gk, gv, gg, gb, gs = out
+        for name, t, ref in (("0", gq, q), ("1", gk, k), ("2", gv, v), ("3", gg, g), ("4", gb, beta)):
+            _need(t, "out[%s]" % name, dt, ref.shape, dev)
+        if gs is not None:
+            _need(gs, "out[5]", torch.float32, (B, Hv, Dk, Dv), dev)
+    nws = lib.gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, code, state is not None, 1)
+    if ckpt is not None:
+        nws -= nck
+    ws = _scratch(nws, dev, workspace)
+    _check(lib.gated_delta_backward(B, T, Hk, Hv, Dk, Dv, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                    beta.data_ptr(), _addr(lengths), _addr(state),
+                                    Dk ** -0.5 if scale is None else scale, _addr(ckpt), nck, go.data_ptr(),
+                                    _addr(gstate), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gg.data_ptr(),
+                                    gb.data_ptr(), _addr(gs), _addr(ws), nws, _raw_stream(dev)),
+           "gated_delta_backward")
+    return gq, gk, gv, gg, gb, gs
 
 
 def gated_delta_decode_step(q, k, v, g, beta, state, scale=None, state_out=None, out=None):

@@ -937,14 +937,32 @@ linrec::DeltaShape delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int
 // Sequences of up to this many tokens are taken token by token.
 bool delta_is_short(int64_t T) { return T <= env_int("LINREC_DELTA_SHORT", 16); }
 
-size_t delta_chunks_bytes(const linrec::DeltaShape& s) {
-    const size_t n = (size_t)linrec::delta_chunks(s);
-    return align256(n * 64 * 64 * sizeof(float)) + align256(n * 64 * sizeof(double));
+// Scratch of the chunked kernels, in this order: the inverses and decays; x and s0 (together
+// with them the checkpoint); ds.  state: a state is carried in.  Returns the end; fills W if given.
+enum { kDeltaPrep, kDeltaCkpt, kDeltaBwd };
+size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws, linrec::DeltaChunks* W) {
+    const size_t n = (size_t)linrec::delta_chunks(s), e = linrec::delta_keeps_f32(s.dtype, state ? &s : nullptr) ? 4 : 2;
+    const size_t block = n * linrec::delta_blocks(s) * 16 * e;  // bytes of a row of every chunk's block matrix
+    size_t at = 0;
+    const auto take = [&](size_t bytes) {
+        char* p = (char*)ws + at;
+        at += align256(bytes);
+        return (void*)p;
+    };
+    linrec::DeltaChunks w{};
+    w.tinv = (float*)take(n * 64 * 64 * sizeof(float));
+    w.gam = (double*)take(n * 64 * sizeof(double));
+    if (upto >= kDeltaCkpt) {
+        w.x = take(block * 64);
+        w.s0 = take(block * linrec::delta_dkp(s));
+    }
+    if (upto >= kDeltaBwd) w.ds = take(block * linrec::delta_dkp(s));
+    if (W) *W = w;
+    return at;
 }
 
-linrec::DeltaChunks delta_chunks_at(const linrec::DeltaShape& s, void* ws) {
-    const size_t n = (size_t)linrec::delta_chunks(s);
-    return {(float*)ws, (double*)((char*)ws + align256(n * 64 * 64 * sizeof(float)))};
+size_t delta_ds_bytes(const linrec::DeltaShape& s, bool state) {
+    return delta_layout(s, state, kDeltaBwd, nullptr, nullptr) - delta_layout(s, state, kDeltaCkpt, nullptr, nullptr);
 }
 
 // out = in (zero without it) over n floats; nothing where they are one buffer.
@@ -956,11 +974,18 @@ hipError_t pass_state(float* out, const float* in, int64_t n, hipStream_t st) {
 }  // namespace
 
 LINREC_API size_t gated_delta_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
-                                             int dtype, int backward) {
-    (void)backward;
+                                             int dtype, int with_state, int backward) {
     if (check_delta_shape(B, T, Hk, Hv, Dk, Dv, dtype) || B == 0 || T == 0 || Hv == 0) return 0;
-    if (delta_is_short(T)) return 0;
-    return delta_chunks_bytes(delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, nullptr, 0.f));
+    if (!backward && delta_is_short(T)) return 0;
+    return delta_layout(delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, nullptr, 0.f), with_state != 0,
+                        backward ? kDeltaBwd : kDeltaPrep, nullptr, nullptr);
+}
+
+LINREC_API size_t gated_delta_checkpoint_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                              int dtype, int with_state) {
+    if (check_delta_shape(B, T, Hk, Hv, Dk, Dv, dtype) || B == 0 || T == 0 || Hv == 0) return 0;
+    return delta_layout(delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, nullptr, 0.f), with_state != 0, kDeltaCkpt,
+                        nullptr, nullptr);
 }
 
 LINREC_API int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
@@ -974,15 +999,75 @@ LINREC_API int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv,
     if (T == 0)
         return hip_status(pass_state(s_out, s_in, B * Hv * Dk * Dv, (hipStream_t)stream), "gated_delta_forward state");
     if ((st = check_ptrs({q, k, v, g, beta, o}, elem_bytes(dtype)))) return st;
-    if ((st = check_ws(workspace, ws_bytes, gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, dtype, 0)))) return st;
+    if ((st = check_ws(workspace, ws_bytes, gated_delta_workspace_size(B, T, Hk, Hv, Dk, Dv, dtype, s_in != nullptr, 0)))) return st;
     const linrec::DeltaShape s = delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, lengths, scale);
     const linrec::DeltaFwdArgs A{q, k, v, g, beta, s_in, o, s_out};
     if (delta_is_short(T))
         return hip_status(linrec::run_delta_recurrent(s, A, (hipStream_t)stream), "gated_delta_forward launch");
-    const linrec::DeltaChunks W = delta_chunks_at(s, workspace);
+    linrec::DeltaChunks W;
+    delta_layout(s, s_in != nullptr, kDeltaPrep, workspace, &W);
     hipError_t e = linrec::run_delta_prepare(s, A, W, (hipStream_t)stream);
     if (e == hipSuccess) e = linrec::run_delta_forward(s, A, W, (hipStream_t)stream);
     return hip_status(e, "gated_delta_forward launch");
+}
+
+LINREC_API int gated_delta_forward_ckpt(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                                        const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                        const int32_t* lengths, const float* s_in, float scale, void* o, float* s_out,
+                                        void* ckpt, size_t ckpt_bytes, void* stream) {
+    int st = check_delta_shape(B, T, Hk, Hv, Dk, Dv, dtype);
+    if (st) return st;
+    if (B == 0 || Hv == 0) return ok();
+    if ((st = check_f32_ptrs({lengths, s_in, s_out}))) return st;
+    if (T == 0)
+        return hip_status(pass_state(s_out, s_in, B * Hv * Dk * Dv, (hipStream_t)stream),
+                          "gated_delta_forward_ckpt state");
+    if ((st = check_ptrs({q, k, v, g, beta, o}, elem_bytes(dtype)))) return st;
+    if ((st = check_ckpt(ckpt, ckpt_bytes, gated_delta_checkpoint_size(B, T, Hk, Hv, Dk, Dv, dtype, s_in != nullptr)))) return st;
+    const linrec::DeltaShape s = delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, lengths, scale);
+    const linrec::DeltaFwdArgs A{q, k, v, g, beta, s_in, o, s_out};
+    linrec::DeltaChunks W;
+    delta_layout(s, s_in != nullptr, kDeltaCkpt, ckpt, &W);
+    hipError_t e = linrec::run_delta_prepare(s, A, W, (hipStream_t)stream);
+    if (e == hipSuccess) e = linrec::run_delta_forward(s, A, W, (hipStream_t)stream);
+    return hip_status(e, "gated_delta_forward_ckpt launch");
+}
+
+LINREC_API int gated_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
+                                    const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                    const int32_t* lengths, const float* s_in, float scale, const void* ckpt,
+                                    size_t ckpt_bytes, const void* go, const float* gs_out, void* gq, void* gk,
+                                    void* gv, void* gg, void* gbeta, float* gs_in, void* workspace, size_t ws_bytes,
+                                    void* stream) {
+    int st = check_delta_shape(B, T, Hk, Hv, Dk, Dv, dtype);
+    if (st) return st;
+    if (B == 0 || Hv == 0) return ok();
+    if ((st = check_f32_ptrs({lengths, s_in, gs_out, gs_in}))) return st;
+    if (T == 0)
+        return hip_status(pass_state(gs_in, gs_out, B * Hv * Dk * Dv, (hipStream_t)stream),
+                          "gated_delta_backward state");
+    if ((st = check_ptrs({q, k, v, g, beta, go, gq, gk, gv, gg, gbeta}, elem_bytes(dtype)))) return st;
+    if (gs_in && !s_in) return fail(LINREC_ERR_INVALID_ARG, "gs_in without s_in");
+    const bool state = s_in != nullptr;
+    const linrec::DeltaShape s = delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, lengths, scale);
+    if (ckpt && (st = check_ckpt(ckpt, ckpt_bytes, gated_delta_checkpoint_size(B, T, Hk, Hv, Dk, Dv, dtype, s_in != nullptr)))) return st;
+    if ((st = check_ws(workspace, ws_bytes, ckpt ? delta_ds_bytes(s, state)
+                                                   : delta_layout(s, state, kDeltaBwd, nullptr, nullptr))))
+        return st;
+    const hipStream_t hs = (hipStream_t)stream;
+    linrec::DeltaChunks W;
+    if (ckpt) {
+        delta_layout(s, state, kDeltaCkpt, const_cast<void*>(ckpt), &W);
+        W.ds = workspace;
+    } else {
+        delta_layout(s, state, kDeltaBwd, workspace, &W);
+        const linrec::DeltaFwdArgs F{q, k, v, g, beta, s_in, nullptr, nullptr};
+        hipError_t e = linrec::run_delta_prepare(s, F, W, hs);
+        if (e == hipSuccess) e = linrec::run_delta_forward(s, F, W, hs);
+        if (e != hipSuccess) return hip_status(e, "gated_delta_backward forward launch");
+    }
+    const linrec::DeltaBwdArgs A{q, k, v, g, beta, s_in, go, gs_out, gq, gk, gv, gg, gbeta, gs_in};
+    return hip_status(linrec::run_delta_backward(s, A, W, hs), "gated_delta_backward launch");
 }
 
 LINREC_API int gated_delta_decode_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,

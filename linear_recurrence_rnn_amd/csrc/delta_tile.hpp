@@ -18,6 +18,7 @@
 #pragma once
 
 #include "elem_types.hpp"
+#include "gated_delta.hpp"
 
 namespace linrec {
 
@@ -89,6 +90,11 @@ __device__ __forceinline__ void load8(const E* __restrict__ p, int c, int D, boo
 
 template <class E> constexpr int kTerms = sizeof(E) == 2 ? 1 : 3;  // bfloat16 terms of an input
 
+// Terms of what the forward keeps for the backward in type KE: written as this many terms'
+// sum, read as this many terms in calls on E (two carry float32 kept for bfloat16 tensors).
+template <class KE> constexpr int kKeptSum = sizeof(KE) == 2 ? 1 : 3;
+template <class E, class KE> constexpr int kKeptTerms = sizeof(KE) == 2 ? 1 : sizeof(E) == 2 ? 2 : 3;
+
 template <class E>
 __device__ __forceinline__ Frag<kTerms<E>> to_frag(const E* x) {
     if constexpr (sizeof(E) == 2) {
@@ -129,6 +135,106 @@ __device__ __forceinline__ bf16x4 read_transposed(const bf16_t* p) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     typedef s16x4 __attribute__((address_space(3)))* lds_ptr;
     return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p));
+}
+
+// Tokens of batch row b.
+__device__ __forceinline__ int row_length(const DeltaShape& s, int64_t b) {
+    int64_t len = s.T;
+    if (s.lengths) {
+        const int64_t n = s.lengths[b];
+        len = n < 0 ? 0 : (n < len ? n : len);
+    }
+    return (int)len;
+}
+
+// Stage rows t0.. of a (B,T,H,D) tensor's head h as bfloat16 terms into dst[term][row][LD]: 256
+// threads, four lanes a row, zero past D (of 32*KT) and past the row's length.
+template <class E, int KT, bool VEC, int LD>
+__device__ __forceinline__ void stage_rows(const void* src, const DeltaShape& s, int64_t b, int H, int h, int D, int t0,
+                                           int len, bf16_t (*dst)[kChunk][LD]) {
+    const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3;
+    const E* p = reinterpret_cast<const E*>(src) + ((b * s.T + t0 + row) * H + h) * (int64_t)D;
+#pragma unroll
+    for (int i = 0; i < KT; ++i) {
+        const int c = 8 * (quarter + 4 * i);
+        E x[8];
+        load8<E, VEC>(p + c, c, D, t0 + row < len, x);
+        const Frag<kTerms<E>> f = to_frag<E>(x);
+#pragma unroll
+        for (int m = 0; m < kTerms<E>; ++m) *reinterpret_cast<bf16x8*>(&dst[m][row][c]) = f.t[m];
+    }
+}
+
+// A chunk's inverse as three bfloat16 terms.
+template <int LD>
+__device__ __forceinline__ void stage_inverse(const float* __restrict__ src, bf16_t (*dst)[kChunk][LD]) {
+    const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = 8 * (quarter + 4 * i);
+        float x[8];
+        load16<float>(src + row * kChunk + c, x);
+        load16<float>(src + row * kChunk + c + 4, x + 4);
+        const Frag<3> f = split<3>(x);
+#pragma unroll
+        for (int m = 0; m < 3; ++m) *reinterpret_cast<bf16x8*>(&dst[m][row][c]) = f.t[m];
+    }
+}
+
+// Row operand (A or B): 8 columns from c of row `row`.
+template <int N, int LD>
+__device__ __forceinline__ Frag<N> read_row(const bf16_t (*m)[kChunk][LD], int row, int c) {
+    Frag<N> f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) f.t[n] = *reinterpret_cast<const bf16x8*>(&m[n][row][c]);
+    return f;
+}
+
+// Column operand of the transposed matrix: rows row0 + 8g.. (32 of them over the wave), columns
+// c0 + c(r); PERM: the columns of D tile `half` of a 32-column block, else 16 in order.
+template <int N, bool PERM, int LD>
+__device__ __forceinline__ Frag<N> read_col(const bf16_t (*m)[kChunk][LD], int row0, int c0, int half) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    const int row = row0 + 8 * g + (r >> 2), c = PERM ? c0 + 8 * (r & 3) + 4 * half : c0 + 4 * (r & 3);
+    Frag<N> f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const bf16x4 lo = read_transposed(&m[n][row][c]), hi = read_transposed(&m[n][row + 4][c]);
+        f.t[n] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    return f;
+}
+
+// B operands of the product with the identity that turns an A operand's 32 rows k into D's
+// columns: columns r = k - 16*which.
+__device__ __forceinline__ Frag<1> identity_frag(int which) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    Frag<1> f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.t[0][i] = (bf16_t)((8 * g + i) == 16 * which + r ? 1.f : 0.f);
+    return f;
+}
+
+// Four consecutive elements.
+template <class E>
+__device__ __forceinline__ void store4(E* p, const f32x4& x) {
+    typedef E E4 __attribute__((ext_vector_type(4)));
+    E4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = (E)x[e];
+    *reinterpret_cast<E4*>(p) = y;
+}
+
+// Columns c..c+3 of a row of D; VEC: D % 4 == 0 and the row 4*sizeof(E)-byte aligned.
+template <class E, bool VEC>
+__device__ __forceinline__ void store_cols(E* row, int c, int D, const f32x4& x) {
+    if constexpr (VEC) {
+        if (c < D) store4<E>(row + c, x);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < D) row[c + e] = (E)x[e];
+    }
 }
 
 }  // namespace linrec

@@ -26,21 +26,48 @@ struct DeltaFwdArgs {
     const void* v;       // (B,T,Hv,Dv)
     const void *g, *beta;  // (B,T,Hv)
     const float* s_in;   // (B,Hv,Dk,Dv), or null (zero)
-    void* o;             // (B,T,Hv,Dv)
+    void* o;             // (B,T,Hv,Dv); null in a call that only keeps for the backward
     float* s_out;        // (B,Hv,Dk,Dv), or null; may be s_in
 };
 
 // What the chunked kernels keep of each chunk of 64 tokens, (B*Hv, chunks, ...):
 //   tinv  (64,64) float32   (I + strictly lower e^{gam_i - gam_j} (k_i.k_j) beta_j)^{-1}
 //   gam   (64) float64      decays cumulated within the chunk
+// and for the backward, in blocks of 16 value channels (delta_blocks(s) of them, zero past Dv),
+// of the tensors' type, or float32 (delta_keeps_f32):
+//   x     (blocks, 64, 16)       x_t of the recurrence
+//   s0    (blocks, dkp, 16)      the state before the chunk, dkp = Dk rounded up (delta_dkp)
+//   ds    (blocks, dkp, 16)      the gradient of the state after the chunk
 struct DeltaChunks {
     float* tinv;
     double* gam;
+    void *x, *s0;  // null: not kept
+    void* ds;
 };
 inline int64_t delta_chunks(const DeltaShape& s) { return s.B * s.Hv * ((s.T + 63) / 64); }
+// A carried state's gradient lands on few tokens (the last ones of a piece), and pieces are
+// chained through it: what is kept is then float32, so that those tokens' gradients are not
+// limited by the rounding of x and the states.
+inline bool delta_keeps_f32(int dtype, const void* s_in) { return dtype == 0 || s_in != nullptr; }
+inline int delta_blocks(const DeltaShape& s) { return (s.Dv + 63) / 64 * 4; }
+inline int delta_dkp(const DeltaShape& s) { return s.Dk <= 32 ? 32 : s.Dk <= 64 ? 64 : 128; }
+
+struct DeltaBwdArgs {
+    const void *q, *k, *v, *g, *beta;
+    const float* s_in;
+    const void* go;       // (B,T,Hv,Dv)
+    const float* gs_out;  // (B,Hv,Dk,Dv), or null (zero)
+    void *gq, *gk;        // (B,T,Hk,Dk)
+    void* gv;             // (B,T,Hv,Dv)
+    void *gg, *gbeta;     // (B,T,Hv)
+    float* gs_in;         // (B,Hv,Dk,Dv), or null; may be gs_out; only with s_in
+};
 
 hipError_t run_delta_prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st);
 hipError_t run_delta_forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st);
+
+// The gradients, from what run_delta_prepare and a keeping run_delta_forward left in W.
+hipError_t run_delta_backward(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st);
 
 // Token by token, the state in registers: decoding and the shortest sequences.
 hipError_t run_delta_recurrent(const DeltaShape& s, const DeltaFwdArgs& A, hipStream_t st);

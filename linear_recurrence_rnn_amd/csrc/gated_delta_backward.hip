@@ -1,0 +1,593 @@
+// gated_delta_backward.hip -- gradients of the gated delta rule, in the forward's chunks.
+//
+// With dO and dS' (the gradient of the state after the chunk), and the forward's G, P, inverse
+// N = (I + G diag(beta))^{-1}, X, and state S before the chunk:
+//   dU = P^T dO + diag(e^{gam_63 - gam}) K dS'
+//   dZ = N^T (beta dU) = dV
+//   dS = e^{gam_63} dS' + scale Q^T diag(e^gam) dO - K^T diag(e^gam) dZ
+// is a chain over the chunks in reverse (first kernel; it writes dV and every dS').  The rest is
+// local to a chunk (second kernel), with H = dO X^T, E = dZ X^T, L_ij = e^{gam_i - gam_j},
+// q' = scale q, W = e^{gam_63 - gam_j} dS' x_j, M_ij = L_ij (q'_i.k_j H_ij - [i > j] k_i.k_j E_ij):
+//   dq_i    = scale (e^{gam_i} S dO_i + sum_{j<=i} L_ij beta_j H_ij k_j)
+//   dk_j    = beta_j (W_j + sum_{i>=j} L_ij H_ij q'_i - sum_{i>j} L_ij E_ij k_i)
+//             - e^{gam_j} S dZ_j - sum_{i<j} L_ji beta_i E_ji k_i
+//   dbeta_j = sum_i M_ij + k_j.W_j
+//   dg_t    = sum_{i>=t} (q'_i.e^{gam_i} S dO_i - k_i.e^{gam_i} S dZ_i) + sum_{j<t} beta_j k_j.W_j
+//             + e^{gam_63} <S, dS'> + sum_{i>=t>j} beta_j M_ij
+// (every pair of a write before t and a read at or after t carries e^{g_t}).
+#include "gated_delta.hpp"
+#include "delta_tile.hpp"
+
+namespace linrec {
+
+namespace {
+
+// ---- the chain of the state's gradient ----------------------------------------------------------
+// The forward chain's layout: four waves, 16*CT value channels each, dS in registers.  NS terms
+// for the gradient of the state and what flows into it: three where a float32 result leaves the
+// kernel or is kept (KE), two (2^-16) where all are bfloat16.
+template <class E, int KT, int NS>
+struct ChainLds {
+    static constexpr int NI = kTerms<E>;
+    static constexpr int LK = 32 * KT + 8, LT = kChunk + 8;
+    bf16_t k[NI][kChunk][LK], q[NI][kChunk][LK];
+    bf16_t t[3][kChunk][LT];
+    bf16_t p[NS][kChunk][LT];  // P^T
+    double gam[kChunk];
+    float eg[kChunk], ew[kChunk], be[kChunk];
+};
+
+template <class E, class KE, int KT, int CT, bool VEC, int NS>
+__global__ __launch_bounds__(256) void delta_chain_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc,
+                                                          int ntile) {
+    typedef ChainLds<E, KT, NS> Lds;
+    constexpr int NI = kTerms<E>;
+    extern __shared__ __align__(16) char lds_raw[];
+    Lds& L = *reinterpret_cast<Lds*>(lds_raw);
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int tile = (int)(blockIdx.x % ntile);
+    const int64_t bh = blockIdx.x / ntile;
+    const int h = (int)(bh % s.Hv), hk = h / (s.Hv / s.Hk);
+    const int64_t b = bh / s.Hv;
+    const int len = row_length(s, b);
+    const int c0 = tile * 64 * CT + wave * 16 * CT;
+    const int Dk = s.Dk, Dv = s.Dv;
+    const int nblk = ntile * 4 * CT;
+
+    f32x4 S[KT][2][CT];  // dS, in the forward's layout of S
+    const int64_t sb = bh * (int64_t)Dk * Dv;
+#pragma unroll
+    for (int kk = 0; kk < KT; ++kk)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 32 * kk + 8 * g + 4 * half + e, col = c0 + 16 * ct + r;
+                    S[kk][half][ct][e] =
+                        (A.gs_out && row < Dk && col < Dv) ? A.gs_out[sb + (int64_t)row * Dv + col] : 0.f;
+                }
+    const Frag<1> ident[2] = {identity_frag(0), identity_frag(1)};
+
+    const int nlive = (len + kChunk - 1) / kChunk;
+    for (int n = nlive - 1; n >= 0; --n) {
+        const int t0 = n * kChunk;
+        const int64_t cb = bh * nc + n;
+        __syncthreads();  // the previous chunk's tiles have been read
+        stage_rows<E, KT, VEC>(A.k, s, b, s.Hk, hk, Dk, t0, len, L.k);
+        stage_rows<E, KT, VEC>(A.q, s, b, s.Hk, hk, Dk, t0, len, L.q);
+        stage_inverse(W.tinv + cb * (kChunk * kChunk), L.t);
+        if (tid < kChunk) {
+            const bool on = t0 + tid < len;
+            const double gm = W.gam[cb * kChunk + tid], end = W.gam[cb * kChunk + kChunk - 1];
+            L.gam[tid] = gm;
+            L.eg[tid] = decay_exp(gm, 0.0);
+            L.ew[tid] = decay_exp(end, gm);
+            L.be[tid] = on ? (float)reinterpret_cast<const E*>(A.beta)[(b * s.T + t0 + tid) * s.Hv + h] : 0.f;
+        }
+        __syncthreads();
+        // P^T, rows 16*wave..: tiles of Q K^T (rows i, columns j), stored as P^T[j][i].
+        {
+            const int j = 16 * wave + r;
+            const double gj = L.gam[j];
+            for (int it = wave & 2; it < 4; ++it) {
+                f32x4 c = {0.f, 0.f, 0.f, 0.f};
+                if (it >= wave)
+#pragma unroll
+                    for (int kk = 0; kk < KT; ++kk) {
+                        const int col = 32 * kk + 8 * g;
+                        mma(c, read_row<NI>(L.q, 16 * it + r, col), read_row<NI>(L.k, j, col));
+                    }
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 16 * it + 4 * g + e;
+                    x[e] = j <= i ? s.scale * decay_exp(L.gam[i], gj) * c[e] : 0.f;
+                    x[4 + e] = 0.f;
+                }
+                const Frag<NS> f = split<NS>(x);
+#pragma unroll
+                for (int m = 0; m < NS; ++m)
+                    *reinterpret_cast<bf16x4*>(&L.p[m][j][16 * it + 4 * g]) =
+                        __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
+            }
+        }
+        // K dS' (dS' is also stored, turned so that a lane holds 4 value channels).
+        f32x4 U[2][2][CT];  // rows 32*k2 + tile_row(m, half)
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) U[k2][half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+            Frag<NS> fs[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                fs[ct] = split_tiles<NS>(S[kk][0][ct], S[kk][1][ct]);
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                    mma<NS, 1, kKeptSum<KE>, 1>(x, fs[ct], ident[which]);
+                    store4<KE>(reinterpret_cast<KE*>(W.ds) +
+                                  ((cb * nblk + c0 / 16 + ct) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
+                              x);
+                }
+            }
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const Frag<NI> fk = read_row<NI>(L.k, 32 * k2 + tile_row(r, half), 32 * kk + 8 * g);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(U[k2][half][ct], fk, fs[ct]);
+                }
+        }
+        // dO in the D layout, as B operand, and scaled for the state's gradient.
+        Frag<NI> fo[2][CT];
+        Frag<NS> fd[2][CT];
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+            f32x4 d[2][CT];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int row = t0 + 32 * k2 + tile_row(r, half);
+                E x[8];
+                const int c = c0 + 8 * g;
+                const bool on = row < len && (CT == 2 || g < 2);
+                load8<E, VEC>(reinterpret_cast<const E*>(A.go) + ((b * s.T + row) * s.Hv + h) * (int64_t)Dv + c, c, Dv,
+                              on, x);
+                const Frag<NI> fv = to_frag<E>(x);
+                const f32x4 ew = *reinterpret_cast<const f32x4*>(&L.ew[32 * k2 + 8 * g + 4 * half]);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    d[half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+                    mma<NI, 1>(d[half][ct], fv, ident[ct]);
+                    U[k2][half][ct] *= ew;
+                }
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                fo[k2][ct] = split_tiles<NI>(d[0][ct], d[1][ct]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    d[half][ct] *= s.scale * *reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
+                fd[k2][ct] = split_tiles<NS>(d[0][ct], d[1][ct]);
+            }
+        }
+        __syncthreads();  // P^T is there
+        Frag<NS> fb[2][CT];  // beta dU
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int kz = k2; kz < 2; ++kz) {
+                    const Frag<NS> fp = read_row<NS>(L.p, 32 * k2 + tile_row(r, half), 32 * kz + 8 * g);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(U[k2][half][ct], fp, fo[kz][ct]);
+                }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    U[k2][half][ct] *= *reinterpret_cast<const f32x4*>(&L.be[32 * k2 + 8 * g + 4 * half]);
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) fb[k2][ct] = split_tiles<NS>(U[k2][0][ct], U[k2][1][ct]);
+        }
+        // dZ = N^T (beta dU).
+        f32x4 Z[2][2][CT];
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) Z[k2][half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kz = k2; kz < 2; ++kz) {
+                    const Frag<NS> ft = read_col<NS, true>(L.t, 32 * kz, 32 * k2, half);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) mma(Z[k2][half][ct], ft, fb[kz][ct]);
+                }
+            }
+        // dV, turned; and -e^gam dZ for the state's gradient.
+        Frag<NS> fz[2][CT];
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const Frag<NI> fx = split_tiles<NI>(Z[k2][0][ct], Z[k2][1][ct]);
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                    mma<NI, 1>(x, fx, ident[which]);
+                    const int t = t0 + 32 * k2 + 16 * which + r;
+                    if (t < s.T)
+                        store_cols<E, VEC>(reinterpret_cast<E*>(A.gv) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv,
+                                           c0 + 16 * ct + 4 * g, Dv, x);
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    Z[k2][half][ct] *= -*reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
+                fz[k2][ct] = split_tiles<NS>(Z[k2][0][ct], Z[k2][1][ct]);
+            }
+        const float end = L.eg[kChunk - 1];
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) S[kk][half][ct] *= end;
+#pragma unroll
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    const Frag<NI> fq = read_col<NI, true>(L.q, 32 * k2, 32 * kk, half);
+                    const Frag<NI> fk = read_col<NI, true>(L.k, 32 * k2, 32 * kk, half);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) {
+                        mma(S[kk][half][ct], fq, fd[k2][ct]);
+                        mma(S[kk][half][ct], fk, fz[k2][ct]);
+                    }
+                }
+            }
+    }
+    for (int64_t t = (int64_t)nlive * kChunk + wave; t < s.T; t += 4) {
+        E* op = reinterpret_cast<E*>(A.gv) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
+        for (int c = tile * 64 * CT + lane; c < (tile + 1) * 64 * CT && c < Dv; c += 64) op[c] = (E)0.f;
+    }
+    if (A.gs_in)
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = 32 * kk + 8 * g + 4 * half + e, col = c0 + 16 * ct + r;
+                        if (row < Dk && col < Dv) A.gs_in[sb + (int64_t)row * Dv + col] = S[kk][half][ct][e];
+                    }
+}
+
+// ---- the gradients of a chunk ---------------------------------------------------------------------
+// A workgroup takes one chunk of one key head and goes through the value heads that read it, so
+// dq and dk are summed over them in head order, in registers.  Wave w owns the chunk's tokens
+// 16w..16w+15 as columns: dq^T, dk^T tiles (rows: key channels), and the tiles of H^T and E^T
+// (rows j <= its i).  Operands are the tensors' own type (one bfloat16 term, or three).
+template <class E, int KT>
+struct GradLds {
+    static constexpr int NI = kTerms<E>;
+    static constexpr int LK = 32 * KT + 8, LT = kChunk + 8;
+    bf16_t k[NI][kChunk][LK], q[NI][kChunk][LK];
+    bf16_t h[NI][kChunk][LT], e[NI][kChunk][LT];  // scale L beta H, L beta E: rows i, columns j
+    double gam[kChunk];
+    float be[kChunk];
+    float col[4][kChunk];  // sums over each wave's i > j of M_ij; M_jj on its own, so that sums that
+                           // ought to cancel in dg hold nothing that does not belong there
+    float row[kChunk], diag[kChunk], a[kChunk], wr[kChunk];
+    float dot[4];
+};
+
+// 8 value channels from 32*kv + 8g of row `row` of a matrix kept in blocks of 16 channels.
+template <class KE, int N>
+__device__ __forceinline__ Frag<N> read_block(const KE* m, int rows, int row, int kv) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const KE* p = m + ((int64_t)(2 * kv + (g >> 1)) * rows + row) * 16 + 8 * (g & 1);
+    KE x[8];
+    load8<KE, true>(p, 0, 8, true, x);
+    if constexpr (sizeof(KE) == 2) return to_frag<KE>(x);
+    else return split<N>(x);
+}
+
+template <class E, class KE, int KT, bool VEC>
+__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc, int nblk) {
+    typedef GradLds<E, KT> Lds;
+    constexpr int NI = kTerms<E>, NK = kKeptTerms<E, KE>, DT = 2 * KT;  // tiles of key channels
+    extern __shared__ __align__(16) char lds_raw[];
+    Lds& L = *reinterpret_cast<Lds*>(lds_raw);
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int n = (int)(blockIdx.x % nc);
+    const int64_t bk = blockIdx.x / nc;
+    const int hk = (int)(bk % s.Hk), rep = s.Hv / s.Hk;
+    const int64_t b = bk / s.Hk;
+    const int len = row_length(s, b), t0 = n * kChunk;
+    const int Dk = s.Dk, Dv = s.Dv;
+    const int mine = 16 * wave + r, tok = t0 + mine;  // this lane's token
+    const int64_t tokh = (b * s.T + tok) * s.Hv;
+    if (t0 >= len) {  // absent tokens: zero gradients
+        for (int i = wave; i < kChunk && t0 + i < s.T; i += 4) {
+            const int64_t at = ((b * s.T + t0 + i) * s.Hk + hk) * (int64_t)Dk;
+            for (int c = lane; c < Dk; c += 64) {
+                reinterpret_cast<E*>(A.gq)[at + c] = (E)0.f;
+                reinterpret_cast<E*>(A.gk)[at + c] = (E)0.f;
+            }
+            for (int c = lane; c < rep; c += 64) {
+                const int64_t p = (b * s.T + t0 + i) * s.Hv + hk * rep + c;
+                reinterpret_cast<E*>(A.gg)[p] = (E)0.f;
+                reinterpret_cast<E*>(A.gbeta)[p] = (E)0.f;
+            }
+        }
+        return;
+    }
+    stage_rows<E, KT, VEC>(A.k, s, b, s.Hk, hk, Dk, t0, len, L.k);
+    stage_rows<E, KT, VEC>(A.q, s, b, s.Hk, hk, Dk, t0, len, L.q);
+    __syncthreads();
+    // q_i.k_j and k_i.k_j: rows j (tiles up to this wave's), columns i.
+    f32x4 qk[4], kk_[4];
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+        qk[jt] = kk_[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (jt <= wave)
+#pragma unroll
+            for (int kk = 0; kk < KT; ++kk) {
+                const int col = 32 * kk + 8 * g;
+                const Frag<NI> fk = read_row<NI>(L.k, 16 * jt + r, col);
+                mma(qk[jt], fk, read_row<NI>(L.q, mine, col));
+                mma(kk_[jt], fk, read_row<NI>(L.k, mine, col));
+            }
+    }
+    f32x4 dq[DT], dk[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) dq[d] = dk[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    for (int hr = 0; hr < rep; ++hr) {
+        const int h = hk * rep + hr;
+        const int64_t cb = (b * s.Hv + h) * nc + n;
+        if (tid < kChunk) {
+            L.gam[tid] = W.gam[cb * kChunk + tid];
+            L.be[tid] = t0 + tid < len
+                            ? (float)reinterpret_cast<const E*>(A.beta)[(b * s.T + t0 + tid) * s.Hv + h]
+                            : 0.f;
+        }
+        // H^T, E^T and the products with S and dS'.
+        const KE* X = reinterpret_cast<const KE*>(W.x) + cb * nblk * (kChunk * 16);
+        const KE* S0 = reinterpret_cast<const KE*>(W.s0) + cb * nblk * (32 * KT * 16);
+        const KE* DS = reinterpret_cast<const KE*>(W.ds) + cb * nblk * (32 * KT * 16);
+        const E* go = reinterpret_cast<const E*>(A.go) + (tokh + h) * Dv;
+        const E* gz = reinterpret_cast<const E*>(A.gv) + (tokh + h) * Dv;
+        f32x4 H[4], Z[4], rq[DT], rk[DT], wk[DT];
+        float dot = 0.f;
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) H[jt] = Z[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int d = 0; d < DT; ++d) rq[d] = rk[d] = wk[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int kv = 0; 32 * kv < Dv; ++kv) {
+            E x[8];
+            const int c = 32 * kv + 8 * g;
+            load8<E, VEC>(go + c, c, Dv, tok < len, x);
+            const Frag<NI> fo = to_frag<E>(x);
+            load8<E, VEC>(gz + c, c, Dv, tok < len, x);
+            const Frag<NI> fz = to_frag<E>(x);
+            const Frag<NK> fx = read_block<KE, NK>(X, kChunk, mine, kv);
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+                if (jt <= wave) {
+                    const Frag<NK> f = read_block<KE, NK>(X, kChunk, 16 * jt + r, kv);
+                    mma(H[jt], f, fo);
+                    mma(Z[jt], f, fz);
+                }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const Frag<NK> f = read_block<KE, NK>(S0, 32 * KT, 16 * d + r, kv);
+                mma(rq[d], f, fo);
+                mma(rk[d], f, fz);
+                const Frag<NK> fd = read_block<KE, NK>(DS, 32 * KT, 16 * d + r, kv);
+                mma(wk[d], fd, fx);
+                if ((d & 3) == wave)  // each wave a quarter of <S, dS'>
+#pragma unroll
+                    for (int m = 0; m < NK; ++m)
+#pragma unroll
+                        for (int o = 0; o < NK; ++o)
+                            if (m + o < NK)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) dot = fmaf((float)f.t[m][i], (float)fd.t[o][i], dot);
+            }
+        }
+        __syncthreads();  // gam, beta are there
+        const double gi = L.gam[mine], gend = L.gam[kChunk - 1];
+        const float eg = decay_exp(gi, 0.0), ew = decay_exp(gend, gi), be = L.be[mine];
+        // M, its sums, and the weights scale L beta H and L beta E.
+        float rowsum = 0.f;
+#pragma unroll
+        for (int jt = 0; jt < 4; ++jt) {
+            if (jt > (wave | 1)) {
+                if (lane < 16) L.col[wave][16 * jt + lane] = 0.f;
+                continue;
+            }
+            float hw[8], ez[8];
+            f32x4 m4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = 16 * jt + 4 * g + e;
+                const float l = j <= mine ? decay_exp(gi, L.gam[j]) : 0.f, ls = j < mine ? l : 0.f;
+                const float bj = L.be[j];
+                const float hh = s.scale * l * H[jt][e], zz = ls * Z[jt][e];
+                m4[e] = qk[jt][e] * hh - kk_[jt][e] * zz;
+                if (j == mine) {
+                    L.diag[mine] = m4[e];
+                    m4[e] = 0.f;
+                }
+                rowsum = fmaf(bj, m4[e], rowsum);
+                hw[e] = bj * hh;
+                ez[e] = bj * zz;
+                hw[4 + e] = ez[4 + e] = 0.f;
+            }
+            const Frag<NI> fh = split<NI>(hw), fe = split<NI>(ez);
+#pragma unroll
+            for (int m = 0; m < NI; ++m) {
+                *reinterpret_cast<bf16x4*>(&L.h[m][mine][16 * jt + 4 * g]) =
+                    __builtin_shufflevector(fh.t[m], fh.t[m], 0, 1, 2, 3);
+                *reinterpret_cast<bf16x4*>(&L.e[m][mine][16 * jt + 4 * g]) =
+                    __builtin_shufflevector(fe.t[m], fe.t[m], 0, 1, 2, 3);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) m4[e] += __shfl_xor(m4[e], o);
+                if (r == 0) L.col[wave][16 * jt + 4 * g + e] = m4[e];
+            }
+        }
+        rowsum += __shfl_xor(rowsum, 16);
+        rowsum += __shfl_xor(rowsum, 32);
+        // Sums with q and k over the key channels, and the parts of dq, dk from S and dS'.
+        float asum = 0.f, wsum = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            f32x4 q4 = {0.f, 0.f, 0.f, 0.f}, k4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = NI - 1; m >= 0; --m) {
+                const bf16x4 a = *reinterpret_cast<const bf16x4*>(&L.q[m][mine][16 * d + 4 * g]);
+                const bf16x4 c = *reinterpret_cast<const bf16x4*>(&L.k[m][mine][16 * d + 4 * g]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) q4[e] += (float)a[e], k4[e] += (float)c[e];
+            }
+            rq[d] *= s.scale * eg;
+            rk[d] *= eg;
+            wk[d] *= ew;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                asum = fmaf(q4[e], rq[d][e], asum);
+                asum = fmaf(-k4[e], rk[d][e], asum);
+                wsum = fmaf(k4[e], wk[d][e], wsum);
+            }
+            dq[d] += rq[d];
+            dk[d] += be * wk[d] - rk[d];
+        }
+        asum += __shfl_xor(asum, 16);
+        asum += __shfl_xor(asum, 32);
+        wsum += __shfl_xor(wsum, 16);
+        wsum += __shfl_xor(wsum, 32);
+        if (g == 0) L.row[mine] = rowsum, L.a[mine] = asum, L.wr[mine] = wsum;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) dot += __shfl_xor(dot, o);
+        if (lane == 0) L.dot[wave] = dot;
+        __syncthreads();  // the weights and the sums are there
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+            // Rows j (for dq) or i (for dk) 32*k2..; this wave's columns see the ones it is coupled to.
+            const bool below = 2 * k2 <= wave, above = 2 * k2 + 1 >= wave;
+            Frag<NI> hr_, ec, er;
+            if (below) hr_ = read_row<NI>(L.h, mine, 32 * k2 + 8 * g), er = read_row<NI>(L.e, mine, 32 * k2 + 8 * g);
+            Frag<NI> hc;
+            if (above) {
+                hc = read_col<NI, false>(L.h, 32 * k2, 16 * wave, 0);
+                ec = read_col<NI, false>(L.e, 32 * k2, 16 * wave, 0);
+#pragma unroll
+                for (int m = 0; m < NI; ++m)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ec.t[m][i] = -ec.t[m][i];
+            }
+            if (below)
+#pragma unroll
+                for (int m = 0; m < NI; ++m)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) er.t[m][i] = -er.t[m][i];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const Frag<NI> fk = read_col<NI, false>(L.k, 32 * k2, 16 * d, 0);
+                if (below) {
+                    mma(dq[d], fk, hr_);
+                    mma(dk[d], fk, er);
+                }
+                if (above) {
+                    mma(dk[d], read_col<NI, false>(L.q, 32 * k2, 16 * d, 0), hc);
+                    mma(dk[d], fk, ec);
+                }
+            }
+        }
+        if (wave == 0) {
+            const float bt = L.be[lane], wr = L.wr[lane];
+            const float cs = L.col[0][lane] + L.col[1][lane] + L.col[2][lane] + L.col[3][lane];
+            const double a = L.a[lane], bw = (double)bt * wr, dcr = (double)bt * cs - (double)L.row[lane];
+            const double sa = wave_cumsum(a), sw = wave_cumsum(bw + dcr);
+            const double through =
+                (double)decay_exp(L.gam[kChunk - 1], 0.0) * ((double)L.dot[0] + L.dot[1] + L.dot[2] + L.dot[3]);
+            const double all = __shfl(sa, 63);
+            const double dg = (all - sa + a) + (sw - bw - dcr) + through;
+            const int t = t0 + lane;
+            if (t < s.T) {
+                const int64_t at = (b * s.T + t) * s.Hv + h;
+                reinterpret_cast<E*>(A.gg)[at] = (E)(t < len ? (float)dg : 0.f);
+                reinterpret_cast<E*>(A.gbeta)[at] = (E)(t < len ? cs + L.diag[lane] + wr : 0.f);
+            }
+        }
+        __syncthreads();  // the next head writes the weights again
+    }
+    if (tok < s.T) {
+        const int64_t at = ((b * s.T + tok) * s.Hk + hk) * (int64_t)Dk;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            store_cols<E, VEC>(reinterpret_cast<E*>(A.gq) + at, 16 * d + 4 * g, Dk, dq[d]);
+            store_cols<E, VEC>(reinterpret_cast<E*>(A.gk) + at, 16 * d + 4 * g, Dk, dk[d]);
+        }
+    }
+}
+
+bool vec_ok(const DeltaShape& s, const DeltaBwdArgs& A) {
+    const uintptr_t all = (uintptr_t)A.q | (uintptr_t)A.k | (uintptr_t)A.go | (uintptr_t)A.gq | (uintptr_t)A.gk |
+                          (uintptr_t)A.gv;
+    return s.Dk % 8 == 0 && s.Dv % 8 == 0 && all % 16 == 0;
+}
+
+template <class K>
+hipError_t launch(K kernel, int64_t blocks, int bytes, hipStream_t st, const DeltaShape& s, const DeltaBwdArgs& A,
+                  const DeltaChunks& W, int last) {
+    // More dynamic LDS than the default 64 KiB has to be asked for.
+    hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), bytes, st, s, A, W,
+                       (int)((s.T + kChunk - 1) / kChunk), last);
+    return hipGetLastError();
+}
+
+template <class E, class KE, int KT, int NS, bool VEC>
+hipError_t backward(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    const int ntile = (s.Dv + 63) / 64;
+    const hipError_t e = launch(delta_chain_kernel<E, KE, KT, 1, VEC, NS>, s.B * s.Hv * ntile,
+                                (int)sizeof(ChainLds<E, KT, NS>), st, s, A, W, ntile);
+    if (e != hipSuccess) return e;
+    return launch(delta_grad_kernel<E, KE, KT, VEC>, s.B * s.Hk * ((s.T + kChunk - 1) / kChunk),
+                  (int)sizeof(GradLds<E, KT>), st, s, A, W, delta_blocks(s));
+}
+
+template <class E, class KE, int NS, bool VEC>
+hipError_t by_width(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    if (s.Dk <= 32) return backward<E, KE, 1, NS, VEC>(s, A, W, st);
+    if (s.Dk <= 64) return backward<E, KE, 2, NS, VEC>(s, A, W, st);
+    return backward<E, KE, 4, NS, VEC>(s, A, W, st);
+}
+
+template <bool VEC>
+hipError_t by_type(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    if (s.dtype != kBf16) return by_width<float, float, 3, VEC>(s, A, W, st);
+    return delta_keeps_f32(s.dtype, A.s_in) ? by_width<bf16_t, float, 3, VEC>(s, A, W, st)
+                                            : by_width<bf16_t, bf16_t, 2, VEC>(s, A, W, st);
+}
+
+}  // namespace
+
+hipError_t run_delta_backward(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    return vec_ok(s, A) ? by_type<true>(s, A, W, st) : by_type<false>(s, A, W, st);
+}
+
+}  // namespace linrec

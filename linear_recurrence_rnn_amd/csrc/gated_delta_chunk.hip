@@ -15,15 +15,6 @@ namespace linrec {
 
 namespace {
 
-__device__ __forceinline__ int row_length(const DeltaShape& s, int64_t b) {
-    int64_t len = s.T;
-    if (s.lengths) {
-        const int64_t n = s.lengths[b];
-        len = n < 0 ? 0 : (n < len ? n : len);
-    }
-    return (int)len;
-}
-
 // ---- the chunks' inverses -------------------------------------------------------------------
 // One wave a chunk.  K's fragments serve as both operands of K K^T (the A and B layouts of a
 // matrix and its transpose are one).  Lane c then solves for column c of the inverse:
@@ -113,11 +104,15 @@ struct FwdLds {
     float eg[kChunk], ew[kChunk], be[kChunk];
 };
 
-template <class E, int KT, int CT, bool VEC>
+// What the chain leaves: o, and what the backward starts from (of type KE).
+constexpr int kOut = 1, kKeep = 2;
+
+template <class E, class KE, int KT, int CT, bool VEC, int MODE>
 __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaFwdArgs A, DeltaChunks W, int nc,
                                                             int ntile) {
     typedef FwdLds<E, KT, CT, VEC> Lds;
     constexpr int NI = kTerms<E>, NO = Lds::NO, NS = 3;
+    constexpr bool OUT = MODE & kOut, KEEP = MODE & kKeep;
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
@@ -128,6 +123,7 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
     const int len = row_length(s, b);
     const int c0 = tile * 64 * CT + wave * 16 * CT;  // this wave's first value channel
     const int Dk = s.Dk, Dv = s.Dv;
+    const int nblk = ntile * 4 * CT;  // blocks of 16 value channels
 
     // State: D tiles S[kk][half][ct], rows 32kk + tile_row(m, half), columns c0 + 16ct + r.
     f32x4 S[KT][2][CT];
@@ -143,11 +139,7 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
                     const int row = 32 * kk + 8 * g + 4 * half + e, col = c0 + 16 * ct + r;
                     S[kk][half][ct][e] = (A.s_in && row < Dk && col < Dv) ? A.s_in[sb + (int64_t)row * Dv + col] : 0.f;
                 }
-    Frag<1> ident[2];  // B operand: rows 16ct.. of it are the identity
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int ct = 0; ct < 2; ++ct) ident[ct].t[0][i] = (bf16_t)((8 * g + i) == 16 * ct + r ? 1.f : 0.f);
+    const Frag<1> ident[2] = {identity_frag(0), identity_frag(1)};
 
     const int nlive = (len + kChunk - 1) / kChunk;
     for (int n = 0; n < nlive; ++n) {
@@ -156,33 +148,9 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
         __syncthreads();  // the previous chunk's tiles have been read
         // Stage K, Q (4 lanes a row), the inverse, the decays.
         {
-            const int row = tid >> 2, quarter = tid & 3;
-            const bool live = t0 + row < len;
-            const int64_t at = ((b * s.T + t0 + row) * s.Hk + hk) * (int64_t)Dk;
-#pragma unroll
-            for (int i = 0; i < KT; ++i) {
-                const int c = 8 * (quarter + 4 * i);
-                E x[8];
-                load8<E, VEC>(reinterpret_cast<const E*>(A.k) + at + c, c, Dk, live, x);
-                Frag<NI> f = to_frag<E>(x);
-#pragma unroll
-                for (int m = 0; m < NI; ++m) *reinterpret_cast<bf16x8*>(&L.k[m][row][c]) = f.t[m];
-                load8<E, VEC>(reinterpret_cast<const E*>(A.q) + at + c, c, Dk, live, x);
-                f = to_frag<E>(x);
-#pragma unroll
-                for (int m = 0; m < NI; ++m) *reinterpret_cast<bf16x8*>(&L.q[m][row][c]) = f.t[m];
-            }
-            const float* ti = W.tinv + cb * (kChunk * kChunk) + row * kChunk;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = 8 * (quarter + 4 * i);
-                float x[8];
-                load16<float>(ti + c, x);
-                load16<float>(ti + c + 4, x + 4);
-                const Frag<3> f = split<3>(x);
-#pragma unroll
-                for (int m = 0; m < 3; ++m) *reinterpret_cast<bf16x8*>(&L.t[m][row][c]) = f.t[m];
-            }
+            stage_rows<E, KT, VEC>(A.k, s, b, s.Hk, hk, Dk, t0, len, L.k);
+            if constexpr (OUT) stage_rows<E, KT, VEC>(A.q, s, b, s.Hk, hk, Dk, t0, len, L.q);
+            stage_inverse(W.tinv + cb * (kChunk * kChunk), L.t);
             if (tid < kChunk) {
                 const bool on = t0 + tid < len;
                 const double gm = W.gam[cb * kChunk + tid], end = W.gam[cb * kChunk + kChunk - 1];
@@ -194,7 +162,7 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
         }
         __syncthreads();
         // P, rows 16*wave..: tiles of K Q^T (rows j, columns i), stored as P[i][j].
-        {
+        if constexpr (OUT) {
             const int i = 16 * wave + r;
             const double gi = L.gam[i];
             for (int jt = 0; jt <= (wave | 1); ++jt) {
@@ -202,13 +170,8 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
                 if (jt <= wave)
 #pragma unroll
                     for (int kk = 0; kk < KT; ++kk) {
-                        Frag<NI> fk, fq;
-#pragma unroll
-                        for (int m = 0; m < NI; ++m) {
-                            fk.t[m] = *reinterpret_cast<const bf16x8*>(&L.k[m][16 * jt + r][32 * kk + 8 * g]);
-                            fq.t[m] = *reinterpret_cast<const bf16x8*>(&L.q[m][i][32 * kk + 8 * g]);
-                        }
-                        mma(c, fk, fq);
+                        const int col = 32 * kk + 8 * g;
+                        mma(c, read_row<NI>(L.k, 16 * jt + r, col), read_row<NI>(L.q, i, col));
                     }
                 float x[8];
 #pragma unroll
@@ -240,21 +203,28 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
             Frag<NS> fs[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) fs[ct] = split_tiles<NS>(S[kk][0][ct], S[kk][1][ct]);
+            if constexpr (KEEP)  // S before the chunk, turned so that a lane holds 4 value channels
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int which = 0; which < 2; ++which) {
+                        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                        mma<NS, 1, kKeptSum<KE>, 1>(x, fs[ct], ident[which]);
+                        store4<KE>(reinterpret_cast<KE*>(W.s0) +
+                                      ((cb * nblk + c0 / 16 + ct) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
+                                  x);
+                    }
 #pragma unroll
             for (int k2 = 0; k2 < 2; ++k2)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    Frag<NI> fk, fq;
+                    const Frag<NI> fk = read_row<NI>(L.k, 32 * k2 + tile_row(r, half), 32 * kk + 8 * g);
 #pragma unroll
-                    for (int m = 0; m < NI; ++m) {
-                        fk.t[m] = *reinterpret_cast<const bf16x8*>(
-                            &L.k[m][32 * k2 + tile_row(r, half)][32 * kk + 8 * g]);
-                        fq.t[m] = *reinterpret_cast<const bf16x8*>(&L.q[m][16 * (2 * k2 + half) + r][32 * kk + 8 * g]);
-                    }
+                    for (int ct = 0; ct < CT; ++ct) mma(Z[k2][half][ct], fk, fs[ct]);
+                    if constexpr (OUT) {
+                        const Frag<NI> fq = read_row<NI>(L.q, 16 * (2 * k2 + half) + r, 32 * kk + 8 * g);
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        mma(Z[k2][half][ct], fk, fs[ct]);
-                        mma<NS, NI, NO, NI>(O[2 * k2 + half][ct], fs[ct], fq);
+                        for (int ct = 0; ct < CT; ++ct) mma<NS, NI, NO, NI>(O[2 * k2 + half][ct], fs[ct], fq);
                     }
                 }
         }
@@ -301,11 +271,7 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
             for (int k2 = kz; k2 < 2; ++k2)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    Frag<3> ft;
-#pragma unroll
-                    for (int m = 0; m < 3; ++m)
-                        ft.t[m] = *reinterpret_cast<const bf16x8*>(
-                            &L.t[m][32 * k2 + tile_row(r, half)][32 * kz + 8 * g]);
+                    const Frag<3> ft = read_row<3>(L.t, 32 * k2 + tile_row(r, half), 32 * kz + 8 * g);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) mma(U[k2][half][ct], ft, fz[ct]);
                 }
@@ -317,6 +283,17 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 f32x4 w[2];
+                if constexpr (KEEP) {  // X, likewise
+                    const Frag<kKeptSum<KE>> fx = split_tiles<kKeptSum<KE>>(U[k2][0][ct], U[k2][1][ct]);
+#pragma unroll
+                    for (int which = 0; which < 2; ++which) {
+                        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                        mma<kKeptSum<KE>, 1>(x, fx, ident[which]);
+                        store4<KE>(reinterpret_cast<KE*>(W.x) +
+                                      ((cb * nblk + c0 / 16 + ct) * kChunk + 32 * k2 + 16 * which + r) * 16 + 4 * g,
+                                  x);
+                    }
+                }
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int row = 32 * k2 + 8 * g + 4 * half;
@@ -336,28 +313,19 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
                 for (int ct = 0; ct < CT; ++ct) S[kk][half][ct] *= end;
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) {
-                    Frag<NI> ft;
-                    const int trow = 32 * k2 + 8 * g + (r >> 2), tcol = 32 * kk + 8 * (r & 3) + 4 * half;
-#pragma unroll
-                    for (int m = 0; m < NI; ++m) {
-                        const bf16x4 lo = read_transposed(&L.k[m][trow][tcol]);
-                        const bf16x4 hi = read_transposed(&L.k[m][trow + 4][tcol]);
-                        ft.t[m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                    }
+                    const Frag<NI> ft = read_col<NI, true>(L.k, 32 * k2, 32 * kk, half);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) mma(S[kk][half][ct], ft, fw[k2][ct]);
                 }
             }
+        if constexpr (OUT) {
         __syncthreads();  // P is there
         // O^T += U^T P^T.
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
 #pragma unroll
             for (int k2 = 0; k2 <= tt / 2; ++k2) {
-                Frag<NO> fp;
-#pragma unroll
-                for (int m = 0; m < NO; ++m)
-                    fp.t[m] = *reinterpret_cast<const bf16x8*>(&L.p[m][16 * tt + r][32 * k2 + 8 * g]);
+                const Frag<NO> fp = read_row<NO>(L.p, 16 * tt + r, 32 * k2 + 8 * g);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) mma(O[tt][ct], fu[k2][ct], fp);
             }
@@ -367,23 +335,15 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
                 const bool live = t < len;
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    const int c = c0 + 16 * ct + 4 * g;
-                    if constexpr (VEC) {
-                        typedef E E4 __attribute__((ext_vector_type(4)));
-                        E4 x;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = (E)(live ? O[tt][ct][e] : 0.f);
-                        if (c < Dv) *reinterpret_cast<E4*>(op + c) = x;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (c + e < Dv) op[c + e] = (E)(live ? O[tt][ct][e] : 0.f);
-                    }
+                    const f32x4 x = live ? O[tt][ct] : f32x4{0.f, 0.f, 0.f, 0.f};
+                    store_cols<E, VEC>(op, c0 + 16 * ct + 4 * g, Dv, x);
                 }
             }
         }
+        }
     }
     // Chunks past the row's length: zero outputs.
+    if constexpr (OUT)
     for (int64_t t = (int64_t)nlive * kChunk + tid / 64; t < s.T; t += 4) {
         E* op = reinterpret_cast<E*>(A.o) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
         for (int c = tile * 64 * CT + lane; c < (tile + 1) * 64 * CT && c < Dv; c += 64) op[c] = (E)0.f;
@@ -415,9 +375,9 @@ hipError_t prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks
     return hipGetLastError();
 }
 
-template <class E, int KT, int CT, bool VEC>
-hipError_t forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    auto kernel = delta_forward_kernel<E, KT, CT, VEC>;
+template <class E, class KE, int KT, int CT, bool VEC, int MODE>
+hipError_t forward_mode(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    auto kernel = delta_forward_kernel<E, KE, KT, CT, VEC, MODE>;
     const int bytes = (int)sizeof(FwdLds<E, KT, CT, VEC>);
     // More dynamic LDS than the default 64 KiB has to be asked for.
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -426,6 +386,16 @@ hipError_t forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks
     hipLaunchKernelGGL(kernel, dim3((unsigned)(s.B * s.Hv * ntile)), dim3(256), bytes, st, s, A, W,
                        (int)((s.T + kChunk - 1) / kChunk), ntile);
     return hipGetLastError();
+}
+
+template <class E, int KT, int CT, bool VEC>
+hipError_t forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    if (!W.x) return forward_mode<E, E, KT, CT, VEC, kOut>(s, A, W, st);
+    if (sizeof(E) == 4 || delta_keeps_f32(s.dtype, A.s_in))
+        return A.o ? forward_mode<E, float, KT, CT, VEC, kOut | kKeep>(s, A, W, st)
+                   : forward_mode<E, float, KT, CT, VEC, kKeep>(s, A, W, st);
+    return A.o ? forward_mode<E, E, KT, CT, VEC, kOut | kKeep>(s, A, W, st)
+               : forward_mode<E, E, KT, CT, VEC, kKeep>(s, A, W, st);
 }
 
 template <class E, bool VEC>

@@ -34,7 +34,7 @@ def delta_call(lib, shape=(2, 70, 1, 2, 16, 16), dtype=F32, q=P, lengths=None, s
 def test_delta_sizes(lib, shape):
     assert delta_call(lib, shape) == INVALID
     assert lib.linrec_last_error()
-    assert lib.gated_delta_workspace_size(*shape, F32, 0) == 0
+    assert lib.gated_delta_workspace_size(*shape, F32, 0, 0) == 0
 
 
 def test_delta_arguments(lib):
@@ -92,3 +92,35 @@ def test_norm_arguments(lib):
     assert bwd(nws=need - 1) == WORKSPACE
     assert bwd(ws=None) == INVALID
     assert bwd(N=0, gw=None) == INVALID
+
+
+def test_checkpoint_and_backward_arguments(lib):
+    shape = (2, 70, 1, 2, 16, 16)
+    nck = lib.gated_delta_checkpoint_size(*shape, F32, 0)
+    full = lib.gated_delta_workspace_size(*shape, F32, 0, 1)
+    assert 0 < nck < full
+    assert lib.gated_delta_checkpoint_size(*shape, BF16, 0) < lib.gated_delta_checkpoint_size(*shape, BF16, 1) == nck
+    assert lib.gated_delta_checkpoint_size(2, 70, 1, 2, 16, 300, F32, 0) == 0
+
+    def keep(ckpt=P, n=nck, o=P):
+        return lib.gated_delta_forward_ckpt(*shape, F32, P, P, P, P, P, None, None, 1.0, o, None, ckpt, n, None)
+    assert keep(n=nck - 1) == WORKSPACE
+    assert keep(ckpt=None) == INVALID
+    assert keep(ckpt=ctypes.c_void_p(0x100004)) == UNSUPPORTED
+    assert keep(o=None) == INVALID
+
+    def bwd(ckpt=None, n=nck, go=P, gq=P, gs_in=None, gs_out=None, ws=P, nws=full, sizes=shape):
+        return lib.gated_delta_backward(*sizes, F32, P, P, P, P, P, None, None, 1.0, ckpt, n, go, gs_out, gq, P, P, P,
+                                        P, gs_in, ws, nws, None)
+    assert bwd(nws=full - 1) == WORKSPACE
+    assert bwd(ckpt=P, nws=full - nck - 1) == WORKSPACE
+    assert bwd(ckpt=P, n=nck - 1) == WORKSPACE
+    assert bwd(go=None) == INVALID
+    assert bwd(gq=None) == INVALID
+    assert bwd(gq=ODD) == UNSUPPORTED
+    assert bwd(gs_in=ODD) == UNSUPPORTED
+    assert bwd(gs_in=P) == INVALID  # without s_in
+    assert bwd(gs_out=ODD) == UNSUPPORTED
+    assert bwd(ws=None) == INVALID
+    assert bwd(sizes=(0, 70, 1, 2, 16, 16), go=None) == OK
+    assert bwd(sizes=(2, 70, 1, 2, 16, 0)) == INVALID
