@@ -909,6 +909,8 @@ int check_delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, 
     if (bh > (1 << 20)) return fail(LINREC_ERR_UNSUPPORTED, "B*Hv=%lld is above 2^20", (long long)bh);
     if (T > (1 << 30) || bh * ceil_div(T, 64) >= (1 << 26))
         return fail(LINREC_ERR_UNSUPPORTED, "B*Hv*T/64 is above 2^26, or T above 2^30");
+    // 64 tokens of a head span less than 2^31 bytes.
+    if (Hv * std::max(Dk, Dv) > (1 << 22)) return fail(LINREC_ERR_UNSUPPORTED, "Hv*max(Dk, Dv) is above 2^22");
     if ((st = check_shape(bt, Hk, Dk, 4)) || (st = check_shape(bt, Hv, Dv, 4)) || (st = check_shape(bh, Dk, Dv, 4)))
         return st;
     return LINREC_OK;

@@ -31,17 +31,23 @@ __device__ __forceinline__ int tile_row(int m, int half) { return 8 * (m >> 2) +
 
 template <int N>
 __device__ __forceinline__ Frag<N> split(const float* x) {
+    // In pairs: one conversion gives two terms, a shift and a mask give them back as float32.
     Frag<N> f;
-    float r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = x[i];
+    for (int i = 0; i < 8; i += 2) {
+        f32x2 r = {x[i], x[i + 1]};
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            f.t[n][i] = (bf16_t)r[i];
-            if (n + 1 < N) r[i] -= (float)f.t[n][i];
+        for (int n = 0; n < N; ++n) {
+            const bf16x2 h = __builtin_convertvector(r, bf16x2);
+            f.t[n][i] = h[0];
+            f.t[n][i + 1] = h[1];
+            if (n + 1 < N) {
+                const unsigned u = __builtin_bit_cast(unsigned, h);
+                r[0] -= __builtin_bit_cast(float, u << 16);
+                r[1] -= __builtin_bit_cast(float, u & 0xffff0000u);
+            }
         }
+    }
     return f;
 }
 
@@ -68,23 +74,73 @@ __device__ __forceinline__ void mma(f32x4& c, const Frag<NA>& a, const Frag<NB>&
             if (i + j < lim) c = mfma(a.t[i], b.t[j], c);
 }
 
-// 8 elements p[0..7] of which those at c.. >= D, or all if !live, are 0.  VEC: D % 8 == 0 and
-// p 16-byte aligned.
+// The same over several tiles that share an operand, the terms outermost so that neighbouring
+// products are independent: c[t] += a[t] b, and c[t] += a b[t].
+template <int T, int NA, int NB, int MA = NA, int MB = NB>
+__device__ __forceinline__ void mma_rows(f32x4* c, const Frag<NA>* a, const Frag<NB>& b) {
+    constexpr int lim = MA > MB ? MA : MB;
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+            if (i + j < lim)
+#pragma unroll
+                for (int t = 0; t < T; ++t) c[t] = mfma(a[t].t[i], b.t[j], c[t]);
+}
+
+template <int T, int NA, int NB, int MA = NA, int MB = NB>
+__device__ __forceinline__ void mma_cols(f32x4* c, const Frag<NA>& a, const Frag<NB>* b) {
+    constexpr int lim = MA > MB ? MA : MB;
+#pragma unroll
+    for (int i = 0; i < MA; ++i)
+#pragma unroll
+        for (int j = 0; j < MB; ++j)
+            if (i + j < lim)
+#pragma unroll
+                for (int t = 0; t < T; ++t) c[t] = mfma(a.t[i], b[t].t[j], c[t]);
+}
+
+// Rows of a (B,T,H,D) tensor's head from token t0 on, through a buffer resource: lanes that
+// must not load (absent tokens, columns past D) give an offset past its end and get 0, so a
+// load is never behind a branch and many are in flight.  64 rows span less than 2^31 bytes
+// (the host checks H*D).
+struct Rows {
+    rsrc_t rs;
+    unsigned stride;  // bytes from token to token
+};
+constexpr unsigned kNowhere = 0x80000000u;
+
+template <class E>
+__device__ __forceinline__ Rows rows_of(const void* base, const DeltaShape& s, int64_t b, int H, int h, int D,
+                                        int64_t t0) {
+    return {make_rsrc(reinterpret_cast<const E*>(base) + ((b * s.T + t0) * H + h) * (int64_t)D, 0x7fffffff),
+            (unsigned)(H * D * (int)sizeof(E))};
+}
+
+// 8 elements of row `row` from column c; those at columns >= D, or all if !live, are 0.
+// VEC: D % 8 == 0 and rows 16-byte aligned.
 template <class E, bool VEC>
-__device__ __forceinline__ void load8(const E* __restrict__ p, int c, int D, bool live, E* __restrict__ out) {
-    constexpr int n = ElemVec<E>::n;
-    typedef typename ElemVec<E>::type V;
+__device__ __forceinline__ void load8(const Rows& R, int row, int c, int D, bool live, E* __restrict__ out) {
+    const unsigned at = (unsigned)row * R.stride + (unsigned)(c * (int)sizeof(E));
     if constexpr (VEC) {
+        constexpr int n = ElemVec<E>::n;
+        typedef typename ElemVec<E>::type V;
+        const unsigned off = live && c < D ? at : kNowhere;
 #pragma unroll
         for (int i = 0; i < 8; i += n) {
-            V t = {};
-            if (live && c < D) t = *reinterpret_cast<const V*>(p + i);
+            const V t = __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(R.rs, off + 4 * i, 0, 0));
 #pragma unroll
             for (int j = 0; j < n; ++j) out[i + j] = t[j];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = (live && c + i < D) ? p[i] : (E)0.f;
+        for (int i = 0; i < 8; ++i) {
+            const unsigned off = live && c + i < D ? at + (unsigned)(i * (int)sizeof(E)) : kNowhere;
+            if constexpr (sizeof(E) == 2)
+                out[i] = __builtin_bit_cast(E, __builtin_amdgcn_raw_buffer_load_b16(R.rs, off, 0, 0));
+            else
+                out[i] = __builtin_bit_cast(E, __builtin_amdgcn_raw_buffer_load_b32(R.rs, off, 0, 0));
+        }
     }
 }
 
@@ -147,39 +203,86 @@ __device__ __forceinline__ int row_length(const DeltaShape& s, int64_t b) {
     return (int)len;
 }
 
-// Stage rows t0.. of a (B,T,H,D) tensor's head h as bfloat16 terms into dst[term][row][LD]: 256
-// threads, four lanes a row, zero past D (of 32*KT) and past the row's length.
-template <class E, int KT, bool VEC, int LD>
-__device__ __forceinline__ void stage_rows(const void* src, const DeltaShape& s, int64_t b, int H, int h, int D, int t0,
-                                           int len, bf16_t (*dst)[kChunk][LD]) {
-    const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3;
-    const E* p = reinterpret_cast<const E*>(src) + ((b * s.T + t0 + row) * H + h) * (int64_t)D;
+// A chunk of a head on its way to LDS: loads issued for one chunk while another is computed.
+// 256 threads, four lanes a row.
+template <class E, int KT>
+struct RowStage {
+    E x[KT][8];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const Rows& R, int D, int len) {  // len: tokens from the chunk's first
+        const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3;
 #pragma unroll
-    for (int i = 0; i < KT; ++i) {
-        const int c = 8 * (quarter + 4 * i);
-        E x[8];
-        load8<E, VEC>(p + c, c, D, t0 + row < len, x);
-        const Frag<kTerms<E>> f = to_frag<E>(x);
-#pragma unroll
-        for (int m = 0; m < kTerms<E>; ++m) *reinterpret_cast<bf16x8*>(&dst[m][row][c]) = f.t[m];
+        for (int i = 0; i < KT; ++i) {
+            const int c = 8 * (quarter + 4 * i);
+            load8<E, VEC>(R, row, c, D, row < len, x[i]);
+        }
     }
-}
+    // As bfloat16 terms into dst[term][row][.], zero past D (of 32*KT) and past the row's length.
+    template <int LD>
+    __device__ __forceinline__ void store(bf16_t (*dst)[kChunk][LD]) const {
+        const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3;
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const Frag<kTerms<E>> f = to_frag<E>(x[i]);
+#pragma unroll
+            for (int m = 0; m < kTerms<E>; ++m)
+                *reinterpret_cast<bf16x8*>(&dst[m][row][8 * (quarter + 4 * i)]) = f.t[m];
+        }
+    }
+};
 
-// A chunk's inverse as three bfloat16 terms.
-template <int LD>
-__device__ __forceinline__ void stage_inverse(const float* __restrict__ src, bf16_t (*dst)[kChunk][LD]) {
-    const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3;
+// A chunk's inverse and decays likewise; the inverse as three bfloat16 terms.
+template <class E>
+struct InverseStage {
+    float x[16];
+    double gam, end;
+    float be;
+    __device__ __forceinline__ void load(const DeltaChunks& W, int64_t cb, const Rows& beta, int len) {
+        const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3, t = threadIdx.x & 63;
+        const float* p = W.tinv + cb * (kChunk * kChunk) + row * kChunk + 8 * quarter;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int c = 8 * (quarter + 4 * i);
-        float x[8];
-        load16<float>(src + row * kChunk + c, x);
-        load16<float>(src + row * kChunk + c + 4, x + 4);
-        const Frag<3> f = split<3>(x);
-#pragma unroll
-        for (int m = 0; m < 3; ++m) *reinterpret_cast<bf16x8*>(&dst[m][row][c]) = f.t[m];
+        for (int i = 0; i < 4; ++i) load16<float>(p + 32 * (i >> 1) + 4 * (i & 1), x + 4 * i);
+        gam = W.gam[cb * kChunk + t];
+        end = W.gam[cb * kChunk + kChunk - 1];
+        const unsigned off = t < len ? (unsigned)t * beta.stride : kNowhere;
+        if constexpr (sizeof(E) == 2)
+            be = (float)__builtin_bit_cast(E, __builtin_amdgcn_raw_buffer_load_b16(beta.rs, off, 0, 0));
+        else
+            be = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(beta.rs, off, 0, 0));
     }
-}
+    template <class Lds>
+    __device__ __forceinline__ void store(Lds& L) const {
+        const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3, t = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Frag<3> f = split<3>(x + 8 * i);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) *reinterpret_cast<bf16x8*>(&L.t[m][row][8 * quarter + 32 * i]) = f.t[m];
+        }
+        if (t < kChunk) {
+            L.gam[t] = gam;
+            L.eg[t] = decay_exp(gam, 0.0);
+            L.ew[t] = decay_exp(end, gam);
+            L.be[t] = be;
+        }
+    }
+};
+
+// A wave's 16 value channels of a chunk, as A operands of the four token tiles (the upper 16 of
+// an operand's 32 columns are 0).
+template <class E>
+struct ColumnStage {
+    E x[4][8];
+    template <bool VEC>
+    __device__ __forceinline__ void load(const Rows& R, int c0, int D, int len) {
+        const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const int row = 32 * (t >> 1) + tile_row(r, t & 1);
+            load8<E, VEC>(R, row, c0 + 8 * g, D, row < len && g < 2, x[t]);
+        }
+    }
+};
 
 // Row operand (A or B): 8 columns from c of row `row`.
 template <int N, int LD>

@@ -23,7 +23,7 @@ namespace linrec {
 namespace {
 
 // ---- the chain of the state's gradient ----------------------------------------------------------
-// The forward chain's layout: four waves, 16*CT value channels each, dS in registers.  NS terms
+// The forward chain's layout: four waves, 16 value channels each, dS in registers.  NS terms
 // for the gradient of the state and what flows into it: three where a float32 result leaves the
 // kernel or is kept (KE), two (2^-16) where all are bfloat16.
 template <class E, int KT, int NS>
@@ -37,9 +37,9 @@ struct ChainLds {
     float eg[kChunk], ew[kChunk], be[kChunk];
 };
 
-template <class E, class KE, int KT, int CT, bool VEC, int NS>
-__global__ __launch_bounds__(256) void delta_chain_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc,
-                                                          int ntile) {
+template <class E, class KE, int KT, bool VEC, int NS>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kernel(DeltaShape s, DeltaBwdArgs A,
+                                                                                  DeltaChunks W, int nc, int ntile) {
     typedef ChainLds<E, KT, NS> Lds;
     constexpr int NI = kTerms<E>;
     extern __shared__ __align__(16) char lds_raw[];
@@ -50,43 +50,44 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaShape s, DeltaBwd
     const int h = (int)(bh % s.Hv), hk = h / (s.Hv / s.Hk);
     const int64_t b = bh / s.Hv;
     const int len = row_length(s, b);
-    const int c0 = tile * 64 * CT + wave * 16 * CT;
+    const int c0 = tile * 64 + wave * 16;
     const int Dk = s.Dk, Dv = s.Dv;
-    const int nblk = ntile * 4 * CT;
+    const int nblk = ntile * 4;
 
-    f32x4 S[KT][2][CT];  // dS, in the forward's layout of S
+    f32x4 S[2 * KT];  // dS, in the forward's layout of S
     const int64_t sb = bh * (int64_t)Dk * Dv;
 #pragma unroll
-    for (int kk = 0; kk < KT; ++kk)
+    for (int d = 0; d < 2 * KT; ++d)
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 32 * kk + 8 * g + 4 * half + e, col = c0 + 16 * ct + r;
-                    S[kk][half][ct][e] =
-                        (A.gs_out && row < Dk && col < Dv) ? A.gs_out[sb + (int64_t)row * Dv + col] : 0.f;
-                }
-    const Frag<1> ident[2] = {identity_frag(0), identity_frag(1)};
+        for (int e = 0; e < 4; ++e) {
+            const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e, col = c0 + r;
+            S[d][e] = (A.gs_out && row < Dk && col < Dv) ? A.gs_out[sb + (int64_t)row * Dv + col] : 0.f;
+        }
 
     const int nlive = (len + kChunk - 1) / kChunk;
+    RowStage<E, KT> sk, sq;
+    InverseStage<E> si;
+    ColumnStage<E> so;
+    const auto fetch = [&](int n) {
+        const int t0 = n * kChunk, left = len - t0;
+        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0), Dk, left);
+        si.load(W, bh * nc + n, rows_of<E>(A.beta, s, b, s.Hv, h, 1, t0), left);
+        so.template load<VEC>(rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0), c0, Dv, left);
+        sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0), Dk, left);
+    };
+    if (nlive > 0) fetch(nlive - 1);
     for (int n = nlive - 1; n >= 0; --n) {
         const int t0 = n * kChunk;
         const int64_t cb = bh * nc + n;
         __syncthreads();  // the previous chunk's tiles have been read
-        stage_rows<E, KT, VEC>(A.k, s, b, s.Hk, hk, Dk, t0, len, L.k);
-        stage_rows<E, KT, VEC>(A.q, s, b, s.Hk, hk, Dk, t0, len, L.q);
-        stage_inverse(W.tinv + cb * (kChunk * kChunk), L.t);
-        if (tid < kChunk) {
-            const bool on = t0 + tid < len;
-            const double gm = W.gam[cb * kChunk + tid], end = W.gam[cb * kChunk + kChunk - 1];
-            L.gam[tid] = gm;
-            L.eg[tid] = decay_exp(gm, 0.0);
-            L.ew[tid] = decay_exp(end, gm);
-            L.be[tid] = on ? (float)reinterpret_cast<const E*>(A.beta)[(b * s.T + t0 + tid) * s.Hv + h] : 0.f;
-        }
+        sk.store(L.k);
+        sq.store(L.q);
+        si.store(L);
+        Frag<NI> fv[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) fv[t] = to_frag<E>(so.x[t]);
         __syncthreads();
+        if (n > 0) fetch(n - 1);  // in flight while this chunk is computed
         // P^T, rows 16*wave..: tiles of Q K^T (rows i, columns j), stored as P^T[j][i].
         {
             const int j = 16 * wave + r;
@@ -114,159 +115,120 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaShape s, DeltaBwd
             }
         }
         // K dS' (dS' is also stored, turned so that a lane holds 4 value channels).
-        f32x4 U[2][2][CT];  // rows 32*k2 + tile_row(m, half)
+        f32x4 U[4];  // rows 32*(t/2) + tile_row(m, t%2)
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) U[k2][half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 4; ++t) U[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = 0; kk < KT; ++kk) {
-            Frag<NS> fs[CT];
+            Frag<NI> fk[4];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                fs[ct] = split_tiles<NS>(S[kk][0][ct], S[kk][1][ct]);
+            for (int t = 0; t < 4; ++t) fk[t] = read_row<NI>(L.k, 32 * (t >> 1) + tile_row(r, t & 1), 32 * kk + 8 * g);
+            const Frag<NS> fs = split_tiles<NS>(S[2 * kk], S[2 * kk + 1]);
+            mma_rows<4>(U, fk, fs);
 #pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-                    mma<NS, 1, kKeptSum<KE>, 1>(x, fs[ct], ident[which]);
-                    store4<KE>(reinterpret_cast<KE*>(W.ds) +
-                                  ((cb * nblk + c0 / 16 + ct) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
-                              x);
-                }
+            for (int which = 0; which < 2; ++which) {
+                f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                mma<NS, 1, kKeptSum<KE>, 1>(x, fs, identity_frag(which));
+                store4<KE>(reinterpret_cast<KE*>(W.ds) +
+                               ((cb * nblk + c0 / 16) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
+                           x);
             }
-#pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const Frag<NI> fk = read_row<NI>(L.k, 32 * k2 + tile_row(r, half), 32 * kk + 8 * g);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(U[k2][half][ct], fk, fs[ct]);
-                }
         }
-        // dO in the D layout, as B operand, and scaled for the state's gradient.
-        Frag<NI> fo[2][CT];
-        Frag<NS> fd[2][CT];
+        // dO in the D layout: as B operand, and scaled for the state's gradient.
+        Frag<NI> fo[2];
+        Frag<NS> fd[2];
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
-            f32x4 d[2][CT];
+            f32x4 d[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int row = t0 + 32 * k2 + tile_row(r, half);
-                E x[8];
-                const int c = c0 + 8 * g;
-                const bool on = row < len && (CT == 2 || g < 2);
-                load8<E, VEC>(reinterpret_cast<const E*>(A.go) + ((b * s.T + row) * s.Hv + h) * (int64_t)Dv + c, c, Dv,
-                              on, x);
-                const Frag<NI> fv = to_frag<E>(x);
-                const f32x4 ew = *reinterpret_cast<const f32x4*>(&L.ew[32 * k2 + 8 * g + 4 * half]);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    d[half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    mma<NI, 1>(d[half][ct], fv, ident[ct]);
-                    U[k2][half][ct] *= ew;
-                }
+                d[half] = f32x4{0.f, 0.f, 0.f, 0.f};
+                mma(d[half], fv[2 * k2 + half], identity_frag(0));
+                U[2 * k2 + half] *= *reinterpret_cast<const f32x4*>(&L.ew[32 * k2 + 8 * g + 4 * half]);
             }
+            fo[k2] = split_tiles<NI>(d[0], d[1]);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                fo[k2][ct] = split_tiles<NI>(d[0][ct], d[1][ct]);
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    d[half][ct] *= s.scale * *reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
-                fd[k2][ct] = split_tiles<NS>(d[0][ct], d[1][ct]);
-            }
+            for (int half = 0; half < 2; ++half)
+                d[half] *= s.scale * *reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
+            fd[k2] = split_tiles<NS>(d[0], d[1]);
         }
         __syncthreads();  // P^T is there
-        Frag<NS> fb[2][CT];  // beta dU
+        // dU += P^T dO (the lower left block is zero), then beta dU.
+        {
+            Frag<NS> fp[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) fp[t] = read_row<NS>(L.p, 32 * (t >> 1) + tile_row(r, t & 1), 32 + 8 * g);
+            mma_rows<4>(U, fp, fo[1]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) fp[t] = read_row<NS>(L.p, tile_row(r, t), 8 * g);
+            mma_rows<2>(U, fp, fo[0]);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) U[t] *= *reinterpret_cast<const f32x4*>(&L.be[32 * (t >> 1) + 8 * g + 4 * (t & 1)]);
+        // dZ = N^T (beta dU).
+        f32x4 Z[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) Z[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        {
+            Frag<NS> ft[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ft[t] = read_col<NS, true>(L.t, 32, 32 * (t >> 1), t & 1);
+            mma_rows<4>(Z, ft, split_tiles<NS>(U[2], U[3]));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) ft[t] = read_col<NS, true>(L.t, 0, 0, t);
+            mma_rows<2>(Z, ft, split_tiles<NS>(U[0], U[1]));
+        }
+        // dV, turned; and -e^gam dZ for the state's gradient.
+        Frag<NS> fz[2];
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
+            const Frag<NI> fx = split_tiles<NI>(Z[2 * k2], Z[2 * k2 + 1]);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                for (int kz = k2; kz < 2; ++kz) {
-                    const Frag<NS> fp = read_row<NS>(L.p, 32 * k2 + tile_row(r, half), 32 * kz + 8 * g);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(U[k2][half][ct], fp, fo[kz][ct]);
-                }
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-                    U[k2][half][ct] *= *reinterpret_cast<const f32x4*>(&L.be[32 * k2 + 8 * g + 4 * half]);
+            for (int which = 0; which < 2; ++which) {
+                f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                mma(x, fx, identity_frag(which));
+                const int t = t0 + 32 * k2 + 16 * which + r;
+                if (t < s.T)
+                    store_cols<E, VEC>(reinterpret_cast<E*>(A.gv) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv,
+                                       c0 + 4 * g, Dv, x);
             }
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) fb[k2][ct] = split_tiles<NS>(U[k2][0][ct], U[k2][1][ct]);
+            for (int half = 0; half < 2; ++half)
+                Z[2 * k2 + half] *= -*reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
+            fz[k2] = split_tiles<NS>(Z[2 * k2], Z[2 * k2 + 1]);
         }
-        // dZ = N^T (beta dU).
-        f32x4 Z[2][2][CT];
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) Z[k2][half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int kz = k2; kz < 2; ++kz) {
-                    const Frag<NS> ft = read_col<NS, true>(L.t, 32 * kz, 32 * k2, half);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(Z[k2][half][ct], ft, fb[kz][ct]);
-                }
-            }
-        // dV, turned; and -e^gam dZ for the state's gradient.
-        Frag<NS> fz[2][CT];
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const Frag<NI> fx = split_tiles<NI>(Z[k2][0][ct], Z[k2][1][ct]);
-#pragma unroll
-                for (int which = 0; which < 2; ++which) {
-                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-                    mma<NI, 1>(x, fx, ident[which]);
-                    const int t = t0 + 32 * k2 + 16 * which + r;
-                    if (t < s.T)
-                        store_cols<E, VEC>(reinterpret_cast<E*>(A.gv) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv,
-                                           c0 + 16 * ct + 4 * g, Dv, x);
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    Z[k2][half][ct] *= -*reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
-                fz[k2][ct] = split_tiles<NS>(Z[k2][0][ct], Z[k2][1][ct]);
-            }
+        // dS = e^{gam_63} dS' + scale Q^T e^gam dO - K^T e^gam dZ, four tiles at a time.
         const float end = L.eg[kChunk - 1];
+        constexpr int T = KT == 1 ? 2 : 4;
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk)
+        for (int d = 0; d < 2 * KT; d += T) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int t = 0; t < T; ++t) S[d + t] *= end;
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) S[kk][half][ct] *= end;
+            for (int k2 = 0; k2 < 2; ++k2) {
+                Frag<NI> fq[T], fk[T];
 #pragma unroll
-                for (int k2 = 0; k2 < 2; ++k2) {
-                    const Frag<NI> fq = read_col<NI, true>(L.q, 32 * k2, 32 * kk, half);
-                    const Frag<NI> fk = read_col<NI, true>(L.k, 32 * k2, 32 * kk, half);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) {
-                        mma(S[kk][half][ct], fq, fd[k2][ct]);
-                        mma(S[kk][half][ct], fk, fz[k2][ct]);
-                    }
+                for (int t = 0; t < T; ++t) {
+                    fq[t] = read_col<NI, true>(L.q, 32 * k2, 32 * ((d + t) >> 1), t & 1);
+                    fk[t] = read_col<NI, true>(L.k, 32 * k2, 32 * ((d + t) >> 1), t & 1);
                 }
+                mma_rows<T>(S + d, fq, fd[k2]);
+                mma_rows<T>(S + d, fk, fz[k2]);
             }
+        }
     }
     for (int64_t t = (int64_t)nlive * kChunk + wave; t < s.T; t += 4) {
         E* op = reinterpret_cast<E*>(A.gv) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
-        for (int c = tile * 64 * CT + lane; c < (tile + 1) * 64 * CT && c < Dv; c += 64) op[c] = (E)0.f;
+        if (tile * 64 + lane < Dv) op[tile * 64 + lane] = (E)0.f;
     }
     if (A.gs_in)
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk)
+        for (int d = 0; d < 2 * KT; ++d)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = 32 * kk + 8 * g + 4 * half + e, col = c0 + 16 * ct + r;
-                        if (row < Dk && col < Dv) A.gs_in[sb + (int64_t)row * Dv + col] = S[kk][half][ct][e];
-                    }
+            for (int e = 0; e < 4; ++e) {
+                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e, col = c0 + r;
+                if (row < Dk && col < Dv) A.gs_in[sb + (int64_t)row * Dv + col] = S[d][e];
+            }
 }
 
 // ---- the gradients of a chunk ---------------------------------------------------------------------
@@ -293,10 +255,16 @@ template <class KE, int N>
 __device__ __forceinline__ Frag<N> read_block(const KE* m, int rows, int row, int kv) {
     const int g = (threadIdx.x & 63) >> 4;
     const KE* p = m + ((int64_t)(2 * kv + (g >> 1)) * rows + row) * 16 + 8 * (g & 1);
-    KE x[8];
-    load8<KE, true>(p, 0, 8, true, x);
-    if constexpr (sizeof(KE) == 2) return to_frag<KE>(x);
-    else return split<N>(x);
+    if constexpr (sizeof(KE) == 2) {
+        Frag<N> f;
+        f.t[0] = *reinterpret_cast<const bf16x8*>(p);
+        return f;
+    } else {
+        float x[8];
+        load16<float>(p, x);
+        load16<float>(p + 4, x + 4);
+        return split<N>(x);
+    }
 }
 
 template <class E, class KE, int KT, bool VEC>
@@ -313,7 +281,6 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
     const int len = row_length(s, b), t0 = n * kChunk;
     const int Dk = s.Dk, Dv = s.Dv;
     const int mine = 16 * wave + r, tok = t0 + mine;  // this lane's token
-    const int64_t tokh = (b * s.T + tok) * s.Hv;
     if (t0 >= len) {  // absent tokens: zero gradients
         for (int i = wave; i < kChunk && t0 + i < s.T; i += 4) {
             const int64_t at = ((b * s.T + t0 + i) * s.Hk + hk) * (int64_t)Dk;
@@ -329,8 +296,13 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
         }
         return;
     }
-    stage_rows<E, KT, VEC>(A.k, s, b, s.Hk, hk, Dk, t0, len, L.k);
-    stage_rows<E, KT, VEC>(A.q, s, b, s.Hk, hk, Dk, t0, len, L.q);
+    {
+        RowStage<E, KT> sk, sq;
+        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0), Dk, len - t0);
+        sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0), Dk, len - t0);
+        sk.store(L.k);
+        sq.store(L.q);
+    }
     __syncthreads();
     // q_i.k_j and k_i.k_j: rows j (tiles up to this wave's), columns i.
     f32x4 qk[4], kk_[4];
@@ -363,8 +335,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
         const KE* X = reinterpret_cast<const KE*>(W.x) + cb * nblk * (kChunk * 16);
         const KE* S0 = reinterpret_cast<const KE*>(W.s0) + cb * nblk * (32 * KT * 16);
         const KE* DS = reinterpret_cast<const KE*>(W.ds) + cb * nblk * (32 * KT * 16);
-        const E* go = reinterpret_cast<const E*>(A.go) + (tokh + h) * Dv;
-        const E* gz = reinterpret_cast<const E*>(A.gv) + (tokh + h) * Dv;
+        const Rows go = rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0), gz = rows_of<E>(A.gv, s, b, s.Hv, h, Dv, t0);
         f32x4 H[4], Z[4], rq[DT], rk[DT], wk[DT];
         float dot = 0.f;
 #pragma unroll
@@ -374,9 +345,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
         for (int kv = 0; 32 * kv < Dv; ++kv) {
             E x[8];
             const int c = 32 * kv + 8 * g;
-            load8<E, VEC>(go + c, c, Dv, tok < len, x);
+            load8<E, VEC>(go, mine, c, Dv, tok < len, x);
             const Frag<NI> fo = to_frag<E>(x);
-            load8<E, VEC>(gz + c, c, Dv, tok < len, x);
+            load8<E, VEC>(gz, mine, c, Dv, tok < len, x);
             const Frag<NI> fz = to_frag<E>(x);
             const Frag<NK> fx = read_block<KE, NK>(X, kChunk, mine, kv);
 #pragma unroll
@@ -563,7 +534,7 @@ hipError_t launch(K kernel, int64_t blocks, int bytes, hipStream_t st, const Del
 template <class E, class KE, int KT, int NS, bool VEC>
 hipError_t backward(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
     const int ntile = (s.Dv + 63) / 64;
-    const hipError_t e = launch(delta_chain_kernel<E, KE, KT, 1, VEC, NS>, s.B * s.Hv * ntile,
+    const hipError_t e = launch(delta_chain_kernel<E, KE, KT, VEC, NS>, s.B * s.Hv * ntile,
                                 (int)sizeof(ChainLds<E, KT, NS>), st, s, A, W, ntile);
     if (e != hipSuccess) return e;
     return launch(delta_grad_kernel<E, KE, KT, VEC>, s.B * s.Hk * ((s.T + kChunk - 1) / kChunk),

@@ -44,15 +44,15 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
         bet[lane] = live ? (float)reinterpret_cast<const E*>(A.beta)[at] : 0.f;
         W.gam[blk * kChunk + lane] = c;
     }
+    const Rows K = rows_of<E>(A.k, s, b, s.Hk, hk, s.Dk, t0);
     Frag<NI> kf[4][KT];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        const int row = t0 + 16 * t + r;
-        const E* p = reinterpret_cast<const E*>(A.k) + ((b * s.T + row) * s.Hk + hk) * (int64_t)s.Dk;
+        const int row = 16 * t + r;
 #pragma unroll
         for (int kk = 0; kk < KT; ++kk) {
             E x[8];
-            load8<E, VEC>(p + 32 * kk + 8 * g, 32 * kk + 8 * g, s.Dk, row < len, x);
+            load8<E, VEC>(K, row, 32 * kk + 8 * g, s.Dk, t0 + row < len, x);
             kf[t][kk] = to_frag<E>(x);
         }
     }
@@ -85,15 +85,15 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
 }
 
 // ---- the chain over a head's chunks -----------------------------------------------------------
-// A workgroup of four waves owns 64*CT columns of the value channels of one head, a wave 16*CT
-// of them, all rows of the state (32*KT, zero past Dk).  K, Q, the inverse and P lie in LDS as
-// bfloat16 terms, shared by the waves; V comes from memory in the A layout and is turned into
-// the D layout by a product with the identity, which is exact.
+// A workgroup of four waves owns 64 value channels of one head, a wave 16 of them, all rows of
+// the state (32*KT, zero past Dk).  K, Q, the inverse and P lie in LDS as bfloat16 terms, shared
+// by the waves; V comes from memory in the A layout and is turned into the D layout by a product
+// with the identity, which is exact.  The next chunk's loads are in flight while one is computed.
 //
 // Terms: the state and what flows into it (Z, beta X) are taken as three bfloat16 terms, so
 // that S keeps float32 precision over any number of chunks; the outputs of bfloat16 calls take
 // two terms of S, P and beta X, so that the rounding of the output itself is all there is.
-template <class E, int KT, int CT, bool VEC>
+template <class E, int KT>
 struct FwdLds {
     static constexpr int NI = kTerms<E>, NO = NI == 1 ? 2 : 3;  // terms of inputs, of the outputs' operands
     static constexpr int LK = 32 * KT + 8, LT = kChunk + 8;
@@ -107,10 +107,10 @@ struct FwdLds {
 // What the chain leaves: o, and what the backward starts from (of type KE).
 constexpr int kOut = 1, kKeep = 2;
 
-template <class E, class KE, int KT, int CT, bool VEC, int MODE>
-__global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaFwdArgs A, DeltaChunks W, int nc,
-                                                            int ntile) {
-    typedef FwdLds<E, KT, CT, VEC> Lds;
+template <class E, class KE, int KT, bool VEC, int MODE>
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_kernel(DeltaShape s, DeltaFwdArgs A,
+                                                                                    DeltaChunks W, int nc, int ntile) {
+    typedef FwdLds<E, KT> Lds;
     constexpr int NI = kTerms<E>, NO = Lds::NO, NS = 3;
     constexpr bool OUT = MODE & kOut, KEEP = MODE & kKeep;
     extern __shared__ __align__(16) char lds_raw[];
@@ -121,46 +121,45 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
     const int h = (int)(bh % s.Hv), hk = h / (s.Hv / s.Hk);
     const int64_t b = bh / s.Hv;
     const int len = row_length(s, b);
-    const int c0 = tile * 64 * CT + wave * 16 * CT;  // this wave's first value channel
+    const int c0 = tile * 64 + wave * 16;  // this wave's first value channel
     const int Dk = s.Dk, Dv = s.Dv;
-    const int nblk = ntile * 4 * CT;  // blocks of 16 value channels
+    const int nblk = ntile * 4;  // blocks of 16 value channels
 
-    // State: D tiles S[kk][half][ct], rows 32kk + tile_row(m, half), columns c0 + 16ct + r.
-    f32x4 S[KT][2][CT];
+    // State: D tiles S[2kk + half], rows 32kk + tile_row(m, half), columns c0 + r.
+    f32x4 S[2 * KT];
     const int64_t sb = bh * (int64_t)Dk * Dv;
 #pragma unroll
-    for (int kk = 0; kk < KT; ++kk)
+    for (int d = 0; d < 2 * KT; ++d)
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 32 * kk + 8 * g + 4 * half + e, col = c0 + 16 * ct + r;
-                    S[kk][half][ct][e] = (A.s_in && row < Dk && col < Dv) ? A.s_in[sb + (int64_t)row * Dv + col] : 0.f;
-                }
-    const Frag<1> ident[2] = {identity_frag(0), identity_frag(1)};
+        for (int e = 0; e < 4; ++e) {
+            const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e, col = c0 + r;
+            S[d][e] = (A.s_in && row < Dk && col < Dv) ? A.s_in[sb + (int64_t)row * Dv + col] : 0.f;
+        }
 
     const int nlive = (len + kChunk - 1) / kChunk;
+    RowStage<E, KT> sk, sq;
+    InverseStage<E> si;
+    ColumnStage<E> sv;
+    const auto fetch = [&](int n) {
+        const int t0 = n * kChunk, left = len - t0;
+        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0), Dk, left);
+        si.load(W, bh * nc + n, rows_of<E>(A.beta, s, b, s.Hv, h, 1, t0), left);
+        sv.template load<VEC>(rows_of<E>(A.v, s, b, s.Hv, h, Dv, t0), c0, Dv, left);
+        if constexpr (OUT) sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0), Dk, left);
+    };
+    if (nlive > 0) fetch(0);
     for (int n = 0; n < nlive; ++n) {
         const int t0 = n * kChunk;
         const int64_t cb = bh * nc + n;
         __syncthreads();  // the previous chunk's tiles have been read
-        // Stage K, Q (4 lanes a row), the inverse, the decays.
-        {
-            stage_rows<E, KT, VEC>(A.k, s, b, s.Hk, hk, Dk, t0, len, L.k);
-            if constexpr (OUT) stage_rows<E, KT, VEC>(A.q, s, b, s.Hk, hk, Dk, t0, len, L.q);
-            stage_inverse(W.tinv + cb * (kChunk * kChunk), L.t);
-            if (tid < kChunk) {
-                const bool on = t0 + tid < len;
-                const double gm = W.gam[cb * kChunk + tid], end = W.gam[cb * kChunk + kChunk - 1];
-                L.gam[tid] = gm;
-                L.eg[tid] = decay_exp(gm, 0.0);
-                L.ew[tid] = decay_exp(end, gm);
-                L.be[tid] = on ? (float)reinterpret_cast<const E*>(A.beta)[(b * s.T + t0 + tid) * s.Hv + h] : 0.f;
-            }
-        }
+        sk.store(L.k);
+        if constexpr (OUT) sq.store(L.q);
+        si.store(L);
+        Frag<NI> fv[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) fv[t] = to_frag<E>(sv.x[t]);
         __syncthreads();
+        if (n + 1 < nlive) fetch(n + 1);
         // P, rows 16*wave..: tiles of K Q^T (rows j, columns i), stored as P[i][j].
         if constexpr (OUT) {
             const int i = 16 * wave + r;
@@ -187,179 +186,127 @@ __global__ __launch_bounds__(256) void delta_forward_kernel(DeltaShape s, DeltaF
                         __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
             }
         }
-        // Z = V - e^gam K S and the state's part of O^T.
-        f32x4 Z[2][2][CT], O[4][CT];  // Z: rows 32*k2 + tile_row(m, half); O^T: columns 16*tt + r
+        // K S and the state's part of O^T.
+        f32x4 Z[4], O[4];  // Z[t]: rows 32*(t/2) + tile_row(m, t%2); O^T[t]: columns 16*t + r
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    Z[k2][half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    O[2 * k2 + half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
+        for (int t = 0; t < 4; ++t) Z[t] = O[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = 0; kk < KT; ++kk) {
-            Frag<NS> fs[CT];
+            Frag<NI> fk[4], fq[4];
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) fs[ct] = split_tiles<NS>(S[kk][0][ct], S[kk][1][ct]);
+            for (int t = 0; t < 4; ++t) {
+                fk[t] = read_row<NI>(L.k, 32 * (t >> 1) + tile_row(r, t & 1), 32 * kk + 8 * g);
+                if constexpr (OUT) fq[t] = read_row<NI>(L.q, 16 * t + r, 32 * kk + 8 * g);
+            }
+            const Frag<NS> fs = split_tiles<NS>(S[2 * kk], S[2 * kk + 1]);
+            mma_rows<4>(Z, fk, fs);
+            if constexpr (OUT) mma_cols<4, NS, NI, NO, NI>(O, fs, fq);
             if constexpr (KEEP)  // S before the chunk, turned so that a lane holds 4 value channels
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int which = 0; which < 2; ++which) {
-                        f32x4 x = {0.f, 0.f, 0.f, 0.f};
-                        mma<NS, 1, kKeptSum<KE>, 1>(x, fs[ct], ident[which]);
-                        store4<KE>(reinterpret_cast<KE*>(W.s0) +
-                                      ((cb * nblk + c0 / 16 + ct) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
-                                  x);
-                    }
-#pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const Frag<NI> fk = read_row<NI>(L.k, 32 * k2 + tile_row(r, half), 32 * kk + 8 * g);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(Z[k2][half][ct], fk, fs[ct]);
-                    if constexpr (OUT) {
-                        const Frag<NI> fq = read_row<NI>(L.q, 16 * (2 * k2 + half) + r, 32 * kk + 8 * g);
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) mma<NS, NI, NO, NI>(O[2 * k2 + half][ct], fs[ct], fq);
-                    }
+                for (int which = 0; which < 2; ++which) {
+                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                    mma<NS, 1, kKeptSum<KE>, 1>(x, fs, identity_frag(which));
+                    store4<KE>(reinterpret_cast<KE*>(W.s0) +
+                                   ((cb * nblk + c0 / 16) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
+                               x);
                 }
         }
+        // Z = V - e^gam K S.
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
+        for (int t = 0; t < 4; ++t) {
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            mma(v, fv[t], identity_frag(0));
+            const f32x4 eg = *reinterpret_cast<const f32x4*>(&L.eg[32 * (t >> 1) + 8 * g + 4 * (t & 1)]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Z[t][e] = fmaf(-eg[e], Z[t][e], v[e]);
+            if constexpr (OUT) O[t] *= s.scale * L.eg[16 * t + r];
+        }
+        // X = inverse Z (its upper right block is zero).
+        f32x4 U[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) U[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        {
+            Frag<3> ft[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) ft[t] = read_row<3>(L.t, 32 * (t >> 1) + tile_row(r, t & 1), 8 * g);
+            mma_rows<4>(U, ft, split_tiles<NS>(Z[0], Z[1]));
+#pragma unroll
+            for (int t = 2; t < 4; ++t) ft[t] = read_row<3>(L.t, 32 + tile_row(r, t & 1), 32 + 8 * g);
+            mma_rows<2>(U + 2, ft + 2, split_tiles<NS>(Z[2], Z[3]));
+        }
+        Frag<NO> fu[2];  // beta X for the outputs
+        Frag<NS> fw[2];  // e^{gam_63 - gam} beta X for the state
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+            if constexpr (KEEP) {  // X, likewise
+                const Frag<kKeptSum<KE>> fx = split_tiles<kKeptSum<KE>>(U[2 * k2], U[2 * k2 + 1]);
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+                    mma(x, fx, identity_frag(which));
+                    store4<KE>(reinterpret_cast<KE*>(W.x) +
+                                   ((cb * nblk + c0 / 16) * kChunk + 32 * k2 + 16 * which + r) * 16 + 4 * g,
+                               x);
+                }
+            }
+            f32x4 w[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int row = t0 + 32 * k2 + tile_row(r, half);
-                f32x4 v[CT];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) v[ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-                E x[8];
-                const int c = c0 + 8 * g;  // 32 columns of one A operand; 16 of them with CT = 1
-                const bool on = row < len && (CT == 2 || g < 2);
-                load8<E, VEC>(reinterpret_cast<const E*>(A.v) + ((b * s.T + row) * s.Hv + h) * (int64_t)Dv + c, c, Dv,
-                              on, x);
-                const Frag<NI> fv = to_frag<E>(x);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) mma<NI, 1>(v[ct], fv, ident[ct]);
-                const f32x4 eg = *reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        Z[k2][half][ct][e] = fmaf(-eg[e], Z[k2][half][ct][e], v[ct][e]);
-                const float so = s.scale * L.eg[16 * (2 * k2 + half) + r];
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) O[2 * k2 + half][ct] *= so;
+                const int row = 32 * k2 + 8 * g + 4 * half;
+                U[2 * k2 + half] *= *reinterpret_cast<const f32x4*>(&L.be[row]);
+                w[half] = U[2 * k2 + half] * *reinterpret_cast<const f32x4*>(&L.ew[row]);
             }
-        // X = inverse Z, then U = beta X.
-        f32x4 U[2][2][CT];
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) U[k2][half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kz = 0; kz < 2; ++kz) {
-            Frag<NS> fz[CT];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) fz[ct] = split_tiles<NS>(Z[kz][0][ct], Z[kz][1][ct]);
-#pragma unroll
-            for (int k2 = kz; k2 < 2; ++k2)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const Frag<3> ft = read_row<3>(L.t, 32 * k2 + tile_row(r, half), 32 * kz + 8 * g);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(U[k2][half][ct], ft, fz[ct]);
-                }
+            if constexpr (OUT) fu[k2] = split_tiles<NO>(U[2 * k2], U[2 * k2 + 1]);
+            fw[k2] = split_tiles<NS>(w[0], w[1]);
         }
-        Frag<NO> fu[2][CT];   // beta X for the outputs
-        Frag<NS> fw[2][CT];   // e^{gam_63 - gam} beta X for the state
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                f32x4 w[2];
-                if constexpr (KEEP) {  // X, likewise
-                    const Frag<kKeptSum<KE>> fx = split_tiles<kKeptSum<KE>>(U[k2][0][ct], U[k2][1][ct]);
-#pragma unroll
-                    for (int which = 0; which < 2; ++which) {
-                        f32x4 x = {0.f, 0.f, 0.f, 0.f};
-                        mma<kKeptSum<KE>, 1>(x, fx, ident[which]);
-                        store4<KE>(reinterpret_cast<KE*>(W.x) +
-                                      ((cb * nblk + c0 / 16 + ct) * kChunk + 32 * k2 + 16 * which + r) * 16 + 4 * g,
-                                  x);
-                    }
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int row = 32 * k2 + 8 * g + 4 * half;
-                    U[k2][half][ct] *= *reinterpret_cast<const f32x4*>(&L.be[row]);
-                    w[half] = U[k2][half][ct] * *reinterpret_cast<const f32x4*>(&L.ew[row]);
-                }
-                fu[k2][ct] = split_tiles<NO>(U[k2][0][ct], U[k2][1][ct]);
-                fw[k2][ct] = split_tiles<NS>(w[0], w[1]);
-            }
-        // S' = e^{gam_63} S + K^T w.
+        // S' = e^{gam_63} S + K^T w, four tiles at a time.
         const float end = L.eg[kChunk - 1];
+        constexpr int T = KT == 1 ? 2 : 4;
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk)
+        for (int d = 0; d < 2 * KT; d += T) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int t = 0; t < T; ++t) S[d + t] *= end;
 #pragma unroll
-                for (int ct = 0; ct < CT; ++ct) S[kk][half][ct] *= end;
+            for (int k2 = 0; k2 < 2; ++k2) {
+                Frag<NI> ft[T];
 #pragma unroll
-                for (int k2 = 0; k2 < 2; ++k2) {
-                    const Frag<NI> ft = read_col<NI, true>(L.k, 32 * k2, 32 * kk, half);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) mma(S[kk][half][ct], ft, fw[k2][ct]);
-                }
-            }
-        if constexpr (OUT) {
-        __syncthreads();  // P is there
-        // O^T += U^T P^T.
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-            for (int k2 = 0; k2 <= tt / 2; ++k2) {
-                const Frag<NO> fp = read_row<NO>(L.p, 16 * tt + r, 32 * k2 + 8 * g);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) mma(O[tt][ct], fu[k2][ct], fp);
-            }
-            const int t = t0 + 16 * tt + r;
-            if (t < s.T) {
-                E* op = reinterpret_cast<E*>(A.o) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
-                const bool live = t < len;
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) {
-                    const f32x4 x = live ? O[tt][ct] : f32x4{0.f, 0.f, 0.f, 0.f};
-                    store_cols<E, VEC>(op, c0 + 16 * ct + 4 * g, Dv, x);
-                }
+                for (int t = 0; t < T; ++t) ft[t] = read_col<NI, true>(L.k, 32 * k2, 32 * ((d + t) >> 1), t & 1);
+                mma_rows<T>(S + d, ft, fw[k2]);
             }
         }
+        if constexpr (OUT) {
+            __syncthreads();  // P is there
+            // O^T += U^T P^T (P's upper right block is zero).
+            Frag<NO> fp[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) fp[t] = read_row<NO>(L.p, 16 * t + r, 8 * g);
+            mma_cols<4>(O, fu[0], fp);
+#pragma unroll
+            for (int t = 2; t < 4; ++t) fp[t] = read_row<NO>(L.p, 16 * t + r, 32 + 8 * g);
+            mma_cols<2>(O + 2, fu[1], fp + 2);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int tok = t0 + 16 * t + r;
+                if (tok < s.T)
+                    store_cols<E, VEC>(reinterpret_cast<E*>(A.o) + ((b * s.T + tok) * s.Hv + h) * (int64_t)Dv,
+                                       c0 + 4 * g, Dv, tok < len ? O[t] : f32x4{0.f, 0.f, 0.f, 0.f});
+            }
         }
     }
     // Chunks past the row's length: zero outputs.
     if constexpr (OUT)
-    for (int64_t t = (int64_t)nlive * kChunk + tid / 64; t < s.T; t += 4) {
-        E* op = reinterpret_cast<E*>(A.o) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
-        for (int c = tile * 64 * CT + lane; c < (tile + 1) * 64 * CT && c < Dv; c += 64) op[c] = (E)0.f;
-    }
+        for (int64_t t = (int64_t)nlive * kChunk + wave; t < s.T; t += 4) {
+            E* op = reinterpret_cast<E*>(A.o) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
+            if (tile * 64 + lane < Dv) op[tile * 64 + lane] = (E)0.f;
+        }
     if (A.s_out)
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk)
+        for (int d = 0; d < 2 * KT; ++d)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int row = 32 * kk + 8 * g + 4 * half + e, col = c0 + 16 * ct + r;
-                        if (row < Dk && col < Dv) A.s_out[sb + (int64_t)row * Dv + col] = S[kk][half][ct][e];
-                    }
+            for (int e = 0; e < 4; ++e) {
+                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e, col = c0 + r;
+                if (row < Dk && col < Dv) A.s_out[sb + (int64_t)row * Dv + col] = S[d][e];
+            }
 }
 
 bool vec_ok(const DeltaShape& s, const DeltaFwdArgs& A) {
@@ -375,27 +322,27 @@ hipError_t prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks
     return hipGetLastError();
 }
 
-template <class E, class KE, int KT, int CT, bool VEC, int MODE>
+template <class E, class KE, int KT, bool VEC, int MODE>
 hipError_t forward_mode(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    auto kernel = delta_forward_kernel<E, KE, KT, CT, VEC, MODE>;
-    const int bytes = (int)sizeof(FwdLds<E, KT, CT, VEC>);
+    auto kernel = delta_forward_kernel<E, KE, KT, VEC, MODE>;
+    const int bytes = (int)sizeof(FwdLds<E, KT>);
     // More dynamic LDS than the default 64 KiB has to be asked for.
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int ntile = (s.Dv + 64 * CT - 1) / (64 * CT);
+    const int ntile = (s.Dv + 63) / 64;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(s.B * s.Hv * ntile)), dim3(256), bytes, st, s, A, W,
                        (int)((s.T + kChunk - 1) / kChunk), ntile);
     return hipGetLastError();
 }
 
-template <class E, int KT, int CT, bool VEC>
+template <class E, int KT, bool VEC>
 hipError_t forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    if (!W.x) return forward_mode<E, E, KT, CT, VEC, kOut>(s, A, W, st);
+    if (!W.x) return forward_mode<E, E, KT, VEC, kOut>(s, A, W, st);
     if (sizeof(E) == 4 || delta_keeps_f32(s.dtype, A.s_in))
-        return A.o ? forward_mode<E, float, KT, CT, VEC, kOut | kKeep>(s, A, W, st)
-                   : forward_mode<E, float, KT, CT, VEC, kKeep>(s, A, W, st);
-    return A.o ? forward_mode<E, E, KT, CT, VEC, kOut | kKeep>(s, A, W, st)
-               : forward_mode<E, E, KT, CT, VEC, kKeep>(s, A, W, st);
+        return A.o ? forward_mode<E, float, KT, VEC, kOut | kKeep>(s, A, W, st)
+                   : forward_mode<E, float, KT, VEC, kKeep>(s, A, W, st);
+    return A.o ? forward_mode<E, E, KT, VEC, kOut | kKeep>(s, A, W, st)
+               : forward_mode<E, E, KT, VEC, kKeep>(s, A, W, st);
 }
 
 template <class E, bool VEC>
@@ -407,9 +354,9 @@ hipError_t prepare_by(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChu
 
 template <class E, bool VEC>
 hipError_t forward_by(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    if (s.Dk <= 32) return forward<E, 1, 1, VEC>(s, A, W, st);
-    if (s.Dk <= 64) return forward<E, 2, 1, VEC>(s, A, W, st);
-    return forward<E, 4, 1, VEC>(s, A, W, st);
+    if (s.Dk <= 32) return forward<E, 1, VEC>(s, A, W, st);
+    if (s.Dk <= 64) return forward<E, 2, VEC>(s, A, W, st);
+    return forward<E, 4, VEC>(s, A, W, st);
 }
 
 }  // namespace
