@@ -100,10 +100,10 @@ __device__ __forceinline__ void mma_cols(f32x4* c, const Frag<NA>& a, const Frag
                 for (int t = 0; t < T; ++t) c[t] = mfma(a.t[i], b[t].t[j], c[t]);
 }
 
-// Rows of a (B,T,H,D) tensor's head from token t0 on, through a buffer resource: lanes that
-// must not load (absent tokens, columns past D) give an offset past its end and get 0, so a
-// load is never behind a branch and many are in flight.  64 rows span less than 2^31 bytes
-// (the host checks H*D).
+// Up to 64 rows of a (B,T,H,D) tensor's head from token t0 on, through a buffer resource that
+// ends with the row's last token: loads past it, and at the offset kNowhere, return 0.  No load
+// is behind a branch, so many are in flight.  (64 rows span less than 2^31 bytes: the host
+// checks H*D.)
 struct Rows {
     rsrc_t rs;
     unsigned stride;  // bytes from token to token
@@ -111,21 +111,24 @@ struct Rows {
 constexpr unsigned kNowhere = 0x80000000u;
 
 template <class E>
-__device__ __forceinline__ Rows rows_of(const void* base, const DeltaShape& s, int64_t b, int H, int h, int D,
-                                        int64_t t0) {
-    return {make_rsrc(reinterpret_cast<const E*>(base) + ((b * s.T + t0) * H + h) * (int64_t)D, 0x7fffffff),
-            (unsigned)(H * D * (int)sizeof(E))};
+__device__ __forceinline__ Rows rows_of(const void* base, const DeltaShape& s, int64_t b, int H, int h, int D, int t0,
+                                        int len) {
+    const unsigned stride = (unsigned)(H * D * (int)sizeof(E));
+    const int left = len - t0 < kChunk ? len - t0 : kChunk;
+    return {make_rsrc(reinterpret_cast<const E*>(base) + ((b * s.T + t0) * H + h) * (int64_t)D,
+                      (int64_t)stride * (left > 0 ? left : 0)),
+            stride};
 }
 
-// 8 elements of row `row` from column c; those at columns >= D, or all if !live, are 0.
+// 8 elements of row `row` from column c; those at columns >= D, or all if !on, are 0.
 // VEC: D % 8 == 0 and rows 16-byte aligned.
 template <class E, bool VEC>
-__device__ __forceinline__ void load8(const Rows& R, int row, int c, int D, bool live, E* __restrict__ out) {
+__device__ __forceinline__ void load8(const Rows& R, int row, int c, int D, bool on, E* __restrict__ out) {
     const unsigned at = (unsigned)row * R.stride + (unsigned)(c * (int)sizeof(E));
     if constexpr (VEC) {
         constexpr int n = ElemVec<E>::n;
         typedef typename ElemVec<E>::type V;
-        const unsigned off = live && c < D ? at : kNowhere;
+        const unsigned off = on && c < D ? at : kNowhere;
 #pragma unroll
         for (int i = 0; i < 8; i += n) {
             const V t = __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(R.rs, off + 4 * i, 0, 0));
@@ -135,7 +138,7 @@ __device__ __forceinline__ void load8(const Rows& R, int row, int c, int D, bool
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const unsigned off = live && c + i < D ? at + (unsigned)(i * (int)sizeof(E)) : kNowhere;
+            const unsigned off = on && c + i < D ? at + (unsigned)(i * (int)sizeof(E)) : kNowhere;
             if constexpr (sizeof(E) == 2)
                 out[i] = __builtin_bit_cast(E, __builtin_amdgcn_raw_buffer_load_b16(R.rs, off, 0, 0));
             else
@@ -143,6 +146,10 @@ __device__ __forceinline__ void load8(const Rows& R, int row, int c, int D, bool
         }
     }
 }
+
+// Registers of the chains: half a SIMD's for a wave, or all where a workgroup of four waves has
+// the CU to itself (LDS in float32 calls; few heads, see delta_wide, at 128 key channels).
+template <class E, int KT, int NW> constexpr int kWavesPerSimd = NW == 8 || (sizeof(E) == 2 && KT < 4) ? 2 : 1;
 
 template <class E> constexpr int kTerms = sizeof(E) == 2 ? 1 : 3;  // bfloat16 terms of an input
 
@@ -203,48 +210,78 @@ __device__ __forceinline__ int row_length(const DeltaShape& s, int64_t b) {
     return (int)len;
 }
 
-// A chunk of a head on its way to LDS: loads issued for one chunk while another is computed.
-// 256 threads, four lanes a row.
-template <class E, int KT>
+// A 64-row matrix in LDS, rows of 32*KT bfloat16 values plus 16 bytes.  Rows lie 16 by 16, row
+// 4x + a of 16 at place 4a + x: neither the row reads (8 lanes: 8 rows, one column) nor the
+// transposed reads (16 lanes: 4 neighbouring rows, 4 columns) then meet in a bank, and every
+// read of a lane is a constant away from one of three places (LanePos).
+template <int KT>
+struct Mat {
+    static constexpr int LD = 32 * KT + 8;
+    bf16_t v[kChunk * LD];
+    __device__ __forceinline__ static int place(int row) { return (row & ~15) | ((row & 3) << 2) | ((row >> 2) & 3); }
+    __device__ __forceinline__ bf16x8* row8(int row, int c) { return reinterpret_cast<bf16x8*>(v + place(row) * LD + c); }
+};
+
+struct LanePos {
+    int r, g;
+    int tile;  // place of row tile_row(r, half) less half
+    int nat;   // place of row r
+    int col;   // place of row 8g + r/4
+    __device__ __forceinline__ LanePos() {
+        const int lane = threadIdx.x & 63;
+        r = lane & 15;
+        g = lane >> 4;
+        tile = 16 * (r >> 3) + 4 * (r & 3) + 2 * ((r >> 2) & 1);
+        nat = 4 * (r & 3) + (r >> 2);
+        col = 16 * (g >> 1) + 4 * (r >> 2) + 2 * (g & 1);
+    }
+};
+
+// A chunk of a head on its way to LDS: loads issued for one chunk while another is computed, NT
+// threads, 16-byte pieces (of bfloat16) in order.
+template <class E, int KT, int NT>
 struct RowStage {
-    E x[KT][8];
+    static constexpr int P = kChunk * 4 * KT, I = (P + NT - 1) / NT;
+    E x[I][8];
     template <bool VEC>
-    __device__ __forceinline__ void load(const Rows& R, int D, int len) {  // len: tokens from the chunk's first
-        const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3;
+    __device__ __forceinline__ void load(const Rows& R, int D) {
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            const int c = 8 * (quarter + 4 * i);
-            load8<E, VEC>(R, row, c, D, row < len, x[i]);
+        for (int i = 0; i < I; ++i) {
+            const int id = (int)threadIdx.x + i * NT, row = id / (4 * KT), c = 8 * (id % (4 * KT));
+            load8<E, VEC>(R, row, c, D, P % NT == 0 || id < P, x[i]);
         }
     }
-    // As bfloat16 terms into dst[term][row][.], zero past D (of 32*KT) and past the row's length.
-    template <int LD>
-    __device__ __forceinline__ void store(bf16_t (*dst)[kChunk][LD]) const {
-        const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3;
+    // As bfloat16 terms, zero past D (of 32*KT) and past the row's length.
+    __device__ __forceinline__ void store(Mat<KT>* dst) const {
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
+        for (int i = 0; i < I; ++i) {
+            const int id = (int)threadIdx.x + i * NT, row = id / (4 * KT), c = 8 * (id % (4 * KT));
             const Frag<kTerms<E>> f = to_frag<E>(x[i]);
+            if (P % NT == 0 || id < P)
 #pragma unroll
-            for (int m = 0; m < kTerms<E>; ++m)
-                *reinterpret_cast<bf16x8*>(&dst[m][row][8 * (quarter + 4 * i)]) = f.t[m];
+                for (int m = 0; m < kTerms<E>; ++m) *dst[m].row8(row, c) = f.t[m];
         }
     }
 };
 
 // A chunk's inverse and decays likewise; the inverse as three bfloat16 terms.
-template <class E>
+template <class E, int NT>
 struct InverseStage {
-    float x[16];
+    static constexpr int I = kChunk * 8 / NT;
+    float x[I][8];
     double gam, end;
     float be;
-    __device__ __forceinline__ void load(const DeltaChunks& W, int64_t cb, const Rows& beta, int len) {
-        const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3, t = threadIdx.x & 63;
-        const float* p = W.tinv + cb * (kChunk * kChunk) + row * kChunk + 8 * quarter;
+    __device__ __forceinline__ void load(const DeltaChunks& W, int64_t cb, const Rows& beta) {
+        const int t = threadIdx.x & 63;
+        const float* p = W.tinv + cb * (kChunk * kChunk) + 8 * threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load16<float>(p + 32 * (i >> 1) + 4 * (i & 1), x + 4 * i);
+        for (int i = 0; i < I; ++i) {
+            load16<float>(p + 8 * NT * i, x[i]);
+            load16<float>(p + 8 * NT * i + 4, x[i] + 4);
+        }
         gam = W.gam[cb * kChunk + t];
         end = W.gam[cb * kChunk + kChunk - 1];
-        const unsigned off = t < len ? (unsigned)t * beta.stride : kNowhere;
+        const unsigned off = (unsigned)t * beta.stride;
         if constexpr (sizeof(E) == 2)
             be = (float)__builtin_bit_cast(E, __builtin_amdgcn_raw_buffer_load_b16(beta.rs, off, 0, 0));
         else
@@ -252,12 +289,13 @@ struct InverseStage {
     }
     template <class Lds>
     __device__ __forceinline__ void store(Lds& L) const {
-        const int row = threadIdx.x >> 2, quarter = threadIdx.x & 3, t = threadIdx.x;
+        const int t = threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const Frag<3> f = split<3>(x + 8 * i);
+        for (int i = 0; i < I; ++i) {
+            const int id = t + i * NT;
+            const Frag<3> f = split<3>(x[i]);
 #pragma unroll
-            for (int m = 0; m < 3; ++m) *reinterpret_cast<bf16x8*>(&L.t[m][row][8 * quarter + 32 * i]) = f.t[m];
+            for (int m = 0; m < 3; ++m) *L.t[m].row8(id >> 3, 8 * (id & 7)) = f.t[m];
         }
         if (t < kChunk) {
             L.gam[t] = gam;
@@ -274,39 +312,61 @@ template <class E>
 struct ColumnStage {
     E x[4][8];
     template <bool VEC>
-    __device__ __forceinline__ void load(const Rows& R, int c0, int D, int len) {
+    __device__ __forceinline__ void load(const Rows& R, int c0, int D) {
         const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const int row = 32 * (t >> 1) + tile_row(r, t & 1);
-            load8<E, VEC>(R, row, c0 + 8 * g, D, row < len && g < 2, x[t]);
+            load8<E, VEC>(R, row, c0 + 8 * g, D, g < 2, x[t]);
         }
     }
 };
 
-// Row operand (A or B): 8 columns from c of row `row`.
-template <int N, int LD>
-__device__ __forceinline__ Frag<N> read_row(const bf16_t (*m)[kChunk][LD], int row, int c) {
+// Row operands (A or B) of columns 32*kk..: rows 32*k2 + tile_row(m, half), or 16*t + m.
+template <int N, int KT>
+__device__ __forceinline__ Frag<N> read_tile(const Mat<KT>* m, const LanePos& p, int k2, int half, int kk) {
     Frag<N> f;
 #pragma unroll
-    for (int n = 0; n < N; ++n) f.t[n] = *reinterpret_cast<const bf16x8*>(&m[n][row][c]);
+    for (int n = 0; n < N; ++n)
+        f.t[n] = *reinterpret_cast<const bf16x8*>(m[n].v + p.tile * Mat<KT>::LD + 8 * p.g +
+                                                  ((32 * k2 + half) * Mat<KT>::LD + 32 * kk));
     return f;
 }
 
-// Column operand of the transposed matrix: rows row0 + 8g.. (32 of them over the wave), columns
-// c0 + c(r); PERM: the columns of D tile `half` of a 32-column block, else 16 in order.
-template <int N, bool PERM, int LD>
-__device__ __forceinline__ Frag<N> read_col(const bf16_t (*m)[kChunk][LD], int row0, int c0, int half) {
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    const int row = row0 + 8 * g + (r >> 2), c = PERM ? c0 + 8 * (r & 3) + 4 * half : c0 + 4 * (r & 3);
+template <int N, int KT>
+__device__ __forceinline__ Frag<N> read_rows(const Mat<KT>* m, const LanePos& p, int t, int kk) {
+    Frag<N> f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        f.t[n] = *reinterpret_cast<const bf16x8*>(m[n].v + p.nat * Mat<KT>::LD + 8 * p.g +
+                                                  (16 * t * Mat<KT>::LD + 32 * kk));
+    return f;
+}
+
+// Operands of the transposed matrix: rows 32*k2.. (the product's inner index); columns 32*kk +
+// tile_row(m, half) (PERM) or c0 + m.
+template <int N, bool PERM, int KT>
+__device__ __forceinline__ Frag<N> read_col(const Mat<KT>* m, const LanePos& p, int k2, int c0, int half) {
     Frag<N> f;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const bf16x4 lo = read_transposed(&m[n][row][c]), hi = read_transposed(&m[n][row + 4][c]);
+        const bf16_t* at = m[n].v + p.col * Mat<KT>::LD + (PERM ? 8 : 4) * (p.r & 3) +
+                           (32 * k2 * Mat<KT>::LD + c0 + 4 * half);
+        const bf16x4 lo = read_transposed(at), hi = read_transposed(at + Mat<KT>::LD);
         f.t[n] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     return f;
 }
+
+// Columns 16*ct + 4g.. of row 16*t + r.
+template <int KT>
+__device__ __forceinline__ bf16x4* quad(Mat<KT>* m, const LanePos& p, int t, int ct) {
+    return reinterpret_cast<bf16x4*>(m->v + p.nat * Mat<KT>::LD + 4 * p.g + (16 * t * Mat<KT>::LD + 16 * ct));
+}
+
+// Nothing is scheduled across: keeps a phase's loads from LDS out of the phase before it, whose
+// registers they would need.
+__device__ __forceinline__ void phase() { __builtin_amdgcn_sched_barrier(0); }
 
 // B operands of the product with the identity that turns an A operand's 32 rows k into D's
 // columns: columns r = k - 16*which.

@@ -49,7 +49,10 @@ inline int64_t delta_chunks(const DeltaShape& s) { return s.B * s.Hv * ((s.T + 6
 // chained through it: what is kept is then float32, so that those tokens' gradients are not
 // limited by the rounding of x and the states.
 inline bool delta_keeps_f32(int dtype, const void* s_in) { return dtype == 0 || s_in != nullptr; }
-inline int delta_blocks(const DeltaShape& s) { return (s.Dv + 63) / 64 * 4; }
+inline int delta_blocks(const DeltaShape& s) { return (s.Dv + 127) / 128 * 8; }
+// Eight waves to a workgroup (bfloat16 calls) where a head has the value channels for them and
+// the heads alone fill most of the chip; four, on twice the CUs, else.
+inline bool delta_wide(const DeltaShape& s) { return s.Dv > 64 && s.B * s.Hv >= 144; }
 inline int delta_dkp(const DeltaShape& s) { return s.Dk <= 32 ? 32 : s.Dk <= 64 ? 64 : 128; }
 
 struct DeltaBwdArgs {

@@ -29,30 +29,30 @@ namespace {
 template <class E, int KT, int NS>
 struct ChainLds {
     static constexpr int NI = kTerms<E>;
-    static constexpr int LK = 32 * KT + 8, LT = kChunk + 8;
-    bf16_t k[NI][kChunk][LK], q[NI][kChunk][LK];
-    bf16_t t[3][kChunk][LT];
-    bf16_t p[NS][kChunk][LT];  // P^T
+    Mat<KT> k[NI], q[NI];
+    Mat<2> t[3], p[NS];  // the inverse, P^T
     double gam[kChunk];
     float eg[kChunk], ew[kChunk], be[kChunk];
 };
 
-template <class E, class KE, int KT, bool VEC, int NS>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kernel(DeltaShape s, DeltaBwdArgs A,
-                                                                                  DeltaChunks W, int nc, int ntile) {
+template <class E, class KE, int KT, int NW, bool VEC, int NS>
+__global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_chain_kernel(DeltaShape s, DeltaBwdArgs A,
+                                                                                      DeltaChunks W, int nc, int ntile,
+                                                                                      int nblk) {
     typedef ChainLds<E, KT, NS> Lds;
     constexpr int NI = kTerms<E>;
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const LanePos pos;
+    const int r = pos.r, g = pos.g;
     const int tile = (int)(blockIdx.x % ntile);
     const int64_t bh = blockIdx.x / ntile;
     const int h = (int)(bh % s.Hv), hk = h / (s.Hv / s.Hk);
     const int64_t b = bh / s.Hv;
     const int len = row_length(s, b);
-    const int c0 = tile * 64 + wave * 16;
+    const int c0 = (tile * NW + wave) * 16;
     const int Dk = s.Dk, Dv = s.Dv;
-    const int nblk = ntile * 4;
 
     f32x4 S[2 * KT];  // dS, in the forward's layout of S
     const int64_t sb = bh * (int64_t)Dk * Dv;
@@ -65,15 +65,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
         }
 
     const int nlive = (len + kChunk - 1) / kChunk;
-    RowStage<E, KT> sk, sq;
-    InverseStage<E> si;
+    RowStage<E, KT, 64 * NW> sk, sq;
+    InverseStage<E, 64 * NW> si;
     ColumnStage<E> so;
     const auto fetch = [&](int n) {
-        const int t0 = n * kChunk, left = len - t0;
-        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0), Dk, left);
-        si.load(W, bh * nc + n, rows_of<E>(A.beta, s, b, s.Hv, h, 1, t0), left);
-        so.template load<VEC>(rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0), c0, Dv, left);
-        sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0), Dk, left);
+        const int t0 = n * kChunk;
+        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0, len), Dk);
+        si.load(W, bh * nc + n, rows_of<E>(A.beta, s, b, s.Hv, h, 1, t0, len));
+        so.template load<VEC>(rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0, len), c0, Dv);
+        sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
     };
     if (nlive > 0) fetch(nlive - 1);
     for (int n = nlive - 1; n >= 0; --n) {
@@ -87,19 +87,16 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
 #pragma unroll
         for (int t = 0; t < 4; ++t) fv[t] = to_frag<E>(so.x[t]);
         __syncthreads();
-        if (n > 0) fetch(n - 1);  // in flight while this chunk is computed
-        // P^T, rows 16*wave..: tiles of Q K^T (rows i, columns j), stored as P^T[j][i].
+        // P^T, rows 16*pt..: tiles of Q K^T (rows i, columns j), stored as P^T[j][i].
         {
-            const int j = 16 * wave + r;
+            const int pt = wave & 3, j = 16 * pt + r;
             const double gj = L.gam[j];
-            for (int it = wave & 2; it < 4; ++it) {
+            for (int it = (pt & 2) + (wave >> 2); it < 4; it += NW / 4) {
                 f32x4 c = {0.f, 0.f, 0.f, 0.f};
-                if (it >= wave)
+                if (it >= pt)
 #pragma unroll
-                    for (int kk = 0; kk < KT; ++kk) {
-                        const int col = 32 * kk + 8 * g;
-                        mma(c, read_row<NI>(L.q, 16 * it + r, col), read_row<NI>(L.k, j, col));
-                    }
+                    for (int kk = 0; kk < KT; ++kk)
+                        mma(c, read_rows<NI>(L.q, pos, it, kk), read_rows<NI>(L.k, pos, pt, kk));
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -110,10 +107,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
                 const Frag<NS> f = split<NS>(x);
 #pragma unroll
                 for (int m = 0; m < NS; ++m)
-                    *reinterpret_cast<bf16x4*>(&L.p[m][j][16 * it + 4 * g]) =
-                        __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
+                    *quad(&L.p[m], pos, pt, it) = __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
             }
         }
+        phase();
         // K dS' (dS' is also stored, turned so that a lane holds 4 value channels).
         f32x4 U[4];  // rows 32*(t/2) + tile_row(m, t%2)
 #pragma unroll
@@ -122,7 +119,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
         for (int kk = 0; kk < KT; ++kk) {
             Frag<NI> fk[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) fk[t] = read_row<NI>(L.k, 32 * (t >> 1) + tile_row(r, t & 1), 32 * kk + 8 * g);
+            for (int t = 0; t < 4; ++t) fk[t] = read_tile<NI>(L.k, pos, t >> 1, t & 1, kk);
             const Frag<NS> fs = split_tiles<NS>(S[2 * kk], S[2 * kk + 1]);
             mma_rows<4>(U, fk, fs);
 #pragma unroll
@@ -134,6 +131,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
                            x);
             }
         }
+        phase();
         // dO in the D layout: as B operand, and scaled for the state's gradient.
         Frag<NI> fo[2];
         Frag<NS> fd[2];
@@ -157,14 +155,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
         {
             Frag<NS> fp[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) fp[t] = read_row<NS>(L.p, 32 * (t >> 1) + tile_row(r, t & 1), 32 + 8 * g);
+            for (int t = 0; t < 4; ++t) fp[t] = read_tile<NS>(L.p, pos, t >> 1, t & 1, 1);
             mma_rows<4>(U, fp, fo[1]);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) fp[t] = read_row<NS>(L.p, tile_row(r, t), 8 * g);
+            for (int t = 0; t < 2; ++t) fp[t] = read_tile<NS>(L.p, pos, 0, t, 0);
             mma_rows<2>(U, fp, fo[0]);
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) U[t] *= *reinterpret_cast<const f32x4*>(&L.be[32 * (t >> 1) + 8 * g + 4 * (t & 1)]);
+        phase();
         // dZ = N^T (beta dU).
         f32x4 Z[4];
 #pragma unroll
@@ -172,12 +171,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
         {
             Frag<NS> ft[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) ft[t] = read_col<NS, true>(L.t, 32, 32 * (t >> 1), t & 1);
+            for (int t = 0; t < 4; ++t) ft[t] = read_col<NS, true>(L.t, pos, 1, 32 * (t >> 1), t & 1);
             mma_rows<4>(Z, ft, split_tiles<NS>(U[2], U[3]));
 #pragma unroll
-            for (int t = 0; t < 2; ++t) ft[t] = read_col<NS, true>(L.t, 0, 0, t);
+            for (int t = 0; t < 2; ++t) ft[t] = read_col<NS, true>(L.t, pos, 0, 0, t);
             mma_rows<2>(Z, ft, split_tiles<NS>(U[0], U[1]));
         }
+        phase();
         // dV, turned; and -e^gam dZ for the state's gradient.
         Frag<NS> fz[2];
 #pragma unroll
@@ -197,6 +197,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
                 Z[2 * k2 + half] *= -*reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
             fz[k2] = split_tiles<NS>(Z[2 * k2], Z[2 * k2 + 1]);
         }
+        phase();
+        if (n > 0) fetch(n - 1);  // in flight for the rest of this chunk
         // dS = e^{gam_63} dS' + scale Q^T e^gam dO - K^T e^gam dZ, four tiles at a time.
         const float end = L.eg[kChunk - 1];
         constexpr int T = KT == 1 ? 2 : 4;
@@ -209,17 +211,17 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
                 Frag<NI> fq[T], fk[T];
 #pragma unroll
                 for (int t = 0; t < T; ++t) {
-                    fq[t] = read_col<NI, true>(L.q, 32 * k2, 32 * ((d + t) >> 1), t & 1);
-                    fk[t] = read_col<NI, true>(L.k, 32 * k2, 32 * ((d + t) >> 1), t & 1);
+                    fq[t] = read_col<NI, true>(L.q, pos, k2, 32 * ((d + t) >> 1), t & 1);
+                    fk[t] = read_col<NI, true>(L.k, pos, k2, 32 * ((d + t) >> 1), t & 1);
                 }
                 mma_rows<T>(S + d, fq, fd[k2]);
                 mma_rows<T>(S + d, fk, fz[k2]);
             }
         }
     }
-    for (int64_t t = (int64_t)nlive * kChunk + wave; t < s.T; t += 4) {
+    for (int64_t t = (int64_t)nlive * kChunk + wave; t < s.T; t += NW) {
         E* op = reinterpret_cast<E*>(A.gv) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
-        if (tile * 64 + lane < Dv) op[tile * 64 + lane] = (E)0.f;
+        for (int c = tile * NW * 16 + lane; c < (tile + 1) * NW * 16 && c < Dv; c += 64) op[c] = (E)0.f;
     }
     if (A.gs_in)
 #pragma unroll
@@ -239,9 +241,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_chain_kerne
 template <class E, int KT>
 struct GradLds {
     static constexpr int NI = kTerms<E>;
-    static constexpr int LK = 32 * KT + 8, LT = kChunk + 8;
-    bf16_t k[NI][kChunk][LK], q[NI][kChunk][LK];
-    bf16_t h[NI][kChunk][LT], e[NI][kChunk][LT];  // scale L beta H, L beta E: rows i, columns j
+    Mat<KT> k[NI], q[NI];
+    Mat<2> h[NI], e[NI];  // scale L beta H, L beta E: rows i, columns j
     double gam[kChunk];
     float be[kChunk];
     float col[4][kChunk];  // sums over each wave's i > j of M_ij; M_jj on its own, so that sums that
@@ -268,12 +269,14 @@ __device__ __forceinline__ Frag<N> read_block(const KE* m, int rows, int row, in
 }
 
 template <class E, class KE, int KT, bool VEC>
-__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc, int nblk) {
+__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc, int, int nblk) {
     typedef GradLds<E, KT> Lds;
     constexpr int NI = kTerms<E>, NK = kKeptTerms<E, KE>, DT = 2 * KT;  // tiles of key channels
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const LanePos pos;
+    const int r = pos.r, g = pos.g;
     const int n = (int)(blockIdx.x % nc);
     const int64_t bk = blockIdx.x / nc;
     const int hk = (int)(bk % s.Hk), rep = s.Hv / s.Hk;
@@ -297,9 +300,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
         return;
     }
     {
-        RowStage<E, KT> sk, sq;
-        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0), Dk, len - t0);
-        sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0), Dk, len - t0);
+        RowStage<E, KT, 256> sk, sq;
+        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0, len), Dk);
+        sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
         sk.store(L.k);
         sq.store(L.q);
     }
@@ -312,10 +315,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
         if (jt <= wave)
 #pragma unroll
             for (int kk = 0; kk < KT; ++kk) {
-                const int col = 32 * kk + 8 * g;
-                const Frag<NI> fk = read_row<NI>(L.k, 16 * jt + r, col);
-                mma(qk[jt], fk, read_row<NI>(L.q, mine, col));
-                mma(kk_[jt], fk, read_row<NI>(L.k, mine, col));
+                const Frag<NI> fk = read_rows<NI>(L.k, pos, jt, kk);
+                mma(qk[jt], fk, read_rows<NI>(L.q, pos, wave, kk));
+                mma(kk_[jt], fk, read_rows<NI>(L.k, pos, wave, kk));
             }
     }
     f32x4 dq[DT], dk[DT];
@@ -335,7 +337,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
         const KE* X = reinterpret_cast<const KE*>(W.x) + cb * nblk * (kChunk * 16);
         const KE* S0 = reinterpret_cast<const KE*>(W.s0) + cb * nblk * (32 * KT * 16);
         const KE* DS = reinterpret_cast<const KE*>(W.ds) + cb * nblk * (32 * KT * 16);
-        const Rows go = rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0), gz = rows_of<E>(A.gv, s, b, s.Hv, h, Dv, t0);
+        const Rows go = rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0, len), gz = rows_of<E>(A.gv, s, b, s.Hv, h, Dv, t0, len);
         f32x4 H[4], Z[4], rq[DT], rk[DT], wk[DT];
         float dot = 0.f;
 #pragma unroll
@@ -345,9 +347,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
         for (int kv = 0; 32 * kv < Dv; ++kv) {
             E x[8];
             const int c = 32 * kv + 8 * g;
-            load8<E, VEC>(go, mine, c, Dv, tok < len, x);
+            load8<E, VEC>(go, mine, c, Dv, true, x);
             const Frag<NI> fo = to_frag<E>(x);
-            load8<E, VEC>(gz, mine, c, Dv, tok < len, x);
+            load8<E, VEC>(gz, mine, c, Dv, true, x);
             const Frag<NI> fz = to_frag<E>(x);
             const Frag<NK> fx = read_block<KE, NK>(X, kChunk, mine, kv);
 #pragma unroll
@@ -406,10 +408,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
             const Frag<NI> fh = split<NI>(hw), fe = split<NI>(ez);
 #pragma unroll
             for (int m = 0; m < NI; ++m) {
-                *reinterpret_cast<bf16x4*>(&L.h[m][mine][16 * jt + 4 * g]) =
-                    __builtin_shufflevector(fh.t[m], fh.t[m], 0, 1, 2, 3);
-                *reinterpret_cast<bf16x4*>(&L.e[m][mine][16 * jt + 4 * g]) =
-                    __builtin_shufflevector(fe.t[m], fe.t[m], 0, 1, 2, 3);
+                *quad(&L.h[m], pos, wave, jt) = __builtin_shufflevector(fh.t[m], fh.t[m], 0, 1, 2, 3);
+                *quad(&L.e[m], pos, wave, jt) = __builtin_shufflevector(fe.t[m], fe.t[m], 0, 1, 2, 3);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -427,8 +427,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
             f32x4 q4 = {0.f, 0.f, 0.f, 0.f}, k4 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int m = NI - 1; m >= 0; --m) {
-                const bf16x4 a = *reinterpret_cast<const bf16x4*>(&L.q[m][mine][16 * d + 4 * g]);
-                const bf16x4 c = *reinterpret_cast<const bf16x4*>(&L.k[m][mine][16 * d + 4 * g]);
+                const bf16x4 a = *quad(&L.q[m], pos, wave, d);
+                const bf16x4 c = *quad(&L.k[m], pos, wave, d);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) q4[e] += (float)a[e], k4[e] += (float)c[e];
             }
@@ -458,11 +458,11 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
             // Rows j (for dq) or i (for dk) 32*k2..; this wave's columns see the ones it is coupled to.
             const bool below = 2 * k2 <= wave, above = 2 * k2 + 1 >= wave;
             Frag<NI> hr_, ec, er;
-            if (below) hr_ = read_row<NI>(L.h, mine, 32 * k2 + 8 * g), er = read_row<NI>(L.e, mine, 32 * k2 + 8 * g);
+            if (below) hr_ = read_rows<NI>(L.h, pos, wave, k2), er = read_rows<NI>(L.e, pos, wave, k2);
             Frag<NI> hc;
             if (above) {
-                hc = read_col<NI, false>(L.h, 32 * k2, 16 * wave, 0);
-                ec = read_col<NI, false>(L.e, 32 * k2, 16 * wave, 0);
+                hc = read_col<NI, false>(L.h, pos, k2, 16 * wave, 0);
+                ec = read_col<NI, false>(L.e, pos, k2, 16 * wave, 0);
 #pragma unroll
                 for (int m = 0; m < NI; ++m)
 #pragma unroll
@@ -475,13 +475,13 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
                     for (int i = 0; i < 8; ++i) er.t[m][i] = -er.t[m][i];
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                const Frag<NI> fk = read_col<NI, false>(L.k, 32 * k2, 16 * d, 0);
+                const Frag<NI> fk = read_col<NI, false>(L.k, pos, k2, 16 * d, 0);
                 if (below) {
                     mma(dq[d], fk, hr_);
                     mma(dk[d], fk, er);
                 }
                 if (above) {
-                    mma(dk[d], read_col<NI, false>(L.q, 32 * k2, 16 * d, 0), hc);
+                    mma(dk[d], read_col<NI, false>(L.q, pos, k2, 16 * d, 0), hc);
                     mma(dk[d], fk, ec);
                 }
             }
@@ -522,23 +522,28 @@ bool vec_ok(const DeltaShape& s, const DeltaBwdArgs& A) {
 
 template <class K>
 hipError_t launch(K kernel, int64_t blocks, int bytes, hipStream_t st, const DeltaShape& s, const DeltaBwdArgs& A,
-                  const DeltaChunks& W, int last) {
+                  const DeltaChunks& W, int threads, int ntile) {
     // More dynamic LDS than the default 64 KiB has to be asked for.
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(256), bytes, st, s, A, W,
-                       (int)((s.T + kChunk - 1) / kChunk), last);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), bytes, st, s, A, W,
+                       (int)((s.T + kChunk - 1) / kChunk), ntile, delta_blocks(s));
     return hipGetLastError();
 }
 
 template <class E, class KE, int KT, int NS, bool VEC>
 hipError_t backward(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    const int ntile = (s.Dv + 63) / 64;
-    const hipError_t e = launch(delta_chain_kernel<E, KE, KT, VEC, NS>, s.B * s.Hv * ntile,
-                                (int)sizeof(ChainLds<E, KT, NS>), st, s, A, W, ntile);
+    const int bytes = (int)sizeof(ChainLds<E, KT, NS>), wide = (s.Dv + 127) / 128, narrow = (s.Dv + 63) / 64;
+    hipError_t e;
+    bool done = false;
+    if constexpr (sizeof(E) == 2)
+        if ((done = delta_wide(s)))
+            e = launch(delta_chain_kernel<E, KE, KT, 8, VEC, NS>, s.B * s.Hv * wide, bytes, st, s, A, W, 512, wide);
+    if (!done)
+        e = launch(delta_chain_kernel<E, KE, KT, 4, VEC, NS>, s.B * s.Hv * narrow, bytes, st, s, A, W, 256, narrow);
     if (e != hipSuccess) return e;
     return launch(delta_grad_kernel<E, KE, KT, VEC>, s.B * s.Hk * ((s.T + kChunk - 1) / kChunk),
-                  (int)sizeof(GradLds<E, KT>), st, s, A, W, delta_blocks(s));
+                  (int)sizeof(GradLds<E, KT>), st, s, A, W, 256, 0);
 }
 
 template <class E, class KE, int NS, bool VEC>

@@ -44,7 +44,7 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
         bet[lane] = live ? (float)reinterpret_cast<const E*>(A.beta)[at] : 0.f;
         W.gam[blk * kChunk + lane] = c;
     }
-    const Rows K = rows_of<E>(A.k, s, b, s.Hk, hk, s.Dk, t0);
+    const Rows K = rows_of<E>(A.k, s, b, s.Hk, hk, s.Dk, t0, len);
     Frag<NI> kf[4][KT];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -52,7 +52,7 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
 #pragma unroll
         for (int kk = 0; kk < KT; ++kk) {
             E x[8];
-            load8<E, VEC>(K, row, 32 * kk + 8 * g, s.Dk, t0 + row < len, x);
+            load8<E, VEC>(K, row, 32 * kk + 8 * g, s.Dk, true, x);
             kf[t][kk] = to_frag<E>(x);
         }
     }
@@ -85,10 +85,11 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
 }
 
 // ---- the chain over a head's chunks -----------------------------------------------------------
-// A workgroup of four waves owns 64 value channels of one head, a wave 16 of them, all rows of
+// A workgroup of NW waves owns 16*NW value channels of one head, a wave 16 of them, all rows of
 // the state (32*KT, zero past Dk).  K, Q, the inverse and P lie in LDS as bfloat16 terms, shared
 // by the waves; V comes from memory in the A layout and is turned into the D layout by a product
-// with the identity, which is exact.  The next chunk's loads are in flight while one is computed.
+// with the identity, which is exact.  The next chunk's loads are in flight during the second half
+// of one.
 //
 // Terms: the state and what flows into it (Z, beta X) are taken as three bfloat16 terms, so
 // that S keeps float32 precision over any number of chunks; the outputs of bfloat16 calls take
@@ -96,10 +97,8 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
 template <class E, int KT>
 struct FwdLds {
     static constexpr int NI = kTerms<E>, NO = NI == 1 ? 2 : 3;  // terms of inputs, of the outputs' operands
-    static constexpr int LK = 32 * KT + 8, LT = kChunk + 8;
-    bf16_t k[NI][kChunk][LK], q[NI][kChunk][LK];
-    bf16_t t[3][kChunk][LT];
-    bf16_t p[NO][kChunk][LT];
+    Mat<KT> k[NI], q[NI];
+    Mat<2> t[3], p[NO];  // the inverse, P
     double gam[kChunk];
     float eg[kChunk], ew[kChunk], be[kChunk];
 };
@@ -107,23 +106,25 @@ struct FwdLds {
 // What the chain leaves: o, and what the backward starts from (of type KE).
 constexpr int kOut = 1, kKeep = 2;
 
-template <class E, class KE, int KT, bool VEC, int MODE>
-__global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_kernel(DeltaShape s, DeltaFwdArgs A,
-                                                                                    DeltaChunks W, int nc, int ntile) {
+template <class E, class KE, int KT, int NW, bool VEC, int MODE>
+__global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_forward_kernel(DeltaShape s, DeltaFwdArgs A,
+                                                                                        DeltaChunks W, int nc,
+                                                                                        int ntile, int nblk) {
     typedef FwdLds<E, KT> Lds;
     constexpr int NI = kTerms<E>, NO = Lds::NO, NS = 3;
     constexpr bool OUT = MODE & kOut, KEEP = MODE & kKeep;
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, r = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const LanePos pos;
+    const int r = pos.r, g = pos.g;
     const int tile = (int)(blockIdx.x % ntile);
     const int64_t bh = blockIdx.x / ntile;
     const int h = (int)(bh % s.Hv), hk = h / (s.Hv / s.Hk);
     const int64_t b = bh / s.Hv;
     const int len = row_length(s, b);
-    const int c0 = tile * 64 + wave * 16;  // this wave's first value channel
+    const int c0 = (tile * NW + wave) * 16;  // this wave's first value channel
     const int Dk = s.Dk, Dv = s.Dv;
-    const int nblk = ntile * 4;  // blocks of 16 value channels
 
     // State: D tiles S[2kk + half], rows 32kk + tile_row(m, half), columns c0 + r.
     f32x4 S[2 * KT];
@@ -137,15 +138,15 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
         }
 
     const int nlive = (len + kChunk - 1) / kChunk;
-    RowStage<E, KT> sk, sq;
-    InverseStage<E> si;
+    RowStage<E, KT, 64 * NW> sk, sq;
+    InverseStage<E, 64 * NW> si;
     ColumnStage<E> sv;
     const auto fetch = [&](int n) {
-        const int t0 = n * kChunk, left = len - t0;
-        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0), Dk, left);
-        si.load(W, bh * nc + n, rows_of<E>(A.beta, s, b, s.Hv, h, 1, t0), left);
-        sv.template load<VEC>(rows_of<E>(A.v, s, b, s.Hv, h, Dv, t0), c0, Dv, left);
-        if constexpr (OUT) sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0), Dk, left);
+        const int t0 = n * kChunk;
+        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0, len), Dk);
+        si.load(W, bh * nc + n, rows_of<E>(A.beta, s, b, s.Hv, h, 1, t0, len));
+        sv.template load<VEC>(rows_of<E>(A.v, s, b, s.Hv, h, Dv, t0, len), c0, Dv);
+        if constexpr (OUT) sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
     };
     if (nlive > 0) fetch(0);
     for (int n = 0; n < nlive; ++n) {
@@ -159,19 +160,16 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
 #pragma unroll
         for (int t = 0; t < 4; ++t) fv[t] = to_frag<E>(sv.x[t]);
         __syncthreads();
-        if (n + 1 < nlive) fetch(n + 1);
-        // P, rows 16*wave..: tiles of K Q^T (rows j, columns i), stored as P[i][j].
+        // P, rows 16*pt..: tiles of K Q^T (rows j, columns i), stored as P[i][j].
         if constexpr (OUT) {
-            const int i = 16 * wave + r;
+            const int pt = wave & 3, i = 16 * pt + r;
             const double gi = L.gam[i];
-            for (int jt = 0; jt <= (wave | 1); ++jt) {
+            for (int jt = wave >> 2; jt <= (pt | 1); jt += NW / 4) {
                 f32x4 c = {0.f, 0.f, 0.f, 0.f};
-                if (jt <= wave)
+                if (jt <= pt)
 #pragma unroll
-                    for (int kk = 0; kk < KT; ++kk) {
-                        const int col = 32 * kk + 8 * g;
-                        mma(c, read_row<NI>(L.k, 16 * jt + r, col), read_row<NI>(L.q, i, col));
-                    }
+                    for (int kk = 0; kk < KT; ++kk)
+                        mma(c, read_rows<NI>(L.k, pos, jt, kk), read_rows<NI>(L.q, pos, pt, kk));
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -182,10 +180,10 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
                 const Frag<NO> f = split<NO>(x);
 #pragma unroll
                 for (int m = 0; m < NO; ++m)
-                    *reinterpret_cast<bf16x4*>(&L.p[m][i][16 * jt + 4 * g]) =
-                        __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
+                    *quad(&L.p[m], pos, pt, jt) = __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
             }
         }
+        phase();
         // K S and the state's part of O^T.
         f32x4 Z[4], O[4];  // Z[t]: rows 32*(t/2) + tile_row(m, t%2); O^T[t]: columns 16*t + r
 #pragma unroll
@@ -195,8 +193,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
             Frag<NI> fk[4], fq[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                fk[t] = read_row<NI>(L.k, 32 * (t >> 1) + tile_row(r, t & 1), 32 * kk + 8 * g);
-                if constexpr (OUT) fq[t] = read_row<NI>(L.q, 16 * t + r, 32 * kk + 8 * g);
+                fk[t] = read_tile<NI>(L.k, pos, t >> 1, t & 1, kk);
+                if constexpr (OUT) fq[t] = read_rows<NI>(L.q, pos, t, kk);
             }
             const Frag<NS> fs = split_tiles<NS>(S[2 * kk], S[2 * kk + 1]);
             mma_rows<4>(Z, fk, fs);
@@ -221,6 +219,7 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
             for (int e = 0; e < 4; ++e) Z[t][e] = fmaf(-eg[e], Z[t][e], v[e]);
             if constexpr (OUT) O[t] *= s.scale * L.eg[16 * t + r];
         }
+        phase();
         // X = inverse Z (its upper right block is zero).
         f32x4 U[4];
 #pragma unroll
@@ -228,12 +227,13 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
         {
             Frag<3> ft[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) ft[t] = read_row<3>(L.t, 32 * (t >> 1) + tile_row(r, t & 1), 8 * g);
+            for (int t = 0; t < 4; ++t) ft[t] = read_tile<3>(L.t, pos, t >> 1, t & 1, 0);
             mma_rows<4>(U, ft, split_tiles<NS>(Z[0], Z[1]));
 #pragma unroll
-            for (int t = 2; t < 4; ++t) ft[t] = read_row<3>(L.t, 32 + tile_row(r, t & 1), 32 + 8 * g);
+            for (int t = 2; t < 4; ++t) ft[t] = read_tile<3>(L.t, pos, 1, t & 1, 1);
             mma_rows<2>(U + 2, ft + 2, split_tiles<NS>(Z[2], Z[3]));
         }
+        phase();
         Frag<NO> fu[2];  // beta X for the outputs
         Frag<NS> fw[2];  // e^{gam_63 - gam} beta X for the state
 #pragma unroll
@@ -259,6 +259,8 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
             if constexpr (OUT) fu[k2] = split_tiles<NO>(U[2 * k2], U[2 * k2 + 1]);
             fw[k2] = split_tiles<NS>(w[0], w[1]);
         }
+        phase();
+        if (n + 1 < nlive) fetch(n + 1);
         // S' = e^{gam_63} S + K^T w, four tiles at a time.
         const float end = L.eg[kChunk - 1];
         constexpr int T = KT == 1 ? 2 : 4;
@@ -270,19 +272,20 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
             for (int k2 = 0; k2 < 2; ++k2) {
                 Frag<NI> ft[T];
 #pragma unroll
-                for (int t = 0; t < T; ++t) ft[t] = read_col<NI, true>(L.k, 32 * k2, 32 * ((d + t) >> 1), t & 1);
+                for (int t = 0; t < T; ++t) ft[t] = read_col<NI, true>(L.k, pos, k2, 32 * ((d + t) >> 1), t & 1);
                 mma_rows<T>(S + d, ft, fw[k2]);
             }
         }
         if constexpr (OUT) {
+            phase();
             __syncthreads();  // P is there
             // O^T += U^T P^T (P's upper right block is zero).
             Frag<NO> fp[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) fp[t] = read_row<NO>(L.p, 16 * t + r, 8 * g);
+            for (int t = 0; t < 4; ++t) fp[t] = read_rows<NO>(L.p, pos, t, 0);
             mma_cols<4>(O, fu[0], fp);
 #pragma unroll
-            for (int t = 2; t < 4; ++t) fp[t] = read_row<NO>(L.p, 16 * t + r, 32 + 8 * g);
+            for (int t = 2; t < 4; ++t) fp[t] = read_rows<NO>(L.p, pos, t, 1);
             mma_cols<2>(O + 2, fu[1], fp + 2);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -295,9 +298,9 @@ __global__ __launch_bounds__(256, sizeof(E) == 2 ? 2 : 1) void delta_forward_ker
     }
     // Chunks past the row's length: zero outputs.
     if constexpr (OUT)
-        for (int64_t t = (int64_t)nlive * kChunk + wave; t < s.T; t += 4) {
+        for (int64_t t = (int64_t)nlive * kChunk + wave; t < s.T; t += NW) {
             E* op = reinterpret_cast<E*>(A.o) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
-            if (tile * 64 + lane < Dv) op[tile * 64 + lane] = (E)0.f;
+            for (int c = tile * NW * 16 + lane; c < (tile + 1) * NW * 16 && c < Dv; c += 64) op[c] = (E)0.f;
         }
     if (A.s_out)
 #pragma unroll
@@ -322,17 +325,24 @@ hipError_t prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks
     return hipGetLastError();
 }
 
-template <class E, class KE, int KT, bool VEC, int MODE>
-hipError_t forward_mode(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    auto kernel = delta_forward_kernel<E, KE, KT, VEC, MODE>;
+template <class E, class KE, int KT, int NW, bool VEC, int MODE>
+hipError_t forward_nw(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    auto kernel = delta_forward_kernel<E, KE, KT, NW, VEC, MODE>;
     const int bytes = (int)sizeof(FwdLds<E, KT>);
     // More dynamic LDS than the default 64 KiB has to be asked for.
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int ntile = (s.Dv + 63) / 64;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(s.B * s.Hv * ntile)), dim3(256), bytes, st, s, A, W,
-                       (int)((s.T + kChunk - 1) / kChunk), ntile);
+    const int ntile = (s.Dv + 16 * NW - 1) / (16 * NW);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(s.B * s.Hv * ntile)), dim3(64 * NW), bytes, st, s, A, W,
+                       (int)((s.T + kChunk - 1) / kChunk), ntile, delta_blocks(s));
     return hipGetLastError();
+}
+
+template <class E, class KE, int KT, bool VEC, int MODE>
+hipError_t forward_mode(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    if constexpr (sizeof(E) == 2)
+        if (delta_wide(s)) return forward_nw<E, KE, KT, 8, VEC, MODE>(s, A, W, st);
+    return forward_nw<E, KE, KT, 4, VEC, MODE>(s, A, W, st);
 }
 
 template <class E, int KT, bool VEC>
