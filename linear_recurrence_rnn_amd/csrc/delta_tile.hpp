@@ -235,6 +235,11 @@ struct LanePos {
         nat = 4 * (r & 3) + (r >> 2);
         col = 16 * (g >> 1) + 4 * (r >> 2) + 2 * (g & 1);
     }
+    // The same values, but addresses formed from them are formed again: in a loop they would
+    // otherwise be kept from before it, in more registers than there are.
+    __device__ __forceinline__ void renew() {
+        asm volatile("" : "+v"(r), "+v"(g), "+v"(tile), "+v"(nat), "+v"(col));
+    }
 };
 
 // A chunk of a head on its way to LDS: loads issued for one chunk while another is computed, NT
@@ -244,11 +249,11 @@ struct RowStage {
     static constexpr int P = kChunk * 4 * KT, I = (P + NT - 1) / NT;
     E x[I][8];
     template <bool VEC>
-    __device__ __forceinline__ void load(const Rows& R, int D) {
+    __device__ __forceinline__ void load(const Rows& R, int D, int c0 = 0) {
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             const int id = (int)threadIdx.x + i * NT, row = id / (4 * KT), c = 8 * (id % (4 * KT));
-            load8<E, VEC>(R, row, c, D, P % NT == 0 || id < P, x[i]);
+            load8<E, VEC>(R, row, c0 + c, D, P % NT == 0 || id < P, x[i]);
         }
     }
     // As bfloat16 terms, zero past D (of 32*KT) and past the row's length.

@@ -234,27 +234,77 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
 }
 
 // ---- the gradients of a chunk ---------------------------------------------------------------------
-// A workgroup takes one chunk of one key head and goes through the value heads that read it, so
-// dq and dk are summed over them in head order, in registers.  Wave w owns the chunk's tokens
-// 16w..16w+15 as columns: dq^T, dk^T tiles (rows: key channels), and the tiles of H^T and E^T
-// (rows j <= its i).  Operands are the tensors' own type (one bfloat16 term, or three).
-template <class E, int KT>
+// A workgroup of eight waves takes one chunk of one key head and goes through the value heads
+// that read it, so dq and dk are summed over them in head order, in registers.  A wave owns 16
+// key channels (all 64 tokens at 128 key channels, 32 or 16 of them at fewer): dq^T, dk^T and the
+// products with S and dS' have its key channels as rows, so every byte of S and dS' is loaded
+// once, straight into operands.  dO, dZ and X, which all waves need, go through LDS, 32*SK value
+// channels at a time.  The tiles of H^T and E^T (rows j <= its columns i) are dealt to the waves.
+//
+// Operands are the tensors' own type (one bfloat16 term, or three); the weights L beta H and
+// L beta E are rounded to two terms in bfloat16 calls.  Bound by memory: at 128x128 a chunk
+// reads about 180 KB and writes 33 KB a head.
+template <class E, class KE, int KT>
 struct GradLds {
-    static constexpr int NI = kTerms<E>;
+    static constexpr int NI = kTerms<E>, NK = kKeptTerms<E, KE>, NH = NI == 1 ? 2 : 3;
+    static constexpr int SK = NI == 1 ? 4 : 1;
+    static constexpr bool ONE = NI == 3;  // no room for both weights: one after the other
     Mat<KT> k[NI], q[NI];
-    Mat<2> h[NI], e[NI];  // scale L beta H, L beta E: rows i, columns j
+    union {
+        struct {
+            Mat<SK> go[NI], gz[NI], x[NK];
+        };
+        struct {
+            Mat<2> h[NH], e[ONE ? 1 : NH];  // scale L beta H, L beta E: rows i, columns j
+        };
+    };
     double gam[kChunk];
     float be[kChunk];
-    float col[4][kChunk];  // sums over each wave's i > j of M_ij; M_jj on its own, so that sums that
+    float col[4][kChunk];  // sums over each tile's i > j of M_ij; M_jj on its own, so that sums that
                            // ought to cancel in dg hold nothing that does not belong there
-    float row[kChunk], diag[kChunk], a[kChunk], wr[kChunk];
-    float dot[4];
+    float row[2][kChunk], diag[kChunk];
+    float a[2 * KT][kChunk], wr[2 * KT][kChunk];
+    float dot[8];
+};
+
+// x in LDS as terms from its blocks of 16 value channels, 32*SK channels from block b0 on.
+template <class KE, int N, int SK>
+struct BlockStage {
+    static constexpr int P = kChunk * 4 * SK, I = (P + 511) / 512;
+    KE x[I][8];
+    __device__ __forceinline__ void load(const KE* m, int b0) {
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int id = (int)threadIdx.x + 512 * i;
+            if (P % 512 != 0 && id >= P) break;
+            const KE* p = m + ((int64_t)b0 * kChunk * 16 + 8 * id);
+            if constexpr (sizeof(KE) == 2) {
+                const bf16x8 t = *reinterpret_cast<const bf16x8*>(p);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[i][j] = t[j];
+            } else {
+                load16<float>(p, x[i]);
+                load16<float>(p + 4, x[i] + 4);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(Mat<SK>* dst) const {
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int id = (int)threadIdx.x + 512 * i, row = (id >> 1) & 63, c = 16 * (id >> 7) + 8 * (id & 1);
+            if (P % 512 != 0 && id >= P) break;
+            Frag<N> f;
+            if constexpr (sizeof(KE) == 2) f = to_frag<KE>(x[i]);
+            else f = split<N>(x[i]);
+#pragma unroll
+            for (int m = 0; m < N; ++m) *dst[m].row8(row, c) = f.t[m];
+        }
+    }
 };
 
 // 8 value channels from 32*kv + 8g of row `row` of a matrix kept in blocks of 16 channels.
 template <class KE, int N>
-__device__ __forceinline__ Frag<N> read_block(const KE* m, int rows, int row, int kv) {
-    const int g = (threadIdx.x & 63) >> 4;
+__device__ __forceinline__ Frag<N> read_block(const KE* m, int rows, int row, int kv, int g) {
     const KE* p = m + ((int64_t)(2 * kv + (g >> 1)) * rows + row) * 16 + 8 * (g & 1);
     if constexpr (sizeof(KE) == 2) {
         Frag<N> f;
@@ -268,24 +318,34 @@ __device__ __forceinline__ Frag<N> read_block(const KE* m, int rows, int row, in
     }
 }
 
+template <int N>
+__device__ __forceinline__ Frag<N> negative(Frag<N> f) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        f.t[n] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, f.t[n]) ^ 0x80008000u);
+    return f;
+}
+
 template <class E, class KE, int KT, bool VEC>
-__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc, int, int nblk) {
-    typedef GradLds<E, KT> Lds;
-    constexpr int NI = kTerms<E>, NK = kKeptTerms<E, KE>, DT = 2 * KT;  // tiles of key channels
+__global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc, int,
+                                                            int nblk) {
+    typedef GradLds<E, KE, KT> Lds;
+    constexpr int NI = Lds::NI, NK = Lds::NK, NH = Lds::NH, SK = Lds::SK;
+    constexpr int DT = 2 * KT, TW = DT / 2;  // tiles of key channels; token tiles of a wave
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const LanePos pos;
-    const int r = pos.r, g = pos.g;
+    LanePos pos;
+    const int d0 = wave % DT, tk0 = (wave / DT) * TW;  // this wave's key channel tile, first token tile
+    const int it = wave & 3, j0 = wave >> 2;           // its tiles of H^T: columns it, rows j0, j0 + 2
     const int n = (int)(blockIdx.x % nc);
     const int64_t bk = blockIdx.x / nc;
     const int hk = (int)(bk % s.Hk), rep = s.Hv / s.Hk;
     const int64_t b = bk / s.Hk;
     const int len = row_length(s, b), t0 = n * kChunk;
     const int Dk = s.Dk, Dv = s.Dv;
-    const int mine = 16 * wave + r, tok = t0 + mine;  // this lane's token
     if (t0 >= len) {  // absent tokens: zero gradients
-        for (int i = wave; i < kChunk && t0 + i < s.T; i += 4) {
+        for (int i = wave; i < kChunk && t0 + i < s.T; i += 8) {
             const int64_t at = ((b * s.T + t0 + i) * s.Hk + hk) * (int64_t)Dk;
             for (int c = lane; c < Dk; c += 64) {
                 reinterpret_cast<E*>(A.gq)[at + c] = (E)0.f;
@@ -299,202 +359,236 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
         }
         return;
     }
-    {
-        RowStage<E, KT, 256> sk, sq;
-        sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0, len), Dk);
-        sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
-        sk.store(L.k);
-        sq.store(L.q);
-    }
-    __syncthreads();
-    // q_i.k_j and k_i.k_j: rows j (tiles up to this wave's), columns i.
-    f32x4 qk[4], kk_[4];
+    RowStage<E, KT, 512> sk, sq;
+    sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0, len), Dk);
+    sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
+
+    f32x4 dq[TW], dk[TW];  // rows 16*d0 + 4g.., columns 16*(tk0 + t) + r
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-        qk[jt] = kk_[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (jt <= wave)
-#pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
-                const Frag<NI> fk = read_rows<NI>(L.k, pos, jt, kk);
-                mma(qk[jt], fk, read_rows<NI>(L.q, pos, wave, kk));
-                mma(kk_[jt], fk, read_rows<NI>(L.k, pos, wave, kk));
-            }
-    }
-    f32x4 dq[DT], dk[DT];
-#pragma unroll
-    for (int d = 0; d < DT; ++d) dq[d] = dk[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < TW; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     for (int hr = 0; hr < rep; ++hr) {
         const int h = hk * rep + hr;
+        pos.renew();
+        const int r = pos.r, g = pos.g;
         const int64_t cb = (b * s.Hv + h) * nc + n;
-        if (tid < kChunk) {
-            L.gam[tid] = W.gam[cb * kChunk + tid];
-            L.be[tid] = t0 + tid < len
-                            ? (float)reinterpret_cast<const E*>(A.beta)[(b * s.T + t0 + tid) * s.Hv + h]
-                            : 0.f;
-        }
-        // H^T, E^T and the products with S and dS'.
         const KE* X = reinterpret_cast<const KE*>(W.x) + cb * nblk * (kChunk * 16);
         const KE* S0 = reinterpret_cast<const KE*>(W.s0) + cb * nblk * (32 * KT * 16);
         const KE* DS = reinterpret_cast<const KE*>(W.ds) + cb * nblk * (32 * KT * 16);
         const Rows go = rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0, len), gz = rows_of<E>(A.gv, s, b, s.Hv, h, Dv, t0, len);
-        f32x4 H[4], Z[4], rq[DT], rk[DT], wk[DT];
+        f32x4 H[2], Z[2], rq[TW], rk[TW], wk[TW];
         float dot = 0.f;
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt) H[jt] = Z[jt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 2; ++i) H[i] = Z[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int d = 0; d < DT; ++d) rq[d] = rk[d] = wk[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int kv = 0; 32 * kv < Dv; ++kv) {
-            E x[8];
-            const int c = 32 * kv + 8 * g;
-            load8<E, VEC>(go, mine, c, Dv, true, x);
-            const Frag<NI> fo = to_frag<E>(x);
-            load8<E, VEC>(gz, mine, c, Dv, true, x);
-            const Frag<NI> fz = to_frag<E>(x);
-            const Frag<NK> fx = read_block<KE, NK>(X, kChunk, mine, kv);
+        for (int t = 0; t < TW; ++t) rq[t] = rk[t] = wk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int kv0 = 0; 32 * kv0 < Dv; kv0 += SK) {
+            RowStage<E, SK, 512> so, sz;
+            BlockStage<KE, NK, SK> sx;
+            so.template load<VEC>(go, Dv, 32 * kv0);
+            sz.template load<VEC>(gz, Dv, 32 * kv0);
+            sx.load(X, 2 * kv0);
+            Frag<NK> fs[SK], fd[SK];
 #pragma unroll
-            for (int jt = 0; jt < 4; ++jt)
-                if (jt <= wave) {
-                    const Frag<NK> f = read_block<KE, NK>(X, kChunk, 16 * jt + r, kv);
-                    mma(H[jt], f, fo);
-                    mma(Z[jt], f, fz);
+            for (int kv = 0; kv < SK; ++kv) {
+                fs[kv] = read_block<KE, NK>(S0, 32 * KT, 16 * d0 + r, kv0 + kv, g);
+                fd[kv] = read_block<KE, NK>(DS, 32 * KT, 16 * d0 + r, kv0 + kv, g);
+            }
+            __syncthreads();  // what lay here has been read
+            if (hr == 0 && kv0 == 0) sk.store(L.k), sq.store(L.q);
+            if (kv0 == 0 && tid < kChunk) {
+                L.gam[tid] = W.gam[cb * kChunk + tid];
+                L.be[tid] = t0 + tid < len
+                                ? (float)reinterpret_cast<const E*>(A.beta)[(b * s.T + t0 + tid) * s.Hv + h]
+                                : 0.f;
+            }
+            so.store(L.go);
+            sz.store(L.gz);
+            sx.store(L.x);
+            __syncthreads();
+#pragma unroll
+            for (int kv = 0; kv < SK; ++kv) {
+                if (32 * (kv0 + kv) >= Dv) break;  // blocks past Dv may not have been written
+                phase();
+                // H^T, E^T: rows j, columns i.
+                const Frag<NI> fo = read_rows<NI>(L.go, pos, it, kv), fz = read_rows<NI>(L.gz, pos, it, kv);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (j0 + 2 * i <= it) {
+                        const Frag<NK> f = read_rows<NK>(L.x, pos, j0 + 2 * i, kv);
+                        mma(H[i], f, fo);
+                        mma(Z[i], f, fz);
+                    }
+                // S dO, S dZ, dS' x: rows key channels, columns tokens.
+                Frag<NI> to[TW], tz[TW];
+                Frag<NK> tx[TW];
+#pragma unroll
+                for (int t = 0; t < TW; ++t) {
+                    to[t] = read_rows<NI>(L.go, pos, tk0 + t, kv);
+                    tz[t] = read_rows<NI>(L.gz, pos, tk0 + t, kv);
+                    tx[t] = read_rows<NK>(L.x, pos, tk0 + t, kv);
                 }
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const Frag<NK> f = read_block<KE, NK>(S0, 32 * KT, 16 * d + r, kv);
-                mma(rq[d], f, fo);
-                mma(rk[d], f, fz);
-                const Frag<NK> fd = read_block<KE, NK>(DS, 32 * KT, 16 * d + r, kv);
-                mma(wk[d], fd, fx);
-                if ((d & 3) == wave)  // each wave a quarter of <S, dS'>
+                mma_cols<TW>(rq, fs[kv], to);
+                mma_cols<TW>(rk, fs[kv], tz);
+                mma_cols<TW>(wk, fd[kv], tx);
+                if (tk0 == 0)  // <S, dS'>, each byte of them once
 #pragma unroll
                     for (int m = 0; m < NK; ++m)
 #pragma unroll
                         for (int o = 0; o < NK; ++o)
                             if (m + o < NK)
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) dot = fmaf((float)f.t[m][i], (float)fd.t[o][i], dot);
+                                for (int i = 0; i < 8; ++i)
+                                    dot = fmaf((float)fs[kv].t[m][i], (float)fd[kv].t[o][i], dot);
             }
         }
-        __syncthreads();  // gam, beta are there
-        const double gi = L.gam[mine], gend = L.gam[kChunk - 1];
-        const float eg = decay_exp(gi, 0.0), ew = decay_exp(gend, gi), be = L.be[mine];
+        phase();
+        __syncthreads();  // the slab has been read: the weights lie over it
+        const double gend = L.gam[kChunk - 1];
         // M, its sums, and the weights scale L beta H and L beta E.
-        float rowsum = 0.f;
+        bf16x4 we[2][NH];
+        {
+            const int mine = 16 * it + r;
+            const double gi = L.gam[mine];
+            float rowsum = 0.f;
 #pragma unroll
-        for (int jt = 0; jt < 4; ++jt) {
-            if (jt > (wave | 1)) {
-                if (lane < 16) L.col[wave][16 * jt + lane] = 0.f;
-                continue;
-            }
-            float hw[8], ez[8];
-            f32x4 m4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = 16 * jt + 4 * g + e;
-                const float l = j <= mine ? decay_exp(gi, L.gam[j]) : 0.f, ls = j < mine ? l : 0.f;
-                const float bj = L.be[j];
-                const float hh = s.scale * l * H[jt][e], zz = ls * Z[jt][e];
-                m4[e] = qk[jt][e] * hh - kk_[jt][e] * zz;
-                if (j == mine) {
-                    L.diag[mine] = m4[e];
-                    m4[e] = 0.f;
+            for (int i = 0; i < 2; ++i) {
+                const int jt = j0 + 2 * i;
+                if (jt > (it | 1)) {
+                    if (lane < 16) L.col[it][16 * jt + lane] = 0.f;
+                    continue;
                 }
-                rowsum = fmaf(bj, m4[e], rowsum);
-                hw[e] = bj * hh;
-                ez[e] = bj * zz;
-                hw[4 + e] = ez[4 + e] = 0.f;
-            }
-            const Frag<NI> fh = split<NI>(hw), fe = split<NI>(ez);
+                f32x4 qk = {0.f, 0.f, 0.f, 0.f}, kk = {0.f, 0.f, 0.f, 0.f};
+                if (jt <= it)
 #pragma unroll
-            for (int m = 0; m < NI; ++m) {
-                *quad(&L.h[m], pos, wave, jt) = __builtin_shufflevector(fh.t[m], fh.t[m], 0, 1, 2, 3);
-                *quad(&L.e[m], pos, wave, jt) = __builtin_shufflevector(fe.t[m], fe.t[m], 0, 1, 2, 3);
-            }
+                    for (int c = 0; c < KT; ++c) {
+                        const Frag<NI> fk = read_rows<NI>(L.k, pos, jt, c);
+                        mma(qk, fk, read_rows<NI>(L.q, pos, it, c));
+                        mma(kk, fk, read_rows<NI>(L.k, pos, it, c));
+                    }
+                float hw[8], ez[8];
+                f32x4 m4;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 16 * jt + 4 * g + e;
+                    const float l = j <= mine ? decay_exp(gi, L.gam[j]) : 0.f, ls = j < mine ? l : 0.f;
+                    const float bj = L.be[j];
+                    const float hh = s.scale * l * H[i][e], zz = ls * Z[i][e];
+                    m4[e] = qk[e] * hh - kk[e] * zz;
+                    if (j == mine) {
+                        L.diag[mine] = m4[e];
+                        m4[e] = 0.f;
+                    }
+                    rowsum = fmaf(bj, m4[e], rowsum);
+                    hw[e] = bj * hh;
+                    ez[e] = bj * zz;
+                    hw[4 + e] = ez[4 + e] = 0.f;
+                }
+                const Frag<NH> fh = split<NH>(hw), fe = split<NH>(ez);
 #pragma unroll
-                for (int o = 1; o < 16; o <<= 1) m4[e] += __shfl_xor(m4[e], o);
-                if (r == 0) L.col[wave][16 * jt + 4 * g + e] = m4[e];
+                for (int m = 0; m < NH; ++m) {
+                    *quad(&L.h[m], pos, it, jt) = __builtin_shufflevector(fh.t[m], fh.t[m], 0, 1, 2, 3);
+                    we[i][m] = __builtin_shufflevector(fe.t[m], fe.t[m], 0, 1, 2, 3);
+                    if constexpr (!Lds::ONE) *quad(&L.e[m], pos, it, jt) = we[i][m];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) m4[e] += __shfl_xor(m4[e], o);
+                    if (r == 0) L.col[it][16 * jt + 4 * g + e] = m4[e];
+                }
             }
+            rowsum += __shfl_xor(rowsum, 16);
+            rowsum += __shfl_xor(rowsum, 32);
+            if (g == 0) L.row[j0][mine] = rowsum;
         }
-        rowsum += __shfl_xor(rowsum, 16);
-        rowsum += __shfl_xor(rowsum, 32);
         // Sums with q and k over the key channels, and the parts of dq, dk from S and dS'.
-        float asum = 0.f, wsum = 0.f;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
+        for (int t = 0; t < TW; ++t) {
+            phase();
+            const int tt = tk0 + t, tok = 16 * tt + r;
+            const double gi = L.gam[tok];
+            const float eg = decay_exp(gi, 0.0), ew = decay_exp(gend, gi), be = L.be[tok];
             f32x4 q4 = {0.f, 0.f, 0.f, 0.f}, k4 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int m = NI - 1; m >= 0; --m) {
-                const bf16x4 a = *quad(&L.q[m], pos, wave, d);
-                const bf16x4 c = *quad(&L.k[m], pos, wave, d);
+                const bf16x4 a = *quad(&L.q[m], pos, tt, d0), c = *quad(&L.k[m], pos, tt, d0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) q4[e] += (float)a[e], k4[e] += (float)c[e];
             }
-            rq[d] *= s.scale * eg;
-            rk[d] *= eg;
-            wk[d] *= ew;
+            rq[t] *= s.scale * eg;
+            rk[t] *= eg;
+            wk[t] *= ew;
+            float asum = 0.f, wsum = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                asum = fmaf(q4[e], rq[d][e], asum);
-                asum = fmaf(-k4[e], rk[d][e], asum);
-                wsum = fmaf(k4[e], wk[d][e], wsum);
+                asum = fmaf(q4[e], rq[t][e], asum);
+                asum = fmaf(-k4[e], rk[t][e], asum);
+                wsum = fmaf(k4[e], wk[t][e], wsum);
             }
-            dq[d] += rq[d];
-            dk[d] += be * wk[d] - rk[d];
+            asum += __shfl_xor(asum, 16);
+            asum += __shfl_xor(asum, 32);
+            wsum += __shfl_xor(wsum, 16);
+            wsum += __shfl_xor(wsum, 32);
+            if (g == 0) L.a[d0][tok] = asum, L.wr[d0][tok] = wsum;
+            dq[t] += rq[t];
+            dk[t] += be * wk[t] - rk[t];
         }
-        asum += __shfl_xor(asum, 16);
-        asum += __shfl_xor(asum, 32);
-        wsum += __shfl_xor(wsum, 16);
-        wsum += __shfl_xor(wsum, 32);
-        if (g == 0) L.row[mine] = rowsum, L.a[mine] = asum, L.wr[mine] = wsum;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) dot += __shfl_xor(dot, o);
         if (lane == 0) L.dot[wave] = dot;
         __syncthreads();  // the weights and the sums are there
+        // dq += L beta H k;  dk += (L beta H)^T q' - (L beta E)^T k - (L beta E) k.
+        const auto with_h = [&](int k2, const Frag<NI>& fk) {
+            const Frag<NI> fq = read_col<NI, false>(L.q, pos, k2, 16 * d0, 0);
+#pragma unroll
+            for (int t = 0; t < TW; ++t) {  // rows 32*k2.. reach down, or up, to this tile's tokens
+                phase();
+                const int tt = tk0 + t;
+                if (2 * k2 <= tt) mma(dq[t], fk, read_rows<NH>(L.h, pos, tt, k2));
+                if (2 * k2 + 1 >= tt) mma(dk[t], fq, read_col<NH, false>(L.h, pos, k2, 16 * tt, 0));
+            }
+        };
+        const auto with_e = [&](int k2, const Frag<NI>& fk, const Mat<2>* e) {
+            const Frag<NI> mk = negative(fk);
+#pragma unroll
+            for (int t = 0; t < TW; ++t) {
+                phase();
+                const int tt = tk0 + t;
+                if (2 * k2 <= tt) mma(dk[t], mk, read_rows<NH>(e, pos, tt, k2));
+                if (2 * k2 + 1 >= tt) mma(dk[t], mk, read_col<NH, false>(e, pos, k2, 16 * tt, 0));
+            }
+        };
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
-            // Rows j (for dq) or i (for dk) 32*k2..; this wave's columns see the ones it is coupled to.
-            const bool below = 2 * k2 <= wave, above = 2 * k2 + 1 >= wave;
-            Frag<NI> hr_, ec, er;
-            if (below) hr_ = read_rows<NI>(L.h, pos, wave, k2), er = read_rows<NI>(L.e, pos, wave, k2);
-            Frag<NI> hc;
-            if (above) {
-                hc = read_col<NI, false>(L.h, pos, k2, 16 * wave, 0);
-                ec = read_col<NI, false>(L.e, pos, k2, 16 * wave, 0);
+            const Frag<NI> fk = read_col<NI, false>(L.k, pos, k2, 16 * d0, 0);
+            with_h(k2, fk);
+            if constexpr (!Lds::ONE) with_e(k2, fk, L.e);
+        }
+        if constexpr (Lds::ONE) {
+            __syncthreads();
 #pragma unroll
-                for (int m = 0; m < NI; ++m)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ec.t[m][i] = -ec.t[m][i];
-            }
-            if (below)
+                for (int m = 0; m < NH; ++m)
+                    if (j0 + 2 * i <= (it | 1)) *quad(&L.h[m], pos, it, j0 + 2 * i) = we[i][m];
+            __syncthreads();
 #pragma unroll
-                for (int m = 0; m < NI; ++m)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) er.t[m][i] = -er.t[m][i];
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const Frag<NI> fk = read_col<NI, false>(L.k, pos, k2, 16 * d, 0);
-                if (below) {
-                    mma(dq[d], fk, hr_);
-                    mma(dk[d], fk, er);
-                }
-                if (above) {
-                    mma(dk[d], read_col<NI, false>(L.q, pos, k2, 16 * d, 0), hc);
-                    mma(dk[d], fk, ec);
-                }
-            }
+            for (int k2 = 0; k2 < 2; ++k2) with_e(k2, read_col<NI, false>(L.k, pos, k2, 16 * d0, 0), L.h);
         }
         if (wave == 0) {
-            const float bt = L.be[lane], wr = L.wr[lane];
-            const float cs = L.col[0][lane] + L.col[1][lane] + L.col[2][lane] + L.col[3][lane];
-            const double a = L.a[lane], bw = (double)bt * wr, dcr = (double)bt * cs - (double)L.row[lane];
+            float cs = 0.f, rs = 0.f, as = 0.f, wr = 0.f, dots = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) cs += L.col[w][lane];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) dots += L.dot[w];
+            rs = L.row[0][lane] + L.row[1][lane];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) as += L.a[d][lane], wr += L.wr[d][lane];
+            const float bt = L.be[lane];
+            const double a = as, bw = (double)bt * wr, dcr = (double)bt * cs - (double)rs;
             const double sa = wave_cumsum(a), sw = wave_cumsum(bw + dcr);
-            const double through =
-                (double)decay_exp(L.gam[kChunk - 1], 0.0) * ((double)L.dot[0] + L.dot[1] + L.dot[2] + L.dot[3]);
-            const double all = __shfl(sa, 63);
-            const double dg = (all - sa + a) + (sw - bw - dcr) + through;
+            const double dg = (__shfl(sa, 63) - sa + a) + (sw - bw - dcr) + (double)decay_exp(gend, 0.0) * (double)dots;
             const int t = t0 + lane;
             if (t < s.T) {
                 const int64_t at = (b * s.T + t) * s.Hv + h;
@@ -502,15 +596,14 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaShape s, DeltaBwdA
                 reinterpret_cast<E*>(A.gbeta)[at] = (E)(t < len ? cs + L.diag[lane] + wr : 0.f);
             }
         }
-        __syncthreads();  // the next head writes the weights again
     }
-    if (tok < s.T) {
-        const int64_t at = ((b * s.T + tok) * s.Hk + hk) * (int64_t)Dk;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            store_cols<E, VEC>(reinterpret_cast<E*>(A.gq) + at, 16 * d + 4 * g, Dk, dq[d]);
-            store_cols<E, VEC>(reinterpret_cast<E*>(A.gk) + at, 16 * d + 4 * g, Dk, dk[d]);
-        }
+    for (int t = 0; t < TW; ++t) {
+        const int tok = t0 + 16 * (tk0 + t) + pos.r;
+        if (tok >= s.T) continue;
+        const int64_t at = ((b * s.T + tok) * s.Hk + hk) * (int64_t)Dk;
+        store_cols<E, VEC>(reinterpret_cast<E*>(A.gq) + at, 16 * d0 + 4 * pos.g, Dk, dq[t]);
+        store_cols<E, VEC>(reinterpret_cast<E*>(A.gk) + at, 16 * d0 + 4 * pos.g, Dk, dk[t]);
     }
 }
 
@@ -543,7 +636,7 @@ hipError_t backward(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunk
         e = launch(delta_chain_kernel<E, KE, KT, 4, VEC, NS>, s.B * s.Hv * narrow, bytes, st, s, A, W, 256, narrow);
     if (e != hipSuccess) return e;
     return launch(delta_grad_kernel<E, KE, KT, VEC>, s.B * s.Hk * ((s.T + kChunk - 1) / kChunk),
-                  (int)sizeof(GradLds<E, KT>), st, s, A, W, 256, 0);
+                  (int)sizeof(GradLds<E, KE, KT>), st, s, A, W, 512, 0);
 }
 
 template <class E, class KE, int NS, bool VEC>
