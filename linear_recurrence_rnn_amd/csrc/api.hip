@@ -952,8 +952,12 @@ size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws,
         return (void*)p;
     };
     linrec::DeltaChunks w{};
-    w.tinv = (float*)take(n * 64 * 64 * sizeof(float));
+    // P's terms: two serve bfloat16 outputs and gradients, three float32 ones.
+    w.np = s.dtype == LINREC_F32 || (upto > kDeltaPrep && e == 4) ? 3 : 2;
+    w.inv = take(n * 3 * 64 * 64 * 2);
+    w.p = take(n * w.np * 64 * 64 * 2);
     w.gam = (double*)take(n * 64 * sizeof(double));
+    w.dec = (float*)take(n * 3 * 64 * sizeof(float));
     if (upto >= kDeltaCkpt) {
         w.x = take(block * 64);
         w.s0 = take(block * linrec::delta_dkp(s));

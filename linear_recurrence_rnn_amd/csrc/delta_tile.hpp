@@ -269,44 +269,22 @@ struct RowStage {
     }
 };
 
-// A chunk's inverse and decays likewise; the inverse as three bfloat16 terms.
-template <class E, int NT>
-struct InverseStage {
-    static constexpr int I = kChunk * 8 / NT;
-    float x[I][8];
-    double gam, end;
-    float be;
-    __device__ __forceinline__ void load(const DeltaChunks& W, int64_t cb, const Rows& beta) {
-        const int t = threadIdx.x & 63;
-        const float* p = W.tinv + cb * (kChunk * kChunk) + 8 * threadIdx.x;
+// N terms of a 64x64 matrix likewise (as stored: the upper right block holds anything), and a
+// chunk's decays.
+template <int N, int NT>
+struct SquareStage {
+    static constexpr int I = N * kChunk * 8 / NT;
+    bf16x8 x[I];
+    __device__ __forceinline__ void load(const void* src, int64_t cb, int planes) {
+        const bf16x8* p = reinterpret_cast<const bf16x8*>(src) + cb * planes * (kChunk * 8) + threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            load16<float>(p + 8 * NT * i, x[i]);
-            load16<float>(p + 8 * NT * i + 4, x[i] + 4);
-        }
-        gam = W.gam[cb * kChunk + t];
-        end = W.gam[cb * kChunk + kChunk - 1];
-        const unsigned off = (unsigned)t * beta.stride;
-        if constexpr (sizeof(E) == 2)
-            be = (float)__builtin_bit_cast(E, __builtin_amdgcn_raw_buffer_load_b16(beta.rs, off, 0, 0));
-        else
-            be = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(beta.rs, off, 0, 0));
+        for (int i = 0; i < I; ++i) x[i] = p[NT * i];
     }
-    template <class Lds>
-    __device__ __forceinline__ void store(Lds& L) const {
-        const int t = threadIdx.x;
+    __device__ __forceinline__ void store(Mat<2>* dst) const {
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            const int id = t + i * NT;
-            const Frag<3> f = split<3>(x[i]);
-#pragma unroll
-            for (int m = 0; m < 3; ++m) *L.t[m].row8(id >> 3, 8 * (id & 7)) = f.t[m];
-        }
-        if (t < kChunk) {
-            L.gam[t] = gam;
-            L.eg[t] = decay_exp(gam, 0.0);
-            L.ew[t] = decay_exp(end, gam);
-            L.be[t] = be;
+            const int id = (int)threadIdx.x + NT * i;
+            *dst[id >> 9].row8((id >> 3) & 63, 8 * (id & 7)) = x[i];
         }
     }
 };

@@ -31,16 +31,22 @@ struct DeltaFwdArgs {
 };
 
 // What the chunked kernels keep of each chunk of 64 tokens, (B*Hv, chunks, ...):
-//   tinv  (64,64) float32   (I + strictly lower e^{gam_i - gam_j} (k_i.k_j) beta_j)^{-1}
+//   inv   (3,64,64)         N = (I + strictly lower e^{gam_i - gam_j} (k_i.k_j) beta_j)^{-1}, as three
+//                           bfloat16 terms
+//   p     (np,64,64)        P_ij = scale e^{gam_i - gam_j} q_i.k_j (i >= j, else 0), as np terms
+//                           (the upper right 32x32 blocks of both are not written)
 //   gam   (64) float64      decays cumulated within the chunk
+//   dec   (3,64) float32    e^gam, e^{gam_63 - gam}, beta
 // and for the backward, in blocks of 16 value channels (delta_blocks(s) of them, zero past Dv),
 // of the tensors' type, or float32 (delta_keeps_f32):
 //   x     (blocks, 64, 16)       x_t of the recurrence
 //   s0    (blocks, dkp, 16)      the state before the chunk, dkp = Dk rounded up (delta_dkp)
 //   ds    (blocks, dkp, 16)      the gradient of the state after the chunk
 struct DeltaChunks {
-    float* tinv;
+    void *inv, *p;
+    int np;
     double* gam;
+    float* dec;
     void *x, *s0;  // null: not kept
     void* ds;
 };

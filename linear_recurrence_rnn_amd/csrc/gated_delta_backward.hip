@@ -30,9 +30,8 @@ template <class E, int KT, int NS>
 struct ChainLds {
     static constexpr int NI = kTerms<E>;
     Mat<KT> k[NI], q[NI];
-    Mat<2> t[3], p[NS];  // the inverse, P^T
-    double gam[kChunk];
-    float eg[kChunk], ew[kChunk], be[kChunk];
+    Mat<2> t[NS], p[NS];  // the inverse, P
+    float eg[kChunk], ew[kChunk], be[kChunk];  // e^gam, e^{gam_63 - gam}, beta
 };
 
 template <class E, class KE, int KT, int NW, bool VEC, int NS>
@@ -66,12 +65,15 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
 
     const int nlive = (len + kChunk - 1) / kChunk;
     RowStage<E, KT, 64 * NW> sk, sq;
-    InverseStage<E, 64 * NW> si;
+    SquareStage<NS, 64 * NW> si, sp;
+    float sd = 0.f;
     ColumnStage<E> so;
     const auto fetch = [&](int n) {
         const int t0 = n * kChunk;
         sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0, len), Dk);
-        si.load(W, bh * nc + n, rows_of<E>(A.beta, s, b, s.Hv, h, 1, t0, len));
+        si.load(W.inv, bh * nc + n, 3);
+        sp.load(W.p, bh * nc + n, W.np);
+        if (tid < 3 * kChunk) sd = W.dec[(bh * nc + n) * (3 * kChunk) + tid];
         so.template load<VEC>(rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0, len), c0, Dv);
         sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
     };
@@ -82,34 +84,13 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
         __syncthreads();  // the previous chunk's tiles have been read
         sk.store(L.k);
         sq.store(L.q);
-        si.store(L);
+        si.store(L.t);
+        sp.store(L.p);
+        if (tid < 3 * kChunk) L.eg[tid] = sd;  // eg, ew, be in a row
         Frag<NI> fv[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) fv[t] = to_frag<E>(so.x[t]);
         __syncthreads();
-        // P^T, rows 16*pt..: tiles of Q K^T (rows i, columns j), stored as P^T[j][i].
-        {
-            const int pt = wave & 3, j = 16 * pt + r;
-            const double gj = L.gam[j];
-            for (int it = (pt & 2) + (wave >> 2); it < 4; it += NW / 4) {
-                f32x4 c = {0.f, 0.f, 0.f, 0.f};
-                if (it >= pt)
-#pragma unroll
-                    for (int kk = 0; kk < KT; ++kk)
-                        mma(c, read_rows<NI>(L.q, pos, it, kk), read_rows<NI>(L.k, pos, pt, kk));
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 16 * it + 4 * g + e;
-                    x[e] = j <= i ? s.scale * decay_exp(L.gam[i], gj) * c[e] : 0.f;
-                    x[4 + e] = 0.f;
-                }
-                const Frag<NS> f = split<NS>(x);
-#pragma unroll
-                for (int m = 0; m < NS; ++m)
-                    *quad(&L.p[m], pos, pt, it) = __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
-            }
-        }
         phase();
         // K dS' (dS' is also stored, turned so that a lane holds 4 value channels).
         f32x4 U[4];  // rows 32*(t/2) + tile_row(m, t%2)
@@ -150,15 +131,15 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
                 d[half] *= s.scale * *reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
             fd[k2] = split_tiles<NS>(d[0], d[1]);
         }
-        __syncthreads();  // P^T is there
+        phase();
         // dU += P^T dO (the lower left block is zero), then beta dU.
         {
             Frag<NS> fp[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) fp[t] = read_tile<NS>(L.p, pos, t >> 1, t & 1, 1);
+            for (int t = 0; t < 4; ++t) fp[t] = read_col<NS, true>(L.p, pos, 1, 32 * (t >> 1), t & 1);
             mma_rows<4>(U, fp, fo[1]);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) fp[t] = read_tile<NS>(L.p, pos, 0, t, 0);
+            for (int t = 0; t < 2; ++t) fp[t] = read_col<NS, true>(L.p, pos, 0, 0, t);
             mma_rows<2>(U, fp, fo[0]);
         }
 #pragma unroll
@@ -627,7 +608,7 @@ hipError_t launch(K kernel, int64_t blocks, int bytes, hipStream_t st, const Del
 template <class E, class KE, int KT, int NS, bool VEC>
 hipError_t backward(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
     const int bytes = (int)sizeof(ChainLds<E, KT, NS>), wide = (s.Dv + 127) / 128, narrow = (s.Dv + 63) / 64;
-    hipError_t e;
+    hipError_t e = hipSuccess;
     bool done = false;
     if constexpr (sizeof(E) == 2)
         if ((done = delta_wide(s)))

@@ -15,16 +15,16 @@ namespace linrec {
 
 namespace {
 
-// ---- the chunks' inverses -------------------------------------------------------------------
+// ---- what depends on a chunk alone -----------------------------------------------------------
 // One wave a chunk.  K's fragments serve as both operands of K K^T (the A and B layouts of a
 // matrix and its transpose are one).  Lane c then solves for column c of the inverse:
 //   t_i = [i = c] - sum_{j<i} A_ij t_j,   A = G diag(beta)
 // with the rows of A read from LDS by all lanes at once.
-template <class E, int KT, bool VEC>
+template <class E, int KT, bool VEC, int NP>
 __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFwdArgs A, DeltaChunks W, int nc) {
     constexpr int NI = kTerms<E>;
     constexpr int LD = 68;
-    __shared__ float a[kChunk * LD];
+    __shared__ __align__(16) float a[kChunk * LD];
     __shared__ double gam[kChunk];
     __shared__ float bet[kChunk];
     const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
@@ -35,28 +35,32 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
     const int64_t b = bh / s.Hv;
     const int len = row_length(s, b), t0 = n * kChunk;
     if (t0 >= len) return;  // nothing of this chunk is used
+    const Rows K = rows_of<E>(A.k, s, b, s.Hk, hk, s.Dk, t0, len), Q = rows_of<E>(A.q, s, b, s.Hk, hk, s.Dk, t0, len);
+    Frag<NI> kf[4][KT];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+            E x[8];
+            load8<E, VEC>(K, 16 * t + r, 32 * kk + 8 * g, s.Dk, true, x);
+            kf[t][kk] = to_frag<E>(x);
+        }
     {
         const bool live = t0 + lane < len;
         const int64_t at = (b * s.T + t0 + lane) * s.Hv + h;
         const double d = live ? decay_of((float)reinterpret_cast<const E*>(A.g)[at]) : 0.0;
         const double c = wave_cumsum(d);
+        const float bb = live ? (float)reinterpret_cast<const E*>(A.beta)[at] : 0.f;
         gam[lane] = c;
-        bet[lane] = live ? (float)reinterpret_cast<const E*>(A.beta)[at] : 0.f;
+        bet[lane] = bb;
         W.gam[blk * kChunk + lane] = c;
-    }
-    const Rows K = rows_of<E>(A.k, s, b, s.Hk, hk, s.Dk, t0, len);
-    Frag<NI> kf[4][KT];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int row = 16 * t + r;
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) {
-            E x[8];
-            load8<E, VEC>(K, row, 32 * kk + 8 * g, s.Dk, true, x);
-            kf[t][kk] = to_frag<E>(x);
-        }
+        float* dec = W.dec + blk * (3 * kChunk) + lane;
+        dec[0] = decay_exp(c, 0.0);
+        dec[kChunk] = decay_exp(__shfl(c, 63), c);
+        dec[2 * kChunk] = bb;
     }
     __syncthreads();
+    // A: tiles of K K^T (rows i, columns j).
 #pragma unroll
     for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -71,16 +75,63 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
                 a[i * LD + j] = i > j ? c[e] * decay_exp(gam[i], gam[j]) * bet[j] : 0.f;
             }
         }
+    // P: tiles of K Q^T (rows j, columns i), stored as P[i][j].
+    bf16_t* p = reinterpret_cast<bf16_t*>(W.p) + blk * (NP * kChunk * kChunk);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        Frag<NI> fq[KT];
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+            E x[8];
+            load8<E, VEC>(Q, 16 * it + r, 32 * kk + 8 * g, s.Dk, true, x);
+            fq[kk] = to_frag<E>(x);
+        }
+        const int i = 16 * it + r;
+        const double gi = gam[i];
+#pragma unroll
+        for (int jt = 0; jt <= (it | 1); ++jt) {
+            f32x4 c = {0.f, 0.f, 0.f, 0.f};
+            if (jt <= it)
+#pragma unroll
+                for (int kk = 0; kk < KT; ++kk) mma(c, kf[jt][kk], fq[kk]);
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = 16 * jt + 4 * g + e;
+                x[e] = j <= i ? s.scale * decay_exp(gi, gam[j]) * c[e] : 0.f;
+                x[4 + e] = 0.f;
+            }
+            const Frag<NP> f = split<NP>(x);
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+                *reinterpret_cast<bf16x4*>(p + (m * kChunk + i) * kChunk + 16 * jt + 4 * g) =
+                    __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
+        }
+    }
     __syncthreads();
     float t[kChunk];
-    float* out = W.tinv + blk * (kChunk * kChunk) + lane;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
         float x = i == lane ? 1.f : 0.f;
 #pragma unroll
         for (int j = 0; j < i; ++j) x = fmaf(-a[i * LD + j], t[j], x);
         t[i] = x;
-        out[i * kChunk] = x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) a[i * LD + lane] = t[i];
+    __syncthreads();
+    // Out as three terms, a row's 16-byte pieces by neighbouring lanes.
+    bf16_t* out = reinterpret_cast<bf16_t*>(W.inv) + blk * (3 * kChunk * kChunk);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int id = lane + 64 * i, row = id >> 3, c = 8 * (id & 7);
+        float x[8];
+        load16<float>(a + row * LD + c, x);
+        load16<float>(a + row * LD + c + 4, x + 4);
+        const Frag<3> f = split<3>(x);
+#pragma unroll
+        for (int m = 0; m < 3; ++m) *reinterpret_cast<bf16x8*>(out + m * kChunk * kChunk + 8 * id) = f.t[m];
     }
 }
 
@@ -99,8 +150,7 @@ struct FwdLds {
     static constexpr int NI = kTerms<E>, NO = NI == 1 ? 2 : 3;  // terms of inputs, of the outputs' operands
     Mat<KT> k[NI], q[NI];
     Mat<2> t[3], p[NO];  // the inverse, P
-    double gam[kChunk];
-    float eg[kChunk], ew[kChunk], be[kChunk];
+    float eg[kChunk], ew[kChunk], be[kChunk];  // e^gam, e^{gam_63 - gam}, beta
 };
 
 // What the chain leaves: o, and what the backward starts from (of type KE).
@@ -139,14 +189,20 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
 
     const int nlive = (len + kChunk - 1) / kChunk;
     RowStage<E, KT, 64 * NW> sk, sq;
-    InverseStage<E, 64 * NW> si;
+    SquareStage<3, 64 * NW> si;
+    SquareStage<NO, 64 * NW> sp;
+    float sd = 0.f;
     ColumnStage<E> sv;
     const auto fetch = [&](int n) {
         const int t0 = n * kChunk;
         sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0, len), Dk);
-        si.load(W, bh * nc + n, rows_of<E>(A.beta, s, b, s.Hv, h, 1, t0, len));
+        si.load(W.inv, bh * nc + n, 3);
+        if (tid < 3 * kChunk) sd = W.dec[(bh * nc + n) * (3 * kChunk) + tid];
         sv.template load<VEC>(rows_of<E>(A.v, s, b, s.Hv, h, Dv, t0, len), c0, Dv);
-        if constexpr (OUT) sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
+        if constexpr (OUT) {
+            sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
+            sp.load(W.p, bh * nc + n, W.np);
+        }
     };
     if (nlive > 0) fetch(0);
     for (int n = 0; n < nlive; ++n) {
@@ -154,35 +210,13 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
         const int64_t cb = bh * nc + n;
         __syncthreads();  // the previous chunk's tiles have been read
         sk.store(L.k);
-        if constexpr (OUT) sq.store(L.q);
-        si.store(L);
+        if constexpr (OUT) sq.store(L.q), sp.store(L.p);
+        si.store(L.t);
+        if (tid < 3 * kChunk) L.eg[tid] = sd;  // eg, ew, be in a row
         Frag<NI> fv[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) fv[t] = to_frag<E>(sv.x[t]);
         __syncthreads();
-        // P, rows 16*pt..: tiles of K Q^T (rows j, columns i), stored as P[i][j].
-        if constexpr (OUT) {
-            const int pt = wave & 3, i = 16 * pt + r;
-            const double gi = L.gam[i];
-            for (int jt = wave >> 2; jt <= (pt | 1); jt += NW / 4) {
-                f32x4 c = {0.f, 0.f, 0.f, 0.f};
-                if (jt <= pt)
-#pragma unroll
-                    for (int kk = 0; kk < KT; ++kk)
-                        mma(c, read_rows<NI>(L.k, pos, jt, kk), read_rows<NI>(L.q, pos, pt, kk));
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = 16 * jt + 4 * g + e;
-                    x[e] = j <= i ? s.scale * decay_exp(gi, L.gam[j]) * c[e] : 0.f;
-                    x[4 + e] = 0.f;
-                }
-                const Frag<NO> f = split<NO>(x);
-#pragma unroll
-                for (int m = 0; m < NO; ++m)
-                    *quad(&L.p[m], pos, pt, jt) = __builtin_shufflevector(f.t[m], f.t[m], 0, 1, 2, 3);
-            }
-        }
         phase();
         // K S and the state's part of O^T.
         f32x4 Z[4], O[4];  // Z[t]: rows 32*(t/2) + tile_row(m, t%2); O^T[t]: columns 16*t + r
@@ -278,7 +312,6 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
         }
         if constexpr (OUT) {
             phase();
-            __syncthreads();  // P is there
             // O^T += U^T P^T (P's upper right block is zero).
             Frag<NO> fp[4];
 #pragma unroll
@@ -319,9 +352,16 @@ bool vec_ok(const DeltaShape& s, const DeltaFwdArgs& A) {
 
 template <class E, int KT, bool VEC>
 hipError_t prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    const int64_t nb = delta_chunks(s);
-    hipLaunchKernelGGL((delta_prepare_kernel<E, KT, VEC>), dim3((unsigned)nb), dim3(64), 0, st, s, A, W,
-                       (int)((s.T + kChunk - 1) / kChunk));
+    const dim3 grid((unsigned)delta_chunks(s));
+    const int nc = (int)((s.T + kChunk - 1) / kChunk);
+    if constexpr (sizeof(E) == 2) {
+        if (W.np == 2)
+            hipLaunchKernelGGL((delta_prepare_kernel<E, KT, VEC, 2>), grid, dim3(64), 0, st, s, A, W, nc);
+        else
+            hipLaunchKernelGGL((delta_prepare_kernel<E, KT, VEC, 3>), grid, dim3(64), 0, st, s, A, W, nc);
+    } else {
+        hipLaunchKernelGGL((delta_prepare_kernel<E, KT, VEC, 3>), grid, dim3(64), 0, st, s, A, W, nc);
+    }
     return hipGetLastError();
 }
 
