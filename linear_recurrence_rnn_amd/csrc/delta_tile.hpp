@@ -100,6 +100,10 @@ __device__ __forceinline__ void mma_cols(f32x4* c, const Frag<NA>& a, const Frag
                 for (int t = 0; t < T; ++t) c[t] = mfma(a.t[i], b[t].t[j], c[t]);
 }
 
+// A value known to be the same in all lanes, as a scalar: what a buffer resource is made of has
+// to be one, or every load through it becomes a loop over the lanes' resources.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // Up to 64 rows of a (B,T,H,D) tensor's head from token t0 on, through a buffer resource that
 // ends with the row's last token: loads past it, and at the offset kNowhere, return 0.  No load
 // is behind a branch, so many are in flight.  (64 rows span less than 2^31 bytes: the host
@@ -115,8 +119,9 @@ __device__ __forceinline__ Rows rows_of(const void* base, const DeltaShape& s, i
                                         int len) {
     const unsigned stride = (unsigned)(H * D * (int)sizeof(E));
     const int left = len - t0 < kChunk ? len - t0 : kChunk;
-    return {make_rsrc(reinterpret_cast<const E*>(base) + ((b * s.T + t0) * H + h) * (int64_t)D,
-                      (int64_t)stride * (left > 0 ? left : 0)),
+    const E* p = reinterpret_cast<const E*>(base) + ((b * s.T + t0) * H + h) * (int64_t)D;
+    return {__builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(p), (short)0,
+                                              uniform((int)stride * (left > 0 ? left : 0)), 0x00020000),
             stride};
 }
 
@@ -200,6 +205,18 @@ __device__ __forceinline__ bf16x4 read_transposed(const bf16_t* p) {
     return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)p));
 }
 
+// A block index as (row, head, rest): rest the fastest of `inner`, then the head of H.
+struct BlockPos {
+    int64_t b;
+    int h, rest;
+    __device__ __forceinline__ BlockPos(unsigned blk, int H, int inner) {
+        const unsigned row = blk / (unsigned)inner;
+        rest = uniform((int)(blk - row * (unsigned)inner));
+        h = uniform((int)(row % (unsigned)H));
+        b = uniform((int)(row / (unsigned)H));
+    }
+};
+
 // Tokens of batch row b.
 __device__ __forceinline__ int row_length(const DeltaShape& s, int64_t b) {
     int64_t len = s.T;
@@ -207,7 +224,7 @@ __device__ __forceinline__ int row_length(const DeltaShape& s, int64_t b) {
         const int64_t n = s.lengths[b];
         len = n < 0 ? 0 : (n < len ? n : len);
     }
-    return (int)len;
+    return uniform((int)len);
 }
 
 // A 64-row matrix in LDS, rows of 32*KT bfloat16 values plus 16 bytes.  Rows lie 16 by 16, row
@@ -289,19 +306,18 @@ struct SquareStage {
     }
 };
 
-// A wave's 16 value channels of a chunk, as A operands of the four token tiles (the upper 16 of
-// an operand's 32 columns are 0).
+// A wave's 16 value channels of a chunk as A operands of 32 columns: operand k2 has token tile
+// 2*k2 in its first 16 columns and tile 2*k2 + 1 in the others, so that products with
+// identity_frag(half) give the D tiles.
 template <class E>
 struct ColumnStage {
-    E x[4][8];
+    E x[2][8];
     template <bool VEC>
     __device__ __forceinline__ void load(const Rows& R, int c0, int D) {
         const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int row = 32 * (t >> 1) + tile_row(r, t & 1);
-            load8<E, VEC>(R, row, c0 + 8 * g, D, g < 2, x[t]);
-        }
+        for (int k2 = 0; k2 < 2; ++k2)
+            load8<E, VEC>(R, 32 * k2 + tile_row(r, g >> 1), c0 + 8 * (g & 1), D, true, x[k2]);
     }
 };
 
@@ -371,15 +387,31 @@ __device__ __forceinline__ void store4(E* p, const f32x4& x) {
     *reinterpret_cast<E4*>(p) = y;
 }
 
-// Columns c..c+3 of a row of D; VEC: D % 4 == 0 and the row 4*sizeof(E)-byte aligned.
+// Columns c..c+3 of row `row`; nothing past D or past the rows of R.  Never behind a branch: the
+// wait for loads issued before the store then need not wait for the store.
 template <class E, bool VEC>
-__device__ __forceinline__ void store_cols(E* row, int c, int D, const f32x4& x) {
+__device__ __forceinline__ void store_rows(const Rows& R, int row, int c, int D, const f32x4& x) {
+    const unsigned at = (unsigned)row * R.stride + (unsigned)(c * (int)sizeof(E));
     if constexpr (VEC) {
-        if (c < D) store4<E>(row + c, x);
+        typedef E E4 __attribute__((ext_vector_type(4)));
+        E4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = (E)x[e];
+        const unsigned off = c < D ? at : kNowhere;
+        if constexpr (sizeof(E) == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), R.rs, off, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), R.rs, off, 0, 0);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < D) row[c + e] = (E)x[e];
+        for (int e = 0; e < 4; ++e) {
+            const unsigned off = c + e < D ? at + (unsigned)(e * (int)sizeof(E)) : kNowhere;
+            const E y = (E)x[e];
+            if constexpr (sizeof(E) == 2)
+                __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, y), R.rs, off, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, y), R.rs, off, 0, 0);
+        }
     }
 }
 

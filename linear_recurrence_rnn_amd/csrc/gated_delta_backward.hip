@@ -45,10 +45,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const LanePos pos;
     const int r = pos.r, g = pos.g;
-    const int tile = (int)(blockIdx.x % ntile);
-    const int64_t bh = blockIdx.x / ntile;
-    const int h = (int)(bh % s.Hv), hk = h / (s.Hv / s.Hk);
-    const int64_t b = bh / s.Hv;
+    const BlockPos at(blockIdx.x, s.Hv, ntile);
+    const int tile = at.rest, h = at.h, hk = uniform(h / (s.Hv / s.Hk));
+    const int64_t b = at.b, bh = b * s.Hv + h;
     const int len = row_length(s, b);
     const int c0 = (tile * NW + wave) * 16;
     const int Dk = s.Dk, Dv = s.Dv;
@@ -87,10 +86,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
         si.store(L.t);
         sp.store(L.p);
         if (tid < 3 * kChunk) L.eg[tid] = sd;  // eg, ew, be in a row
-        Frag<NI> fv[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) fv[t] = to_frag<E>(so.x[t]);
+        const Frag<NI> fv[2] = {to_frag<E>(so.x[0]), to_frag<E>(so.x[1])};
         __syncthreads();
+        if (n > 0) fetch(n - 1);  // in flight while this chunk is computed
         phase();
         // K dS' (dS' is also stored, turned so that a lane holds 4 value channels).
         f32x4 U[4];  // rows 32*(t/2) + tile_row(m, t%2)
@@ -122,7 +120,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 d[half] = f32x4{0.f, 0.f, 0.f, 0.f};
-                mma(d[half], fv[2 * k2 + half], identity_frag(0));
+                mma(d[half], fv[k2], identity_frag(half));
                 U[2 * k2 + half] *= *reinterpret_cast<const f32x4*>(&L.ew[32 * k2 + 8 * g + 4 * half]);
             }
             fo[k2] = split_tiles<NI>(d[0], d[1]);
@@ -159,6 +157,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
             mma_rows<2>(Z, ft, split_tiles<NS>(U[0], U[1]));
         }
         phase();
+        const Rows out = rows_of<E>(A.gv, s, b, s.Hv, h, Dv, t0, (int)s.T);
         // dV, turned; and -e^gam dZ for the state's gradient.
         Frag<NS> fz[2];
 #pragma unroll
@@ -168,10 +167,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
             for (int which = 0; which < 2; ++which) {
                 f32x4 x = {0.f, 0.f, 0.f, 0.f};
                 mma(x, fx, identity_frag(which));
-                const int t = t0 + 32 * k2 + 16 * which + r;
-                if (t < s.T)
-                    store_cols<E, VEC>(reinterpret_cast<E*>(A.gv) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv,
-                                       c0 + 4 * g, Dv, x);
+                store_rows<E, VEC>(out, 32 * k2 + 16 * which + r, c0 + 4 * g, Dv, x);
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half)
@@ -179,7 +175,6 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
             fz[k2] = split_tiles<NS>(Z[2 * k2], Z[2 * k2 + 1]);
         }
         phase();
-        if (n > 0) fetch(n - 1);  // in flight for the rest of this chunk
         // dS = e^{gam_63} dS' + scale Q^T e^gam dO - K^T e^gam dZ, four tiles at a time.
         const float end = L.eg[kChunk - 1];
         constexpr int T = KT == 1 ? 2 : 4;
@@ -319,10 +314,9 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
     LanePos pos;
     const int d0 = wave % DT, tk0 = (wave / DT) * TW;  // this wave's key channel tile, first token tile
     const int it = wave & 3, j0 = wave >> 2;           // its tiles of H^T: columns it, rows j0, j0 + 2
-    const int n = (int)(blockIdx.x % nc);
-    const int64_t bk = blockIdx.x / nc;
-    const int hk = (int)(bk % s.Hk), rep = s.Hv / s.Hk;
-    const int64_t b = bk / s.Hk;
+    const BlockPos at(blockIdx.x, s.Hk, nc);
+    const int n = at.rest, hk = at.h, rep = s.Hv / s.Hk;
+    const int64_t b = at.b;
     const int len = row_length(s, b), t0 = n * kChunk;
     const int Dk = s.Dk, Dv = s.Dv;
     if (t0 >= len) {  // absent tokens: zero gradients
@@ -580,11 +574,9 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
     }
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
-        const int tok = t0 + 16 * (tk0 + t) + pos.r;
-        if (tok >= s.T) continue;
-        const int64_t at = ((b * s.T + tok) * s.Hk + hk) * (int64_t)Dk;
-        store_cols<E, VEC>(reinterpret_cast<E*>(A.gq) + at, 16 * d0 + 4 * pos.g, Dk, dq[t]);
-        store_cols<E, VEC>(reinterpret_cast<E*>(A.gk) + at, 16 * d0 + 4 * pos.g, Dk, dk[t]);
+        const int row = 16 * (tk0 + t) + pos.r, c = 16 * d0 + 4 * pos.g;
+        store_rows<E, VEC>(rows_of<E>(A.gq, s, b, s.Hk, hk, Dk, t0, (int)s.T), row, c, Dk, dq[t]);
+        store_rows<E, VEC>(rows_of<E>(A.gk, s, b, s.Hk, hk, Dk, t0, (int)s.T), row, c, Dk, dk[t]);
     }
 }
 

@@ -29,10 +29,9 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
     __shared__ float bet[kChunk];
     const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
     const int64_t blk = blockIdx.x;
-    const int n = (int)(blk % nc);
-    const int64_t bh = blk / nc;
-    const int h = (int)(bh % s.Hv), hk = h / (s.Hv / s.Hk);
-    const int64_t b = bh / s.Hv;
+    const BlockPos at(blockIdx.x, s.Hv, nc);
+    const int n = at.rest, h = at.h, hk = uniform(h / (s.Hv / s.Hk));
+    const int64_t b = at.b;
     const int len = row_length(s, b), t0 = n * kChunk;
     if (t0 >= len) return;  // nothing of this chunk is used
     const Rows K = rows_of<E>(A.k, s, b, s.Hk, hk, s.Dk, t0, len), Q = rows_of<E>(A.q, s, b, s.Hk, hk, s.Dk, t0, len);
@@ -47,10 +46,10 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
         }
     {
         const bool live = t0 + lane < len;
-        const int64_t at = (b * s.T + t0 + lane) * s.Hv + h;
-        const double d = live ? decay_of((float)reinterpret_cast<const E*>(A.g)[at]) : 0.0;
+        const int64_t tok = (b * s.T + t0 + lane) * s.Hv + h;
+        const double d = live ? decay_of((float)reinterpret_cast<const E*>(A.g)[tok]) : 0.0;
         const double c = wave_cumsum(d);
-        const float bb = live ? (float)reinterpret_cast<const E*>(A.beta)[at] : 0.f;
+        const float bb = live ? (float)reinterpret_cast<const E*>(A.beta)[tok] : 0.f;
         gam[lane] = c;
         bet[lane] = bb;
         W.gam[blk * kChunk + lane] = c;
@@ -139,8 +138,7 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
 // A workgroup of NW waves owns 16*NW value channels of one head, a wave 16 of them, all rows of
 // the state (32*KT, zero past Dk).  K, Q, the inverse and P lie in LDS as bfloat16 terms, shared
 // by the waves; V comes from memory in the A layout and is turned into the D layout by a product
-// with the identity, which is exact.  The next chunk's loads are in flight during the second half
-// of one.
+// with the identity, which is exact.  The next chunk's loads are in flight while one is computed.
 //
 // Terms: the state and what flows into it (Z, beta X) are taken as three bfloat16 terms, so
 // that S keeps float32 precision over any number of chunks; the outputs of bfloat16 calls take
@@ -168,10 +166,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const LanePos pos;
     const int r = pos.r, g = pos.g;
-    const int tile = (int)(blockIdx.x % ntile);
-    const int64_t bh = blockIdx.x / ntile;
-    const int h = (int)(bh % s.Hv), hk = h / (s.Hv / s.Hk);
-    const int64_t b = bh / s.Hv;
+    const BlockPos at(blockIdx.x, s.Hv, ntile);
+    const int tile = at.rest, h = at.h, hk = uniform(h / (s.Hv / s.Hk));
+    const int64_t b = at.b, bh = b * s.Hv + h;
     const int len = row_length(s, b);
     const int c0 = (tile * NW + wave) * 16;  // this wave's first value channel
     const int Dk = s.Dk, Dv = s.Dv;
@@ -213,10 +210,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
         if constexpr (OUT) sq.store(L.q), sp.store(L.p);
         si.store(L.t);
         if (tid < 3 * kChunk) L.eg[tid] = sd;  // eg, ew, be in a row
-        Frag<NI> fv[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) fv[t] = to_frag<E>(sv.x[t]);
+        const Frag<NI> fv[2] = {to_frag<E>(sv.x[0]), to_frag<E>(sv.x[1])};
         __syncthreads();
+        if (n + 1 < nlive) fetch(n + 1);  // in flight while this chunk is computed
         phase();
         // K S and the state's part of O^T.
         f32x4 Z[4], O[4];  // Z[t]: rows 32*(t/2) + tile_row(m, t%2); O^T[t]: columns 16*t + r
@@ -247,7 +243,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             f32x4 v = {0.f, 0.f, 0.f, 0.f};
-            mma(v, fv[t], identity_frag(0));
+            mma(v, fv[t >> 1], identity_frag(t & 1));
             const f32x4 eg = *reinterpret_cast<const f32x4*>(&L.eg[32 * (t >> 1) + 8 * g + 4 * (t & 1)]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) Z[t][e] = fmaf(-eg[e], Z[t][e], v[e]);
@@ -294,7 +290,6 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
             fw[k2] = split_tiles<NS>(w[0], w[1]);
         }
         phase();
-        if (n + 1 < nlive) fetch(n + 1);
         // S' = e^{gam_63} S + K^T w, four tiles at a time.
         const float end = L.eg[kChunk - 1];
         constexpr int T = KT == 1 ? 2 : 4;
@@ -312,6 +307,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
         }
         if constexpr (OUT) {
             phase();
+            const Rows out = rows_of<E>(A.o, s, b, s.Hv, h, Dv, t0, (int)s.T);
             // O^T += U^T P^T (P's upper right block is zero).
             Frag<NO> fp[4];
 #pragma unroll
@@ -321,12 +317,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
             for (int t = 2; t < 4; ++t) fp[t] = read_rows<NO>(L.p, pos, t, 1);
             mma_cols<2>(O + 2, fu[1], fp + 2);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int tok = t0 + 16 * t + r;
-                if (tok < s.T)
-                    store_cols<E, VEC>(reinterpret_cast<E*>(A.o) + ((b * s.T + tok) * s.Hv + h) * (int64_t)Dv,
-                                       c0 + 4 * g, Dv, tok < len ? O[t] : f32x4{0.f, 0.f, 0.f, 0.f});
-            }
+            for (int t = 0; t < 4; ++t)
+                store_rows<E, VEC>(out, 16 * t + r, c0 + 4 * g, Dv,
+                                   t0 + 16 * t + r < len ? O[t] : f32x4{0.f, 0.f, 0.f, 0.f});
         }
     }
     // Chunks past the row's length: zero outputs.
