@@ -939,8 +939,8 @@ linrec::DeltaShape delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int
 // Sequences of up to this many tokens are taken token by token.
 bool delta_is_short(int64_t T) { return T <= env_int("LINREC_DELTA_SHORT", 16); }
 
-// Scratch of the chunked kernels, in this order: the inverses and decays; x and s0 (together
-// with them the checkpoint); ds.  state: a state is carried in.  Returns the end; fills W if given.
+// Scratch of the chunked kernels, in this order: what depends on chunks alone; x and s0 (a
+// checkpoint has them too); ds; the segments' maps and states.  state: a state is carried in.  Returns the end; fills W if given.
 enum { kDeltaPrep, kDeltaCkpt, kDeltaBwd };
 size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws, linrec::DeltaChunks* W) {
     const size_t n = (size_t)linrec::delta_chunks(s), e = linrec::delta_keeps_f32(s.dtype, state ? &s : nullptr) ? 4 : 2;
@@ -963,6 +963,11 @@ size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws,
         w.s0 = take(block * linrec::delta_dkp(s));
     }
     if (upto >= kDeltaBwd) w.ds = take(block * linrec::delta_dkp(s));
+    w.segs = linrec::delta_segments(s);
+    w.seg_len = (int)ceil_div(ceil_div(s.T, 64), w.segs);
+    const size_t heads = (size_t)(s.B * s.Hv), dkp = linrec::delta_dkp(s);
+    w.map = (float*)take(heads * (w.segs - 1) * dkp * (16 * linrec::delta_blocks(s) + dkp) * sizeof(float));
+    w.start = (float*)take(w.segs > 1 ? heads * w.segs * s.Dk * s.Dv * sizeof(float) : 0);
     if (W) *W = w;
     return at;
 }

@@ -49,6 +49,12 @@ struct DeltaChunks {
     float* dec;
     void *x, *s0;  // null: not kept
     void* ds;
+    // Long rows of few heads are walked in `segs` segments of `seg_len` chunks (1: in one).  A
+    // chunk maps the state to (matrix) state + (matrix), so a segment does: `map` holds, for all
+    // but the last, (dkp, 16*blocks + dkp) float32, the map's constant part and its matrix;
+    // `start` the state before every segment, (segs, B, Hv, Dk, Dv) float32.
+    int segs, seg_len;
+    float *map, *start;
 };
 inline int64_t delta_chunks(const DeltaShape& s) { return s.B * s.Hv * ((s.T + 63) / 64); }
 // A carried state's gradient lands on few tokens (the last ones of a piece), and pieces are
@@ -58,7 +64,7 @@ inline bool delta_keeps_f32(int dtype, const void* s_in) { return dtype == 0 || 
 inline int delta_blocks(const DeltaShape& s) { return (s.Dv + 127) / 128 * 8; }
 // Eight waves to a workgroup (bfloat16 calls) where a head has the value channels for them and
 // the heads alone fill most of the chip; four, on twice the CUs, else.
-inline bool delta_wide(const DeltaShape& s) { return s.Dv > 64 && s.B * s.Hv >= 144; }
+inline bool delta_wide(const DeltaShape& s, int segs = 1) { return s.Dv > 64 && s.B * s.Hv * segs >= 144; }
 inline int delta_dkp(const DeltaShape& s) { return s.Dk <= 32 ? 32 : s.Dk <= 64 ? 64 : 128; }
 
 struct DeltaBwdArgs {
@@ -71,6 +77,16 @@ struct DeltaBwdArgs {
     void *gg, *gbeta;     // (B,T,Hv)
     float* gs_in;         // (B,Hv,Dk,Dv), or null; may be gs_out; only with s_in
 };
+
+// Segments: as many as fill the chip with workgroups, of eight chunks at least, where that
+// divides the chain by six or more (a segment is walked twice, the first time with Dk columns
+// more); else one.
+inline int delta_segments(const DeltaShape& s) {
+    const int64_t nc = (s.T + 63) / 64, cols = s.dtype == 1 ? 128 : 64;
+    int64_t n = 256 / (s.B * s.Hv * ((s.Dv + cols - 1) / cols));
+    n = n < nc / 8 ? n : nc / 8;
+    return n >= 6 ? (int)n : 1;
+}
 
 hipError_t run_delta_prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st);
 hipError_t run_delta_forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st);

@@ -151,40 +151,48 @@ struct FwdLds {
     float eg[kChunk], ew[kChunk], be[kChunk];  // e^gam, e^{gam_63 - gam}, beta
 };
 
-// What the chain leaves: o, and what the backward starts from (of type KE).
-constexpr int kOut = 1, kKeep = 2;
+// What the chain leaves: o, what the backward starts from (of type KE), or a segment's map:
+// tiles of its constant part (the walk from a zero state) and then of its matrix (the walk of
+// the identity's columns with no values).
+constexpr int kOut = 1, kKeep = 2, kMap = 4;
 
 template <class E, class KE, int KT, int NW, bool VEC, int MODE>
 __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_forward_kernel(DeltaShape s, DeltaFwdArgs A,
                                                                                         DeltaChunks W, int nc,
-                                                                                        int ntile, int nblk) {
+                                                                                        int ntile, int ntile_v,
+                                                                                        int segs, int nblk) {
     typedef FwdLds<E, KT> Lds;
     constexpr int NI = kTerms<E>, NO = Lds::NO, NS = 3;
-    constexpr bool OUT = MODE & kOut, KEEP = MODE & kKeep;
+    constexpr bool OUT = MODE & kOut, KEEP = MODE & kKeep, MAP = MODE & kMap;
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const LanePos pos;
     const int r = pos.r, g = pos.g;
-    const BlockPos at(blockIdx.x, s.Hv, ntile);
-    const int tile = at.rest, h = at.h, hk = uniform(h / (s.Hv / s.Hk));
+    const BlockPos at(blockIdx.x, s.Hv, ntile * segs);
+    const int tile = uniform(at.rest % ntile), seg = uniform(at.rest / ntile), h = at.h, hk = uniform(h / (s.Hv / s.Hk));
     const int64_t b = at.b, bh = b * s.Hv + h;
     const int len = row_length(s, b);
-    const int c0 = (tile * NW + wave) * 16;  // this wave's first value channel
+    const bool matrix = MAP && tile >= ntile_v;  // a tile of the map's matrix
+    const int c0 = ((matrix ? tile - ntile_v : tile) * NW + wave) * 16;  // this wave's first value channel, or column
     const int Dk = s.Dk, Dv = s.Dv;
 
     // State: D tiles S[2kk + half], rows 32kk + tile_row(m, half), columns c0 + r.
     f32x4 S[2 * KT];
     const int64_t sb = bh * (int64_t)Dk * Dv;
+    // (With segments also the first one's: the last may write s_out, which may be s_in.)
+    const float* s_in = W.segs == 1 ? A.s_in : W.start + (int64_t)seg * (s.B * s.Hv * (int64_t)Dk * Dv);
 #pragma unroll
     for (int d = 0; d < 2 * KT; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e, col = c0 + r;
-            S[d][e] = (A.s_in && row < Dk && col < Dv) ? A.s_in[sb + (int64_t)row * Dv + col] : 0.f;
+            if constexpr (MAP) S[d][e] = matrix && row == col ? 1.f : 0.f;
+            else S[d][e] = (s_in && row < Dk && col < Dv) ? s_in[sb + (int64_t)row * Dv + col] : 0.f;
         }
 
-    const int nlive = (len + kChunk - 1) / kChunk;
+    const int live = (len + kChunk - 1) / kChunk, first = seg * W.seg_len, past = min(first + W.seg_len, nc);
+    const int nlive = min(live, past);  // chunks first..nlive-1 are walked
     RowStage<E, KT, 64 * NW> sk, sq;
     SquareStage<3, 64 * NW> si;
     SquareStage<NO, 64 * NW> sp;
@@ -195,14 +203,14 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
         sk.template load<VEC>(rows_of<E>(A.k, s, b, s.Hk, hk, Dk, t0, len), Dk);
         si.load(W.inv, bh * nc + n, 3);
         if (tid < 3 * kChunk) sd = W.dec[(bh * nc + n) * (3 * kChunk) + tid];
-        sv.template load<VEC>(rows_of<E>(A.v, s, b, s.Hv, h, Dv, t0, len), c0, Dv);
+        sv.template load<VEC>(rows_of<E>(A.v, s, b, s.Hv, h, Dv, t0, len), c0, matrix ? 0 : Dv);
         if constexpr (OUT) {
             sq.template load<VEC>(rows_of<E>(A.q, s, b, s.Hk, hk, Dk, t0, len), Dk);
             sp.load(W.p, bh * nc + n, W.np);
         }
     };
-    if (nlive > 0) fetch(0);
-    for (int n = 0; n < nlive; ++n) {
+    if (first < nlive) fetch(first);
+    for (int n = first; n < nlive; ++n) {
         const int t0 = n * kChunk;
         const int64_t cb = bh * nc + n;
         __syncthreads();  // the previous chunk's tiles have been read
@@ -324,11 +332,22 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
     }
     // Chunks past the row's length: zero outputs.
     if constexpr (OUT)
-        for (int64_t t = (int64_t)nlive * kChunk + wave; t < s.T; t += NW) {
+        for (int64_t t = (int64_t)max(live, first) * kChunk + wave; t < s.T && t < (int64_t)past * kChunk; t += NW) {
             E* op = reinterpret_cast<E*>(A.o) + ((b * s.T + t) * s.Hv + h) * (int64_t)Dv;
             for (int c = tile * NW * 16 + lane; c < (tile + 1) * NW * 16 && c < Dv; c += 64) op[c] = (E)0.f;
         }
-    if (A.s_out)
+    if constexpr (MAP) {
+        float* m = W.map + ((bh * (W.segs - 1) + seg) * (32 * KT)) * (int64_t)(16 * nblk + 32 * KT);
+#pragma unroll
+        for (int d = 0; d < 2 * KT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e;
+                if (!matrix || c0 < 32 * KT)
+                    m[row * (16 * nblk + 32 * KT) + (matrix ? 16 * nblk : 0) + c0 + r] = S[d][e];
+            }
+    }
+    if (!MAP && A.s_out && past == nc)
 #pragma unroll
         for (int d = 0; d < 2 * KT; ++d)
 #pragma unroll
@@ -336,6 +355,56 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
                 const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e, col = c0 + r;
                 if (row < Dk && col < Dv) A.s_out[sb + (int64_t)row * Dv + col] = S[d][e];
             }
+}
+
+// ---- the states before the segments ---------------------------------------------------------------
+// start_{g+1} = matrix_g start_g + constant_g, in order, 64 value channels of a head a workgroup, 16
+// a wave; the state stays in registers, three terms each of it and of the matrix.
+template <int KT>
+__global__ __launch_bounds__(256) void delta_join_kernel(DeltaShape s, DeltaFwdArgs A, DeltaChunks W, int ntile,
+                                                         int nblk) {
+    const int wave = threadIdx.x >> 6;
+    const LanePos pos;
+    const int r = pos.r, g = pos.g;
+    const BlockPos at(blockIdx.x, s.Hv, ntile);
+    const int64_t bh = at.b * s.Hv + at.h;
+    const int col = (at.rest * 4 + wave) * 16 + r, Dk = s.Dk, Dv = s.Dv, ld = 16 * nblk + 32 * KT;
+    f32x4 S[2 * KT];
+#pragma unroll
+    for (int d = 0; d < 2 * KT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e;
+            S[d][e] = (A.s_in && row < Dk && col < Dv) ? A.s_in[(bh * Dk + row) * Dv + col] : 0.f;
+        }
+    for (int seg = 0; seg < W.segs; ++seg) {
+        float* out = W.start + ((int64_t)seg * s.B * s.Hv + bh) * Dk * Dv;
+#pragma unroll
+        for (int d = 0; d < 2 * KT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e;
+                if (row < Dk && col < Dv) out[(int64_t)row * Dv + col] = S[d][e];
+            }
+        if (seg + 1 == W.segs) break;
+        const float* m = W.map + ((bh * (W.segs - 1) + seg) * (32 * KT)) * (int64_t)ld;
+        Frag<3> fs[KT];
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) fs[kk] = split_tiles<3>(S[2 * kk], S[2 * kk + 1]);
+#pragma unroll
+        for (int d = 0; d < 2 * KT; ++d) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[d][e] = m[(32 * (d >> 1) + 8 * g + 4 * (d & 1) + e) * ld + col];
+#pragma unroll
+            for (int kk = 0; kk < KT; ++kk) {
+                float x[8];
+                const float* p = m + (32 * (d >> 1) + tile_row(r, d & 1)) * ld + 16 * nblk + 32 * kk + 8 * g;
+                load16<float>(p, x);
+                load16<float>(p + 4, x + 4);
+                mma(S[d], split<3>(x), fs[kk]);
+            }
+        }
+    }
 }
 
 bool vec_ok(const DeltaShape& s, const DeltaFwdArgs& A) {
@@ -365,21 +434,30 @@ hipError_t forward_nw(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChu
     // More dynamic LDS than the default 64 KiB has to be asked for.
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int ntile = (s.Dv + 16 * NW - 1) / (16 * NW);
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(s.B * s.Hv * ntile)), dim3(64 * NW), bytes, st, s, A, W,
-                       (int)((s.T + kChunk - 1) / kChunk), ntile, delta_blocks(s));
+    const int ntile_v = (s.Dv + 16 * NW - 1) / (16 * NW);
+    const int ntile = ntile_v + (MODE & kMap ? (32 * KT + 16 * NW - 1) / (16 * NW) : 0);
+    const int segs = MODE & kMap ? W.segs - 1 : W.segs;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(s.B * s.Hv * ntile * segs)), dim3(64 * NW), bytes, st, s, A, W,
+                       (int)((s.T + kChunk - 1) / kChunk), ntile, ntile_v, segs, delta_blocks(s));
     return hipGetLastError();
 }
 
 template <class E, class KE, int KT, bool VEC, int MODE>
 hipError_t forward_mode(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
     if constexpr (sizeof(E) == 2)
-        if (delta_wide(s)) return forward_nw<E, KE, KT, 8, VEC, MODE>(s, A, W, st);
+        if (delta_wide(s, W.segs)) return forward_nw<E, KE, KT, 8, VEC, MODE>(s, A, W, st);
     return forward_nw<E, KE, KT, 4, VEC, MODE>(s, A, W, st);
 }
 
 template <class E, int KT, bool VEC>
 hipError_t forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
+    if (W.segs > 1) {
+        hipError_t e = forward_mode<E, E, KT, VEC, kMap>(s, A, W, st);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((delta_join_kernel<KT>), dim3((unsigned)(s.B * s.Hv * ((s.Dv + 63) / 64))), dim3(256), 0, st,
+                           s, A, W, (s.Dv + 63) / 64, delta_blocks(s));
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     if (!W.x) return forward_mode<E, E, KT, VEC, kOut>(s, A, W, st);
     if (sizeof(E) == 4 || delta_keeps_f32(s.dtype, A.s_in))
         return A.o ? forward_mode<E, float, KT, VEC, kOut | kKeep>(s, A, W, st)

@@ -112,6 +112,24 @@ def test_long_row(L):
     check(L, (1, 3000, 1, 1, 64, 64), "f32", decay=0.01)
 
 
+# Few heads and many chunks: the row is walked in segments that are joined (six or more of at
+# least eight chunks each), also where rows end in different segments.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape,lengths", [((1, 3200, 1, 1, 64, 64), None), ((1, 3137, 1, 2, 128, 128), None),
+                                           ((2, 4000, 1, 1, 24, 40), [4000, 777]), ((3, 3500, 1, 2, 64, 160), [0, 1, 3499])],
+                         ids=str)
+def test_segments(L, shape, lengths, dtype):
+    check(L, shape, dtype, state=True, lengths=lengths, decay=0.01, seed=shape[1])
+    d = make_delta(*shape, 5, dtype, 0.01)
+    args = [to_dev(d[n], dtype) for n in INS]
+    s = to_dev(d["s_in"])
+    ln = None if lengths is None else to_dev(np.asarray(lengths, np.int32))
+    o, ref = L.gated_delta_forward(*args, state=s, lengths=ln)
+    o2, s2, _ = L.gated_delta_forward_ckpt(*args, state=s, lengths=ln)
+    L.gated_delta_forward(*args, state=s, lengths=ln, out=(o2, s))  # in place
+    assert np.array_equal(host(o), host(o2)) and np.array_equal(host(s), host(ref)) and np.array_equal(host(s2), host(ref))
+
+
 def test_in_place_state_and_no_state(L):
     import torch
     d = make_delta(2, 100, 1, 2, 64, 64, 14)

@@ -121,6 +121,11 @@ def test_long_row(L):
     check(L, (1, 2000, 1, 1, 64, 64), "f32", decay=0.01)
 
 
+def test_segments(L):
+    check(L, (1, 3300, 1, 1, 64, 48), "bf16", decay=0.01)
+    check(L, (2, 3137, 1, 2, 32, 64), "f32", decay=0.01, lengths=[3137, 900], ckpt=False)
+
+
 def test_against_differences_of_the_forward(L):
     # <grad, direction> against the forward's own difference quotient along it, in float32: the
     # quotient's truncation is of order eps^2 = 1e-4 relative, its rounding about 1e-6/eps = 1e-4.
