@@ -358,52 +358,57 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
 }
 
 // ---- the states before the segments ---------------------------------------------------------------
-// start_{g+1} = matrix_g start_g + constant_g, in order, 64 value channels of a head a workgroup, 16
-// a wave; the state stays in registers, three terms each of it and of the matrix.
+// start_{g+1} = matrix_g start_g + constant_g, in order.  A workgroup takes 16 value channels of a
+// head, a wave 16 rows of the state: the matrix's rows do not depend on the state, so the next
+// segment's are on their way while one is multiplied, and a segment costs little more than the
+// two barriers around the exchange of the state through LDS.  Three terms of both.
 template <int KT>
-__global__ __launch_bounds__(256) void delta_join_kernel(DeltaShape s, DeltaFwdArgs A, DeltaChunks W, int ntile,
-                                                         int nblk) {
-    const int wave = threadIdx.x >> 6;
+__global__ __launch_bounds__(128 * KT) void delta_join_kernel(DeltaShape s, DeltaFwdArgs A, DeltaChunks W, int ntile,
+                                                              int nblk) {
+    __shared__ float st[32 * KT][17];
+    const int d = threadIdx.x >> 6;
     const LanePos pos;
     const int r = pos.r, g = pos.g;
     const BlockPos at(blockIdx.x, s.Hv, ntile);
     const int64_t bh = at.b * s.Hv + at.h;
-    const int col = (at.rest * 4 + wave) * 16 + r, Dk = s.Dk, Dv = s.Dv, ld = 16 * nblk + 32 * KT;
-    f32x4 S[2 * KT];
-#pragma unroll
-    for (int d = 0; d < 2 * KT; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e;
-            S[d][e] = (A.s_in && row < Dk && col < Dv) ? A.s_in[(bh * Dk + row) * Dv + col] : 0.f;
-        }
-    for (int seg = 0; seg < W.segs; ++seg) {
-        float* out = W.start + ((int64_t)seg * s.B * s.Hv + bh) * Dk * Dv;
-#pragma unroll
-        for (int d = 0; d < 2 * KT; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 32 * (d >> 1) + 8 * g + 4 * (d & 1) + e;
-                if (row < Dk && col < Dv) out[(int64_t)row * Dv + col] = S[d][e];
-            }
-        if (seg + 1 == W.segs) break;
+    const int c0 = at.rest * 16, Dk = s.Dk, Dv = s.Dv, ld = 16 * nblk + 32 * KT;
+    const int cell = threadIdx.x & 15;  // this thread's column of the rows threadIdx.x / 16 + 8*KT*i
+    for (int row = threadIdx.x >> 4; row < 32 * KT; row += 8 * KT)
+        st[row][cell] = (A.s_in && row < Dk && c0 + cell < Dv) ? A.s_in[(bh * Dk + row) * Dv + c0 + cell] : 0.f;
+    float x[KT][8], c[4];
+    const auto fetch = [&](int seg) {
         const float* m = W.map + ((bh * (W.segs - 1) + seg) * (32 * KT)) * (int64_t)ld;
-        Frag<3> fs[KT];
+        const float* p = m + (32 * (d >> 1) + tile_row(r, d & 1)) * ld + 16 * nblk + 8 * g;
 #pragma unroll
-        for (int kk = 0; kk < KT; ++kk) fs[kk] = split_tiles<3>(S[2 * kk], S[2 * kk + 1]);
-#pragma unroll
-        for (int d = 0; d < 2 * KT; ++d) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[d][e] = m[(32 * (d >> 1) + 8 * g + 4 * (d & 1) + e) * ld + col];
-#pragma unroll
-            for (int kk = 0; kk < KT; ++kk) {
-                float x[8];
-                const float* p = m + (32 * (d >> 1) + tile_row(r, d & 1)) * ld + 16 * nblk + 32 * kk + 8 * g;
-                load16<float>(p, x);
-                load16<float>(p + 4, x + 4);
-                mma(S[d], split<3>(x), fs[kk]);
-            }
+        for (int kk = 0; kk < KT; ++kk) {
+            load16<float>(p + 32 * kk, x[kk]);
+            load16<float>(p + 32 * kk + 4, x[kk] + 4);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = m[(32 * (d >> 1) + 8 * g + 4 * (d & 1) + e) * ld + c0 + r];
+    };
+    fetch(0);
+    for (int seg = 0;; ++seg) {
+        __syncthreads();  // the state before this segment is there
+        float* out = W.start + ((int64_t)seg * s.B * s.Hv + bh) * Dk * Dv;
+        for (int row = threadIdx.x >> 4; row < Dk; row += 8 * KT)
+            if (c0 + cell < Dv) out[(int64_t)row * Dv + c0 + cell] = st[row][cell];
+        if (seg + 1 == W.segs) return;
+        f32x4 S = {c[0], c[1], c[2], c[3]};
+        Frag<3> fm[KT];
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) fm[kk] = split<3>(x[kk]);
+        if (seg + 2 < W.segs) fetch(seg + 1);
+#pragma unroll
+        for (int kk = 0; kk < KT; ++kk) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = st[32 * kk + 8 * g + i][r];
+            mma(S, fm[kk], split<3>(y));
+        }
+        __syncthreads();  // all have read it
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[32 * (d >> 1) + 8 * g + 4 * (d & 1) + e][r] = S[e];
     }
 }
 
@@ -454,8 +459,8 @@ hipError_t forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks
     if (W.segs > 1) {
         hipError_t e = forward_mode<E, E, KT, VEC, kMap>(s, A, W, st);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((delta_join_kernel<KT>), dim3((unsigned)(s.B * s.Hv * ((s.Dv + 63) / 64))), dim3(256), 0, st,
-                           s, A, W, (s.Dv + 63) / 64, delta_blocks(s));
+        hipLaunchKernelGGL((delta_join_kernel<KT>), dim3((unsigned)(s.B * s.Hv * ((s.Dv + 15) / 16))), dim3(128 * KT), 0,
+                           st, s, A, W, (s.Dv + 15) / 16, delta_blocks(s));
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!W.x) return forward_mode<E, E, KT, VEC, kOut>(s, A, W, st);
