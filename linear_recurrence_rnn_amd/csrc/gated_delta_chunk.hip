@@ -17,9 +17,8 @@ namespace {
 
 // ---- what depends on a chunk alone -----------------------------------------------------------
 // One wave a chunk.  K's fragments serve as both operands of K K^T (the A and B layouts of a
-// matrix and its transpose are one).  Lane c then solves for column c of the inverse:
-//   t_i = [i = c] - sum_{j<i} A_ij t_j,   A = G diag(beta)
-// with the rows of A read from LDS by all lanes at once.
+// matrix and its transpose are one).  With A = G diag(beta), the inverse's diagonal 32x32 blocks
+// come by substitution, the block below them by two products.
 template <class E, int KT, bool VEC, int NP>
 __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFwdArgs A, DeltaChunks W, int nc) {
     constexpr int NI = kTerms<E>;
@@ -108,18 +107,61 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
         }
     }
     __syncthreads();
-    float t[kChunk];
+    // The inverses of A's two 32x32 diagonal blocks, over them: lane 32*m + c solves for column c
+    // of block m, t_i = [i = c] - sum_{j<i} A_ij t_j, A's rows read from LDS by all its lanes at once.
+    {
+        float* const blkm = a + (lane >> 5) * (32 * LD + 32);
+        const int c = lane & 31;
+        float t[32];
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-        float x = i == lane ? 1.f : 0.f;
+        for (int i = 0; i < 32; ++i) {
+            float x = i == c ? 1.f : 0.f;
 #pragma unroll
-        for (int j = 0; j < i; ++j) x = fmaf(-a[i * LD + j], t[j], x);
-        t[i] = x;
+            for (int j = 0; j < i; ++j) x = fmaf(-blkm[i * LD + j], t[j], x);
+            t[i] = x;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) blkm[i * LD + c] = t[i];
+        __syncthreads();
     }
-    __syncthreads();
+    // The block below them: -N_1 (A_10 N_0), three terms of each factor.
+    {
+        f32x4 y[2][2];  // A_10 N_0: rows tile_row(m, half), columns 16*ct + r
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) a[i * LD + lane] = t[i];
-    __syncthreads();
+        for (int ct = 0; ct < 2; ++ct) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = a[(8 * g + i) * LD + 16 * ct + r];
+            const Frag<3> f = split<3>(x);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float* p = a + (32 + tile_row(r, half)) * LD + 8 * g;
+                load16<float>(p, x);
+                load16<float>(p + 4, x + 4);
+                y[half][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+                mma(y[half][ct], split<3>(x), f);
+            }
+        }
+        const Frag<3> fy[2] = {split_tiles<3>(y[0][0], y[1][0]), split_tiles<3>(y[0][1], y[1][1])};
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            float x[8];
+            const float* p = a + (32 + 16 * t + r) * LD + 32 + 8 * g;
+            load16<float>(p, x);
+            load16<float>(p + 4, x + 4);
+            const Frag<3> f = split<3>(x);
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                f32x4 z = {0.f, 0.f, 0.f, 0.f};
+                mma(z, f, fy[ct]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[(32 + 16 * t + 4 * g + e) * LD + 16 * ct + r] = -z[e];
+            }
+        }
+        __syncthreads();
+    }
     // Out as three terms, a row's 16-byte pieces by neighbouring lanes.
     bf16_t* out = reinterpret_cast<bf16_t*>(W.inv) + blk * (3 * kChunk * kChunk);
 #pragma unroll
