@@ -286,16 +286,20 @@ struct RowStage {
     }
 };
 
-// N terms of a 64x64 matrix likewise (as stored: the upper right block holds anything), and a
-// chunk's decays.
+// N terms of a 64x64 matrix likewise; its upper right 32x32 block, never written, comes as 0.
 template <int N, int NT>
 struct SquareStage {
     static constexpr int I = N * kChunk * 8 / NT;
     bf16x8 x[I];
     __device__ __forceinline__ void load(const void* src, int64_t cb, int planes) {
-        const bf16x8* p = reinterpret_cast<const bf16x8*>(src) + cb * planes * (kChunk * 8) + threadIdx.x;
+        const char* p = reinterpret_cast<const char*>(src) + cb * planes * (kChunk * kChunk * 2);
+        const rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), (short)0, N * kChunk * kChunk * 2, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < I; ++i) x[i] = p[NT * i];
+        for (int i = 0; i < I; ++i) {
+            const int id = (int)threadIdx.x + NT * i;
+            const bool upper = (id & 7) >= 4 && ((id >> 3) & 63) < 32;
+            x[i] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rs, upper ? kNowhere : 16u * id, 0, 0));
+        }
     }
     __device__ __forceinline__ void store(Mat<2>* dst) const {
 #pragma unroll

@@ -34,7 +34,16 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
     const int len = row_length(s, b), t0 = n * kChunk;
     if (t0 >= len) return;  // nothing of this chunk is used
     const Rows K = rows_of<E>(A.k, s, b, s.Hk, hk, s.Dk, t0, len), Q = rows_of<E>(A.q, s, b, s.Hk, hk, s.Dk, t0, len);
+    const bool live = t0 + lane < len;
+    float gv = 0.f, bb = 0.f;
+    if (live) {
+        const int64_t tok = (b * s.T + t0 + lane) * s.Hv + h;
+        gv = (float)reinterpret_cast<const E*>(A.g)[tok];
+        bb = (float)reinterpret_cast<const E*>(A.beta)[tok];
+    }
+    // All of K and, at one term a value, of Q is on its way before anything is waited for.
     Frag<NI> kf[4][KT];
+    E qx[NI == 1 ? 4 : 1][KT][8];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -43,12 +52,13 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
             load8<E, VEC>(K, 16 * t + r, 32 * kk + 8 * g, s.Dk, true, x);
             kf[t][kk] = to_frag<E>(x);
         }
+    if constexpr (NI == 1)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int kk = 0; kk < KT; ++kk) load8<E, VEC>(Q, 16 * t + r, 32 * kk + 8 * g, s.Dk, true, qx[t][kk]);
     {
-        const bool live = t0 + lane < len;
-        const int64_t tok = (b * s.T + t0 + lane) * s.Hv + h;
-        const double d = live ? decay_of((float)reinterpret_cast<const E*>(A.g)[tok]) : 0.0;
-        const double c = wave_cumsum(d);
-        const float bb = live ? (float)reinterpret_cast<const E*>(A.beta)[tok] : 0.f;
+        const double c = wave_cumsum(decay_of(gv));
         gam[lane] = c;
         bet[lane] = bb;
         W.gam[blk * kChunk + lane] = c;
@@ -80,9 +90,8 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
         Frag<NI> fq[KT];
 #pragma unroll
         for (int kk = 0; kk < KT; ++kk) {
-            E x[8];
-            load8<E, VEC>(Q, 16 * it + r, 32 * kk + 8 * g, s.Dk, true, x);
-            fq[kk] = to_frag<E>(x);
+            if constexpr (NI > 1) load8<E, VEC>(Q, 16 * it + r, 32 * kk + 8 * g, s.Dk, true, qx[0][kk]);
+            fq[kk] = to_frag<E>(qx[NI == 1 ? it : 0][kk]);
         }
         const int i = 16 * it + r;
         const double gi = gam[i];
@@ -167,6 +176,7 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int id = lane + 64 * i, row = id >> 3, c = 8 * (id & 7);
+        if (row < 32 && c >= 32) continue;
         float x[8];
         load16<float>(a + row * LD + c, x);
         load16<float>(a + row * LD + c + 4, x + 4);
