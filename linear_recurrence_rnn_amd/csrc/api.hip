@@ -961,7 +961,7 @@ size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws,
     w.gam = (double*)take(n * 64 * sizeof(double));
     w.dec = (float*)take(n * 3 * 64 * sizeof(float));
     if (upto >= kDeltaCkpt) {
-        w.x = take(block * 64);
+        w.x = (float*)take(n * linrec::delta_blocks(s) * 16 * 64 * sizeof(float));
         w.s0 = take(block * linrec::delta_dkp(s));
     }
     if (upto >= kDeltaBwd) w.ds = take(block * linrec::delta_dkp(s));

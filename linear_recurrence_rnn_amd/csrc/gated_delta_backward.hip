@@ -217,18 +217,18 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
 // once, straight into operands.  dO, dZ and X, which all waves need, go through LDS, 32*SK value
 // channels at a time.  The tiles of H^T and E^T (rows j <= its columns i) are dealt to the waves.
 //
-// Operands are the tensors' own type (one bfloat16 term, or three); the weights L beta H and
-// L beta E are rounded to two terms in bfloat16 calls.  Bound by memory: at 128x128 a chunk
+// Operands are the tensors' own type (one bfloat16 term, or three); x and the weights L beta H
+// and L beta E are two terms in bfloat16 calls.  Bound by memory: at 128x128 a chunk
 // reads about 180 KB and writes 33 KB a head.
 template <class E, class KE, int KT>
 struct GradLds {
-    static constexpr int NI = kTerms<E>, NK = kKeptTerms<E, KE>, NH = NI == 1 ? 2 : 3;
+    static constexpr int NI = kTerms<E>, NK = kKeptTerms<E, KE>, NX = NI == 1 ? 2 : 3, NH = NX;
     static constexpr int SK = NI == 1 ? 4 : 1;
     static constexpr bool ONE = NI == 3;  // no room for both weights: one after the other
     Mat<KT> k[NI], q[NI];
     union {
         struct {
-            Mat<SK> go[NI], gz[NI], x[NK];
+            Mat<SK> go[NI], gz[NI], x[NX];
         };
         struct {
             Mat<2> h[NH], e[ONE ? 1 : NH];  // scale L beta H, L beta E: rows i, columns j
@@ -244,24 +244,18 @@ struct GradLds {
 };
 
 // x in LDS as terms from its blocks of 16 value channels, 32*SK channels from block b0 on.
-template <class KE, int N, int SK>
+template <int N, int SK>
 struct BlockStage {
     static constexpr int P = kChunk * 4 * SK, I = (P + 511) / 512;
-    KE x[I][8];
-    __device__ __forceinline__ void load(const KE* m, int b0) {
+    float x[I][8];
+    __device__ __forceinline__ void load(const float* m, int b0) {
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             const int id = (int)threadIdx.x + 512 * i;
             if (P % 512 != 0 && id >= P) break;
-            const KE* p = m + ((int64_t)b0 * kChunk * 16 + 8 * id);
-            if constexpr (sizeof(KE) == 2) {
-                const bf16x8 t = *reinterpret_cast<const bf16x8*>(p);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[i][j] = t[j];
-            } else {
-                load16<float>(p, x[i]);
-                load16<float>(p + 4, x[i] + 4);
-            }
+            const float* p = m + ((int64_t)b0 * kChunk * 16 + 8 * id);
+            load16<float>(p, x[i]);
+            load16<float>(p + 4, x[i] + 4);
         }
     }
     __device__ __forceinline__ void store(Mat<SK>* dst) const {
@@ -269,9 +263,7 @@ struct BlockStage {
         for (int i = 0; i < I; ++i) {
             const int id = (int)threadIdx.x + 512 * i, row = (id >> 1) & 63, c = 16 * (id >> 7) + 8 * (id & 1);
             if (P % 512 != 0 && id >= P) break;
-            Frag<N> f;
-            if constexpr (sizeof(KE) == 2) f = to_frag<KE>(x[i]);
-            else f = split<N>(x[i]);
+            const Frag<N> f = split<N>(x[i]);
 #pragma unroll
             for (int m = 0; m < N; ++m) *dst[m].row8(row, c) = f.t[m];
         }
@@ -306,7 +298,7 @@ template <class E, class KE, int KT, bool VEC>
 __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc, int,
                                                             int nblk) {
     typedef GradLds<E, KE, KT> Lds;
-    constexpr int NI = Lds::NI, NK = Lds::NK, NH = Lds::NH, SK = Lds::SK;
+    constexpr int NI = Lds::NI, NK = Lds::NK, NX = Lds::NX, NH = Lds::NH, SK = Lds::SK;
     constexpr int DT = 2 * KT, TW = DT / 2;  // tiles of key channels; token tiles of a wave
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
@@ -347,7 +339,7 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
         pos.renew();
         const int r = pos.r, g = pos.g;
         const int64_t cb = (b * s.Hv + h) * nc + n;
-        const KE* X = reinterpret_cast<const KE*>(W.x) + cb * nblk * (kChunk * 16);
+        const float* X = W.x + cb * nblk * (kChunk * 16);
         const KE* S0 = reinterpret_cast<const KE*>(W.s0) + cb * nblk * (32 * KT * 16);
         const KE* DS = reinterpret_cast<const KE*>(W.ds) + cb * nblk * (32 * KT * 16);
         const Rows go = rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0, len), gz = rows_of<E>(A.gv, s, b, s.Hv, h, Dv, t0, len);
@@ -359,7 +351,7 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
         for (int t = 0; t < TW; ++t) rq[t] = rk[t] = wk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int kv0 = 0; 32 * kv0 < Dv; kv0 += SK) {
             RowStage<E, SK, 512> so, sz;
-            BlockStage<KE, NK, SK> sx;
+            BlockStage<NX, SK> sx;
             so.template load<VEC>(go, Dv, 32 * kv0);
             sz.template load<VEC>(gz, Dv, 32 * kv0);
             sx.load(X, 2 * kv0);
@@ -390,18 +382,18 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (j0 + 2 * i <= it) {
-                        const Frag<NK> f = read_rows<NK>(L.x, pos, j0 + 2 * i, kv);
+                        const Frag<NX> f = read_rows<NX>(L.x, pos, j0 + 2 * i, kv);
                         mma(H[i], f, fo);
                         mma(Z[i], f, fz);
                     }
                 // S dO, S dZ, dS' x: rows key channels, columns tokens.
                 Frag<NI> to[TW], tz[TW];
-                Frag<NK> tx[TW];
+                Frag<NX> tx[TW];
 #pragma unroll
                 for (int t = 0; t < TW; ++t) {
                     to[t] = read_rows<NI>(L.go, pos, tk0 + t, kv);
                     tz[t] = read_rows<NI>(L.gz, pos, tk0 + t, kv);
-                    tx[t] = read_rows<NK>(L.x, pos, tk0 + t, kv);
+                    tx[t] = read_rows<NX>(L.x, pos, tk0 + t, kv);
                 }
                 mma_cols<TW>(rq, fs[kv], to);
                 mma_cols<TW>(rk, fs[kv], tz);

@@ -329,12 +329,12 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
             if constexpr (KEEP) {  // X, likewise
-                const Frag<kKeptSum<KE>> fx = split_tiles<kKeptSum<KE>>(U[2 * k2], U[2 * k2 + 1]);
+                const Frag<3> fx = split_tiles<3>(U[2 * k2], U[2 * k2 + 1]);
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
                     f32x4 x = {0.f, 0.f, 0.f, 0.f};
                     mma(x, fx, identity_frag(which));
-                    store4<KE>(reinterpret_cast<KE*>(W.x) +
+                    store4<float>(W.x +
                                    ((cb * nblk + c0 / 16) * kChunk + 32 * k2 + 16 * which + r) * 16 + 4 * g,
                                x);
                 }
