@@ -17,6 +17,12 @@
  *                                 Sequences", diagonal complex recurrence, eq. lr-xx)
  *   linrec_scan_real_backward,    the adjoints (backward passes) of the two scans
  *   linrec_scan_complex_backward
+ *   gated_delta_forward,          a recurrence with a (Dk, Dv) matrix of state per head: forward,
+ *   gated_delta_decode_step,      one token, training (checkpoint and backward)
+ *   gated_delta_forward_ckpt,
+ *   gated_delta_backward
+ *   group_norm_act (+ backward)   the norm of each token's channel groups, with an activation or
+ *                                 a gate, that follows such a recurrence
  *   linrec_scan_mingru, _minlstm, gated variants of the real scan (minGRU, minLSTM, one decay
  *   _real_decay                   per channel) and the LRU with normalised input, and their
  *   linrec_scan_complex_normalized adjoints (*_backward)
@@ -55,6 +61,8 @@
  *    while kernels run surface on the stream, as for any HIP work.
  *  - Input values are not inspected (that would need a device read): non-finite inputs
  *    propagate to the outputs.
+ *  - The gated delta rule and the group norm take float32 or bfloat16 tensors (their own rules
+ *    of sizes stand with them); what follows here and above on types is of the other calls.
  *  - Arithmetic is float32 (complex64 as float32 pairs); results match an fp64 evaluation
  *    of the same definition to a relative error of about 1e-5 of the per-sequence RMS.
  */

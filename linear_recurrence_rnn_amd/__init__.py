@@ -1,5 +1,6 @@
 """MI355X (gfx950) per-channel linear recurrences: RWKV-4 WKV forward/backward and
-real/complex diagonal scans with their adjoints, as hand-written HIP kernels behind a C ABI
+real/complex diagonal scans with their adjoints, the gated delta rule (a matrix of state per head)
+and the per-token group norm that follows it, as hand-written HIP kernels behind a C ABI
 (``include/linrec.h``).  The Python functions here marshal torch tensors to that ABI.
 
 The binding is imported lazily so that ``linear_recurrence_rnn_amd.workloads`` (the seeded
