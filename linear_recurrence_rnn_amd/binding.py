@@ -730,6 +730,8 @@ def _dtype_code(t, name):
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s is on %s, expected a ROCm device" % (name, t.device))
     return code
 
 
@@ -743,8 +745,15 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle alone: 0.1 us, where the Stream object around it takes 1.8, a fifth
+# of a whole call on few tokens.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _current_raw_stream(device.index)
 
 
 def _delta_shape(q, k, v, g, beta, lead):

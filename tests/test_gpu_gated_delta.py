@@ -270,6 +270,8 @@ def test_refusals(L):
     with pytest.raises(L.LinrecError, match="multiple"):
         call(v=torch.cat([a["v"], a["v"][:, :, :1]], 2), g=torch.cat([a["g"], a["g"][..., :1]], 2),
              beta=torch.cat([a["beta"], a["beta"][..., :1]], 2))
+    with pytest.raises(ValueError, match="expected a ROCm device"):
+        L.gated_delta_forward(*(a[n].cpu() for n in INS))
     wide = torch.zeros(1, 4, 1, 129, device="cuda")
     one = torch.zeros(1, 4, 1, device="cuda")
     with pytest.raises(L.LinrecError, match="widths"):

@@ -143,6 +143,8 @@ def test_refusals(L):
         L.group_norm_act(x, 4, w, w, gate=x[:2])
     with pytest.raises(L.LinrecError, match="eps"):
         L.group_norm_act(x, 4, w, w, eps=-1.0)
+    with pytest.raises(ValueError, match="expected a ROCm device"):
+        L.group_norm_act(x.cpu(), 4, w.cpu(), w.cpu())
     big = torch.zeros(1, 8193, device="cuda")
     with pytest.raises(L.LinrecError, match="8193 channels"):
         L.group_norm_act(big, 1, big[0], big[0])
