@@ -218,8 +218,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
 // channels at a time.  The tiles of H^T and E^T (rows j <= its columns i) are dealt to the waves.
 //
 // Operands are the tensors' own type (one bfloat16 term, or three); x and the weights L beta H
-// and L beta E are two terms in bfloat16 calls.  Bound by memory: at 128x128 a chunk
-// reads about 180 KB and writes 33 KB a head.
+// and L beta E are two terms in bfloat16 calls.  At 128x128 a chunk reads about 200 KB and writes
+// 33 KB a head: 705 us for 10240 (3.4 TB/s), bound by one workgroup's loads, products and five
+// barriers following each other (its LDS is over half of a CU's).
 template <class E, class KE, int KT>
 struct GradLds {
     static constexpr int NI = kTerms<E>, NK = kKeptTerms<E, KE>, NX = NI == 1 ? 2 : 3, NH = NX;
