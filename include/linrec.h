@@ -535,7 +535,8 @@ int wkv4_forward_noalloc(int64_t B, int64_t T, int64_t C,
  *
  * Long sequences are taken in chunks of 64 tokens; a value that is not finite then reaches
  * the outputs of its own chunk, earlier tokens among them.  The states are float32 throughout.
- * Any of B, T, Hk, Hv equal to 0 enqueues nothing but s_out.
+ * Any of B, T, Hk, Hv equal to 0 enqueues nothing but s_out.  LINREC_ERR_UNSUPPORTED beyond
+ * B*Hv = 2^20, T = 2^30, B*Hv*T/64 = 2^26 - 1 or Hv*max(Dk, Dv) = 2^22.
  */
 int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
                         const void *q, const void *k, const void *v, const void *g, const void *beta,
@@ -591,7 +592,7 @@ int gated_delta_decode_step(int64_t B, int64_t Hk, int64_t Hv, int64_t Dk, int64
  *
  *   x, gate, out (N,C) of type dtype (gate may be NULL); weight, bias (C) float32
  *   act  LINREC_ACT_NONE or LINREC_ACT_SILU (t * sigmoid(t));  eps >= 0
- *   G divides C; C/G <= 8192
+ *   G divides C; C/G <= 8192, C <= 2^24 (else LINREC_ERR_UNSUPPORTED)
  */
 #define LINREC_ACT_NONE 0
 #define LINREC_ACT_SILU 1
