@@ -552,8 +552,9 @@ size_t gated_delta_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, 
  * Training.  gated_delta_forward_ckpt is gated_delta_forward that also keeps, in `ckpt` (of
  * gated_delta_checkpoint_size bytes, 16-byte aligned), what the backward starts from: each
  * chunk's inverse, its x and the state before it.  gated_delta_backward takes that checkpoint
- * (of a call with the same sizes and inputs), or NULL and forms it again in its workspace.  What
- * is kept has the tensors' type, or float32 where a state is carried in (s_in).
+ * (of a call with the same sizes and inputs), or NULL and forms it again in its workspace.  x and
+ * the states are kept in float32 for either type; the inverse and P as bfloat16 terms, of which P
+ * has one less in bfloat16 calls without s_in.
  *
  *   go      (B,T,Hv,Dv) upstream gradient of o; gs_out (B,Hv,Dk,Dv) float32 that of s_out, or NULL
  *   gq, gk, gv, gg, gbeta   gradients, in the shape and type of q, k, v, g, beta (gq and gk summed

@@ -942,11 +942,12 @@ linrec::DeltaShape delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int
 bool delta_is_short(int64_t T) { return T <= 12; }
 
 // Scratch of the chunked kernels, in this order: what depends on chunks alone; x and s0 (a
-// checkpoint has them too); ds; the segments' maps and states.  state: a state is carried in.  Returns the end; fills W if given.
+// checkpoint has them too); ds and dz; the segments' maps and states.  state: a state is carried in.
+// Returns the end; fills W if given.
 enum { kDeltaPrep, kDeltaCkpt, kDeltaBwd };
 size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws, linrec::DeltaChunks* W) {
-    const size_t n = (size_t)linrec::delta_chunks(s), e = linrec::delta_keeps_f32(s.dtype, state ? &s : nullptr) ? 4 : 2;
-    const size_t block = n * linrec::delta_blocks(s) * 16 * e;  // bytes of a row of every chunk's block matrix
+    const size_t n = (size_t)linrec::delta_chunks(s);
+    const size_t block = n * linrec::delta_blocks(s) * 16 * sizeof(float);  // a row of every chunk's block matrix
     size_t at = 0;
     const auto take = [&](size_t bytes) {
         char* p = (char*)ws + at;
@@ -954,17 +955,20 @@ size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws,
         return (void*)p;
     };
     linrec::DeltaChunks w{};
-    // P's terms: two serve bfloat16 outputs and gradients, three float32 ones.
-    w.np = s.dtype == LINREC_F32 || (upto > kDeltaPrep && e == 4) ? 3 : 2;
+    // P's terms: two serve bfloat16 outputs and gradients, three float32 ones (that of a carried state).
+    w.np = s.dtype == LINREC_F32 || (upto > kDeltaPrep && state) ? 3 : 2;
     w.inv = take(n * 3 * 64 * 64 * 2);
     w.p = take(n * w.np * 64 * 64 * 2);
     w.gam = (double*)take(n * 64 * sizeof(double));
     w.dec = (float*)take(n * 3 * 64 * sizeof(float));
     if (upto >= kDeltaCkpt) {
-        w.x = (float*)take(n * linrec::delta_blocks(s) * 16 * 64 * sizeof(float));
-        w.s0 = take(block * linrec::delta_dkp(s));
+        w.x = (float*)take(block * 64);
+        w.s0 = (float*)take(block * linrec::delta_dkp(s));
     }
-    if (upto >= kDeltaBwd) w.ds = take(block * linrec::delta_dkp(s));
+    if (upto >= kDeltaBwd) {
+        w.ds = (float*)take(block * linrec::delta_dkp(s));
+        w.dz = take(s.dtype == LINREC_BF16 ? (size_t)(s.B * s.T * s.Hv * s.Dv) * 2 : 0);
+    }
     w.segs = linrec::delta_segments(s);
     w.seg_len = (int)ceil_div(ceil_div(s.T, 64), w.segs);
     const size_t heads = (size_t)(s.B * s.Hv), dkp = linrec::delta_dkp(s);
@@ -974,6 +978,7 @@ size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws,
     return at;
 }
 
+// Of those, what the backward from a checkpoint needs for itself: ds and dz.
 size_t delta_ds_bytes(const linrec::DeltaShape& s, bool state) {
     return delta_layout(s, state, kDeltaBwd, nullptr, nullptr) - delta_layout(s, state, kDeltaCkpt, nullptr, nullptr);
 }
@@ -1070,8 +1075,11 @@ LINREC_API int gated_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t Hv
     const hipStream_t hs = (hipStream_t)stream;
     linrec::DeltaChunks W;
     if (ckpt) {
+        linrec::DeltaChunks own;
         delta_layout(s, state, kDeltaCkpt, const_cast<void*>(ckpt), &W);
-        W.ds = workspace;
+        delta_layout(s, state, kDeltaBwd, workspace, &own);  // for dz's place behind ds
+        W.ds = (float*)workspace;
+        W.dz = (char*)workspace + ((char*)own.dz - (char*)own.ds);
     } else {
         delta_layout(s, state, kDeltaBwd, workspace, &W);
         const linrec::DeltaFwdArgs F{q, k, v, g, beta, s_in, nullptr, nullptr};

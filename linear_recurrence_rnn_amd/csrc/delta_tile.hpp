@@ -158,10 +158,9 @@ template <class E, int KT, int NW> constexpr int kWavesPerSimd = NW == 8 || (siz
 
 template <class E> constexpr int kTerms = sizeof(E) == 2 ? 1 : 3;  // bfloat16 terms of an input
 
-// Terms of what the forward keeps for the backward in type KE: written as this many terms'
-// sum, read as this many terms in calls on E (two carry float32 kept for bfloat16 tensors).
-template <class KE> constexpr int kKeptSum = sizeof(KE) == 2 ? 1 : 3;
-template <class E, class KE> constexpr int kKeptTerms = sizeof(KE) == 2 ? 1 : sizeof(E) == 2 ? 2 : 3;
+// Terms in which the gradients' products take what is kept in float32 (x, the states and their
+// gradients) and dZ: two in calls on bfloat16, 2^-16 before each result's own rounding.
+template <class E> constexpr int kKeptTerms = sizeof(E) == 2 ? 2 : 3;
 
 template <class E>
 __device__ __forceinline__ Frag<kTerms<E>> to_frag(const E* x) {

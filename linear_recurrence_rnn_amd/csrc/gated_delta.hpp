@@ -37,20 +37,23 @@ struct DeltaFwdArgs {
 //                           (the upper right 32x32 blocks of both are not written)
 //   gam   (64) float64      decays cumulated within the chunk
 //   dec   (3,64) float32    e^gam, e^{gam_63 - gam}, beta
-// and for the backward, in blocks of 16 value channels (delta_blocks(s) of them, zero past Dv);
-// the states in the tensors' type, or float32 (delta_keeps_f32).  x enters every gradient:
-// kept in bfloat16 it raised the error of dk and dbeta (2-norm, relative) from 2.5e-3 and less to
-// 3e-3, where the final rounding's is 1.7e-3, and saved 6% of a training step.
-//   x     (blocks, 64, 16)       x_t of the recurrence, float32
+// and for the backward, in float32, in blocks of 16 value channels (delta_blocks(s) of them, zero
+// past Dv).  They enter every gradient: with the states in bfloat16 and dZ as rounded in dV, the
+// errors (2-norm) of bfloat16 gradients were 1.2 to 2.2 times their final rounding's where decays are
+// slow or a gradient of the final state comes in; so they are that rounding's, to three digits.
+//   x     (blocks, 64, 16)       x_t of the recurrence
 //   s0    (blocks, dkp, 16)      the state before the chunk, dkp = Dk rounded up (delta_dkp)
 //   ds    (blocks, dkp, 16)      the gradient of the state after the chunk
+// and, laid out as v, what the bfloat16 result dV = dZ leaves of dZ (bfloat16 calls only):
+//   dz    (B,T,Hv,Dv) bfloat16   dZ - dV
 struct DeltaChunks {
     void *inv, *p;
     int np;
     double* gam;
     float* dec;
     float* x;  // null: nothing is kept
-    void *s0, *ds;
+    float *s0, *ds;
+    void* dz;
     // Long rows of few heads are walked in `segs` segments of `seg_len` chunks (1: in one).  A
     // chunk maps the state to (matrix) state + (matrix), so a segment does: `map` holds, for all
     // but the last, (dkp, 16*blocks + dkp) float32, the map's constant part and its matrix;
@@ -59,10 +62,6 @@ struct DeltaChunks {
     float *map, *start;
 };
 inline int64_t delta_chunks(const DeltaShape& s) { return s.B * s.Hv * ((s.T + 63) / 64); }
-// A carried state's gradient lands on few tokens (the last ones of a piece), and pieces are
-// chained through it: what is kept is then float32, so that those tokens' gradients are not
-// limited by the rounding of x and the states.
-inline bool delta_keeps_f32(int dtype, const void* s_in) { return dtype == 0 || s_in != nullptr; }
 inline int delta_blocks(const DeltaShape& s) { return (s.Dv + 127) / 128 * 8; }
 // Eight waves to a workgroup (bfloat16 calls) where a head has the value channels for them and
 // the heads alone fill most of the chip; four, on twice the CUs, else.

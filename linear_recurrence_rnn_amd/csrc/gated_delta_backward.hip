@@ -5,9 +5,10 @@
 //   dU = P^T dO + diag(e^{gam_63 - gam}) K dS'
 //   dZ = N^T (beta dU) = dV
 //   dS = e^{gam_63} dS' + scale Q^T diag(e^gam) dO - K^T diag(e^gam) dZ
-// is a chain over the chunks in reverse (first kernel; it writes dV and every dS').  The rest is
-// local to a chunk (second kernel), with H = dO X^T, E = dZ X^T, L_ij = e^{gam_i - gam_j},
-// q' = scale q, W = e^{gam_63 - gam_j} dS' x_j, M_ij = L_ij (q'_i.k_j H_ij - [i > j] k_i.k_j E_ij):
+// is a chain over the chunks in reverse (first kernel; it writes dV, in bfloat16 calls also what its
+// rounding left of dZ, and every dS').  The rest is local to a chunk (second kernel), with
+// H = dO X^T, E = dZ X^T, L_ij = e^{gam_i - gam_j}, q' = scale q, W = e^{gam_63 - gam_j} dS' x_j,
+// M_ij = L_ij (q'_i.k_j H_ij - [i > j] k_i.k_j E_ij):
 //   dq_i    = scale (e^{gam_i} S dO_i + sum_{j<=i} L_ij beta_j H_ij k_j)
 //   dk_j    = beta_j (W_j + sum_{i>=j} L_ij H_ij q'_i - sum_{i>j} L_ij E_ij k_i)
 //             - e^{gam_j} S dZ_j - sum_{i<j} L_ji beta_i E_ji k_i
@@ -23,9 +24,9 @@ namespace linrec {
 namespace {
 
 // ---- the chain of the state's gradient ----------------------------------------------------------
-// The forward chain's layout: four waves, 16 value channels each, dS in registers.  NS terms
-// for the gradient of the state and what flows into it: three where a float32 result leaves the
-// kernel or is kept (KE), two (2^-16) where all are bfloat16.
+// The forward chain's layout: 16 value channels a wave, dS in registers.  NS terms for the gradient
+// of the state and what flows into it: three where it leaves the call in float32, as the gradient
+// of a carried state; two (2^-16) where all results are bfloat16.
 template <class E, int KT, int NS>
 struct ChainLds {
     static constexpr int NI = kTerms<E>;
@@ -34,12 +35,12 @@ struct ChainLds {
     float eg[kChunk], ew[kChunk], be[kChunk];  // e^gam, e^{gam_63 - gam}, beta
 };
 
-template <class E, class KE, int KT, int NW, bool VEC, int NS>
+template <class E, int KT, int NW, bool VEC, int NS>
 __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_chain_kernel(DeltaShape s, DeltaBwdArgs A,
                                                                                       DeltaChunks W, int nc, int ntile,
                                                                                       int nblk) {
     typedef ChainLds<E, KT, NS> Lds;
-    constexpr int NI = kTerms<E>;
+    constexpr int NI = kTerms<E>, NZ = kKeptTerms<E>;
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
@@ -104,10 +105,8 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 f32x4 x = {0.f, 0.f, 0.f, 0.f};
-                mma<NS, 1, kKeptSum<KE>, 1>(x, fs, identity_frag(which));
-                store4<KE>(reinterpret_cast<KE*>(W.ds) +
-                               ((cb * nblk + c0 / 16) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
-                           x);
+                mma(x, fs, identity_frag(which));
+                store4<float>(W.ds + ((cb * nblk + c0 / 16) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g, x);
             }
         }
         phase();
@@ -162,12 +161,18 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
         Frag<NS> fz[2];
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
-            const Frag<NI> fx = split_tiles<NI>(Z[2 * k2], Z[2 * k2 + 1]);
+            const Frag<NZ> fx = split_tiles<NZ>(Z[2 * k2], Z[2 * k2 + 1]);
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 f32x4 x = {0.f, 0.f, 0.f, 0.f};
-                mma(x, fx, identity_frag(which));
+                mma<NZ, 1, NI, 1>(x, fx, identity_frag(which));
                 store_rows<E, VEC>(out, 32 * k2 + 16 * which + r, c0 + 4 * g, Dv, x);
+                if constexpr (NI < NZ) {  // what the rounding left
+                    f32x4 y = {0.f, 0.f, 0.f, 0.f};
+                    mma(y, Frag<1>{{fx.t[1]}}, identity_frag(which));
+                    store_rows<E, VEC>(rows_of<E>(W.dz, s, b, s.Hv, h, Dv, t0, (int)s.T), 32 * k2 + 16 * which + r,
+                                       c0 + 4 * g, Dv, y);
+                }
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half)
@@ -217,19 +222,20 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
 // once, straight into operands.  dO, dZ and X, which all waves need, go through LDS, 32*SK value
 // channels at a time.  The tiles of H^T and E^T (rows j <= its columns i) are dealt to the waves.
 //
-// Operands are the tensors' own type (one bfloat16 term, or three); x and the weights L beta H
-// and L beta E are two terms in bfloat16 calls.  At 128x128 a chunk reads about 200 KB and writes
-// 33 KB a head: 705 us for 10240 (3.4 TB/s), bound by one workgroup's loads, products and five
-// barriers following each other (its LDS is over half of a CU's).
-template <class E, class KE, int KT>
+// Operands are the tensors' own type (one bfloat16 term, or three); what is kept (x, S, dS'), dZ and
+// the weights L beta H and L beta E are two terms in bfloat16 calls.  At 128x128 a bfloat16 chunk reads
+// 240 KB (half of it S and dS') and writes 33 KB a head: 1035 us for 10240 (2.8 TB/s), bound by one
+// workgroup's loads, products and five barriers following each other (its LDS is over half of a
+// CU's).  With S and dS' kept in bfloat16 and dZ as rounded in dV it took 705, see DeltaChunks.
+template <class E, int KT>
 struct GradLds {
-    static constexpr int NI = kTerms<E>, NK = kKeptTerms<E, KE>, NX = NI == 1 ? 2 : 3, NH = NX;
+    static constexpr int NI = kTerms<E>, NX = kKeptTerms<E>, NH = NX;
     static constexpr int SK = NI == 1 ? 4 : 1;
     static constexpr bool ONE = NI == 3;  // no room for both weights: one after the other
     Mat<KT> k[NI], q[NI];
     union {
         struct {
-            Mat<SK> go[NI], gz[NI], x[NX];
+            Mat<SK> go[NI], gz[NX], x[NX];
         };
         struct {
             Mat<2> h[NH], e[ONE ? 1 : NH];  // scale L beta H, L beta E: rows i, columns j
@@ -271,19 +277,16 @@ struct BlockStage {
     }
 };
 
-// 8 value channels from 32*kv + 8g of row `row` of a matrix kept in blocks of 16 channels.
-template <class KE, int N>
-__device__ __forceinline__ Frag<N> read_block(const KE* m, int rows, int row, int kv, int g) {
-    const KE* p = m + ((int64_t)(2 * kv + (g >> 1)) * rows + row) * 16 + 8 * (g & 1);
-    if constexpr (sizeof(KE) == 2) {
-        Frag<N> f;
-        f.t[0] = *reinterpret_cast<const bf16x8*>(p);
-        return f;
-    } else {
-        float x[8];
-        load16<float>(p, x);
-        load16<float>(p + 4, x + 4);
-        return split<N>(x);
+// 8 value channels from 32*kv + 8g of row `row` of a matrix kept in blocks of 16 channels.  Through
+// a buffer resource: what depends on the lane is one register for all of them.
+__device__ __forceinline__ void load_block(const rsrc_t& m, int rows, int row, int kv, int g, float* x) {
+    const unsigned lane = 64u * ((g >> 1) * rows + row) + 32u * (g & 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const f32x4 t = __builtin_bit_cast(
+            f32x4, __builtin_amdgcn_raw_buffer_load_b128(m, lane + 16u * i, uniform(128 * kv * rows), 0));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * i + e] = t[e];
     }
 }
 
@@ -295,11 +298,11 @@ __device__ __forceinline__ Frag<N> negative(Frag<N> f) {
     return f;
 }
 
-template <class E, class KE, int KT, bool VEC>
+template <class E, int KT, bool VEC>
 __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaBwdArgs A, DeltaChunks W, int nc, int,
                                                             int nblk) {
-    typedef GradLds<E, KE, KT> Lds;
-    constexpr int NI = Lds::NI, NK = Lds::NK, NX = Lds::NX, NH = Lds::NH, SK = Lds::SK;
+    typedef GradLds<E, KT> Lds;
+    constexpr int NI = Lds::NI, NX = Lds::NX, NH = Lds::NH, SK = Lds::SK;
     constexpr int DT = 2 * KT, TW = DT / 2;  // tiles of key channels; token tiles of a wave
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
@@ -341,9 +344,10 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
         const int r = pos.r, g = pos.g;
         const int64_t cb = (b * s.Hv + h) * nc + n;
         const float* X = W.x + cb * nblk * (kChunk * 16);
-        const KE* S0 = reinterpret_cast<const KE*>(W.s0) + cb * nblk * (32 * KT * 16);
-        const KE* DS = reinterpret_cast<const KE*>(W.ds) + cb * nblk * (32 * KT * 16);
+        const int kept = nblk * (32 * KT * 16);  // of a chunk
+        const rsrc_t S0 = make_rsrc(W.s0 + cb * kept, 4 * kept), DS = make_rsrc(W.ds + cb * kept, 4 * kept);
         const Rows go = rows_of<E>(A.go, s, b, s.Hv, h, Dv, t0, len), gz = rows_of<E>(A.gv, s, b, s.Hv, h, Dv, t0, len);
+        const Rows gl = rows_of<E>(W.dz, s, b, s.Hv, h, Dv, t0, len);  // dZ is gz + gl in bfloat16 calls
         f32x4 H[2], Z[2], rq[TW], rk[TW], wk[TW];
         float dot = 0.f;
 #pragma unroll
@@ -351,17 +355,23 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
 #pragma unroll
         for (int t = 0; t < TW; ++t) rq[t] = rk[t] = wk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         for (int kv0 = 0; 32 * kv0 < Dv; kv0 += SK) {
-            RowStage<E, SK, 512> so, sz;
+            RowStage<E, SK, 512> so, sz, sl;
             BlockStage<NX, SK> sx;
             so.template load<VEC>(go, Dv, 32 * kv0);
             sz.template load<VEC>(gz, Dv, 32 * kv0);
+            if constexpr (NI < NX) sl.template load<VEC>(gl, Dv, 32 * kv0);
             sx.load(X, 2 * kv0);
-            Frag<NK> fs[SK], fd[SK];
+            // S and dS': half of them on their way with what goes through LDS, the others in the
+            // registers that that leaves.
+            float xs[SK][8], xd[SK][8];
+            const auto states = [&](int from, int to) {
 #pragma unroll
-            for (int kv = 0; kv < SK; ++kv) {
-                fs[kv] = read_block<KE, NK>(S0, 32 * KT, 16 * d0 + r, kv0 + kv, g);
-                fd[kv] = read_block<KE, NK>(DS, 32 * KT, 16 * d0 + r, kv0 + kv, g);
-            }
+                for (int kv = from; kv < to; ++kv) {
+                    load_block(S0, 32 * KT, 16 * d0 + r, kv0 + kv, g, xs[kv]);
+                    load_block(DS, 32 * KT, 16 * d0 + r, kv0 + kv, g, xd[kv]);
+                }
+            };
+            states(0, (SK + 1) / 2);
             __syncthreads();  // what lay here has been read
             if (hr == 0 && kv0 == 0) sk.store(L.k), sq.store(L.q);
             if (kv0 == 0 && tid < kChunk) {
@@ -372,14 +382,17 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
             }
             so.store(L.go);
             sz.store(L.gz);
+            if constexpr (NI < NX) sl.store(L.gz + 1);
             sx.store(L.x);
+            states((SK + 1) / 2, SK);
             __syncthreads();
 #pragma unroll
             for (int kv = 0; kv < SK; ++kv) {
                 if (32 * (kv0 + kv) >= Dv) break;  // blocks past Dv may not have been written
                 phase();
                 // H^T, E^T: rows j, columns i.
-                const Frag<NI> fo = read_rows<NI>(L.go, pos, it, kv), fz = read_rows<NI>(L.gz, pos, it, kv);
+                const Frag<NI> fo = read_rows<NI>(L.go, pos, it, kv);
+                const Frag<NX> fz = read_rows<NX>(L.gz, pos, it, kv);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (j0 + 2 * i <= it) {
@@ -388,26 +401,21 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
                         mma(Z[i], f, fz);
                     }
                 // S dO, S dZ, dS' x: rows key channels, columns tokens.
-                Frag<NI> to[TW], tz[TW];
-                Frag<NX> tx[TW];
+                Frag<NI> to[TW];
+                Frag<NX> tz[TW], tx[TW];
 #pragma unroll
                 for (int t = 0; t < TW; ++t) {
                     to[t] = read_rows<NI>(L.go, pos, tk0 + t, kv);
-                    tz[t] = read_rows<NI>(L.gz, pos, tk0 + t, kv);
+                    tz[t] = read_rows<NX>(L.gz, pos, tk0 + t, kv);
                     tx[t] = read_rows<NX>(L.x, pos, tk0 + t, kv);
                 }
-                mma_cols<TW>(rq, fs[kv], to);
-                mma_cols<TW>(rk, fs[kv], tz);
-                mma_cols<TW>(wk, fd[kv], tx);
+                const Frag<NX> fs = split<NX>(xs[kv]), fd = split<NX>(xd[kv]);
+                mma_cols<TW>(rq, fs, to);
+                mma_cols<TW>(rk, fs, tz);
+                mma_cols<TW>(wk, fd, tx);
                 if (tk0 == 0)  // <S, dS'>, each byte of them once
 #pragma unroll
-                    for (int m = 0; m < NK; ++m)
-#pragma unroll
-                        for (int o = 0; o < NK; ++o)
-                            if (m + o < NK)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    dot = fmaf((float)fs[kv].t[m][i], (float)fd[kv].t[o][i], dot);
+                    for (int i = 0; i < 8; ++i) dot = fmaf(xs[kv][i], xd[kv][i], dot);
             }
         }
         phase();
@@ -590,33 +598,32 @@ hipError_t launch(K kernel, int64_t blocks, int bytes, hipStream_t st, const Del
     return hipGetLastError();
 }
 
-template <class E, class KE, int KT, int NS, bool VEC>
+template <class E, int KT, int NS, bool VEC>
 hipError_t backward(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
     const int bytes = (int)sizeof(ChainLds<E, KT, NS>), wide = (s.Dv + 127) / 128, narrow = (s.Dv + 63) / 64;
     hipError_t e = hipSuccess;
     bool done = false;
     if constexpr (sizeof(E) == 2)
         if ((done = delta_wide(s)))
-            e = launch(delta_chain_kernel<E, KE, KT, 8, VEC, NS>, s.B * s.Hv * wide, bytes, st, s, A, W, 512, wide);
+            e = launch(delta_chain_kernel<E, KT, 8, VEC, NS>, s.B * s.Hv * wide, bytes, st, s, A, W, 512, wide);
     if (!done)
-        e = launch(delta_chain_kernel<E, KE, KT, 4, VEC, NS>, s.B * s.Hv * narrow, bytes, st, s, A, W, 256, narrow);
+        e = launch(delta_chain_kernel<E, KT, 4, VEC, NS>, s.B * s.Hv * narrow, bytes, st, s, A, W, 256, narrow);
     if (e != hipSuccess) return e;
-    return launch(delta_grad_kernel<E, KE, KT, VEC>, s.B * s.Hk * ((s.T + kChunk - 1) / kChunk),
-                  (int)sizeof(GradLds<E, KE, KT>), st, s, A, W, 512, 0);
+    return launch(delta_grad_kernel<E, KT, VEC>, s.B * s.Hk * ((s.T + kChunk - 1) / kChunk),
+                  (int)sizeof(GradLds<E, KT>), st, s, A, W, 512, 0);
 }
 
-template <class E, class KE, int NS, bool VEC>
+template <class E, int NS, bool VEC>
 hipError_t by_width(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    if (s.Dk <= 32) return backward<E, KE, 1, NS, VEC>(s, A, W, st);
-    if (s.Dk <= 64) return backward<E, KE, 2, NS, VEC>(s, A, W, st);
-    return backward<E, KE, 4, NS, VEC>(s, A, W, st);
+    if (s.Dk <= 32) return backward<E, 1, NS, VEC>(s, A, W, st);
+    if (s.Dk <= 64) return backward<E, 2, NS, VEC>(s, A, W, st);
+    return backward<E, 4, NS, VEC>(s, A, W, st);
 }
 
 template <bool VEC>
 hipError_t by_type(const DeltaShape& s, const DeltaBwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    if (s.dtype != kBf16) return by_width<float, float, 3, VEC>(s, A, W, st);
-    return delta_keeps_f32(s.dtype, A.s_in) ? by_width<bf16_t, float, 3, VEC>(s, A, W, st)
-                                            : by_width<bf16_t, bf16_t, 2, VEC>(s, A, W, st);
+    if (s.dtype != kBf16) return by_width<float, 3, VEC>(s, A, W, st);
+    return A.s_in ? by_width<bf16_t, 3, VEC>(s, A, W, st) : by_width<bf16_t, 2, VEC>(s, A, W, st);
 }
 
 }  // namespace

@@ -210,12 +210,12 @@ struct FwdLds {
     float eg[kChunk], ew[kChunk], be[kChunk];  // e^gam, e^{gam_63 - gam}, beta
 };
 
-// What the chain leaves: o, what the backward starts from (of type KE), or a segment's map:
+// What the chain leaves: o, what the backward starts from, or a segment's map:
 // tiles of its constant part (the walk from a zero state) and then of its matrix (the walk of
 // the identity's columns with no values).
 constexpr int kOut = 1, kKeep = 2, kMap = 4;
 
-template <class E, class KE, int KT, int NW, bool VEC, int MODE>
+template <class E, int KT, int NW, bool VEC, int MODE>
 __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_forward_kernel(DeltaShape s, DeltaFwdArgs A,
                                                                                         DeltaChunks W, int nc,
                                                                                         int ntile, int ntile_v,
@@ -300,10 +300,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
                     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-                    mma<NS, 1, kKeptSum<KE>, 1>(x, fs, identity_frag(which));
-                    store4<KE>(reinterpret_cast<KE*>(W.s0) +
-                                   ((cb * nblk + c0 / 16) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
-                               x);
+                    mma(x, fs, identity_frag(which));
+                    store4<float>(W.s0 + ((cb * nblk + c0 / 16) * (32 * KT) + 32 * kk + 16 * which + r) * 16 + 4 * g,
+                                  x);
                 }
         }
         // Z = V - e^gam K S.
@@ -491,9 +490,9 @@ hipError_t prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks
     return hipGetLastError();
 }
 
-template <class E, class KE, int KT, int NW, bool VEC, int MODE>
+template <class E, int KT, int NW, bool VEC, int MODE>
 hipError_t forward_nw(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
-    auto kernel = delta_forward_kernel<E, KE, KT, NW, VEC, MODE>;
+    auto kernel = delta_forward_kernel<E, KT, NW, VEC, MODE>;
     const int bytes = (int)sizeof(FwdLds<E, KT>);
     // More dynamic LDS than the default 64 KiB has to be asked for.
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -506,28 +505,24 @@ hipError_t forward_nw(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChu
     return hipGetLastError();
 }
 
-template <class E, class KE, int KT, bool VEC, int MODE>
+template <class E, int KT, bool VEC, int MODE>
 hipError_t forward_mode(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
     if constexpr (sizeof(E) == 2)
-        if (delta_wide(s, W.segs)) return forward_nw<E, KE, KT, 8, VEC, MODE>(s, A, W, st);
-    return forward_nw<E, KE, KT, 4, VEC, MODE>(s, A, W, st);
+        if (delta_wide(s, W.segs)) return forward_nw<E, KT, 8, VEC, MODE>(s, A, W, st);
+    return forward_nw<E, KT, 4, VEC, MODE>(s, A, W, st);
 }
 
 template <class E, int KT, bool VEC>
 hipError_t forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st) {
     if (W.segs > 1) {
-        hipError_t e = forward_mode<E, E, KT, VEC, kMap>(s, A, W, st);
+        hipError_t e = forward_mode<E, KT, VEC, kMap>(s, A, W, st);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((delta_join_kernel<KT>), dim3((unsigned)(s.B * s.Hv * ((s.Dv + 15) / 16))), dim3(128 * KT), 0,
                            st, s, A, W, (s.Dv + 15) / 16, delta_blocks(s));
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (!W.x) return forward_mode<E, E, KT, VEC, kOut>(s, A, W, st);
-    if (sizeof(E) == 4 || delta_keeps_f32(s.dtype, A.s_in))
-        return A.o ? forward_mode<E, float, KT, VEC, kOut | kKeep>(s, A, W, st)
-                   : forward_mode<E, float, KT, VEC, kKeep>(s, A, W, st);
-    return A.o ? forward_mode<E, E, KT, VEC, kOut | kKeep>(s, A, W, st)
-               : forward_mode<E, E, KT, VEC, kKeep>(s, A, W, st);
+    if (!W.x) return forward_mode<E, KT, VEC, kOut>(s, A, W, st);
+    return A.o ? forward_mode<E, KT, VEC, kOut | kKeep>(s, A, W, st) : forward_mode<E, KT, VEC, kKeep>(s, A, W, st);
 }
 
 template <class E, bool VEC>
