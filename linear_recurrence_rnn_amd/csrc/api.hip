@@ -970,7 +970,7 @@ size_t delta_layout(const linrec::DeltaShape& s, bool state, int upto, void* ws,
         w.dz = take(s.dtype == LINREC_BF16 ? (size_t)(s.B * s.T * s.Hv * s.Dv) * 2 : 0);
     }
     w.segs = linrec::delta_segments(s);
-    w.seg_len = (int)ceil_div(ceil_div(s.T, 64), w.segs);
+    w.seg_len = linrec::delta_segment_length(s, w.segs);
     const size_t heads = (size_t)(s.B * s.Hv), dkp = linrec::delta_dkp(s);
     w.map = (float*)take(heads * (w.segs - 1) * dkp * (16 * linrec::delta_blocks(s) + dkp) * sizeof(float));
     w.start = (float*)take(w.segs > 1 ? heads * w.segs * s.Dk * s.Dv * sizeof(float) : 0);

@@ -81,13 +81,17 @@ struct DeltaBwdArgs {
 
 // Segments: as many as fill the chip with workgroups, of eight chunks at least, where that
 // divides the chain by six or more (a segment is walked twice, the first time with Dk columns
-// more); else one.
+// more); else one.  Each takes delta_segment_length chunks, the last what is left, and none is empty:
+// the last one's workgroups alone write the final state.
 inline int delta_segments(const DeltaShape& s) {
     const int64_t nc = (s.T + 63) / 64, cols = s.dtype == 1 ? 128 : 64;
     int64_t n = 256 / (s.B * s.Hv * ((s.Dv + cols - 1) / cols));
     n = n < nc / 8 ? n : nc / 8;
-    return n >= 6 ? (int)n : 1;
+    if (n < 6) return 1;
+    const int64_t len = (nc + n - 1) / n;
+    return (int)((nc + len - 1) / len);
 }
+inline int delta_segment_length(const DeltaShape& s, int segs) { return (int)(((s.T + 63) / 64 + segs - 1) / segs); }
 
 hipError_t run_delta_prepare(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st);
 hipError_t run_delta_forward(const DeltaShape& s, const DeltaFwdArgs& A, const DeltaChunks& W, hipStream_t st);

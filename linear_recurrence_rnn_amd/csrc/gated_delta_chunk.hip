@@ -405,7 +405,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
                     m[row * (16 * nblk + 32 * KT) + (matrix ? 16 * nblk : 0) + c0 + r] = S[d][e];
             }
     }
-    if (!MAP && A.s_out && past == nc)
+    if (!MAP && A.s_out && seg == segs - 1)
 #pragma unroll
         for (int d = 0; d < 2 * KT; ++d)
 #pragma unroll
