@@ -166,7 +166,8 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
             for (int which = 0; which < 2; ++which) {
                 f32x4 x = {0.f, 0.f, 0.f, 0.f};
                 mma<NZ, 1, NI, 1>(x, fx, identity_frag(which));
-                store_rows<E, VEC>(out, 32 * k2 + 16 * which + r, c0 + 4 * g, Dv, x);
+                store_rows<E, VEC>(out, 32 * k2 + 16 * which + r, c0 + 4 * g, Dv,
+                                   t0 + 32 * k2 + 16 * which + r < len ? x : f32x4{0.f, 0.f, 0.f, 0.f});
                 if constexpr (NI < NZ) {  // what the rounding left
                     f32x4 y = {0.f, 0.f, 0.f, 0.f};
                     mma(y, Frag<1>{{fx.t[1]}}, identity_frag(which));
@@ -576,6 +577,7 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
         const int row = 16 * (tk0 + t) + pos.r, c = 16 * d0 + 4 * pos.g;
+        if (t0 + row >= len) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};  // absent, whatever its chunk holds
         store_rows<E, VEC>(rows_of<E>(A.gq, s, b, s.Hk, hk, Dk, t0, (int)s.T), row, c, Dk, dq[t]);
         store_rows<E, VEC>(rows_of<E>(A.gk, s, b, s.Hk, hk, Dk, t0, (int)s.T), row, c, Dk, dk[t]);
     }
