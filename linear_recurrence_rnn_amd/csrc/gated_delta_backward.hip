@@ -166,8 +166,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
             for (int which = 0; which < 2; ++which) {
                 f32x4 x = {0.f, 0.f, 0.f, 0.f};
                 mma<NZ, 1, NI, 1>(x, fx, identity_frag(which));
-                store_rows<E, VEC>(out, 32 * k2 + 16 * which + r, c0 + 4 * g, Dv,
-                                   t0 + 32 * k2 + 16 * which + r < len ? x : f32x4{0.f, 0.f, 0.f, 0.f});
+                if (t0 + kChunk > len)  // absent tokens: zero, whatever their chunk holds
+                    if (t0 + 32 * k2 + 16 * which + r >= len) x = f32x4{0.f, 0.f, 0.f, 0.f};
+                store_rows<E, VEC>(out, 32 * k2 + 16 * which + r, c0 + 4 * g, Dv, x);
                 if constexpr (NI < NZ) {  // what the rounding left
                     f32x4 y = {0.f, 0.f, 0.f, 0.f};
                     mma(y, Frag<1>{{fx.t[1]}}, identity_frag(which));
@@ -307,7 +308,7 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
     constexpr int DT = 2 * KT, TW = DT / 2;  // tiles of key channels; token tiles of a wave
     extern __shared__ __align__(16) char lds_raw[];
     Lds& L = *reinterpret_cast<Lds*>(lds_raw);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63;
     LanePos pos;
     const int d0 = wave % DT, tk0 = (wave / DT) * TW;  // this wave's key channel tile, first token tile
     const int it = wave & 3, j0 = wave >> 2;           // its tiles of H^T: columns it, rows j0, j0 + 2
@@ -362,8 +363,8 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
             sz.template load<VEC>(gz, Dv, 32 * kv0);
             if constexpr (NI < NX) sl.template load<VEC>(gl, Dv, 32 * kv0);
             sx.load(X, 2 * kv0);
-            // S and dS': half of them on their way with what goes through LDS, the others in the
-            // registers that that leaves.
+            // S and dS': the first of them on their way with what goes through LDS, the others in the
+            // registers that that leaves (more at first were spilled, which waits for every load).
             float xs[SK][8], xd[SK][8];
             const auto states = [&](int from, int to) {
 #pragma unroll
@@ -372,7 +373,7 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
                     load_block(DS, 32 * KT, 16 * d0 + r, kv0 + kv, g, xd[kv]);
                 }
             };
-            states(0, (SK + 1) / 2);
+            states(0, 1);
             __syncthreads();  // what lay here has been read
             if (hr == 0 && kv0 == 0) sk.store(L.k), sq.store(L.q);
             if (kv0 == 0 && tid < kChunk) {
@@ -385,8 +386,9 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
             sz.store(L.gz);
             if constexpr (NI < NX) sl.store(L.gz + 1);
             sx.store(L.x);
-            states((SK + 1) / 2, SK);
+            states(1, SK);
             __syncthreads();
+            pos.renew();
 #pragma unroll
             for (int kv = 0; kv < SK; ++kv) {
                 if (32 * (kv0 + kv) >= Dv) break;  // blocks past Dv may not have been written
@@ -421,6 +423,7 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
         }
         phase();
         __syncthreads();  // the slab has been read: the weights lie over it
+        pos.renew();
         const double gend = L.gam[kChunk - 1];
         // M, its sums, and the weights scale L beta H and L beta E.
         bf16x4 we[2][NH];
@@ -577,7 +580,8 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
         const int row = 16 * (tk0 + t) + pos.r, c = 16 * d0 + 4 * pos.g;
-        if (t0 + row >= len) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};  // absent, whatever its chunk holds
+        if (t0 + kChunk > len)  // absent tokens, as above
+            if (t0 + row >= len) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         store_rows<E, VEC>(rows_of<E>(A.gq, s, b, s.Hk, hk, Dk, t0, (int)s.T), row, c, Dk, dq[t]);
         store_rows<E, VEC>(rows_of<E>(A.gk, s, b, s.Hk, hk, Dk, t0, (int)s.T), row, c, Dk, dk[t]);
     }
