@@ -3,8 +3,10 @@
 //
 //   n = (x - mean) / sqrt(var + eps),  y = n w + b,  out = act(y)  or  y act(gate)
 //
-// mean and var are over the D channels of one token's group (biased variance), taken in two
-// passes over registers: no sum of squares, so a large mean costs no digits.
+// mean and var are over the D channels of one token's group (biased variance), taken in passes over
+// registers: the mean, then the mean of what it leaves (the float32 mean's own rounding, which would
+// be a common offset of every n: 1e-4 of it at a mean of 1000 times the spread), then the squares.
+// A mean that is large beside the spread so costs no digits that the inputs have.
 //
 // Backward, with dy = go act'(y) (no gate) or go act(gate):
 //   dw = sum_tokens dy n,  db = sum_tokens dy,  dgate = go y act'(gate)
@@ -107,10 +109,17 @@ __device__ __forceinline__ float normalise(float* __restrict__ x, int gl, int D,
 #pragma unroll
     for (int i = 0; i < EPL; ++i) s += x[i];
     const float mean = group_sum<LPR>(s, lds) * inv;
-    float q = 0.f;
+    s = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         x[i] = chan<LPR, VEC>(i, gl) < D ? x[i] - mean : 0.f;
+        s += x[i];
+    }
+    const float rest = group_sum<LPR>(s, lds) * inv;
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        x[i] = chan<LPR, VEC>(i, gl) < D ? x[i] - rest : 0.f;
         q = fmaf(x[i], x[i], q);
     }
     const float rstd = rsqrtf(fmaf(group_sum<LPR>(q, lds), inv, eps));
