@@ -11,6 +11,7 @@ projections and the optimizer are torch's.
 
 from __future__ import annotations
 
+import functools
 import math
 import os
 import sys
@@ -23,6 +24,19 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import linear_recurrence_rnn_amd as L  # noqa: E402
 
 
+def first_derivative(backward):
+    """Refuses a backward that is to be differentiated itself (create_graph): the calls in it leave no
+    graph, so every second derivative through them would silently be zero."""
+
+    @functools.wraps(backward)
+    def checked(ctx, *grads):
+        if torch.is_grad_enabled():
+            raise RuntimeError("this function has no second derivative")
+        return backward(ctx, *grads)
+
+    return checked
+
+
 class GatedDelta(torch.autograd.Function):
     """(o, state_out) of the gated delta rule; the backward starts from the forward's checkpoint."""
 
@@ -33,6 +47,7 @@ class GatedDelta(torch.autograd.Function):
         return o, s
 
     @staticmethod
+    @first_derivative
     def backward(ctx, go, gs):
         q, k, v, g, beta, state, lengths, ckpt = ctx.saved_tensors
         gs = None if gs is None else gs.contiguous()
@@ -50,6 +65,7 @@ class HeadNorm(torch.autograd.Function):
         return L.group_norm_act(o, heads, weight, bias, gate=gate)
 
     @staticmethod
+    @first_derivative
     def backward(ctx, gy):
         o, weight, bias, gate = ctx.saved_tensors
         gx, gw, gb, gg = L.group_norm_act_backward(o, ctx.heads, weight, bias, gy.contiguous(), gate=gate)
@@ -63,6 +79,7 @@ class TokenShift(torch.autograd.Function):
         return L.token_shift(x, mu, x_prev)
 
     @staticmethod
+    @first_derivative
     def backward(ctx, g):
         x, mu, x_prev = ctx.saved_tensors
         return L.token_shift_backward(x, mu, g.contiguous(), x_prev)[:2] + (None,)
