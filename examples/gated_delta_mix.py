@@ -183,7 +183,8 @@ def serve(mix, lengths=(70, 1, 33), more=5, seed=1):
     whole = [mix(x[b:b + 1, :n + more].contiguous())[0][0] for b, n in enumerate(lengths)]
     for i in range(more):
         at = lens.long() + i
-        y = mix.step(x[rows, at].contiguous(), x[rows, at - 1].contiguous(), state)
+        prev = x[rows, at - 1] * (at > 0)[:, None]  # an empty prompt's first token has none before it
+        y = mix.step(x[rows, at].contiguous(), prev, state)
         for b, n in enumerate(lengths):
             ref = whole[b][n + i]
             worst = max(worst, ((y[b] - ref).abs().max() / ref.square().mean().sqrt()).item())
