@@ -23,6 +23,7 @@
 namespace linrec {
 
 constexpr int kChunk = 64;  // tokens of a chunk: four D tiles
+constexpr int kEw = kChunk, kBe = 2 * kChunk;  // where these start in a chunk's DeltaChunks::dec
 
 template <int N> struct Frag { bf16x8 t[N]; };
 

@@ -32,7 +32,7 @@ struct ChainLds {
     static constexpr int NI = kTerms<E>;
     Mat<KT> k[NI], q[NI];
     Mat<2> t[NS], p[NS];  // the inverse, P
-    float eg[kChunk], ew[kChunk], be[kChunk];  // e^gam, e^{gam_63 - gam}, beta
+    float dec[3 * kChunk];  // e^gam, e^{gam_63 - gam} (from kEw), beta (from kBe)
 };
 
 template <class E, int KT, int NW, bool VEC, int NS>
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
         sq.store(L.q);
         si.store(L.t);
         sp.store(L.p);
-        if (tid < 3 * kChunk) L.eg[tid] = sd;  // eg, ew, be in a row
+        if (tid < 3 * kChunk) L.dec[tid] = sd;
         const Frag<NI> fv[2] = {to_frag<E>(so.x[0]), to_frag<E>(so.x[1])};
         __syncthreads();
         if (n > 0) fetch(n - 1);  // in flight while this chunk is computed
@@ -120,12 +120,12 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
             for (int half = 0; half < 2; ++half) {
                 d[half] = f32x4{0.f, 0.f, 0.f, 0.f};
                 mma(d[half], fv[k2], identity_frag(half));
-                U[2 * k2 + half] *= *reinterpret_cast<const f32x4*>(&L.ew[32 * k2 + 8 * g + 4 * half]);
+                U[2 * k2 + half] *= *reinterpret_cast<const f32x4*>(&L.dec[kEw + 32 * k2 + 8 * g + 4 * half]);
             }
             fo[k2] = split_tiles<NI>(d[0], d[1]);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                d[half] *= s.scale * *reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
+                d[half] *= s.scale * *reinterpret_cast<const f32x4*>(&L.dec[32 * k2 + 8 * g + 4 * half]);
             fd[k2] = split_tiles<NS>(d[0], d[1]);
         }
         phase();
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
             mma_rows<2>(U, fp, fo[0]);
         }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) U[t] *= *reinterpret_cast<const f32x4*>(&L.be[32 * (t >> 1) + 8 * g + 4 * (t & 1)]);
+        for (int t = 0; t < 4; ++t) U[t] *= *reinterpret_cast<const f32x4*>(&L.dec[kBe + 32 * (t >> 1) + 8 * g + 4 * (t & 1)]);
         phase();
         // dZ = N^T (beta dU).
         f32x4 Z[4];
@@ -178,12 +178,12 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                Z[2 * k2 + half] *= -*reinterpret_cast<const f32x4*>(&L.eg[32 * k2 + 8 * g + 4 * half]);
+                Z[2 * k2 + half] *= -*reinterpret_cast<const f32x4*>(&L.dec[32 * k2 + 8 * g + 4 * half]);
             fz[k2] = split_tiles<NS>(Z[2 * k2], Z[2 * k2 + 1]);
         }
         phase();
         // dS = e^{gam_63} dS' + scale Q^T e^gam dO - K^T e^gam dZ, four tiles at a time.
-        const float end = L.eg[kChunk - 1];
+        const float end = L.dec[kChunk - 1];
         constexpr int T = KT == 1 ? 2 : 4;
 #pragma unroll
         for (int d = 0; d < 2 * KT; d += T) {

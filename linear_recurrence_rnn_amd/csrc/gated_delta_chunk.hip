@@ -66,8 +66,8 @@ __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFw
         W.gam[blk * kChunk + lane] = c;
         float* dec = W.dec + blk * (3 * kChunk) + lane;
         dec[0] = decay_exp(c, 0.0);
-        dec[kChunk] = decay_exp(__shfl(c, 63), c);
-        dec[2 * kChunk] = bb;
+        dec[kEw] = decay_exp(__shfl(c, 63), c);
+        dec[kBe] = bb;
     }
     __syncthreads();
     // A: tiles of K K^T (rows i, columns j).
@@ -207,7 +207,7 @@ struct FwdLds {
     static constexpr int NI = kTerms<E>, NO = NI == 1 ? 2 : 3;  // terms of inputs, of the outputs' operands
     Mat<KT> k[NI], q[NI];
     Mat<2> t[3], p[NO];  // the inverse, P
-    float eg[kChunk], ew[kChunk], be[kChunk];  // e^gam, e^{gam_63 - gam}, beta
+    float dec[3 * kChunk];  // e^gam, e^{gam_63 - gam} (from kEw), beta (from kBe)
 };
 
 // What the chain leaves: o, what the backward starts from, or a segment's map:
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
         sk.store(L.k);
         if constexpr (OUT) sq.store(L.q), sp.store(L.p);
         si.store(L.t);
-        if (tid < 3 * kChunk) L.eg[tid] = sd;  // eg, ew, be in a row
+        if (tid < 3 * kChunk) L.dec[tid] = sd;
         const Frag<NI> fv[2] = {to_frag<E>(sv.x[0]), to_frag<E>(sv.x[1])};
         __syncthreads();
         if (n + 1 < nlive) fetch(n + 1);  // in flight while this chunk is computed
@@ -310,10 +310,10 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
         for (int t = 0; t < 4; ++t) {
             f32x4 v = {0.f, 0.f, 0.f, 0.f};
             mma(v, fv[t >> 1], identity_frag(t & 1));
-            const f32x4 eg = *reinterpret_cast<const f32x4*>(&L.eg[32 * (t >> 1) + 8 * g + 4 * (t & 1)]);
+            const f32x4 eg = *reinterpret_cast<const f32x4*>(&L.dec[32 * (t >> 1) + 8 * g + 4 * (t & 1)]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) Z[t][e] = fmaf(-eg[e], Z[t][e], v[e]);
-            if constexpr (OUT) O[t] *= s.scale * L.eg[16 * t + r];
+            if constexpr (OUT) O[t] *= s.scale * L.dec[16 * t + r];
         }
         phase();
         // X = inverse Z (its upper right block is zero).
@@ -349,15 +349,15 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_for
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int row = 32 * k2 + 8 * g + 4 * half;
-                U[2 * k2 + half] *= *reinterpret_cast<const f32x4*>(&L.be[row]);
-                w[half] = U[2 * k2 + half] * *reinterpret_cast<const f32x4*>(&L.ew[row]);
+                U[2 * k2 + half] *= *reinterpret_cast<const f32x4*>(&L.dec[kBe + row]);
+                w[half] = U[2 * k2 + half] * *reinterpret_cast<const f32x4*>(&L.dec[kEw + row]);
             }
             if constexpr (OUT) fu[k2] = split_tiles<NO>(U[2 * k2], U[2 * k2 + 1]);
             fw[k2] = split_tiles<NS>(w[0], w[1]);
         }
         phase();
         // S' = e^{gam_63} S + K^T w, four tiles at a time.
-        const float end = L.eg[kChunk - 1];
+        const float end = L.dec[kChunk - 1];
         constexpr int T = KT == 1 ? 2 : 4;
 #pragma unroll
         for (int d = 0; d < 2 * KT; d += T) {
