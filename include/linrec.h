@@ -536,7 +536,8 @@ int wkv4_forward_noalloc(int64_t B, int64_t T, int64_t C,
  * Long sequences are taken in chunks of 64 tokens; a value that is not finite then reaches
  * the outputs of its own chunk, earlier tokens among them.  The states are float32 throughout.
  * Any of B, T, Hk, Hv equal to 0 enqueues nothing but s_out.  LINREC_ERR_UNSUPPORTED beyond
- * B*Hv = 2^20, T = 2^30, B*Hv*T/64 = 2^26 - 1 or Hv*max(Dk, Dv) = 2^22.
+ * B*Hv = 2^20, T = 2^30, B*Hv*T/64 = 2^26 - 1 or Hv*max(Dk, Dv) = 2^22 (in the backward also
+ * B*Hk*T/64 = 2^23 - 1).
  */
 int gated_delta_forward(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, int dtype,
                         const void *q, const void *k, const void *v, const void *g, const void *beta,

@@ -905,14 +905,21 @@ int check_delta_shape(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, 
     if (__builtin_mul_overflow(B, T, &bt) || __builtin_mul_overflow(B, Hv, &bh))
         return fail(LINREC_ERR_INVALID_ARG, "B*T or B*Hv overflows int64");
     // What a grid can hold: fewer than 2^32 lanes, at most 8 column tiles of 256 lanes a head
-    // and 64 lanes a chunk.
+    // and 64 lanes a chunk (the backward's 512: check_delta_backward).
     if (bh > (1 << 20)) return fail(LINREC_ERR_UNSUPPORTED, "B*Hv=%lld is above 2^20", (long long)bh);
     if (T > (1 << 30) || bh * ceil_div(T, 64) >= (1 << 26))
         return fail(LINREC_ERR_UNSUPPORTED, "B*Hv*T/64 is above 2^26, or T above 2^30");
     // 64 tokens of a head span less than 2^31 bytes.
-    if (Hv * std::max(Dk, Dv) > (1 << 22)) return fail(LINREC_ERR_UNSUPPORTED, "Hv*max(Dk, Dv) is above 2^22");
+    if (Hv > (1 << 22) / std::max(Dk, Dv)) return fail(LINREC_ERR_UNSUPPORTED, "Hv*max(Dk, Dv) is above 2^22");
     if ((st = check_shape(bt, Hk, Dk, 4)) || (st = check_shape(bt, Hv, Dv, 4)) || (st = check_shape(bh, Dk, Dv, 4)))
         return st;
+    return LINREC_OK;
+}
+
+// The gradients take 512 lanes a chunk and key head.
+int check_delta_backward(int64_t B, int64_t T, int64_t Hk) {
+    if (B * Hk * ceil_div(T, 64) >= (1 << 23))
+        return fail(LINREC_ERR_UNSUPPORTED, "B*Hk*T/64 is above 2^23 in a backward");
     return LINREC_OK;
 }
 
@@ -994,6 +1001,7 @@ hipError_t pass_state(float* out, const float* in, int64_t n, hipStream_t st) {
 LINREC_API size_t gated_delta_workspace_size(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
                                              int dtype, int with_state, int backward) {
     if (check_delta_shape(B, T, Hk, Hv, Dk, Dv, dtype) || B == 0 || T == 0 || Hv == 0) return 0;
+    if (backward && check_delta_backward(B, T, Hk)) return 0;
     if (!backward && delta_is_short(T)) return 0;
     return delta_layout(delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, nullptr, 0.f), with_state != 0,
                         backward ? kDeltaBwd : kDeltaPrep, nullptr, nullptr);
@@ -1066,6 +1074,7 @@ LINREC_API int gated_delta_backward(int64_t B, int64_t T, int64_t Hk, int64_t Hv
                           "gated_delta_backward state");
     if ((st = check_ptrs({q, k, v, g, beta, go, gq, gk, gv, gg, gbeta}, elem_bytes(dtype)))) return st;
     if (gs_in && !s_in) return fail(LINREC_ERR_INVALID_ARG, "gs_in without s_in");
+    if ((st = check_delta_backward(B, T, Hk))) return st;
     const bool state = s_in != nullptr;
     const linrec::DeltaShape s = delta_shape(B, T, Hk, Hv, Dk, Dv, dtype, lengths, scale);
     if (ckpt && (st = check_ckpt(ckpt, ckpt_bytes, gated_delta_checkpoint_size(B, T, Hk, Hv, Dk, Dv, dtype, s_in != nullptr)))) return st;
