@@ -567,8 +567,10 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
             for (int d = 0; d < DT; ++d) as += L.a[d][lane], wr += L.wr[d][lane];
             const float bt = L.be[lane];
             const double a = as, bw = (double)bt * wr, dcr = (double)bt * cs - (double)rs;
-            const double sa = wave_cumsum(a), sw = wave_cumsum(bw + dcr);
-            const double dg = (__shfl(sa, 63) - sa + a) + (sw - bw - dcr) + (double)decay_exp(gend, 0.0) * (double)dots;
+            // Sums over the tokens before this one: not the inclusive sum less this token's part, which
+            // is far larger than they are where decays are strong.
+            const double sa = wave_cumsum(a), sw = __shfl_up(wave_cumsum(bw + dcr), 1);
+            const double dg = (__shfl(sa, 63) - sa + a) + (lane ? sw : 0.0) + (double)decay_exp(gend, 0.0) * (double)dots;
             const int t = t0 + lane;
             if (t < s.T) {
                 const int64_t at = (b * s.T + t) * s.Hv + h;
