@@ -64,8 +64,13 @@ struct DeltaChunks {
 inline int64_t delta_chunks(const DeltaShape& s) { return s.B * s.Hv * ((s.T + 63) / 64); }
 inline int delta_blocks(const DeltaShape& s) { return (s.Dv + 127) / 128 * 8; }
 // Eight waves to a workgroup (bfloat16 calls) where a head has the value channels for them and
-// the heads alone fill most of the chip; four, on twice the CUs, else.
-inline bool delta_wide(const DeltaShape& s, int segs = 1) { return s.Dv > 64 && s.B * s.Hv * segs >= 144; }
+// workgroups of four would be more than the 256 CUs; four, on twice the CUs, else.  1024 tokens,
+// four against eight: 128 heads of 128x128 107 us against 122, 136 heads 182 against 133 (training
+// step 467 against 525, 661 against 565); of 128x256 64 heads 97 against 115, 68 heads 165 against
+// 117; of 64x128 128 heads 78 against 90, 136 heads 108 against 98.
+inline bool delta_wide(const DeltaShape& s, int segs = 1) {
+    return s.Dv > 64 && s.B * s.Hv * segs * ((s.Dv + 63) / 64) > 256;
+}
 inline int delta_dkp(const DeltaShape& s) { return s.Dk <= 32 ? 32 : s.Dk <= 64 ? 64 : 128; }
 
 struct DeltaBwdArgs {
@@ -81,7 +86,9 @@ struct DeltaBwdArgs {
 
 // Segments: as many as fill the chip with workgroups, of eight chunks at least, where that
 // divides the chain by six or more (a segment is walked twice, the first time with Dk columns
-// more); else one.  Each takes delta_segment_length chunks, the last what is left, and none is empty:
+// more); else one.  One walk against segments, bfloat16 128x128: one head of 48 chunks in six 207
+// against 101 us, 42 heads of 96 in six 497 against 374.  Fewer gain less (64 heads of 96 in four
+// 550 against 528, one head of 24 in three 111 against 92) and are not taken.  Each takes delta_segment_length chunks, the last what is left, and none is empty:
 // the last one's workgroups alone write the final state.
 inline int delta_segments(const DeltaShape& s) {
     const int64_t nc = (s.T + 63) / 64, cols = s.dtype == 1 ? 128 : 64;
