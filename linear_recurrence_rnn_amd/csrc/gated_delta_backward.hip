@@ -363,8 +363,9 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
             sz.template load<VEC>(gz, Dv, 32 * kv0);
             if constexpr (NI < NX) sl.template load<VEC>(gl, Dv, 32 * kv0);
             sx.load(X, 2 * kv0);
-            // S and dS': the first of them on their way with what goes through LDS, the others in the
-            // registers that that leaves (more at first were spilled, which waits for every load).
+            // S and dS', two slabs of 32 value channels ahead: the first on its way with what goes through
+            // LDS, the second in the registers that that leaves, the others as those before are used
+            // (more at once were spilled, which waits for every load in flight).
             float xs[SK][8], xd[SK][8];
             const auto states = [&](int from, int to) {
 #pragma unroll
@@ -386,7 +387,7 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
             sz.store(L.gz);
             if constexpr (NI < NX) sl.store(L.gz + 1);
             sx.store(L.x);
-            states(1, SK);
+            states(1, SK < 2 ? SK : 2);
             __syncthreads();
             pos.renew();
 #pragma unroll
@@ -419,6 +420,7 @@ __global__ __launch_bounds__(512, 2) void delta_grad_kernel(DeltaShape s, DeltaB
                 if (tk0 == 0)  // <S, dS'>, each byte of them once
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dot = fmaf(xs[kv][i], xd[kv][i], dot);
+                if (kv + 2 < SK) states(kv + 2, kv + 3);
             }
         }
         phase();
