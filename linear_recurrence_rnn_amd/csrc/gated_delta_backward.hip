@@ -226,9 +226,9 @@ __global__ __launch_bounds__(64 * NW, (kWavesPerSimd<E, KT, NW>)) void delta_cha
 //
 // Operands are the tensors' own type (one bfloat16 term, or three); what is kept (x, S, dS'), dZ and
 // the weights L beta H and L beta E are two terms in bfloat16 calls.  At 128x128 a bfloat16 chunk reads
-// 240 KB (half of it S and dS') and writes 33 KB a head: 1035 us for 10240 (2.8 TB/s), bound by one
-// workgroup's loads, products and five barriers following each other (its LDS is over half of a
-// CU's).  With S and dS' kept in bfloat16 and dZ as rounded in dV it took 705, see DeltaChunks.
+// 240 KB (half of it S and dS') and writes 33 KB a head: 794 us for 10240 (2.9 GB by the counters, 3.6
+// TB/s), bound by one workgroup's loads, products and five barriers following each other (its LDS
+// is over half of a CU's; half of its waves' time is waiting).
 template <class E, int KT>
 struct GradLds {
     static constexpr int NI = kTerms<E>, NX = kKeptTerms<E>, NH = NX;
