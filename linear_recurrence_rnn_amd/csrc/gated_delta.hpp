@@ -89,8 +89,9 @@ struct DeltaBwdArgs {
 // divides the chain by six or more (a segment is walked twice, the first time with Dk columns
 // more); else one.  One walk against segments, bfloat16 128x128: one head of 48 chunks in six 207
 // against 101 us, 42 heads of 96 in six 497 against 374.  Fewer gain less (64 heads of 96 in four
-// 550 against 528, one head of 24 in three 111 against 92) and are not taken.  Each takes delta_segment_length chunks, the last what is left, and none is empty:
-// the last one's workgroups alone write the final state.
+// 550 against 528, one head of 24 in three 111 against 92) and are not taken.  Each segment takes
+// delta_segment_length chunks, the last what is left, and none is empty: the last one's workgroups
+// alone write the final state.
 inline int delta_segments(const DeltaShape& s) {
     const int64_t nc = (s.T + 63) / 64, cols = s.dtype == 1 ? 128 : 64;
     int64_t n = 256 / (s.B * s.Hv * ((s.Dv + cols - 1) / cols));

@@ -8,10 +8,10 @@
 // A workgroup of 256 threads owns TV = 4*LC columns of one head's state: LC lanes across the
 // columns (four each, one 16-byte load per row) and 256/LC row lanes, each holding every
 // (256/LC)-th row.  LC = 8 (128-byte pieces of rows, four workgroups a head at 128 channels)
-// measured no slower than 16 or 32 anywhere: 37.6, 38.1 and 39.2 us at 64 users x 20 heads of
-// 128x128 (4.5 TB/s), 10.5 us at one user, where the call from Python is what takes the time.
-//  Sums over rows: shuffles within the wave, then the four waves' partial
-// sums through LDS in wave order.  One token moves 8 Dk Dv bytes a head for 9 Dk Dv
+// measured no slower than 16 or 32 anywhere: 37.6, 38.1 and 39.2 us a call from Python at 64 users x
+// 20 heads of 128x128 (the kernel alone 30: 5.6 TB/s), 8.9 us at one user, half of it the call.
+// Sums over rows: shuffles within the wave, then the four waves' partial sums through LDS in wave
+// order.  One token moves 8 Dk Dv bytes a head for 9 Dk Dv
 // operations, so it is bound by memory where there are many heads and by the latency of one
 // dependent load, two barriers and the launch where there are few.
 #include "gated_delta.hpp"
