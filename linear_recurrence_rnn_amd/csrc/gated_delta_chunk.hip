@@ -19,7 +19,7 @@ namespace {
 // One wave a chunk.  K's fragments serve as both operands of K K^T (the A and B layouts of a
 // matrix and its transpose are one).  With A = G diag(beta), the inverse's diagonal 32x32 blocks
 // come by substitution, the block below them by two products.  Bound by memory where there are many
-// chunks: 10240 of 128 key channels take 140 us for 0.63 GB (4.5 TB/s).  Four waves a chunk, each with
+// chunks: 10240 of 128 key channels take 140 us for 0.67 GB (4.8 TB/s).  Four waves a chunk, each with
 // its own tokens, took 10.1 us instead of 12.4 on one chunk of 12 heads but 204 on the 10240.
 template <class E, int KT, bool VEC, int NP>
 __global__ __launch_bounds__(64) void delta_prepare_kernel(DeltaShape s, DeltaFwdArgs A, DeltaChunks W, int nc) {
