@@ -23,6 +23,12 @@
  *   gated_delta_backward
  *   group_norm_act (+ backward)   the norm of each token's channel groups, with an activation or
  *                                 a gate, that follows such a recurrence
+ *   linrec_scan_selective,        a state space scan whose decay, input and output maps depend on
+ *   _ckpt, _backward,             the token: forward, training (checkpoint and backward), one token
+ *   _decode_step
+ *   short_conv_act (+ backward,   the short causal convolution of each channel before such a scan
+ *   short_conv_decode_step)
+ *   rms_norm_add (+ backward)     the root-mean-square norm behind a residual's addition
  *   linrec_scan_mingru, _minlstm, gated variants of the real scan (minGRU, minLSTM, one decay
  *   _real_decay                   per channel) and the LRU with normalised input, and their
  *   linrec_scan_complex_normalized adjoints (*_backward)
@@ -611,6 +617,136 @@ int group_norm_act_backward(int64_t N, int64_t C, int64_t G, int dtype, const vo
                             void *stream);
 
 size_t group_norm_act_backward_workspace_size(int64_t N, int64_t C, int64_t G);
+
+/*
+ * Selective state space scan.  Per batch row, channel c and state n (of N), with the channels in G
+ * groups of C/G and g = c / (C/G):
+ *
+ *   d_t    = softplus(dt_t + dt_bias)   (softplus nonzero), or dt_t + dt_bias itself
+ *   h_t[n] = e^{d_t A[n]} h_{t-1}[n] + d_t u_t B_t[g,n]
+ *   y_t    = (sum_n C_t[g,n] h_t[n] + D u_t) * silu(z_t)
+ *
+ *   u, dt, z, y (B,T,C), Bm, Cm (B,T,G,N)  of type dtype; z may be NULL (no gate)
+ *   A (C,N) float32, finite, usually negative;  D, dt_bias (C) float32 or NULL (zero)
+ *   lengths  (B) int32 or NULL: tokens t >= lengths[b] (clamped to 0..T) of row b are absent:
+ *            they leave the state alone, y is 0 there, and nothing of them is used
+ *   s_in     (B,C,N) float32 or NULL (zero);  s_out (B,C,N) float32 or NULL: the state after the last
+ *            token (s_in with T = 0).  It may be s_in itself, here and in the decode step.
+ *
+ * G divides C; 1 <= N <= 128.  B or C equal to 0 enqueues nothing.  The states are float32
+ * throughout.  LINREC_ERR_UNSUPPORTED beyond B = 2^20, T = 2^30, C = 2^22, C*N = 2^26, B*C*N = 2^31,
+ * B*C/64 = 2^22 (every group counted in whole 64s) or B*T*C, B*T*G*N = 2^44, and in the backward
+ * beyond B*T*C/4096 = 2^23 (blocks of 64 tokens and of 64 channels of a group).
+ */
+int linrec_scan_selective(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype, const void *u,
+                          const void *dt, const float *A, const void *Bm, const void *Cm, const float *D,
+                          const void *z, const float *dt_bias, int softplus, const int32_t *lengths,
+                          const float *s_in, void *y, float *s_out, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace of linrec_scan_selective and _ckpt (backward = 0), of _backward without a
+ * checkpoint (backward = 1) and with one (backward = 2). */
+size_t linrec_scan_selective_workspace_size(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype,
+                                            int backward);
+
+/*
+ * Training.  linrec_scan_selective_ckpt is linrec_scan_selective that also keeps, in `ckpt` (of
+ * linrec_scan_selective_checkpoint_size bytes, 16-byte aligned), the state before every 16th token
+ * in float32.  The backward takes that checkpoint (of a call with the same sizes and inputs), or NULL
+ * and forms it again in its workspace.
+ *
+ *   gy      (B,T,C) upstream gradient of y; gs_out (B,C,N) float32 that of s_out, or NULL
+ *   gu, gdt, gB, gC, gz   gradients, in the shape and type of u, dt, Bm, Cm, z; zero for absent
+ *           tokens; gB and gC summed over a group's channels in a fixed order
+ *   gA (C,N), gD, gdt_bias (C) float32, summed over tokens and rows in a fixed order
+ *   gs_in   (B,C,N) float32 gradient of s_in, or NULL (as it must be without s_in); it may be gs_out
+ *   gD, gz, gdt_bias are NULL exactly when D, z, dt_bias are
+ *
+ * With B or T = 0 the sums gA, gD, gdt_bias are zero-filled and gs_in is gs_out.
+ */
+size_t linrec_scan_selective_checkpoint_size(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype);
+
+int linrec_scan_selective_ckpt(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype, const void *u,
+                               const void *dt, const float *A, const void *Bm, const void *Cm, const float *D,
+                               const void *z, const float *dt_bias, int softplus, const int32_t *lengths,
+                               const float *s_in, void *y, float *s_out, void *ckpt, size_t ckpt_bytes,
+                               void *workspace, size_t ws_bytes, void *stream);
+
+int linrec_scan_selective_backward(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype, const void *u,
+                                   const void *dt, const float *A, const void *Bm, const void *Cm, const float *D,
+                                   const void *z, const float *dt_bias, int softplus, const int32_t *lengths,
+                                   const float *s_in, const void *ckpt, size_t ckpt_bytes, const void *gy,
+                                   const float *gs_out, void *gu, void *gdt, float *gA, void *gB, void *gC,
+                                   float *gD, void *gz, float *gdt_bias, float *gs_in, void *workspace,
+                                   size_t ws_bytes, void *stream);
+
+/* One token (u, dt, z, y (B,C), Bm, Cm (B,G,N)), for decoding.  s_in may be NULL (zero); s_out may be
+ * s_in (updated in place).  No workspace. */
+int linrec_scan_selective_decode_step(int64_t B, int64_t C, int64_t G, int64_t N, int dtype, const void *u,
+                                      const void *dt, const float *A, const void *Bm, const void *Cm,
+                                      const float *D, const void *z, const float *dt_bias, int softplus,
+                                      const float *s_in, void *y, float *s_out, void *stream);
+
+/*
+ * Short causal convolution: each channel's own filter of K taps over its last K inputs, then an
+ * activation.
+ *
+ *   y_t = act(bias + sum_k weight[k] x_{t-K+1+k})
+ *
+ *   x, y (B,T,C) of type dtype;  weight (C,K), bias (C) float32 (bias may be NULL);  1 <= K <= 8
+ *   act      LINREC_ACT_NONE or LINREC_ACT_SILU
+ *   s_in     (B,K-1,C) of type dtype, the inputs before token 0 in their order, or NULL (zero)
+ *   s_out    (B,K-1,C) of type dtype or NULL: the last K-1 inputs (of s_in where there are fewer
+ *            tokens).  It may be s_in itself.
+ *   lengths  (B) int32 or NULL: tokens t >= lengths[b] (clamped to 0..T) of row b are absent: y is 0
+ *            there, and nothing of them is used
+ *
+ * No workspace.  With K = 1 the states have no elements and are ignored.  LINREC_ERR_UNSUPPORTED beyond
+ * B = 2^20, T = 2^30, C = 2^24 or about B*T*C/16 = 2^31.
+ */
+int short_conv_act(int64_t B, int64_t T, int64_t C, int64_t K, int dtype, const void *x, const float *weight,
+                   const float *bias, int act, const int32_t *lengths, const void *s_in, void *y, void *s_out,
+                   void *stream);
+
+/* One token (x, y (B,C)), for decoding: s_out (required for K > 1) may be s_in. */
+int short_conv_decode_step(int64_t B, int64_t C, int64_t K, int dtype, const void *x, const float *weight,
+                           const float *bias, int act, const void *s_in, void *y, void *s_out, void *stream);
+
+/* Its gradients for the upstream gradients gy (B,T,C) of y and gs_out (B,K-1,C) of s_out (or NULL):
+ * gx (B,T,C) of type dtype, zero for absent tokens; gweight (C,K), gbias (C) float32, summed over
+ * tokens and rows in a fixed order (gbias NULL exactly when bias is); gs_in (B,K-1,C) of type dtype
+ * or NULL (as it must be without s_in), not gs_out. */
+int short_conv_act_backward(int64_t B, int64_t T, int64_t C, int64_t K, int dtype, const void *x,
+                            const float *weight, const float *bias, int act, const int32_t *lengths,
+                            const void *s_in, const void *gy, const void *gs_out, void *gx, float *gweight,
+                            float *gbias, void *gs_in, void *workspace, size_t ws_bytes, void *stream);
+
+size_t short_conv_act_backward_workspace_size(int64_t B, int64_t T, int64_t C, int64_t K, int dtype);
+
+/*
+ * Root-mean-square norm of each token's channels behind the addition of the residual; x (N,C) has
+ * the channels last.
+ *
+ *   s = x + residual,   y = s / sqrt(mean(s^2) + eps) * weight
+ *
+ *   x, y (N,C) of type dtype; residual, sum (N,C) of type rtype (dtype, or LINREC_F32), both or neither:
+ *   sum is s, rounded to rtype, and the norm is that of s as stored there.  Without them s is x.
+ *   weight (C) float32;  eps >= 0;  C <= 8192 (else LINREC_ERR_UNSUPPORTED)
+ *   sum may be residual itself.
+ */
+int rms_norm_add(int64_t N, int64_t C, int dtype, int rtype, const void *x, const void *residual,
+                 const float *weight, float eps, void *y, void *sum, void *stream);
+
+/* Its gradients, from the sum as rms_norm_add stored it (x, and rtype = dtype, without a residual), for
+ * the upstream gradients gy (N,C) of type dtype of y and gsum (N,C) of type rtype of sum (or NULL):
+ *   gs       (N,C) of type rtype: the gradient of the residual and of x; it may be gsum
+ *   gx       (N,C) of type dtype: the same for x in its own type, or NULL (as it must be where rtype
+ *            is dtype)
+ *   gweight  (C) float32, summed over the N tokens in a fixed order (zero for N = 0). */
+int rms_norm_add_backward(int64_t N, int64_t C, int dtype, int rtype, const void *sum, const float *weight,
+                          const void *gy, const void *gsum, float eps, void *gx, void *gs, float *gweight,
+                          void *workspace, size_t ws_bytes, void *stream);
+
+size_t rms_norm_add_backward_workspace_size(int64_t N, int64_t C);
 
 #ifdef __cplusplus
 }

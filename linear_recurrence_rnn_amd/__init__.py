@@ -1,6 +1,7 @@
 """MI355X (gfx950) per-channel linear recurrences: RWKV-4 WKV forward/backward and
 real/complex diagonal scans with their adjoints, the gated delta rule (a matrix of state per head)
-and the per-token group norm that follows it, as hand-written HIP kernels behind a C ABI
+and the per-token group norm that follows it, and the parts of a selective state space layer (its scan,
+the short causal convolution, the root-mean-square norm), as hand-written HIP kernels behind a C ABI
 (``include/linrec.h``).  The Python functions here marshal torch tensors to that ABI.
 
 The binding is imported lazily so that ``linear_recurrence_rnn_amd.workloads`` (the seeded
@@ -14,7 +15,11 @@ __all__ = ["wkv4_forward", "wkv4_forward_noalloc", "wkv4_forward_ex", "wkv4_deco
            "scan_real_decay_backward", "scan_complex_normalized_backward", "workspace_size", "LinrecError",
            "gated_delta_forward", "gated_delta_forward_ckpt", "gated_delta_backward", "gated_delta_checkpoint_size",
            "gated_delta_decode_step", "gated_delta_workspace_size",
-           "group_norm_act", "group_norm_act_backward", "group_norm_act_workspace_size"]
+           "group_norm_act", "group_norm_act_backward", "group_norm_act_workspace_size",
+           "scan_selective", "scan_selective_ckpt", "scan_selective_backward", "scan_selective_decode_step",
+           "scan_selective_workspace_size", "scan_selective_checkpoint_size",
+           "short_conv_act", "short_conv_act_backward", "short_conv_decode_step", "short_conv_act_workspace_size",
+           "rms_norm_add", "rms_norm_add_backward", "rms_norm_add_workspace_size"]
 
 
 def __getattr__(name):

@@ -8,6 +8,7 @@ if the library is missing or a call fails, a ``LinrecError`` is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -120,6 +121,34 @@ def load(path: str | None = None):
         lib.group_norm_act_backward_workspace_size.argtypes = [_I64] * 3
         lib.group_norm_act_backward.restype = _INT
         lib.group_norm_act_backward.argtypes = ([_I64] * 3 + [_INT] + [_VP] * 5 + [_F, _INT] + [_VP] * 5 + [_SZ, _VP])
+        lib.linrec_scan_selective_workspace_size.restype = _SZ
+        lib.linrec_scan_selective_workspace_size.argtypes = [_I64] * 5 + [_INT, _INT]
+        lib.linrec_scan_selective_checkpoint_size.restype = _SZ
+        lib.linrec_scan_selective_checkpoint_size.argtypes = [_I64] * 5 + [_INT]
+        lib.linrec_scan_selective.restype = _INT
+        lib.linrec_scan_selective.argtypes = [_I64] * 5 + [_INT] + [_VP] * 8 + [_INT] + [_VP] * 5 + [_SZ, _VP]
+        lib.linrec_scan_selective_ckpt.restype = _INT
+        lib.linrec_scan_selective_ckpt.argtypes = ([_I64] * 5 + [_INT] + [_VP] * 8 + [_INT] + [_VP] * 5 +
+                                                   [_SZ, _VP, _SZ, _VP])
+        lib.linrec_scan_selective_backward.restype = _INT
+        lib.linrec_scan_selective_backward.argtypes = ([_I64] * 5 + [_INT] + [_VP] * 8 + [_INT] + [_VP] * 3 + [_SZ] +
+                                                       [_VP] * 12 + [_SZ, _VP])
+        lib.linrec_scan_selective_decode_step.restype = _INT
+        lib.linrec_scan_selective_decode_step.argtypes = [_I64] * 4 + [_INT] + [_VP] * 8 + [_INT] + [_VP] * 4
+        lib.short_conv_act.restype = _INT
+        lib.short_conv_act.argtypes = [_I64] * 4 + [_INT] + [_VP] * 3 + [_INT] + [_VP] * 5
+        lib.short_conv_decode_step.restype = _INT
+        lib.short_conv_decode_step.argtypes = [_I64] * 3 + [_INT] + [_VP] * 3 + [_INT] + [_VP] * 4
+        lib.short_conv_act_backward_workspace_size.restype = _SZ
+        lib.short_conv_act_backward_workspace_size.argtypes = [_I64] * 4 + [_INT]
+        lib.short_conv_act_backward.restype = _INT
+        lib.short_conv_act_backward.argtypes = ([_I64] * 4 + [_INT] + [_VP] * 3 + [_INT] + [_VP] * 9 + [_SZ, _VP])
+        lib.rms_norm_add.restype = _INT
+        lib.rms_norm_add.argtypes = [_I64] * 2 + [_INT] * 2 + [_VP] * 3 + [_F] + [_VP] * 3
+        lib.rms_norm_add_backward_workspace_size.restype = _SZ
+        lib.rms_norm_add_backward_workspace_size.argtypes = [_I64] * 2
+        lib.rms_norm_add_backward.restype = _INT
+        lib.rms_norm_add_backward.argtypes = [_I64] * 2 + [_INT] * 2 + [_VP] * 4 + [_F] + [_VP] * 4 + [_SZ, _VP]
         if path is None:
             _lib = lib
         return lib
@@ -979,3 +1008,358 @@ def group_norm_act_backward(x, groups, weight, bias, gout, gate=None, act="silu"
                                        gb.data_ptr(), _addr(gg), _addr(ws), nws, _raw_stream(dev)),
            "group_norm_act_backward")
     return gx, gw, gb, gg
+
+
+# ---- selective scan, short convolution, root-mean-square norm ----------------------------------
+# A call on tensors of a device that is not the current one makes it current while it lasts: kernels
+# are launched on the current device.
+
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on_device(call):
+    @functools.wraps(call)
+    def checked(x, *args, **kw):
+        if isinstance(x, torch.Tensor) and x.is_cuda and x.device.index != _get_device():
+            with torch.cuda.device(x.device):
+                return call(x, *args, **kw)
+        return call(x, *args, **kw)
+
+    return checked
+
+
+def _selective_shape(u, dt, A, B, C, D, z, dt_bias, lead):
+    """Type code and sizes of the selective scan's inputs (``lead`` leading axes), checked against
+    each other."""
+    code = _dtype_code(u, "u")
+    if u.dim() != lead + 1 or not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("u must have %d axes and A two" % (lead + 1))
+    if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
+        raise ValueError("B and C must have %d axes" % (lead + 2))
+    shape, ty, dev = u.shape, u.dtype, u.device
+    ch, (G, N) = shape[lead], B.shape[lead:]
+    _need(u, "u", ty, shape, dev)
+    _need(dt, "dt", ty, shape, dev)
+    _need(A, "A", torch.float32, (ch, N), dev)
+    _need(B, "B", ty, shape[:lead] + (G, N), dev)
+    _need(C, "C", ty, shape[:lead] + (G, N), dev)
+    if D is not None:
+        _need(D, "D", torch.float32, (ch,), dev)
+    if z is not None:
+        _need(z, "z", ty, shape, dev)
+    if dt_bias is not None:
+        _need(dt_bias, "dt_bias", torch.float32, (ch,), dev)
+    return code, ch, G, N, dev
+
+
+def scan_selective_workspace_size(B, T, C, G, N, dtype=torch.float32, backward=False, ckpt=True) -> int:
+    """Bytes of workspace of scan_selective and scan_selective_ckpt, or of scan_selective_backward
+    with or without a checkpoint."""
+    return int(load().linrec_scan_selective_workspace_size(B, T, C, G, N, _DTYPES[dtype],
+                                                           (2 if ckpt else 1) if backward else 0))
+
+
+def scan_selective_checkpoint_size(B, T, C, G, N, dtype=torch.float32) -> int:
+    """Bytes of what scan_selective_ckpt keeps for the backward."""
+    return int(load().linrec_scan_selective_checkpoint_size(B, T, C, G, N, _DTYPES[dtype]))
+
+
+def _selective(name, keep, u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, want_state, out, workspace):
+    lib = load()
+    code, ch, G, N, dev = _selective_shape(u, dt, A, B, C, D, z, dt_bias, 2)
+    Bn, T = u.shape[:2]
+    if state is not None:
+        _need(state, "state", torch.float32, (Bn, ch, N), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (Bn,), dev)
+    nck = lib.linrec_scan_selective_checkpoint_size(Bn, T, ch, G, N, code) if keep else 0
+    ckpt = None
+    if out is None:
+        y = torch.empty_like(u)
+        s_out = torch.empty((Bn, ch, N), dtype=torch.float32, device=dev) if want_state else None
+        if keep:
+            ckpt = torch.empty(nck, dtype=torch.uint8, device=dev)
+    else:
+        y, s_out = out[:2]
+        _need(y, "out[0]", u.dtype, u.shape, dev)
+        if s_out is not None:
+            _need(s_out, "out[1]", torch.float32, (Bn, ch, N), dev)
+        if keep:
+            ckpt = out[2]
+            _need(ckpt, "out[2]", torch.uint8, (nck,), dev)
+    nws = lib.linrec_scan_selective_workspace_size(Bn, T, ch, G, N, code, 0)
+    ws = _scratch(nws, dev, workspace)
+    args = [Bn, T, ch, G, N, code, u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _addr(D),
+            _addr(z), _addr(dt_bias), int(bool(softplus)), _addr(lengths), _addr(state), y.data_ptr(), _addr(s_out)]
+    if keep:
+        args += [ckpt.data_ptr(), nck]
+    _check(getattr(lib, name)(*args, _addr(ws), nws, _raw_stream(dev)), name)
+    return (y, s_out, ckpt) if keep else (y, s_out)
+
+
+@_on_device
+def scan_selective(u, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, state=None, lengths=None,
+                   want_state=True, out=None, workspace=None):
+    """(y, state_out) of the selective state space scan: with d = softplus(dt + dt_bias) (or dt +
+    dt_bias), h = e^(d A) h + d u B and y = (sum_n C h + D u) silu(z), per batch row and channel.
+
+    u, dt, z (B,T,C), B, C (B,T,G,N), all float32 or all bfloat16; channel c reads group
+    c // (C // G); A (C,N), D, dt_bias (C,) float32.  ``state`` (B,C,N) float32 or None (zero);
+    ``lengths`` (B,) int32 on the device: tokens at or beyond a row's length are absent (y is 0
+    there).  state_out is None unless ``want_state``; ``out`` = (y, state_out) buffers."""
+    return _selective("linrec_scan_selective", False, u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, want_state,
+                      out, workspace)
+
+
+@_on_device
+def scan_selective_ckpt(u, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, state=None, lengths=None, out=None,
+                        workspace=None):
+    """(y, state_out, ckpt): scan_selective that also keeps what scan_selective_backward starts
+    from; ``out`` = (y, state_out, ckpt) buffers."""
+    return _selective("linrec_scan_selective_ckpt", True, u, dt, A, B, C, D, z, dt_bias, softplus, state, lengths, True,
+                      out, workspace)
+
+
+@_on_device
+def scan_selective_backward(u, dt, A, B, C, gy, D=None, z=None, dt_bias=None, softplus=True, state=None, gstate=None,
+                            lengths=None, ckpt=None, out=None, workspace=None):
+    """(gu, gdt, gA, gB, gC, gD, gz, gdt_bias, gstate_in) of scan_selective for the upstream gradients
+    ``gy`` of y and ``gstate`` (or None) of the final state; the gradient of an input that is None
+    is None.  ``ckpt`` is what scan_selective_ckpt kept of the same inputs (formed again if None);
+    ``out`` gives the nine buffers."""
+    lib = load()
+    code, ch, G, N, dev = _selective_shape(u, dt, A, B, C, D, z, dt_bias, 2)
+    Bn, T = u.shape[:2]
+    ty, f32 = u.dtype, torch.float32
+    _need(gy, "gy", ty, u.shape, dev)
+    if state is not None:
+        _need(state, "state", f32, (Bn, ch, N), dev)
+    if gstate is not None:
+        _need(gstate, "gstate", f32, (Bn, ch, N), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (Bn,), dev)
+    nck = lib.linrec_scan_selective_checkpoint_size(Bn, T, ch, G, N, code)
+    if ckpt is not None:
+        _need(ckpt, "ckpt", torch.uint8, (nck,), dev)
+    ins = (u, dt, A, B, C, D, z, dt_bias, state)
+    if out is None:
+        out = tuple(None if t is None else torch.empty_like(t) for t in ins)
+    else:
+        out = tuple(out)
+        for i, (o, t) in enumerate(zip(out, ins)):
+            if (o is None) != (t is None) and i != 8:
+                raise ValueError("out[%d] must be given exactly when its input is" % i)
+            if o is not None:
+                _need(o, "out[%d]" % i, f32 if t is None else t.dtype, (Bn, ch, N) if t is None else t.shape, dev)
+    nws = lib.linrec_scan_selective_workspace_size(Bn, T, ch, G, N, code, 1 if ckpt is None else 2)
+    ws = _scratch(nws, dev, workspace)
+    _check(lib.linrec_scan_selective_backward(Bn, T, ch, G, N, code, u.data_ptr(), dt.data_ptr(), A.data_ptr(),
+                                              B.data_ptr(), C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias),
+                                              int(bool(softplus)), _addr(lengths), _addr(state), _addr(ckpt), nck,
+                                              gy.data_ptr(), _addr(gstate), *(_addr(o) for o in out), _addr(ws), nws,
+                                              _raw_stream(dev)), "linrec_scan_selective_backward")
+    return out
+
+
+@_on_device
+def scan_selective_decode_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, softplus=True, state_out=None,
+                               out=None):
+    """One token of the selective scan: u, dt, z (B,C), B, C (B,G,N), all float32 or all bfloat16;
+    ``state`` (B,C,N) float32, updated IN PLACE unless ``state_out`` is given.  Returns y (B,C)."""
+    lib = load()
+    code, ch, G, N, dev = _selective_shape(u, dt, A, B, C, D, z, dt_bias, 1)
+    Bn = u.shape[0]
+    _need(state, "state", torch.float32, (Bn, ch, N), dev)
+    if state_out is None:
+        state_out = state
+    else:
+        _need(state_out, "state_out", torch.float32, (Bn, ch, N), dev)
+    if out is None:
+        out = torch.empty_like(u)
+    else:
+        _need(out, "out", u.dtype, u.shape, dev)
+    _check(lib.linrec_scan_selective_decode_step(Bn, ch, G, N, code, u.data_ptr(), dt.data_ptr(), A.data_ptr(),
+                                                 B.data_ptr(), C.data_ptr(), _addr(D), _addr(z), _addr(dt_bias),
+                                                 int(bool(softplus)), state.data_ptr(), out.data_ptr(),
+                                                 state_out.data_ptr(), _raw_stream(dev)),
+           "linrec_scan_selective_decode_step")
+    return out
+
+
+def _conv_shape(x, weight, bias, act, lead):
+    code = _dtype_code(x, "x")
+    if x.dim() != lead + 1 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("x must have %d axes and weight two" % (lead + 1))
+    C, K, dev = x.shape[lead], weight.shape[1], x.device
+    _need(x, "x", x.dtype, x.shape, dev)
+    _need(weight, "weight", torch.float32, (C, K), dev)
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (C,), dev)
+    if act not in _ACTS:
+        raise ValueError("act must be one of %s, got %r" % (sorted(_ACTS), act))
+    return code, C, K, dev
+
+
+@_on_device
+def short_conv_act(x, weight, bias=None, act="silu", state=None, lengths=None, want_state=True, out=None):
+    """(y, state_out) of the short causal convolution: y_t = act(bias + sum_k weight[:, k]
+    x_(t-K+1+k)), x (B,T,C) float32 or bfloat16, weight (C,K), bias (C,) float32; act 'silu' or
+    'none'.  ``state`` (B,K-1,C) of x's type holds the inputs before the first token (None: zero);
+    state_out, None unless ``want_state``, the last K-1 inputs.  ``lengths`` (B,) int32 on the
+    device: tokens at or beyond a row's length are absent (y is 0 there)."""
+    lib = load()
+    code, C, K, dev = _conv_shape(x, weight, bias, act, 2)
+    B, T = x.shape[:2]
+    if state is not None:
+        _need(state, "state", x.dtype, (B, K - 1, C), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+    if out is None:
+        y = torch.empty_like(x)
+        s_out = torch.empty((B, K - 1, C), dtype=x.dtype, device=dev) if want_state else None
+    else:
+        y, s_out = out
+        _need(y, "out[0]", x.dtype, x.shape, dev)
+        if s_out is not None:
+            _need(s_out, "out[1]", x.dtype, (B, K - 1, C), dev)
+    _check(lib.short_conv_act(B, T, C, K, code, x.data_ptr(), weight.data_ptr(), _addr(bias), _ACTS[act], _addr(lengths),
+                              _addr(state), y.data_ptr(), _addr(s_out), _raw_stream(dev)), "short_conv_act")
+    return y, s_out
+
+
+@_on_device
+def short_conv_decode_step(x, weight, state, bias=None, act="silu", state_out=None, out=None):
+    """One token of the short convolution: x (B,C); ``state`` (B,K-1,C) of x's type, updated IN
+    PLACE unless ``state_out`` is given.  Returns y (B,C)."""
+    lib = load()
+    code, C, K, dev = _conv_shape(x, weight, bias, act, 1)
+    B = x.shape[0]
+    _need(state, "state", x.dtype, (B, K - 1, C), dev)
+    if state_out is None:
+        state_out = state
+    else:
+        _need(state_out, "state_out", x.dtype, (B, K - 1, C), dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", x.dtype, x.shape, dev)
+    _check(lib.short_conv_decode_step(B, C, K, code, x.data_ptr(), weight.data_ptr(), _addr(bias), _ACTS[act],
+                                      state.data_ptr(), out.data_ptr(), state_out.data_ptr(), _raw_stream(dev)),
+           "short_conv_decode_step")
+    return out
+
+
+def short_conv_act_workspace_size(B, T, C, K, dtype=torch.float32) -> int:
+    """Bytes of workspace of short_conv_act_backward."""
+    return int(load().short_conv_act_backward_workspace_size(B, T, C, K, _DTYPES[dtype]))
+
+
+@_on_device
+def short_conv_act_backward(x, weight, gy, bias=None, act="silu", state=None, gstate=None, lengths=None, out=None,
+                            workspace=None):
+    """(gx, gweight, gbias, gstate_in) of short_conv_act for the upstream gradients ``gy`` of y and
+    ``gstate`` (or None) of state_out; gbias is None without ``bias``, gstate_in without ``state``.
+    ``out`` gives the four buffers."""
+    lib = load()
+    code, C, K, dev = _conv_shape(x, weight, bias, act, 2)
+    B, T = x.shape[:2]
+    _need(gy, "gy", x.dtype, x.shape, dev)
+    for name, t in (("state", state), ("gstate", gstate)):
+        if t is not None:
+            _need(t, name, x.dtype, (B, K - 1, C), dev)
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, (B,), dev)
+    if out is None:
+        gx, gw = torch.empty_like(x), torch.empty_like(weight)
+        gb = torch.empty_like(bias) if bias is not None else None
+        gs = torch.empty_like(state) if state is not None else None
+    else:
+        gx, gw, gb, gs = out
+        _need(gx, "out[0]", x.dtype, x.shape, dev)
+        _need(gw, "out[1]", torch.float32, (C, K), dev)
+        if gb is not None:
+            _need(gb, "out[2]", torch.float32, (C,), dev)
+        if gs is not None:
+            _need(gs, "out[3]", x.dtype, (B, K - 1, C), dev)
+    nws = lib.short_conv_act_backward_workspace_size(B, T, C, K, code)
+    ws = _scratch(nws, dev, workspace)
+    _check(lib.short_conv_act_backward(B, T, C, K, code, x.data_ptr(), weight.data_ptr(), _addr(bias), _ACTS[act],
+                                       _addr(lengths), _addr(state), gy.data_ptr(), _addr(gstate), gx.data_ptr(),
+                                       gw.data_ptr(), _addr(gb), _addr(gs), _addr(ws), nws, _raw_stream(dev)),
+           "short_conv_act_backward")
+    return gx, gw, gb, gs
+
+
+def _rms_shape(x, weight, other, name):
+    """Type codes of x and of ``other`` (x's if None), tokens, channels."""
+    code = _dtype_code(x, "x" if name == "residual" else "gy")
+    if x.dim() < 1:
+        raise ValueError("x must have a channel axis")
+    shape, C, dev = x.shape, x.shape[-1], x.device
+    _need(x, "x" if name == "residual" else "gy", x.dtype, shape, dev)
+    _need(weight, "weight", torch.float32, (C,), dev)
+    rcode = code
+    if other is not None:
+        rcode = _dtype_code(other, name)
+        if rcode != code and other.dtype is not torch.float32:
+            raise TypeError("%s must be %s or float32, got %s" % (name, x.dtype, other.dtype))
+        _need(other, name, other.dtype, shape, dev)
+    N = 1
+    for n in shape[:-1]:
+        N *= n
+    return code, rcode, N, C, dev
+
+
+@_on_device
+def rms_norm_add(x, weight, residual=None, eps=1e-5, out=None):
+    """(y, s): s = x + residual in the residual's type (x itself without one) and y the
+    root-mean-square norm of s over the channels times ``weight``, in x's type.  x (..., C) float32
+    or bfloat16; residual of x's shape, its type or float32; weight (C,) float32.  ``out`` = (y, s)
+    buffers, s of which may be the residual."""
+    lib = load()
+    code, rcode, N, C, dev = _rms_shape(x, weight, residual, "residual")
+    if out is None:
+        y, s = torch.empty_like(x), torch.empty_like(residual) if residual is not None else None
+    else:
+        y, s = out
+        _need(y, "out[0]", x.dtype, x.shape, dev)
+        if residual is not None:
+            _need(s, "out[1]", residual.dtype, x.shape, dev)
+        else:
+            s = None
+    _check(lib.rms_norm_add(N, C, code, rcode, x.data_ptr(), _addr(residual), weight.data_ptr(), eps, y.data_ptr(),
+                            _addr(s), _raw_stream(dev)), "rms_norm_add")
+    return y, (x if s is None else s)
+
+
+def rms_norm_add_workspace_size(N, C) -> int:
+    """Bytes of workspace of rms_norm_add_backward over N tokens."""
+    return int(load().rms_norm_add_backward_workspace_size(N, C))
+
+
+@_on_device
+def rms_norm_add_backward(s, weight, gy, gsum=None, eps=1e-5, out=None, workspace=None):
+    """(gx, gs, gweight) of rms_norm_add, from the s it returned, for the upstream gradients ``gy``
+    of y and ``gsum`` (or None) of s: gs, in s's type, is the residual's gradient, and gx the
+    same in gy's type (gs itself where the types are one).  ``out`` gives the three buffers."""
+    lib = load()
+    code, rcode, N, C, dev = _rms_shape(gy, weight, s, "s")
+    if gsum is not None:
+        _need(gsum, "gsum", s.dtype, s.shape, dev)
+    if out is None:
+        gs, gw = torch.empty_like(s), torch.empty_like(weight)
+        gx = torch.empty_like(gy) if rcode != code else gs
+    else:
+        gx, gs, gw = out
+        _need(gs, "out[1]", s.dtype, s.shape, dev)
+        _need(gw, "out[2]", torch.float32, (C,), dev)
+        if rcode != code:
+            _need(gx, "out[0]", gy.dtype, gy.shape, dev)
+        else:
+            gx = gs
+    nws = lib.rms_norm_add_backward_workspace_size(N, C)
+    ws = _scratch(nws, dev, workspace)
+    _check(lib.rms_norm_add_backward(N, C, code, rcode, s.data_ptr(), weight.data_ptr(), gy.data_ptr(), _addr(gsum), eps,
+                                     gx.data_ptr() if rcode != code else None, gs.data_ptr(), gw.data_ptr(), _addr(ws),
+                                     nws, _raw_stream(dev)), "rms_norm_add_backward")
+    return gx, gs, gw

@@ -17,6 +17,9 @@
 #include "token_shift.hpp"
 #include "gated_delta.hpp"
 #include "group_norm.hpp"
+#include "rms_norm.hpp"
+#include "selective_scan.hpp"
+#include "short_conv.hpp"
 
 #define LINREC_API extern "C" __attribute__((visibility("default")))
 
@@ -1172,4 +1175,376 @@ LINREC_API int group_norm_act_backward(int64_t N, int64_t C, int64_t G, int dtyp
     A.gweight = gweight, A.gbias = gbias, A.part = (float*)workspace;
     A.N = N, A.C = C, A.G = (int)G, A.D = (int)(C / G), A.eps = eps, A.act = act, A.dtype = dtype;
     return hip_status(linrec::run_group_norm_backward(A, (hipStream_t)stream), "group_norm_act_backward launch");
+}
+
+namespace {
+
+// Sizes of the selective scan: what the kernels take, tensors addressable, grids of fewer than 2^32
+// lanes.
+int check_sel_shape(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype) {
+    int st = check_dtype(dtype);
+    if (st) return st;
+    if (B < 0 || T < 0 || C < 0)
+        return fail(LINREC_ERR_INVALID_ARG, "negative size: B=%lld T=%lld C=%lld", (long long)B, (long long)T,
+                    (long long)C);
+    if (N < 1 || N > linrec::kSelMaxN)
+        return fail(LINREC_ERR_INVALID_ARG, "N=%lld outside 1..%d", (long long)N, linrec::kSelMaxN);
+    if (G < 1 || C % G != 0) return fail(LINREC_ERR_INVALID_ARG, "G=%lld does not divide C=%lld", (long long)G, (long long)C);
+    if (B > (1 << 20) || T > (1 << 30)) return fail(LINREC_ERR_UNSUPPORTED, "B is above 2^20, or T above 2^30");
+    if (C > (1 << 22) || C * N > (1 << 26)) return fail(LINREC_ERR_UNSUPPORTED, "C is above 2^22, or C*N above 2^26");
+    if (C == 0) return LINREC_OK;
+    // Here B*C*N < 2^46 and B*T*C < 2^72 / 4.
+    if (B * T > ((int64_t)1 << 44) / C || B * T > ((int64_t)1 << 44) / (G * N))
+        return fail(LINREC_ERR_UNSUPPORTED, "B*T*C or B*T*G*N is above 2^44");
+    if (B * C * ((N + 3) / 4 * 4) >= ((int64_t)1 << 31) || B * G * ceil_div(C / G, 64) >= (1 << 22))
+        return fail(LINREC_ERR_UNSUPPORTED, "B*C*N is above 2^31, or B*G*C/64 above 2^22");
+    return LINREC_OK;
+}
+
+linrec::SelShape sel_shape(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype, int softplus,
+                           const int32_t* lengths) {
+    return {B, T, C, (int)G, (int)N, dtype, softplus, lengths};
+}
+
+// The backward's workgroups: one a block of 64 tokens and channels, at most 8 waves.
+int check_sel_backward(const linrec::SelShape& s) {
+    const int64_t rows = s.B * linrec::sel_blocks(s) * s.G, Cg = s.C / s.G;
+    if (rows >= (1 << 23) || rows * ceil_div(Cg, 64) >= (1 << 23) ||
+        rows * ceil_div(Cg, linrec::sel_cut(s)) * ceil_div(s.N, 16) >= (1 << 24))
+        return fail(LINREC_ERR_UNSUPPORTED, "B*T*C/4096 is above 2^23 in a backward");
+    return LINREC_OK;
+}
+
+// Scratch of the forward (bc, agg, sum) at ws; returns its size, fills W if given.
+size_t sel_forward_layout(const linrec::SelShape& s, void* ws, linrec::SelScratch* W) {
+    const linrec::SelPlan p = linrec::sel_plan(s);
+    size_t at = 0;
+    const auto take = [&](size_t floats) {
+        float* r = (float*)((char*)ws + at);
+        at += align256(floats * sizeof(float));
+        return r;
+    };
+    linrec::SelScratch w{};
+    w.bc = take(linrec::sel_bc_floats(s, p));
+    if (p.segs > 1) {
+        w.agg = take((size_t)(s.B * p.segs * s.C) * linrec::sel_n4(s) * 4);
+        w.sum = take((size_t)(s.B * p.segs * s.C));
+    }
+    if (W) *W = w;
+    return at;
+}
+
+size_t sel_keep_bytes(const linrec::SelShape& s) {
+    return align256((size_t)(s.B * linrec::sel_tiles(s) * s.C) * linrec::sel_n4(s) * 4 * sizeof(float));
+}
+
+// Scratch of the backward, behind bc.  gA's shares take the place of what enters the blocks: a lane
+// of the gradients' kernel reads the one before it writes the other.
+size_t sel_backward_layout(const linrec::SelShape& s, void* ws, linrec::SelBwdScratch* W) {
+    const linrec::SelPlan p = linrec::sel_plan(s);
+    const int64_t rows = s.B * linrec::sel_blocks(s);
+    size_t at = align256(linrec::sel_bc_floats(s, p) * sizeof(float));
+    const auto take = [&](size_t floats) {
+        float* r = (float*)((char*)ws + at);
+        at += align256(floats * sizeof(float));
+        return r;
+    };
+    linrec::SelBwdScratch w{};
+    w.carry = w.gA = take((size_t)(rows * s.C) * linrec::sel_n4(s) * 4);
+    w.sum = take((size_t)(rows * s.C));
+    w.gDb = take((size_t)(rows * 2 * s.C));
+    w.cut = linrec::sel_cut(s);
+    w.cuts = ceil_div(s.C / s.G, w.cut);
+    w.gBC = take((size_t)(w.cuts * s.B * s.T * s.G) * 2 * linrec::sel_n4(s) * 4);
+    w.q = take(s.N > 16 ? (size_t)ceil_div(s.N, 16) * (size_t)(s.B * s.T * s.C) * 3 : 0);
+    if (W) *W = w;
+    return at;
+}
+
+// Scratch of a backward that forms the kept states itself: those, and either what its forward or what
+// its own kernels need.
+size_t sel_backward_bytes(const linrec::SelShape& s, bool kept) {
+    const size_t own = sel_backward_layout(s, nullptr, nullptr);
+    if (kept) return own;
+    return sel_keep_bytes(s) + std::max(own, sel_forward_layout(s, nullptr, nullptr));
+}
+
+int check_sel_ptrs(const linrec::SelArgs& A, int64_t elem, const int32_t* lengths) {
+    int st = check_ptrs({A.u, A.dt, A.Bm, A.Cm}, elem);
+    if (st || (st = check_ptrs({A.A}, 4))) return st;
+    if (A.z && !aligned(A.z, elem)) return fail(LINREC_ERR_UNSUPPORTED, "pointer not %lld-byte aligned", (long long)elem);
+    return check_f32_ptrs({A.D, A.bias, A.s_in, A.s_out, lengths});
+}
+
+int sel_forward(const linrec::SelShape& s, const linrec::SelArgs& A, float* keep, void* workspace, hipStream_t st) {
+    linrec::SelScratch W;
+    sel_forward_layout(s, workspace, &W);
+    const linrec::SelPlan p = linrec::sel_plan(s);
+    hipError_t e = linrec::run_sel_prepare(s, A, p, W, st);
+    if (e == hipSuccess) e = linrec::run_sel_forward(s, A, p, W, keep, st);
+    return hip_status(e, "linrec_scan_selective launch");
+}
+
+}  // namespace
+
+LINREC_API size_t linrec_scan_selective_workspace_size(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype,
+                                                       int backward) {
+    if (check_sel_shape(B, T, C, G, N, dtype) || B == 0 || T == 0 || C == 0) return 0;
+    const linrec::SelShape s = sel_shape(B, T, C, G, N, dtype, 1, nullptr);
+    if (!backward) return sel_forward_layout(s, nullptr, nullptr);
+    return check_sel_backward(s) ? 0 : sel_backward_bytes(s, backward == 2);
+}
+
+LINREC_API size_t linrec_scan_selective_checkpoint_size(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N,
+                                                        int dtype) {
+    if (check_sel_shape(B, T, C, G, N, dtype) || B == 0 || T == 0 || C == 0) return 0;
+    return sel_keep_bytes(sel_shape(B, T, C, G, N, dtype, 1, nullptr));
+}
+
+LINREC_API int linrec_scan_selective(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype, const void* u,
+                                     const void* dt, const float* A, const void* Bm, const void* Cm, const float* D,
+                                     const void* z, const float* dt_bias, int softplus, const int32_t* lengths,
+                                     const float* s_in, void* y, float* s_out, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+    int st = check_sel_shape(B, T, C, G, N, dtype);
+    if (st) return st;
+    if (B == 0 || C == 0) return ok();
+    const linrec::SelArgs X{u, dt, A, Bm, Cm, D, dt_bias, z, s_in, y, s_out};
+    if (T == 0) {
+        if ((st = check_f32_ptrs({s_in, s_out}))) return st;
+        return hip_status(pass_state(s_out, s_in, B * C * N, (hipStream_t)stream), "linrec_scan_selective state");
+    }
+    if ((st = check_sel_ptrs(X, elem_bytes(dtype), lengths)) || (st = check_ptrs({y}, elem_bytes(dtype)))) return st;
+    const linrec::SelShape s = sel_shape(B, T, C, G, N, dtype, softplus != 0, lengths);
+    if ((st = check_ws(workspace, ws_bytes, sel_forward_layout(s, nullptr, nullptr)))) return st;
+    return sel_forward(s, X, nullptr, workspace, (hipStream_t)stream);
+}
+
+LINREC_API int linrec_scan_selective_ckpt(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype,
+                                          const void* u, const void* dt, const float* A, const void* Bm, const void* Cm,
+                                          const float* D, const void* z, const float* dt_bias, int softplus,
+                                          const int32_t* lengths, const float* s_in, void* y, float* s_out, void* ckpt,
+                                          size_t ckpt_bytes, void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_sel_shape(B, T, C, G, N, dtype);
+    if (st) return st;
+    if (B == 0 || C == 0) return ok();
+    const linrec::SelArgs X{u, dt, A, Bm, Cm, D, dt_bias, z, s_in, y, s_out};
+    if (T == 0) {
+        if ((st = check_f32_ptrs({s_in, s_out}))) return st;
+        return hip_status(pass_state(s_out, s_in, B * C * N, (hipStream_t)stream), "linrec_scan_selective_ckpt state");
+    }
+    if ((st = check_sel_ptrs(X, elem_bytes(dtype), lengths)) || (st = check_ptrs({y}, elem_bytes(dtype)))) return st;
+    const linrec::SelShape s = sel_shape(B, T, C, G, N, dtype, softplus != 0, lengths);
+    if ((st = check_ckpt(ckpt, ckpt_bytes, sel_keep_bytes(s))) ||
+        (st = check_ws(workspace, ws_bytes, sel_forward_layout(s, nullptr, nullptr))))
+        return st;
+    return sel_forward(s, X, (float*)ckpt, workspace, (hipStream_t)stream);
+}
+
+LINREC_API int linrec_scan_selective_backward(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype,
+                                              const void* u, const void* dt, const float* A, const void* Bm,
+                                              const void* Cm, const float* D, const void* z, const float* dt_bias,
+                                              int softplus, const int32_t* lengths, const float* s_in, const void* ckpt,
+                                              size_t ckpt_bytes, const void* gy, const float* gs_out, void* gu,
+                                              void* gdt, float* gA, void* gB, void* gC, float* gD, void* gz,
+                                              float* gdt_bias, float* gs_in, void* workspace, size_t ws_bytes,
+                                              void* stream) {
+    int st = check_sel_shape(B, T, C, G, N, dtype);
+    if (st) return st;
+    if (C == 0) return ok();
+    const hipStream_t hs = (hipStream_t)stream;
+    if ((st = check_ptrs({gA}, 4)) || (st = check_f32_ptrs({gD, gdt_bias, gs_out, gs_in}))) return st;
+    if (!D != !gD || !dt_bias != !gdt_bias || !z != !gz)
+        return fail(LINREC_ERR_INVALID_ARG, "D and gD, z and gz, dt_bias and gdt_bias must be given together");
+    if (gs_in && !s_in) return fail(LINREC_ERR_INVALID_ARG, "gs_in without s_in");
+    if (B == 0 || T == 0) {
+        hipError_t e = linrec::run_fill_zero(gA, C * N, hs);
+        if (e == hipSuccess && gD) e = linrec::run_fill_zero(gD, C, hs);
+        if (e == hipSuccess && gdt_bias) e = linrec::run_fill_zero(gdt_bias, C, hs);
+        if (e == hipSuccess) e = pass_state(gs_in, gs_out, B * C * N, hs);
+        return hip_status(e, "linrec_scan_selective_backward zero fill");
+    }
+    const int64_t elem = elem_bytes(dtype);
+    const linrec::SelArgs X{u, dt, A, Bm, Cm, D, dt_bias, z, s_in, nullptr, nullptr};
+    if ((st = check_sel_ptrs(X, elem, lengths)) || (st = check_ptrs({gy, gu, gdt, gB, gC}, elem))) return st;
+    if (gz && !aligned(gz, elem)) return fail(LINREC_ERR_UNSUPPORTED, "pointer not %lld-byte aligned", (long long)elem);
+    const linrec::SelShape s = sel_shape(B, T, C, G, N, dtype, softplus != 0, lengths);
+    if ((st = check_sel_backward(s))) return st;
+    if (ckpt && (st = check_ckpt(ckpt, ckpt_bytes, sel_keep_bytes(s)))) return st;
+    if ((st = check_ws(workspace, ws_bytes, sel_backward_bytes(s, ckpt != nullptr)))) return st;
+    const linrec::SelPlan p = linrec::sel_plan(s);
+    char* ws = (char*)workspace;
+    const float* keep = (const float*)ckpt;
+    linrec::SelScratch F{};
+    if (!ckpt) {
+        float* own = (float*)ws;
+        ws += sel_keep_bytes(s);
+        if ((st = sel_forward(s, X, own, ws, hs))) return st;
+        keep = own;
+        F.bc = (float*)ws;
+    } else {
+        F.bc = (float*)ws;
+        const hipError_t e = linrec::run_sel_prepare(s, X, p, F, hs);
+        if (e != hipSuccess) return hip_status(e, "linrec_scan_selective_backward prepare launch");
+    }
+    linrec::SelBwdScratch W;
+    sel_backward_layout(s, ws, &W);
+    const linrec::SelBwdArgs g{gy, gs_out, gu, gdt, gB, gC, gz, gA, gD, gdt_bias, gs_in};
+    return hip_status(linrec::run_sel_backward(s, X, g, p, F.bc, keep, W, hs), "linrec_scan_selective_backward launch");
+}
+
+LINREC_API int linrec_scan_selective_decode_step(int64_t B, int64_t C, int64_t G, int64_t N, int dtype, const void* u,
+                                                 const void* dt, const float* A, const void* Bm, const void* Cm,
+                                                 const float* D, const void* z, const float* dt_bias, int softplus,
+                                                 const float* s_in, void* y, float* s_out, void* stream) {
+    int st = check_sel_shape(B, 1, C, G, N, dtype);
+    if (st) return st;
+    if (B == 0 || C == 0) return ok();
+    const linrec::SelArgs X{u, dt, A, Bm, Cm, D, dt_bias, z, s_in, y, s_out};
+    if ((st = check_sel_ptrs(X, elem_bytes(dtype), nullptr)) || (st = check_ptrs({y}, elem_bytes(dtype))) ||
+        (st = check_ptrs({s_out}, 4)))
+        return st;
+    return hip_status(linrec::run_sel_step(sel_shape(B, 1, C, G, N, dtype, softplus != 0, nullptr), X, (hipStream_t)stream),
+                      "linrec_scan_selective_decode_step launch");
+}
+
+namespace {
+
+int check_conv_shape(int64_t B, int64_t T, int64_t C, int64_t K, int dtype, int act) {
+    int st = check_dtype(dtype);
+    if (st) return st;
+    if (B < 0 || T < 0 || C < 0)
+        return fail(LINREC_ERR_INVALID_ARG, "negative size: B=%lld T=%lld C=%lld", (long long)B, (long long)T,
+                    (long long)C);
+    if (K < 1 || K > linrec::kConvMaxK)
+        return fail(LINREC_ERR_INVALID_ARG, "K=%lld outside 1..%d", (long long)K, linrec::kConvMaxK);
+    if (act != LINREC_ACT_NONE && act != LINREC_ACT_SILU) return fail(LINREC_ERR_INVALID_ARG, "unknown act %d", act);
+    if (B > (1 << 20) || T > (1 << 30) || C > (1 << 24))
+        return fail(LINREC_ERR_UNSUPPORTED, "B is above 2^20, T above 2^30 or C above 2^24");
+    // Fewer than 2^32 lanes: one to 16 tokens (of a row of its own) and at least one channel.
+    if (B * (ceil_div(T, 16) + 1) >= ((int64_t)1 << 31) / (C + 256))
+        return fail(LINREC_ERR_UNSUPPORTED, "B*T*C/16 is above 2^31");
+    return LINREC_OK;
+}
+
+int check_conv_ptrs(const linrec::ConvArgs& A, int64_t elem, const int32_t* lengths) {
+    int st = check_ptrs({A.weight}, 4);
+    if (st) return st;
+    if ((A.s_in && !aligned(A.s_in, elem)) || (A.s_out && !aligned(A.s_out, elem)))
+        return fail(LINREC_ERR_UNSUPPORTED, "pointer not %lld-byte aligned", (long long)elem);
+    return check_f32_ptrs({A.bias, lengths});
+}
+
+}  // namespace
+
+LINREC_API int short_conv_act(int64_t B, int64_t T, int64_t C, int64_t K, int dtype, const void* x, const float* weight,
+                              const float* bias, int act, const int32_t* lengths, const void* s_in, void* y, void* s_out,
+                              void* stream) {
+    int st = check_conv_shape(B, T, C, K, dtype, act);
+    if (st) return st;
+    if (K == 1) s_in = nullptr, s_out = nullptr;  // a state of no inputs
+    if (B == 0 || C == 0 || (T == 0 && !s_out)) return ok();
+    const linrec::ConvArgs A{x, weight, bias, s_in, y, s_out};
+    if ((st = check_conv_ptrs(A, elem_bytes(dtype), lengths))) return st;
+    if (T > 0 && (st = check_ptrs({x, y}, elem_bytes(dtype)))) return st;
+    const linrec::ConvShape s{B, T, C, (int)K, act, dtype, lengths};
+    return hip_status(linrec::run_short_conv(s, A, (hipStream_t)stream), "short_conv_act launch");
+}
+
+LINREC_API int short_conv_decode_step(int64_t B, int64_t C, int64_t K, int dtype, const void* x, const float* weight,
+                                      const float* bias, int act, const void* s_in, void* y, void* s_out, void* stream) {
+    if (K > 1 && !s_out) return fail(LINREC_ERR_INVALID_ARG, "a required pointer is NULL");
+    return short_conv_act(B, 1, C, K, dtype, x, weight, bias, act, nullptr, s_in, y, s_out, stream);
+}
+
+LINREC_API size_t short_conv_act_backward_workspace_size(int64_t B, int64_t T, int64_t C, int64_t K, int dtype) {
+    if (check_conv_shape(B, T, C, K, dtype, 0) || B == 0 || C == 0) return 0;
+    return align256(linrec::short_conv_backward_ws_bytes(linrec::ConvShape{B, T, C, (int)K, 0, dtype, nullptr}));
+}
+
+LINREC_API int short_conv_act_backward(int64_t B, int64_t T, int64_t C, int64_t K, int dtype, const void* x,
+                                       const float* weight, const float* bias, int act, const int32_t* lengths,
+                                       const void* s_in, const void* gy, const void* gs_out, void* gx, float* gweight,
+                                       float* gbias, void* gs_in, void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_conv_shape(B, T, C, K, dtype, act);
+    if (st) return st;
+    if (C == 0) return ok();
+    const hipStream_t hs = (hipStream_t)stream;
+    if ((st = check_ptrs({gweight}, 4)) || (st = check_f32_ptrs({gbias}))) return st;
+    if (!bias != !gbias) return fail(LINREC_ERR_INVALID_ARG, "bias and gbias must be given together");
+    if (gs_in && !s_in) return fail(LINREC_ERR_INVALID_ARG, "gs_in without s_in");
+    if (gs_in && gs_in == gs_out) return fail(LINREC_ERR_INVALID_ARG, "gs_in is gs_out");
+    if (K == 1) s_in = gs_out = nullptr, gs_in = nullptr;
+    if (B == 0) {
+        hipError_t e = linrec::run_fill_zero(gweight, C * K, hs);
+        if (e == hipSuccess && gbias) e = linrec::run_fill_zero(gbias, C, hs);
+        return hip_status(e, "short_conv_act_backward zero fill");
+    }
+    const int64_t elem = elem_bytes(dtype);
+    const linrec::ConvArgs A{x, weight, bias, s_in, nullptr, nullptr};
+    if ((st = check_conv_ptrs(A, elem, lengths))) return st;
+    for (const void* p : {(const void*)gs_out, (const void*)gs_in})
+        if (p && !aligned(p, elem)) return fail(LINREC_ERR_UNSUPPORTED, "pointer not %lld-byte aligned", (long long)elem);
+    if (T > 0 && (st = check_ptrs({x, gy, gx}, elem))) return st;
+    const linrec::ConvShape s{B, T, C, (int)K, act, dtype, lengths};
+    if ((st = check_ws(workspace, ws_bytes, align256(linrec::short_conv_backward_ws_bytes(s))))) return st;
+    const linrec::ConvBwdArgs g{gy, gs_out, gx, gweight, gbias, gs_in, (float*)workspace};
+    return hip_status(linrec::run_short_conv_backward(s, A, g, hs), "short_conv_act_backward launch");
+}
+
+namespace {
+
+int check_rms(int64_t N, int64_t C, int dtype, int rtype, float eps) {
+    int st = check_dtype(dtype);
+    if (st || (st = check_dtype(rtype))) return st;
+    if (rtype != dtype && rtype != LINREC_F32)
+        return fail(LINREC_ERR_INVALID_ARG, "the sum's type must be x's or LINREC_F32");
+    if ((st = check_shape(1, N, C, 4))) return st;
+    if (C > linrec::kRmsMaxC)
+        return fail(LINREC_ERR_UNSUPPORTED, "C=%lld; at most %d", (long long)C, linrec::kRmsMaxC);
+    if (!(eps >= 0.f)) return fail(LINREC_ERR_INVALID_ARG, "eps must be >= 0");
+    return LINREC_OK;
+}
+
+}  // namespace
+
+LINREC_API int rms_norm_add(int64_t N, int64_t C, int dtype, int rtype, const void* x, const void* residual,
+                            const float* weight, float eps, void* y, void* sum, void* stream) {
+    int st = check_rms(N, C, dtype, rtype, eps);
+    if (st) return st;
+    if (!residual != !sum) return fail(LINREC_ERR_INVALID_ARG, "residual and sum must be given together");
+    if (N == 0 || C == 0) return ok();
+    if ((st = check_ptrs({x, y}, elem_bytes(dtype))) || (st = check_ptrs({weight}, 4))) return st;
+    if (residual && (st = check_ptrs({residual, sum}, elem_bytes(rtype)))) return st;
+    linrec::RmsArgs A{};
+    A.N = N, A.C = C, A.dtype = dtype, A.rtype = residual ? rtype : dtype, A.eps = eps;
+    A.x = x, A.res = residual, A.weight = weight, A.y = y, A.sum = sum;
+    return hip_status(linrec::run_rms_norm(A, (hipStream_t)stream), "rms_norm_add launch");
+}
+
+LINREC_API size_t rms_norm_add_backward_workspace_size(int64_t N, int64_t C) {
+    if (check_rms(N, C, LINREC_F32, LINREC_F32, 0.f) || N == 0 || C == 0) return 0;
+    return align256(linrec::rms_norm_backward_ws_bytes(N, C));
+}
+
+LINREC_API int rms_norm_add_backward(int64_t N, int64_t C, int dtype, int rtype, const void* sum, const float* weight,
+                                     const void* gy, const void* gsum, float eps, void* gx, void* gs, float* gweight,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+    int st = check_rms(N, C, dtype, rtype, eps);
+    if (st) return st;
+    if (C == 0) return ok();
+    if ((st = check_ptrs({gweight}, 4))) return st;
+    if (gx && rtype == dtype) return fail(LINREC_ERR_INVALID_ARG, "gx with a sum of x's type: gs is x's gradient");
+    if (N == 0) return hip_status(linrec::run_fill_zero(gweight, C, (hipStream_t)stream), "rms_norm_add_backward zero fill");
+    if ((st = check_ptrs({sum, gs}, elem_bytes(rtype))) || (st = check_ptrs({gy}, elem_bytes(dtype))) ||
+        (st = check_ptrs({weight}, 4)))
+        return st;
+    if (gx && (st = check_ptrs({gx}, elem_bytes(dtype)))) return st;
+    if (gsum && (st = check_ptrs({gsum}, elem_bytes(rtype)))) return st;
+    if ((st = check_ws(workspace, ws_bytes, rms_norm_add_backward_workspace_size(N, C)))) return st;
+    linrec::RmsArgs A{};
+    A.N = N, A.C = C, A.dtype = dtype, A.rtype = rtype, A.eps = eps;
+    A.s = sum, A.weight = weight, A.gy = gy, A.gsum = gsum, A.gx = gx, A.gs = gs, A.gweight = gweight;
+    A.part = (float*)workspace;
+    return hip_status(linrec::run_rms_norm_backward(A, (hipStream_t)stream), "rms_norm_add_backward launch");
 }

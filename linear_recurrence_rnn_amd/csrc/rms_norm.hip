@@ -1,0 +1,292 @@
+// rms_norm.hip -- the root-mean-square norm of each token's channels behind the addition of the
+// residual, and its gradients; x (N,C), the channels last.
+//
+//   s = x + r (stored in r's type),  n = s / sqrt(mean(s^2) + eps),  y = n w
+//
+// The norm is that of s as stored, so that the backward, which starts from the stored s, is
+// its gradient.  With rstd = 1/sqrt(mean(s^2) + eps) and v = gy w:
+//   gs = gsum + rstd (v - n mean(v n)),  gw = sum_tokens gy n
+// gs is the gradient of x and of r alike.
+//
+// LPR lanes hold a token's row, 8 NV channels each in registers: one pass over memory.  A wave
+// (LPR 64) or a workgroup (LPR 256) walks down the tokens with its weights, and backwards its sums
+// of gw, in registers; the walkers' sums go to the workspace and are added in walker order.
+#include "rms_norm.hpp"
+#include "elem_types.hpp"
+
+namespace linrec {
+
+namespace {
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Sum over the LPR lanes of a row, the same bits in every lane.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
+#pragma unroll
+    for (int o = 1; o < (LPR < 64 ? LPR : 64); o <<= 1) v += __shfl_xor(v, o);
+    if constexpr (LPR > 64) {
+        __syncthreads();  // the previous sum has been read
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = lds[0];
+#pragma unroll
+        for (int w = 1; w < LPR / 64; ++w) v += lds[w];
+    }
+    return v;
+}
+
+// Channels of a lane: 8 neighbouring ones from each of NV stretches of LPR * 8.
+template <int LPR>
+__device__ __forceinline__ int chan(int i, int rl) { return (i / 8) * (LPR * 8) + rl * 8 + i % 8; }
+
+// 8 NV elements of type code `type` from p, zero past C.
+template <int LPR, int NV, bool WIDE, bool NT>
+__device__ __forceinline__ void load_row(const void* p, int type, int64_t at, int rl, int C, float (&out)[8 * NV]) {
+#pragma unroll
+    for (int i = 0; i < 8 * NV; i += 8) {
+        const int c = chan<LPR>(i, rl);
+        if constexpr (WIDE) {
+            if (c < C) {
+                if (type == kBf16) {
+                    load16<bf16_t, NT>(reinterpret_cast<const bf16_t*>(p) + at + c, out + i);
+                } else {
+                    load16<float, NT>(reinterpret_cast<const float*>(p) + at + c, out + i);
+                    load16<float, NT>(reinterpret_cast<const float*>(p) + at + c + 4, out + i + 4);
+                }
+                continue;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            out[i + j] = 0.f;
+            if (!WIDE && c + j < C)
+                out[i + j] = type == kBf16 ? (float)reinterpret_cast<const bf16_t*>(p)[at + c + j]
+                                           : reinterpret_cast<const float*>(p)[at + c + j];
+        }
+    }
+}
+
+template <int LPR, int NV, bool WIDE>
+__device__ __forceinline__ void store_row(void* p, int type, int64_t at, int rl, int C, const float (&in)[8 * NV]) {
+#pragma unroll
+    for (int i = 0; i < 8 * NV; i += 8) {
+        const int c = chan<LPR>(i, rl);
+        if constexpr (WIDE) {
+            if (c >= C) continue;
+            if (type == kBf16) {
+                store16<bf16_t, true>(reinterpret_cast<bf16_t*>(p) + at + c, in + i);
+            } else {
+                store16<float, true>(reinterpret_cast<float*>(p) + at + c, in + i);
+                store16<float, true>(reinterpret_cast<float*>(p) + at + c + 4, in + i + 4);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (c + j >= C) continue;
+                if (type == kBf16) reinterpret_cast<bf16_t*>(p)[at + c + j] = (bf16_t)in[i + j];
+                else reinterpret_cast<float*>(p)[at + c + j] = in[i + j];
+            }
+        }
+    }
+}
+
+template <int LPR, int NV>
+__device__ __forceinline__ void load_weight(const float* __restrict__ p, int rl, int C, float (&out)[8 * NV]) {
+#pragma unroll
+    for (int i = 0; i < 8 * NV; ++i) {
+        const int c = chan<LPR>(i, rl);
+        out[i] = c < C ? p[c] : 0.f;
+    }
+}
+
+// Where a lane works: its place in the row, and its walker among the tokens.
+template <int LPR>
+struct Walk {
+    int rl;
+    int64_t first, step;
+    __device__ Walk() {
+        constexpr int R = 256 / LPR;  // rows of a workgroup
+        rl = (int)threadIdx.x % LPR;
+        first = (int64_t)blockIdx.x * R + threadIdx.x / LPR;
+        step = (int64_t)gridDim.x * R;
+    }
+};
+
+template <int DT, int RT, int LPR, int NV, bool WIDE, bool RES>
+__global__ __launch_bounds__(256) void rms_norm_kernel(RmsArgs A) {
+    __shared__ float lds[4];
+    const Walk<LPR> P;
+    const int C = (int)A.C;
+    const float inv = 1.f / (float)C;
+    float w[8 * NV];
+    load_weight<LPR, NV>(A.weight, P.rl, C, w);
+    for (int64_t n = P.first; n < A.N; n += P.step) {
+        float x[8 * NV], r[RES ? 8 * NV : 8];
+        load_row<LPR, NV, WIDE, true>(A.x, DT, n * A.C, P.rl, C, x);
+        if constexpr (RES) {
+            load_row<LPR, NV, WIDE, true>(A.res, RT, n * A.C, P.rl, C, r);
+#pragma unroll
+            for (int i = 0; i < 8 * NV; ++i) {
+                x[i] += r[i];
+                if constexpr (RT == kBf16) x[i] = (float)(bf16_t)x[i];
+            }
+            store_row<LPR, NV, WIDE>(A.sum, RT, n * A.C, P.rl, C, x);
+        }
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) q = fmaf(x[i], x[i], q);
+        const float rstd = rsqrtf(fmaf(row_sum<LPR>(q, lds), inv, A.eps));
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) x[i] = x[i] * rstd * w[i];
+        store_row<LPR, NV, WIDE>(A.y, DT, n * A.C, P.rl, C, x);
+    }
+}
+
+template <int DT, int RT, int LPR, int NV, bool WIDE, bool GSUM>
+__global__ __launch_bounds__(256) void rms_norm_bwd_kernel(RmsArgs A) {
+    constexpr int R = 256 / LPR;
+    __shared__ float lds[4];
+    __shared__ float acc[R > 1 ? 256 : 1];
+    const Walk<LPR> P;
+    const int C = (int)A.C;
+    const float inv = 1.f / (float)C;
+    float w[8 * NV], gw[8 * NV];
+    load_weight<LPR, NV>(A.weight, P.rl, C, w);
+#pragma unroll
+    for (int i = 0; i < 8 * NV; ++i) gw[i] = 0.f;
+    for (int64_t n = P.first; n < A.N; n += P.step) {
+        float x[8 * NV], v[8 * NV], r[GSUM ? 8 * NV : 8];
+        load_row<LPR, NV, WIDE, true>(A.s, RT, n * A.C, P.rl, C, x);
+        load_row<LPR, NV, WIDE, true>(A.gy, DT, n * A.C, P.rl, C, v);
+        if constexpr (GSUM) load_row<LPR, NV, WIDE, true>(A.gsum, RT, n * A.C, P.rl, C, r);
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) q = fmaf(x[i], x[i], q);
+        const float rstd = rsqrtf(fmaf(row_sum<LPR>(q, lds), inv, A.eps));
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) {
+            x[i] *= rstd;
+            gw[i] = fmaf(v[i], x[i], gw[i]);
+            v[i] *= w[i];
+            m = fmaf(v[i], x[i], m);
+        }
+        m = row_sum<LPR>(m, lds) * inv;
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) {
+            v[i] = rstd * fmaf(-x[i], m, v[i]);
+            if constexpr (GSUM) v[i] += r[i];
+        }
+        store_row<LPR, NV, WIDE>(A.gs, RT, n * A.C, P.rl, C, v);
+        if (DT != RT && A.gx) store_row<LPR, NV, WIDE>(A.gx, DT, n * A.C, P.rl, C, v);
+    }
+    // This workgroup's sums, the rows' walkers in order.
+    float* const part = A.part + (int64_t)blockIdx.x * A.C;
+#pragma unroll
+    for (int i = 0; i < 8 * NV; ++i) {
+        float v = gw[i];
+        const int c = chan<LPR>(i, P.rl);
+        if constexpr (R > 1) {
+            __syncthreads();
+            acc[threadIdx.x] = v;
+            __syncthreads();
+            if ((int)threadIdx.x >= LPR) continue;
+#pragma unroll
+            for (int k = 1; k < R; ++k) v += acc[k * LPR + threadIdx.x];
+        }
+        if (c < C) part[c] = v;
+    }
+}
+
+// Sum of the walkers' partial sums, 16 strips of walkers at once, then the strips in order.
+__global__ __launch_bounds__(256) void rms_norm_fold_kernel(const float* __restrict__ part, int64_t rows, int64_t C,
+                                                            float* __restrict__ gw) {
+    __shared__ float lds[16][17];
+    const int cx = threadIdx.x & 15, strip = threadIdx.x >> 4;
+    const int64_t j = (int64_t)blockIdx.x * 16 + cx;
+    float v = 0.f;
+    if (j < C)
+#pragma unroll 4
+        for (int64_t r = strip; r < rows; r += 16) v += part[r * C + j];
+    lds[strip][cx] = v;
+    __syncthreads();
+    if (strip != 0 || j >= C) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += lds[i][cx];
+    gw[j] = v;
+}
+
+struct RmsPlan {
+    int lpr, nv;
+    int64_t wg;
+};
+
+RmsPlan plan(int64_t N, int64_t C, bool backward) {
+    RmsPlan p{};
+    p.lpr = C <= 128 ? 16 : C <= 1024 ? 64 : 256;
+    p.nv = C <= 512 ? 1 : C <= 1024 ? 2 : C <= 2048 ? 1 : C <= 4096 ? 2 : 4;
+    p.wg = ceil_div(N, 256 / p.lpr);
+    // Workgroups to fill the chip; backward fewer, as the partial sums grow with them.
+    const int64_t most = backward ? 1024 : 2048;
+    if (p.wg > most) p.wg = most;
+    return p;
+}
+
+template <int DT, int RT, int LPR, int NV, bool WIDE>
+hipError_t launch(const RmsArgs& A, const RmsPlan& p, bool backward, hipStream_t st) {
+    const dim3 grid((unsigned)p.wg);
+    if (!backward) {
+        if (A.res) hipLaunchKernelGGL((rms_norm_kernel<DT, RT, LPR, NV, WIDE, true>), grid, dim3(256), 0, st, A);
+        else hipLaunchKernelGGL((rms_norm_kernel<DT, RT, LPR, NV, WIDE, false>), grid, dim3(256), 0, st, A);
+    } else {
+        if (A.gsum) hipLaunchKernelGGL((rms_norm_bwd_kernel<DT, RT, LPR, NV, WIDE, true>), grid, dim3(256), 0, st, A);
+        else hipLaunchKernelGGL((rms_norm_bwd_kernel<DT, RT, LPR, NV, WIDE, false>), grid, dim3(256), 0, st, A);
+    }
+    return hipGetLastError();
+}
+
+template <int DT, int RT, bool WIDE>
+hipError_t by_size(const RmsArgs& A, const RmsPlan& p, bool backward, hipStream_t st) {
+    if (p.lpr == 16) return launch<DT, RT, 16, 1, WIDE>(A, p, backward, st);
+    if (p.lpr == 64 && p.nv == 1) return launch<DT, RT, 64, 1, WIDE>(A, p, backward, st);
+    if (p.lpr == 64) return launch<DT, RT, 64, 2, WIDE>(A, p, backward, st);
+    if (p.nv == 1) return launch<DT, RT, 256, 1, WIDE>(A, p, backward, st);
+    if (p.nv == 2) return launch<DT, RT, 256, 2, WIDE>(A, p, backward, st);
+    return launch<DT, RT, 256, 4, WIDE>(A, p, backward, st);
+}
+
+template <int DT, int RT>
+hipError_t by_alignment(const RmsArgs& A, bool backward, hipStream_t st) {
+    // 16-byte accesses where every lane's 8 channels of every tensor start on 16 bytes.
+    const RmsPlan p = plan(A.N, A.C, backward);
+    uintptr_t all = backward ? ((uintptr_t)A.s | (uintptr_t)A.gy | (uintptr_t)A.gsum | (uintptr_t)A.gx | (uintptr_t)A.gs)
+                             : ((uintptr_t)A.x | (uintptr_t)A.res | (uintptr_t)A.y | (uintptr_t)A.sum);
+    const bool wide = A.C % 8 == 0 && all % 16 == 0;
+    return wide ? by_size<DT, RT, true>(A, p, backward, st) : by_size<DT, RT, false>(A, p, backward, st);
+}
+
+hipError_t by_type(const RmsArgs& A, bool backward, hipStream_t st) {
+    if (A.dtype == kF32) return by_alignment<kF32, kF32>(A, backward, st);
+    if (A.rtype == kF32) return by_alignment<kBf16, kF32>(A, backward, st);
+    return by_alignment<kBf16, kBf16>(A, backward, st);
+}
+
+}  // namespace
+
+hipError_t run_rms_norm(const RmsArgs& A, hipStream_t st) { return by_type(A, false, st); }
+
+size_t rms_norm_backward_ws_bytes(int64_t N, int64_t C) {
+    return (size_t)plan(N, C, true).wg * (size_t)C * sizeof(float);
+}
+
+hipError_t run_rms_norm_backward(const RmsArgs& A, hipStream_t st) {
+    const hipError_t e = by_type(A, true, st);
+    if (e != hipSuccess) return e;
+    const RmsPlan p = plan(A.N, A.C, true);
+    hipLaunchKernelGGL(rms_norm_fold_kernel, dim3((unsigned)ceil_div(A.C, 16)), dim3(256), 0, st, A.part, p.wg, A.C,
+                       A.gweight);
+    return hipGetLastError();
+}
+
+}  // namespace linrec

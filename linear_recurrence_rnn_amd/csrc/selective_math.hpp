@@ -1,0 +1,71 @@
+// selective_math.hpp -- what the kernels of the selective scan share: the step's softplus and its
+// derivative, the gate, scalar loads and the place of a lane's channel.
+#pragma once
+
+#include "selective_scan.hpp"
+#include "elem_types.hpp"
+
+namespace linrec {
+
+constexpr float kLn2 = 0.69314718055994531f;
+
+// e^x for x <= 0.  The product with log2(e) is taken to twice float32's digits: rounded once, it
+// would cost x * 2^-24 of the result, five digits' worth of a step of 1e-3.
+__device__ __forceinline__ float exp_neg(float x) {
+    x = x < -104.f ? -104.f : x;  // 0 there; a NaN stays one
+    const float p = x * kLog2e;
+    const float r = fmaf(x, 1.925963033500e-8f, fmaf(x, kLog2e, -p));
+    const float e = fast_exp2(p);
+    return fmaf(e * kLn2, r, e);
+}
+
+// softplus(x) = max(x, 0) + log(1 + e^{-|x|}).  The logarithm of w = 1 + e as rounded, and what
+// that rounding lost, e - (w - 1), which is all there is left of a small e.
+// sig: the logistic function of x, softplus's derivative.
+__device__ __forceinline__ float softplus(float x, float& sig) {
+    const float e = exp_neg(-fabsf(x));
+    const float w = 1.f + e;
+    const float r = __builtin_amdgcn_rcpf(w);
+    sig = x >= 0.f ? r : e * r;
+    return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(w), kLn2, e - (w - 1.f));
+}
+
+__device__ __forceinline__ float logistic(float t) {
+    // e^{-t} may be infinite: the reciprocal is then 0.
+    return __builtin_amdgcn_rcpf(1.f + fast_exp2(-t * kLog2e));
+}
+
+// Floats at a wave-uniform address, by scalar loads.
+template <int N> struct SelVec { typedef float type __attribute__((ext_vector_type(N))); };
+template <> struct SelVec<1> { typedef float type; };
+
+template <int N>
+__device__ __forceinline__ void load_uniform(const float* p, float* out) {
+    typedef typename SelVec<(N > 16 ? 16 : N)>::type V;
+    typedef const __attribute__((address_space(4))) V* P;
+    const P q = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(p));
+    if constexpr (N == 1) {
+        out[0] = *q;
+    } else {
+#pragma unroll
+        for (int k = 0; k < (N > 16 ? N / 16 : 1); ++k) {
+            const V v = q[k];
+#pragma unroll
+            for (int i = 0; i < (N > 16 ? 16 : N); ++i) out[k * 16 + i] = v[i];
+        }
+    }
+}
+
+// Tokens of row b that are there.
+__device__ __forceinline__ int64_t row_length(const SelShape& s, int64_t b) {
+    if (!s.lengths) return s.T;
+    const int64_t n = s.lengths[b];
+    return n < 0 ? 0 : (n < s.T ? n : s.T);
+}
+
+// Element (row, n, c) of an array of states between kernels.
+__device__ __forceinline__ int64_t state_at(const SelShape& s, int64_t row, int n, int64_t c) {
+    return ((row * ((s.N + 3) / 4) + n / 4) * s.C + c) * 4 + (n & 3);
+}
+
+}  // namespace linrec

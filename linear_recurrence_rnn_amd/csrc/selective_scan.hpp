@@ -1,0 +1,91 @@
+// selective_scan.hpp -- host-visible interface of the selective state space scan (internal).
+//
+// Per batch row b, channel c (of C, in G groups of C/G) and state n (of N), with g = c / (C/G):
+//   d_t = softplus(dt_t + bias)  (or dt_t + bias)
+//   h_t[n] = e^{d_t A[n]} h_{t-1}[n] + d_t u_t B_t[g,n]
+//   y_t = (sum_n C_t[g,n] h_t[n] + D u_t) silu(z_t)      (without z: no gate)
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace linrec {
+
+constexpr int kSelMaxN = 128;  // states of a channel: 16 a lane, 8 waves
+constexpr int kSelTile = 16;   // tokens between two kept states, and staged at once
+constexpr int kSelBlock = 64;  // tokens of a workgroup of the backward
+
+struct SelShape {
+    int64_t B, T, C;
+    int G, N;
+    int dtype;           // kF32 or kBf16: u, dt, z, B, C, y and their gradients
+    int softplus;
+    const int* lengths;  // (B) device, or null: tokens at or beyond a row's length are absent
+};
+
+struct SelArgs {
+    const void *u, *dt;        // (B,T,C)
+    const float* A;            // (C,N)
+    const void *Bm, *Cm;       // (B,T,G,N)
+    const float *D, *bias;     // (C), or null
+    const void* z;             // (B,T,C), or null
+    const float* s_in;         // (B,C,N), or null (zero)
+    void* y;                   // (B,T,C); null in a call that only keeps for the backward
+    float* s_out;              // (B,C,N), or null; may be s_in
+};
+
+struct SelBwdArgs {
+    const void* gy;            // (B,T,C)
+    const float* gs_out;       // (B,C,N), or null
+    void *gu, *gdt, *gB, *gC, *gz;  // as u, dt, Bm, Cm, z (gz null without z)
+    float *gA, *gD, *gbias;    // as A, D, bias (null where those are)
+    float* gs_in;              // (B,C,N), or null; may be gs_out
+};
+
+// States between kernels are laid out (rows, N/4 rounded up, C, 4).
+inline int sel_n4(const SelShape& s) { return (s.N + 3) / 4; }
+inline int64_t sel_tiles(const SelShape& s) { return (s.T + kSelTile - 1) / kSelTile; }
+inline int64_t sel_blocks(const SelShape& s) { return (s.T + kSelBlock - 1) / kSelBlock; }
+
+// How the forward is split: states of a lane, waves of a workgroup, segments of the rows.
+struct SelPlan {
+    int npt, waves;
+    int64_t segs, seg_tiles;  // segments, and tiles of one
+};
+SelPlan sel_plan(const SelShape& s);
+
+// Scratch of the forward: bc, and where the rows are cut into segments `agg` and `sum`.
+struct SelScratch {
+    float* bc;    // (B,T,G,waves,2,npt): B and C in float32, zero for absent tokens
+    float* agg;   // (B,segs) rows of states
+    float* sum;   // (B,segs,C) sums of d
+};
+size_t sel_bc_floats(const SelShape& s, const SelPlan& p);
+
+// Scratch of the backward.
+struct SelBwdScratch {
+    float* carry;  // (B,blocks) rows of states: the gradient that enters each block from its right
+    float* sum;    // (B,blocks,C) sums of d
+    float* gA;     // (B*blocks) rows of states
+    float* gDb;    // (B*blocks,2,C): D's gradient, bias's
+    float* gBC;    // (cuts,B,T,G,2,4*n4): B's and C's gradients by channel ranges of `cut` of a group
+    float* q;      // (tiles of 16 states,B,T,C,3) where N > 16: sums over the states of one
+    int64_t cut, cuts;
+};
+int64_t sel_cut(const SelShape& s);
+
+// keep: (B,tiles) rows of states, the state before each tile; null: not kept.
+hipError_t run_sel_prepare(const SelShape& s, const SelArgs& A, const SelPlan& p, const SelScratch& W, hipStream_t st);
+hipError_t run_sel_forward(const SelShape& s, const SelArgs& A, const SelPlan& p, const SelScratch& W, float* keep,
+                           hipStream_t st);
+hipError_t run_sel_step(const SelShape& s, const SelArgs& A, hipStream_t st);
+// v (B,blocks) rows of states holding each block's share h_k -> the state entering each, in place,
+// by s_{k+1} = e^{A sum_k} s_k + h_k from s_0 = in (zero if null), forwards, or backwards with
+// reverse; the last result goes to `out` if given.
+hipError_t run_sel_join(const SelShape& s, const float* A, float* v, const float* sum, int64_t blocks, const float* in,
+                        float* out, bool reverse, hipStream_t st);
+hipError_t run_sel_backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const SelPlan& p, const float* bc,
+                            const float* keep, const SelBwdScratch& W, hipStream_t st);
+
+}  // namespace linrec
