@@ -35,26 +35,28 @@ __device__ __forceinline__ float logistic(float t) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-t * kLog2e));
 }
 
-// Floats at a wave-uniform address, by scalar loads.
-template <int N> struct SelVec { typedef float type __attribute__((ext_vector_type(N))); };
-template <> struct SelVec<1> { typedef float type; };
+// What the states of one wave need of a few tokens: B and C by scalar loads, 32 floats, and the
+// channels' own pair of floats from LDS.  Scalar loads come back in any order, so a wait for one is a
+// wait for all of them and for LDS: both are asked for together, one group ahead of their use.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-template <int N>
-__device__ __forceinline__ void load_uniform(const float* p, float* out) {
-    typedef typename SelVec<(N > 16 ? 16 : N)>::type V;
-    typedef const __attribute__((address_space(4))) V* P;
-    const P q = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(p));
-    if constexpr (N == 1) {
-        out[0] = *q;
-    } else {
+template <int NPT>
+struct SelGroup {
+    static constexpr int kTok = 16 / NPT;             // tokens of a group
+    static constexpr int kGroups = kSelTile / kTok;   // groups of a tile
+    f32x16 bc[2];
+    f32x2 x[kTok];
+    // row: the wave's 2*NPT floats of the tile's first token, those of its other tokens behind them.
+    __device__ __forceinline__ void fetch(const float* row, const f32x2 (*din)[64], int lane, int q) {
+        typedef const __attribute__((address_space(4))) f32x16* P;
+        const P p = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + q * 32));
+        bc[0] = p[0], bc[1] = p[1];
 #pragma unroll
-        for (int k = 0; k < (N > 16 ? N / 16 : 1); ++k) {
-            const V v = q[k];
-#pragma unroll
-            for (int i = 0; i < (N > 16 ? 16 : N); ++i) out[k * 16 + i] = v[i];
-        }
+        for (int k = 0; k < kTok; ++k) x[k] = din[q * kTok + k][lane];
     }
-}
+    __device__ __forceinline__ float B(int k, int i) const { return bc[(k * 2 * NPT + i) / 16][(k * 2 * NPT + i) % 16]; }
+    __device__ __forceinline__ float C(int k, int i) const { return B(k, NPT + i); }
+};
 
 // Tokens of row b that are there.
 __device__ __forceinline__ int64_t row_length(const SelShape& s, int64_t b) {

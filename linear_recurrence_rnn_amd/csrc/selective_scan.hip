@@ -26,19 +26,23 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// B and C as float32, (B,T,G,W,2,NPT), zero beyond N and for absent tokens.
+// B and C as float32, (B,tiles,G,W,16 tokens,2,NPT), zero beyond N, for absent tokens and behind T.
 template <class E>
 __global__ __launch_bounds__(256) void sel_prepare_kernel(SelShape s, const E* __restrict__ Bm,
                                                           const E* __restrict__ Cm, float* __restrict__ bc, int npt,
-                                                          int np, int64_t total) {
+                                                          int waves, int tiles, int64_t total) {
+    const unsigned row = kSelTile * 2 * npt;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int j = (int)(i % (2 * np));
-        const int64_t tok = i / (2 * np) / s.G;  // b * T + t
-        const int w = j / (2 * npt), r = j % (2 * npt);
+        const unsigned j = (unsigned)(i % row), r = j % (2 * npt);
+        int64_t k = i / row;
+        const int w = (int)(k % waves);
+        k /= waves;
+        const int g = (int)(k % s.G);
+        k /= s.G;
+        const int64_t b = k / tiles, t = k % tiles * kSelTile + j / (2 * npt);
         const int n = w * npt + r % npt;
-        const int64_t b = tok / s.T;
         float v = 0.f;
-        if (n < s.N && tok - b * s.T < row_length(s, b)) v = (float)(r < npt ? Bm : Cm)[i / (2 * np) * s.N + n];
+        if (n < s.N && t < row_length(s, b)) v = (float)((int)r < npt ? Bm : Cm)[((b * s.T + t) * s.G + g) * s.N + n];
         bc[i] = v;
     }
 }
@@ -47,31 +51,33 @@ __global__ __launch_bounds__(256) void sel_prepare_kernel(SelShape s, const E* _
 template <class E, int W, int NPT, bool AGG>
 __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs A, const float* __restrict__ bc,
                                                              float* __restrict__ agg, float* __restrict__ sum,
-                                                             float* __restrict__ keep, int64_t segs,
-                                                             int64_t seg_tiles, int group_tiles) {
+                                                             float* __restrict__ keep, int segs, int seg_tiles,
+                                                             int group_tiles) {
     constexpr int TW = kSelTile / W;  // tokens a wave stages
-    __shared__ f32x2 din[kSelTile][64];                       // d, d u
+    __shared__ f32x2 din[kSelTile][64];                          // d, d u
     __shared__ float part[AGG ? 1 : W][AGG ? 1 : kSelTile][64];  // the waves' shares of y
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t blk = blockIdx.x;
-    const int tile = (int)(blk % (s.G * group_tiles));
-    blk /= s.G * group_tiles;
-    const int64_t seg = blk % segs, b = blk / segs;
+    const int runs = AGG ? segs - 1 : segs;  // nothing needs the last segment's share
+    unsigned blk = blockIdx.x;
+    const int tile = (int)(blk % (unsigned)(s.G * group_tiles));
+    blk /= (unsigned)(s.G * group_tiles);
+    const int seg = (int)(blk % (unsigned)runs);
+    const int64_t b = blk / (unsigned)runs;
     const int grp = tile / group_tiles, Cg = (int)(s.C / s.G);
     const int in_group = (tile % group_tiles) * 64 + lane;
     const bool live = in_group < Cg;
-    const int64_t c = (int64_t)grp * Cg + (live ? in_group : Cg - 1);
-    const int64_t t_begin = seg * seg_tiles * kSelTile;
-    const int64_t t_end = seg == segs - 1 ? s.T : t_begin + seg_tiles * kSelTile;
-    const int64_t len = row_length(s, b);
-    const bool last = seg == segs - 1;
+    const unsigned c = (unsigned)(grp * Cg + (live ? in_group : Cg - 1));
+    const int T = (int)s.T, tiles = (T + kSelTile - 1) / kSelTile;
+    const int t_begin = seg * seg_tiles * kSelTile;
+    const int t_end = seg == segs - 1 ? T : t_begin + seg_tiles * kSelTile;
+    const int len = (int)row_length(s, b);
     const int n0 = w * NPT, Np = (s.N + 3) / 4 * 4;
 
     float h[NPT], a2[NPT];
 #pragma unroll
     for (int i = 0; i < NPT; ++i) {
         const int n = n0 + i;
-        a2[i] = n < s.N ? A.A[c * s.N + n] * kLog2e : 0.f;
+        a2[i] = n < s.N ? A.A[(int64_t)c * s.N + n] * kLog2e : 0.f;
         h[i] = 0.f;
         if (!AGG && n < s.N) {
             if (segs > 1) h[i] = agg[state_at(s, b * segs + seg, n, c)];
@@ -82,65 +88,93 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
     const float Dc = A.D ? A.D[c] : 0.f;
     float total = 0.f;
 
-    for (int64_t t0 = t_begin; t0 < t_end; t0 += kSelTile) {
-        if constexpr (!AGG) {
-            if (keep && live) {
-#pragma unroll
-                for (int i = 0; i < NPT; ++i)
-                    if (n0 + i < Np)
-                        keep[state_at(s, b * ((s.T + kSelTile - 1) / kSelTile) + t0 / kSelTile, n0 + i, c)] = h[i];
-            }
-        }
-        // This wave's tokens of the tile.
-        float u[TW], z[TW];
+    // This wave's tokens of a tile, read while the tile before is worked on.  Tokens behind the row's end
+    // are read as the last one and not used.
+    E ur[TW], dr[TW], zr[TW];
+    const auto fetch = [&](int t0) {
+        const int64_t base = (b * T + t0) * s.C;
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
-            const int64_t t = t0 + w * TW + i;
-            const bool there = live && t < len && t < t_end;
-            const int64_t at = (b * s.T + t) * s.C + c;
-            u[i] = z[i] = 0.f;
-            float d = 0.f;
-            if (there) {
-                u[i] = (float)reinterpret_cast<const E*>(A.u)[at];
-                d = (float)reinterpret_cast<const E*>(A.dt)[at] + bias;
-                if (!AGG && A.z) z[i] = (float)reinterpret_cast<const E*>(A.z)[at];
-                float sig;
-                if (s.softplus) d = softplus(d, sig);
-            }
-            const f32x2 v = {d, d * u[i]};
-            din[w * TW + i][lane] = v;
+            const int last = T - 1 - t0, k = w * TW + i < last ? w * TW + i : last;
+            const unsigned off = (unsigned)(k < 0 ? 0 : k) * (unsigned)s.C + c;
+            ur[i] = (reinterpret_cast<const E*>(A.u) + base)[off];
+            dr[i] = (reinterpret_cast<const E*>(A.dt) + base)[off];
+            if (!AGG && A.z) zr[i] = (reinterpret_cast<const E*>(A.z) + base)[off];
         }
-        __syncthreads();
-        const float* row = bc + (((b * s.T + t0) * s.G + grp) * W + w) * (2 * NPT);
-        const int64_t row_step = (int64_t)s.G * W * (2 * NPT);
-        const int m = t_end - t0 < kSelTile ? (int)(t_end - t0) : kSelTile;
-        float subtotal = 0.f;
-        for (int t = 0; t < m; ++t) {
-            float v[2 * NPT];
-            load_uniform<2 * NPT>(row + t * row_step, v);
-            const f32x2 x = din[t][lane];
-            float y = 0.f;
+    };
+    fetch(t_begin);
+    for (int t0 = t_begin; t0 < t_end; t0 += kSelTile) {
+        if constexpr (!AGG) {
+            if (keep && live) {
+                const int64_t at = state_at(s, b * tiles + t0 / kSelTile, n0, c);
+                if constexpr (NPT % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < NPT; ++i) {
-                h[i] = fmaf(fast_exp2(x[0] * a2[i]), h[i], x[1] * v[i]);
-                y = fmaf(v[NPT + i], h[i], y);
+                    for (int i = 0; i < NPT; i += 4)
+                        if (n0 + i < Np) store16<float>(keep + at + i * s.C, h + i);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NPT; ++i) keep[at + i] = h[i];
+                }
             }
-            if constexpr (AGG) subtotal += x[0];
-            else part[w][t][lane] = y;
         }
-        total += subtotal;
+        float u[TW], z[TW];
+        if (t0 < len) {
+#pragma unroll
+            for (int i = 0; i < TW; ++i) {
+                const bool there = live && t0 + w * TW + i < len;
+                u[i] = there ? (float)ur[i] : 0.f;
+                float d = (float)dr[i] + bias, sig;
+                if (s.softplus) d = softplus(d, sig);
+                d = there ? d : 0.f;
+                z[i] = !AGG && A.z && there ? (float)zr[i] : 0.f;
+                const f32x2 v = {d, d * u[i]};
+                din[w * TW + i][lane] = v;
+            }
+        }
+        if (t0 + kSelTile < t_end) fetch(t0 + kSelTile);
+        __syncthreads();
+        if (t0 < len) {
+            const float* row = bc + (((b * tiles + t0 / kSelTile) * s.G + grp) * W + w) * (kSelTile * 2 * NPT);
+            float subtotal = 0.f;
+            SelGroup<NPT> grp_of[2];
+            grp_of[0].fetch(row, din, lane, 0);
+#pragma unroll
+            for (int q = 0; q < SelGroup<NPT>::kGroups; ++q) {
+                const SelGroup<NPT>& v = grp_of[q & 1];
+                if (q + 1 < SelGroup<NPT>::kGroups) grp_of[(q + 1) & 1].fetch(row, din, lane, q + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = 0; k < SelGroup<NPT>::kTok; ++k) {
+                    const f32x2 x = v.x[k];
+                    float y = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NPT; ++i) {
+                        h[i] = fmaf(fast_exp2(x[0] * a2[i]), h[i], x[1] * v.B(k, i));
+                        y = fmaf(v.C(k, i), h[i], y);
+                    }
+                    if constexpr (AGG) subtotal += x[0];
+                    else part[w][q * SelGroup<NPT>::kTok + k][lane] = y;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            total += subtotal;
+        }
         __syncthreads();
         if constexpr (!AGG) {
             if (A.y && live) {
+                E* const out = reinterpret_cast<E*>(A.y) + (b * T + t0) * s.C;
 #pragma unroll
                 for (int i = 0; i < TW; ++i) {
-                    const int64_t t = t0 + w * TW + i;
+                    const int t = t0 + w * TW + i;
                     if (t >= t_end) break;
-                    float y = Dc * u[i];
+                    float y = 0.f;
+                    if (t < len) {
+                        y = Dc * u[i];
 #pragma unroll
-                    for (int k = 0; k < W; ++k) y += part[k][w * TW + i][lane];
-                    if (A.z) y *= z[i] * logistic(z[i]);
-                    reinterpret_cast<E*>(A.y)[(b * s.T + t) * s.C + c] = (E)(t < len ? y : 0.f);
+                        for (int k = 0; k < W; ++k) y += part[k][w * TW + i][lane];
+                        if (A.z) y *= z[i] * logistic(z[i]);
+                    }
+                    out[(unsigned)(w * TW + i) * (unsigned)s.C + c] = (E)y;
                 }
             }
         }
@@ -151,7 +185,7 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
         for (int i = 0; i < NPT; ++i)
             if (n0 + i < Np) agg[state_at(s, b * segs + seg, n0 + i, c)] = h[i];
         if (w == 0) sum[(b * segs + seg) * s.C + c] = total;
-    } else if (last && A.s_out) {
+    } else if (seg == segs - 1 && A.s_out) {
 #pragma unroll
         for (int i = 0; i < NPT; ++i)
             if (n0 + i < s.N) A.s_out[(b * s.C + c) * s.N + n0 + i] = h[i];
@@ -174,6 +208,10 @@ __global__ __launch_bounds__(256) void sel_join_kernel(SelShape s, const float* 
     float x = in && n < s.N ? in[at] : 0.f;
     for (int64_t i = 0; i < blocks; ++i) {
         const int64_t k = b * blocks + (REV ? blocks - 1 - i : i);
+        if (!REV && i == blocks - 1) {  // what leaves the last one is not asked for, and was not formed
+            v[k * per + e] = x;
+            break;
+        }
         const float own = v[k * per + e];
         v[k * per + e] = x;
         x = fmaf(fast_exp2(a2 * sum[k * s.C + c]), x, own);
@@ -242,16 +280,17 @@ template <class E, int W, int NPT>
 hipError_t forward(const SelShape& s, const SelArgs& A, const SelPlan& p, const SelScratch& S, float* keep,
                    hipStream_t st) {
     const int group_tiles = (int)ceil_div(s.C / s.G, 64);
-    const dim3 grid((unsigned)(s.B * p.segs * s.G * group_tiles));
-    if (p.segs > 1) {
-        hipLaunchKernelGGL((sel_forward_kernel<E, W, NPT, true>), grid, dim3(64 * W), 0, st, s, A, S.bc, S.agg, S.sum,
-                           (float*)nullptr, p.segs, p.seg_tiles, group_tiles);
+    const int64_t wg = s.B * s.G * group_tiles;
+    const int segs = (int)p.segs, seg_tiles = (int)p.seg_tiles;
+    if (segs > 1) {
+        hipLaunchKernelGGL((sel_forward_kernel<E, W, NPT, true>), dim3((unsigned)(wg * (segs - 1))), dim3(64 * W), 0, st,
+                           s, A, S.bc, S.agg, S.sum, (float*)nullptr, segs, seg_tiles, group_tiles);
         hipError_t e = hipGetLastError();
         if (e == hipSuccess) e = run_sel_join(s, A.A, S.agg, S.sum, p.segs, A.s_in, nullptr, false, st);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((sel_forward_kernel<E, W, NPT, false>), grid, dim3(64 * W), 0, st, s, A, S.bc, S.agg, S.sum,
-                       keep, p.segs, p.seg_tiles, group_tiles);
+    hipLaunchKernelGGL((sel_forward_kernel<E, W, NPT, false>), dim3((unsigned)(wg * segs)), dim3(64 * W), 0, st, s, A,
+                       S.bc, S.agg, S.sum, keep, segs, seg_tiles, group_tiles);
     return hipGetLastError();
 }
 
@@ -286,20 +325,20 @@ SelPlan sel_plan(const SelShape& s) {
 }
 
 size_t sel_bc_floats(const SelShape& s, const SelPlan& p) {
-    return (size_t)(s.B * s.T * s.G) * 2 * (size_t)(p.npt * p.waves);
+    return (size_t)(s.B * sel_tiles(s) * kSelTile * s.G) * 2 * (size_t)(p.npt * p.waves);
 }
 
 hipError_t run_sel_prepare(const SelShape& s, const SelArgs& A, const SelPlan& p, const SelScratch& W, hipStream_t st) {
     const int64_t total = (int64_t)sel_bc_floats(s, p);
     int64_t blocks = ceil_div(total, 256);
     if (blocks > 4096) blocks = 4096;
-    const int np = p.npt * p.waves;
+    const int tiles = (int)sel_tiles(s);
     if (s.dtype == kBf16)
         hipLaunchKernelGGL((sel_prepare_kernel<bf16_t>), dim3((unsigned)blocks), dim3(256), 0, st, s,
-                           (const bf16_t*)A.Bm, (const bf16_t*)A.Cm, W.bc, p.npt, np, total);
+                           (const bf16_t*)A.Bm, (const bf16_t*)A.Cm, W.bc, p.npt, p.waves, tiles, total);
     else
         hipLaunchKernelGGL((sel_prepare_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, st, s,
-                           (const float*)A.Bm, (const float*)A.Cm, W.bc, p.npt, np, total);
+                           (const float*)A.Bm, (const float*)A.Cm, W.bc, p.npt, p.waves, tiles, total);
     return hipGetLastError();
 }
 

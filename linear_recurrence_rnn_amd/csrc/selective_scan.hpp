@@ -57,7 +57,7 @@ SelPlan sel_plan(const SelShape& s);
 
 // Scratch of the forward: bc, and where the rows are cut into segments `agg` and `sum`.
 struct SelScratch {
-    float* bc;    // (B,T,G,waves,2,npt): B and C in float32, zero for absent tokens
+    float* bc;    // (B,tiles,G,waves,16,2,npt): B and C in float32, zero for absent tokens and behind T
     float* agg;   // (B,segs) rows of states
     float* sum;   // (B,segs,C) sums of d
 };

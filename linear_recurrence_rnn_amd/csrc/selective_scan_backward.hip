@@ -31,66 +31,86 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The G that leaves each block on its left, from zero, and the sum of its steps.
 template <class E, int W, int NPT>
-__global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs A, const void* __restrict__ gy,
+__global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs A, const E* __restrict__ gy,
                                                              const float* __restrict__ bc, float* __restrict__ out,
-                                                             float* __restrict__ sum, int64_t blocks,
-                                                             int group_tiles) {
+                                                             float* __restrict__ sum, int blocks, int group_tiles) {
     constexpr int TW = kSelTile / W;
     __shared__ f32x2 din[kSelTile][64];  // d, p
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int64_t blk = blockIdx.x;
-    const int tile = (int)(blk % (s.G * group_tiles));
-    blk /= s.G * group_tiles;
-    const int64_t k = blk % blocks, b = blk / blocks;
+    unsigned blk = blockIdx.x;
+    const int tile = (int)(blk % (unsigned)(s.G * group_tiles));
+    blk /= (unsigned)(s.G * group_tiles);
+    const int k = (int)(blk % (unsigned)blocks);
+    const int64_t b = blk / (unsigned)blocks;
     const int grp = tile / group_tiles, Cg = (int)(s.C / s.G);
     const int in_group = (tile % group_tiles) * 64 + lane;
     const bool live = in_group < Cg;
-    const int64_t c = (int64_t)grp * Cg + (live ? in_group : Cg - 1);
-    const int64_t t_begin = k * kSelBlock, len = row_length(s, b);
+    const unsigned c = (unsigned)(grp * Cg + (live ? in_group : Cg - 1));
+    const int T = (int)s.T, tiles = (T + kSelTile - 1) / kSelTile;
+    const int t_begin = k * kSelBlock, len = (int)row_length(s, b);
     const int n0 = w * NPT, Np = (s.N + 3) / 4 * 4;
     float g[NPT], a2[NPT];
 #pragma unroll
     for (int i = 0; i < NPT; ++i) {
         g[i] = 0.f;
-        a2[i] = n0 + i < s.N ? A.A[c * s.N + n0 + i] * kLog2e : 0.f;
+        a2[i] = n0 + i < s.N ? A.A[(int64_t)c * s.N + n0 + i] * kLog2e : 0.f;
     }
     const float bias = A.bias ? A.bias[c] : 0.f;
     float total = 0.f;
-    for (int q = kSelBlock / kSelTile - 1; q >= 0; --q) {
-        const int64_t t0 = t_begin + q * kSelTile;
-        if (t0 >= s.T) continue;
-        __syncthreads();
+    // This wave's tokens of a tile, read while the tile behind it is worked on.  Tokens behind the
+    // row's end are read as the last one and not used.
+    E dr[TW], zr[TW], gr[TW];
+    const auto fetch = [&](int t0) {
+        const int64_t base = (b * T + t0) * s.C;
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
-            const int64_t t = t0 + w * TW + i;
-            f32x2 v = {0.f, 0.f};
-            if (live && t < len) {
-                const int64_t at = (b * s.T + t) * s.C + c;
-                float sig;
-                v[0] = (float)reinterpret_cast<const E*>(A.dt)[at] + bias;
-                if (s.softplus) v[0] = softplus(v[0], sig);
-                v[1] = (float)reinterpret_cast<const E*>(gy)[at];
-                if (A.z) {
-                    const float z = (float)reinterpret_cast<const E*>(A.z)[at];
-                    v[1] *= z * logistic(z);
-                }
+            const int last = T - 1 - t0, j = w * TW + i < last ? w * TW + i : last;
+            const unsigned off = (unsigned)j * (unsigned)s.C + c;
+            dr[i] = (reinterpret_cast<const E*>(A.dt) + base)[off];
+            gr[i] = (gy + base)[off];
+            if (A.z) zr[i] = (reinterpret_cast<const E*>(A.z) + base)[off];
+        }
+    };
+    // Tiles of absent tokens alone change nothing.
+    const int end = t_begin + kSelBlock < len ? t_begin + kSelBlock : len;
+    int t0 = end > t_begin ? (end - 1) / kSelTile * kSelTile : -1;
+    if (t0 >= 0) fetch(t0);
+    for (; t0 >= t_begin; t0 -= kSelTile) {
+#pragma unroll
+        for (int i = 0; i < TW; ++i) {
+            const bool there = live && t0 + w * TW + i < len;
+            float d = (float)dr[i] + bias, sig, p = there ? (float)gr[i] : 0.f;
+            if (s.softplus) d = softplus(d, sig);
+            if (A.z) {
+                const float z = there ? (float)zr[i] : 0.f;
+                p *= z * logistic(z);
             }
+            const f32x2 v = {there ? d : 0.f, p};
             din[w * TW + i][lane] = v;
         }
+        if (t0 > t_begin) fetch(t0 - kSelTile);
         __syncthreads();
-        const float* row = bc + (((b * s.T + t0) * s.G + grp) * W + w) * (2 * NPT) + NPT;
-        const int64_t row_step = (int64_t)s.G * W * (2 * NPT);
-        const int m = s.T - t0 < kSelTile ? (int)(s.T - t0) : kSelTile;
+        const float* row = bc + (((b * tiles + t0 / kSelTile) * s.G + grp) * W + w) * (kSelTile * 2 * NPT);
+        constexpr int kGroups = SelGroup<NPT>::kGroups, kTok = SelGroup<NPT>::kTok;
         float subtotal = 0.f;
-        for (int t = m - 1; t >= 0; --t) {
-            float v[NPT];
-            load_uniform<NPT>(row + t * row_step, v);
-            const f32x2 x = din[t][lane];
+        SelGroup<NPT> grp_of[2];
+        grp_of[0].fetch(row, din, lane, kGroups - 1);
 #pragma unroll
-            for (int i = 0; i < NPT; ++i) g[i] = fast_exp2(x[0] * a2[i]) * fmaf(v[i], x[1], g[i]);
-            subtotal += x[0];
+        for (int q = 0; q < kGroups; ++q) {
+            const SelGroup<NPT>& v = grp_of[q & 1];
+            if (q + 1 < kGroups) grp_of[(q + 1) & 1].fetch(row, din, lane, kGroups - 2 - q);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = kTok - 1; k >= 0; --k) {
+                const f32x2 x = v.x[k];
+#pragma unroll
+                for (int i = 0; i < NPT; ++i) g[i] = fast_exp2(x[0] * a2[i]) * fmaf(v.C(k, i), x[1], g[i]);
+                subtotal += x[0];
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         total += subtotal;
+        __syncthreads();
     }
     if (!live) return;
 #pragma unroll
@@ -220,7 +240,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void sel_gradient_kernel(SelShape 
                 const int n = n0 + i;
                 a2[i] = n < s.N ? A.A[c * s.N + n] * kLog2e : 0.f;
                 h0[i] = G[i] = 0.f;
-                if (n < Np) {
+                if (n < s.N) {
                     h0[i] = keep[state_at(s, b * tiles + t0 / kSelTile, n, c)];
                     if (t0 + kSelTile >= s.T || q == kSelBlock / kSelTile - 1)
                         G[i] = W.carry[state_at(s, b * blocks + k, n, c)];
@@ -443,7 +463,7 @@ hipError_t reverse(const SelShape& s, const SelArgs& A, const void* gy, const fl
     const int group_tiles = (int)ceil_div(s.C / s.G, 64);
     const int64_t blocks = sel_blocks(s);
     hipLaunchKernelGGL((sel_reverse_kernel<E, W, NPT>), dim3((unsigned)(s.B * blocks * s.G * group_tiles)),
-                       dim3(64 * W), 0, st, s, A, gy, bc, out, sum, blocks, group_tiles);
+                       dim3(64 * W), 0, st, s, A, (const E*)gy, bc, out, sum, (int)blocks, group_tiles);
     return hipGetLastError();
 }
 
