@@ -1241,7 +1241,7 @@ size_t sel_keep_bytes(const linrec::SelShape& s) {
 // Scratch of the backward, behind bc.  gA's shares take the place of what enters the blocks: a lane
 // of the gradients' kernel reads the one before it writes the other.
 size_t sel_backward_layout(const linrec::SelShape& s, void* ws, linrec::SelBwdScratch* W) {
-    const linrec::SelPlan p = linrec::sel_plan(s);
+    const linrec::SelPlan p = linrec::sel_backward_plan(s);
     const int64_t rows = s.B * linrec::sel_blocks(s);
     size_t at = align256(linrec::sel_bc_floats(s, p) * sizeof(float));
     const auto take = [&](size_t floats) {
@@ -1280,7 +1280,7 @@ int sel_forward(const linrec::SelShape& s, const linrec::SelArgs& A, float* keep
     linrec::SelScratch W;
     sel_forward_layout(s, workspace, &W);
     const linrec::SelPlan p = linrec::sel_plan(s);
-    hipError_t e = linrec::run_sel_prepare(s, A, p, W, st);
+    hipError_t e = linrec::run_sel_prepare(s, A, p, W.bc, st);
     if (e == hipSuccess) e = linrec::run_sel_forward(s, A, p, W, keep, st);
     return hip_status(e, "linrec_scan_selective launch");
 }
@@ -1372,25 +1372,21 @@ LINREC_API int linrec_scan_selective_backward(int64_t B, int64_t T, int64_t C, i
     if ((st = check_sel_backward(s))) return st;
     if (ckpt && (st = check_ckpt(ckpt, ckpt_bytes, sel_keep_bytes(s)))) return st;
     if ((st = check_ws(workspace, ws_bytes, sel_backward_bytes(s, ckpt != nullptr)))) return st;
-    const linrec::SelPlan p = linrec::sel_plan(s);
     char* ws = (char*)workspace;
     const float* keep = (const float*)ckpt;
-    linrec::SelScratch F{};
     if (!ckpt) {
         float* own = (float*)ws;
         ws += sel_keep_bytes(s);
         if ((st = sel_forward(s, X, own, ws, hs))) return st;
         keep = own;
-        F.bc = (float*)ws;
-    } else {
-        F.bc = (float*)ws;
-        const hipError_t e = linrec::run_sel_prepare(s, X, p, F, hs);
-        if (e != hipSuccess) return hip_status(e, "linrec_scan_selective_backward prepare launch");
     }
+    float* const bc = (float*)ws;  // the forward's, if there was one, is not needed any more
     linrec::SelBwdScratch W;
     sel_backward_layout(s, ws, &W);
+    const hipError_t e = linrec::run_sel_prepare(s, X, linrec::sel_backward_plan(s), bc, hs);
+    if (e != hipSuccess) return hip_status(e, "linrec_scan_selective_backward prepare launch");
     const linrec::SelBwdArgs g{gy, gs_out, gu, gdt, gB, gC, gz, gA, gD, gdt_bias, gs_in};
-    return hip_status(linrec::run_sel_backward(s, X, g, p, F.bc, keep, W, hs), "linrec_scan_selective_backward launch");
+    return hip_status(linrec::run_sel_backward(s, X, g, bc, keep, W, hs), "linrec_scan_selective_backward launch");
 }
 
 LINREC_API int linrec_scan_selective_decode_step(int64_t B, int64_t C, int64_t G, int64_t N, int dtype, const void* u,

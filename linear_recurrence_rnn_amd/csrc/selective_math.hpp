@@ -35,22 +35,42 @@ __device__ __forceinline__ float logistic(float t) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-t * kLog2e));
 }
 
-// What the states of one wave need of a few tokens: B and C by scalar loads, 32 floats, and the
+// One element at a wave-uniform base and a lane's byte offset: the form that takes two scalar registers
+// and one vector register for the address.
+template <class E>
+__device__ __forceinline__ E load_elem(const void* base, unsigned at) {
+    return *reinterpret_cast<const E*>(reinterpret_cast<const char*>(base) + at);
+}
+template <class E>
+__device__ __forceinline__ void store_elem(void* base, unsigned at, float x) {
+    *reinterpret_cast<E*>(reinterpret_cast<char*>(base) + at) = (E)x;
+}
+template <class E>
+__device__ __forceinline__ const void* elems(const void* p, int64_t first) {
+    return reinterpret_cast<const E*>(p) + first;
+}
+
+// A vector of N floats; one is a float.
+template <int N> struct SelVec { typedef float type __attribute__((ext_vector_type(N))); };
+template <> struct SelVec<1> { typedef float type; };
+
+// What the states of one wave need of a few tokens: B and C by scalar loads, NF floats, and the
 // channels' own pair of floats from LDS.  Scalar loads come back in any order, so a wait for one is a
 // wait for all of them and for LDS: both are asked for together, one group ahead of their use.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-template <int NPT>
+template <int NPT, int NF = 32>
 struct SelGroup {
-    static constexpr int kTok = 16 / NPT;             // tokens of a group
+    static constexpr int kTok = NF / 2 / NPT;         // tokens of a group
     static constexpr int kGroups = kSelTile / kTok;   // groups of a tile
-    f32x16 bc[2];
+    f32x16 bc[NF / 16];
     f32x2 x[kTok];
     // row: the wave's 2*NPT floats of the tile's first token, those of its other tokens behind them.
     __device__ __forceinline__ void fetch(const float* row, const f32x2 (*din)[64], int lane, int q) {
         typedef const __attribute__((address_space(4))) f32x16* P;
-        const P p = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + q * 32));
-        bc[0] = p[0], bc[1] = p[1];
+        const P p = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + q * NF));
+#pragma unroll
+        for (int k = 0; k < NF / 16; ++k) bc[k] = p[k];
 #pragma unroll
         for (int k = 0; k < kTok; ++k) x[k] = din[q * kTok + k][lane];
     }

@@ -26,7 +26,7 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// B and C as float32, (B,tiles,G,W,16 tokens,2,NPT), zero beyond N, for absent tokens and behind T.
+// B and C as float32, (B,tiles,G,waves,16 tokens,2,npt), zero beyond N, for absent tokens and behind T.
 template <class E>
 __global__ __launch_bounds__(256) void sel_prepare_kernel(SelShape s, const E* __restrict__ Bm,
                                                           const E* __restrict__ Cm, float* __restrict__ bc, int npt,
@@ -312,6 +312,7 @@ hipError_t forward_by_states(const SelShape& s, const SelArgs& A, const SelPlan&
 
 SelPlan sel_plan(const SelShape& s) {
     SelPlan p{};
+    p.tiles_n = 1;
     p.npt = s.N <= 1 ? 1 : s.N <= 2 ? 2 : s.N <= 16 ? 4 : s.N <= 64 ? 8 : 16;
     p.waves = s.N <= 4 ? 1 : s.N <= 8 ? 2 : s.N <= 32 ? 4 : 8;
     // Segments until the chip has four waves a SIMD, of four tiles at least.
@@ -325,20 +326,20 @@ SelPlan sel_plan(const SelShape& s) {
 }
 
 size_t sel_bc_floats(const SelShape& s, const SelPlan& p) {
-    return (size_t)(s.B * sel_tiles(s) * kSelTile * s.G) * 2 * (size_t)(p.npt * p.waves);
+    return (size_t)(s.B * sel_tiles(s) * kSelTile * s.G) * 2 * (size_t)(p.npt * p.waves * p.tiles_n);
 }
 
-hipError_t run_sel_prepare(const SelShape& s, const SelArgs& A, const SelPlan& p, const SelScratch& W, hipStream_t st) {
+hipError_t run_sel_prepare(const SelShape& s, const SelArgs& A, const SelPlan& p, float* bc, hipStream_t st) {
     const int64_t total = (int64_t)sel_bc_floats(s, p);
     int64_t blocks = ceil_div(total, 256);
     if (blocks > 4096) blocks = 4096;
     const int tiles = (int)sel_tiles(s);
     if (s.dtype == kBf16)
         hipLaunchKernelGGL((sel_prepare_kernel<bf16_t>), dim3((unsigned)blocks), dim3(256), 0, st, s,
-                           (const bf16_t*)A.Bm, (const bf16_t*)A.Cm, W.bc, p.npt, p.waves, tiles, total);
+                           (const bf16_t*)A.Bm, (const bf16_t*)A.Cm, bc, p.npt, p.tiles_n * p.waves, tiles, total);
     else
         hipLaunchKernelGGL((sel_prepare_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, st, s,
-                           (const float*)A.Bm, (const float*)A.Cm, W.bc, p.npt, p.waves, tiles, total);
+                           (const float*)A.Bm, (const float*)A.Cm, bc, p.npt, p.tiles_n * p.waves, tiles, total);
     return hipGetLastError();
 }
 

@@ -50,14 +50,15 @@ inline int64_t sel_blocks(const SelShape& s) { return (s.T + kSelBlock - 1) / kS
 
 // How the forward is split: states of a lane, waves of a workgroup, segments of the rows.
 struct SelPlan {
-    int npt, waves;
+    int npt, waves, tiles_n;  // workgroups share the states: tiles_n of them (forward: 1)
     int64_t segs, seg_tiles;  // segments, and tiles of one
 };
 SelPlan sel_plan(const SelShape& s);
+SelPlan sel_backward_plan(const SelShape& s);  // (no segments: the backward has blocks)
 
 // Scratch of the forward: bc, and where the rows are cut into segments `agg` and `sum`.
 struct SelScratch {
-    float* bc;    // (B,tiles,G,waves,16,2,npt): B and C in float32, zero for absent tokens and behind T
+    float* bc;    // (B,tiles,G,tiles_n*waves,16,2,npt): B and C in float32, zero for absent tokens and behind T
     float* agg;   // (B,segs) rows of states
     float* sum;   // (B,segs,C) sums of d
 };
@@ -70,13 +71,13 @@ struct SelBwdScratch {
     float* gA;     // (B*blocks) rows of states
     float* gDb;    // (B*blocks,2,C): D's gradient, bias's
     float* gBC;    // (cuts,B,T,G,2,4*n4): B's and C's gradients by channel ranges of `cut` of a group
-    float* q;      // (tiles of 16 states,B,T,C,3) where N > 16: sums over the states of one
+    float* q;      // (tiles of 16 states,3,B,T,C) where N > 16: sums over the states of one
     int64_t cut, cuts;
 };
 int64_t sel_cut(const SelShape& s);
 
 // keep: (B,tiles) rows of states, the state before each tile; null: not kept.
-hipError_t run_sel_prepare(const SelShape& s, const SelArgs& A, const SelPlan& p, const SelScratch& W, hipStream_t st);
+hipError_t run_sel_prepare(const SelShape& s, const SelArgs& A, const SelPlan& p, float* bc, hipStream_t st);
 hipError_t run_sel_forward(const SelShape& s, const SelArgs& A, const SelPlan& p, const SelScratch& W, float* keep,
                            hipStream_t st);
 hipError_t run_sel_step(const SelShape& s, const SelArgs& A, hipStream_t st);
@@ -85,7 +86,7 @@ hipError_t run_sel_step(const SelShape& s, const SelArgs& A, hipStream_t st);
 // reverse; the last result goes to `out` if given.
 hipError_t run_sel_join(const SelShape& s, const float* A, float* v, const float* sum, int64_t blocks, const float* in,
                         float* out, bool reverse, hipStream_t st);
-hipError_t run_sel_backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const SelPlan& p, const float* bc,
-                            const float* keep, const SelBwdScratch& W, hipStream_t st);
+hipError_t run_sel_backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const float* bc, const float* keep,
+                            const SelBwdScratch& W, hipStream_t st);
 
 }  // namespace linrec

@@ -15,10 +15,13 @@
 // all blocks at once, the states formed again from those the forward kept every 16 tokens.
 //
 // The last kernel sums over states (for each token and channel) and over channels (for each token
-// and state).  A wave holds 8 channels x 8 NT states, lane = 8 (state) + channel: sums over states go
-// across lane bits 3 to 5, 16 tokens at once, each step halving the tokens a lane holds, so that
-// they end at the lane that has the token's own inputs.  Sums over channels are kept per lane for the
-// 16 tokens and over all channel sets the wave walks through, and cross its 8 channel lanes once.
+// and state).  Like the forward, a wave holds 64 channels, a lane each, and 4 states of them, with B and C by
+// scalar loads; sums over the states are added in the lane and over the waves through LDS.  Sums over the
+// lanes go through the matrix unit, which is idle otherwise: a value as one operand of the 16x16x4 product
+// and a column of ones as the other add the lanes 16 apart and put the result into that column, so
+// that 16 products into one accumulator leave 16 values side by side, with 16 shares each, four of them in a
+// lane; two folds across the lanes add the rest for 64 values at once.  In float32, and 11 cycles of
+// the vector unit a state where folds alone would take 24.
 // Sums over blocks, batch rows and channel ranges are partial sums in the workspace, added in
 // order by small kernels at the end: nothing depends on timing.
 #include "selective_math.hpp"
@@ -29,17 +32,22 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int kBwdNpt = 4;  // states of a lane in the kernels below; a workgroup of W waves has 4 W
+
 // The G that leaves each block on its left, from zero, and the sum of its steps.
-template <class E, int W, int NPT>
+template <class E, int W>
 __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs A, const E* __restrict__ gy,
                                                              const float* __restrict__ bc, float* __restrict__ out,
-                                                             float* __restrict__ sum, int blocks, int group_tiles) {
-    constexpr int TW = kSelTile / W;
+                                                             float* __restrict__ sum, int blocks, int group_tiles,
+                                                             int ntiles) {
+    constexpr int TW = kSelTile / W, NPT = kBwdNpt;
     __shared__ f32x2 din[kSelTile][64];  // d, p
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     unsigned blk = blockIdx.x;
     const int tile = (int)(blk % (unsigned)(s.G * group_tiles));
     blk /= (unsigned)(s.G * group_tiles);
+    const int nt = (int)(blk % (unsigned)ntiles);
+    blk /= (unsigned)ntiles;
     const int k = (int)(blk % (unsigned)blocks);
     const int64_t b = blk / (unsigned)blocks;
     const int grp = tile / group_tiles, Cg = (int)(s.C / s.G);
@@ -48,7 +56,7 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
     const unsigned c = (unsigned)(grp * Cg + (live ? in_group : Cg - 1));
     const int T = (int)s.T, tiles = (T + kSelTile - 1) / kSelTile;
     const int t_begin = k * kSelBlock, len = (int)row_length(s, b);
-    const int n0 = w * NPT, Np = (s.N + 3) / 4 * 4;
+    const int n0 = (nt * W + w) * NPT;
     float g[NPT], a2[NPT];
 #pragma unroll
     for (int i = 0; i < NPT; ++i) {
@@ -56,41 +64,40 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
         a2[i] = n0 + i < s.N ? A.A[(int64_t)c * s.N + n0 + i] * kLog2e : 0.f;
     }
     const float bias = A.bias ? A.bias[c] : 0.f;
+    const bool gated = A.z != nullptr, soft = s.softplus != 0;
+    const void* const zp = gated ? A.z : A.dt;
     float total = 0.f;
-    // This wave's tokens of a tile, read while the tile behind it is worked on.  Tokens behind the
-    // row's end are read as the last one and not used.
+    // This wave's tokens of a tile, read while the tile behind it is worked on.  Absent ones are read as
+    // the last that is there and not used.
     E dr[TW], zr[TW], gr[TW];
     const auto fetch = [&](int t0) {
         const int64_t base = (b * T + t0) * s.C;
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
-            const int last = T - 1 - t0, j = w * TW + i < last ? w * TW + i : last;
-            const unsigned off = (unsigned)j * (unsigned)s.C + c;
-            dr[i] = (reinterpret_cast<const E*>(A.dt) + base)[off];
-            gr[i] = (gy + base)[off];
-            if (A.z) zr[i] = (reinterpret_cast<const E*>(A.z) + base)[off];
+            const int j = t0 + w * TW + i < len ? w * TW + i : len - 1 - t0;
+            const unsigned at = ((unsigned)j * (unsigned)s.C + c) * (unsigned)sizeof(E);
+            dr[i] = load_elem<E>(elems<E>(A.dt, base), at);
+            gr[i] = load_elem<E>(elems<E>(gy, base), at);
+            zr[i] = load_elem<E>(elems<E>(zp, base), at);
         }
     };
     // Tiles of absent tokens alone change nothing.
     const int end = t_begin + kSelBlock < len ? t_begin + kSelBlock : len;
-    int t0 = end > t_begin ? (end - 1) / kSelTile * kSelTile : -1;
-    if (t0 >= 0) fetch(t0);
+    int t0 = end > t_begin ? (end - 1) / kSelTile * kSelTile : t_begin - kSelTile;
+    if (t0 >= t_begin) fetch(t0);
     for (; t0 >= t_begin; t0 -= kSelTile) {
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
             const bool there = live && t0 + w * TW + i < len;
-            float d = (float)dr[i] + bias, sig, p = there ? (float)gr[i] : 0.f;
-            if (s.softplus) d = softplus(d, sig);
-            if (A.z) {
-                const float z = there ? (float)zr[i] : 0.f;
-                p *= z * logistic(z);
-            }
-            const f32x2 v = {there ? d : 0.f, p};
+            const float raw = (float)dr[i] + bias, z = there ? (float)zr[i] : 0.f, p = there ? (float)gr[i] : 0.f;
+            float sig;
+            const float d = soft ? softplus(raw, sig) : raw;
+            const f32x2 v = {there ? d : 0.f, gated ? p * (z * logistic(z)) : p};
             din[w * TW + i][lane] = v;
         }
-        if (t0 > t_begin) fetch(t0 - kSelTile);
+        fetch(t0 > t_begin ? t0 - kSelTile : t0);
         __syncthreads();
-        const float* row = bc + (((b * tiles + t0 / kSelTile) * s.G + grp) * W + w) * (kSelTile * 2 * NPT);
+        const float* row = bc + ((((b * tiles + t0 / kSelTile) * s.G + grp) * ntiles + nt) * W + w) * (kSelTile * 2 * NPT);
         constexpr int kGroups = SelGroup<NPT>::kGroups, kTok = SelGroup<NPT>::kTok;
         float subtotal = 0.f;
         SelGroup<NPT> grp_of[2];
@@ -101,10 +108,10 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
             if (q + 1 < kGroups) grp_of[(q + 1) & 1].fetch(row, din, lane, kGroups - 2 - q);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int k = kTok - 1; k >= 0; --k) {
-                const f32x2 x = v.x[k];
+            for (int r = kTok - 1; r >= 0; --r) {
+                const f32x2 x = v.x[r];
 #pragma unroll
-                for (int i = 0; i < NPT; ++i) g[i] = fast_exp2(x[0] * a2[i]) * fmaf(v.C(k, i), x[1], g[i]);
+                for (int i = 0; i < NPT; ++i) g[i] = fast_exp2(x[0] * a2[i]) * fmaf(v.C(r, i), x[1], g[i]);
                 subtotal += x[0];
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -113,10 +120,8 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
         __syncthreads();
     }
     if (!live) return;
-#pragma unroll
-    for (int i = 0; i < NPT; ++i)
-        if (n0 + i < Np) out[state_at(s, b * blocks + k, n0 + i, c)] = g[i];
-    if (w == 0) sum[(b * blocks + k) * s.C + c] = total;
+    if (n0 < s.N) store16<float>(out + state_at(s, b * blocks + k, n0, c), g);
+    if (nt == 0 && w == 0) sum[(b * blocks + k) * s.C + c] = total;
 }
 
 // ---- sums across the lanes of a wave ---------------------------------------------------
@@ -130,291 +135,351 @@ __device__ __forceinline__ float fold16(float a, float b) {
     const u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-// The same with the DPP permutation CTRL, an involution: lanes with `up` false get a's sum.
-template <int CTRL>
-__device__ __forceinline__ float fold_dpp(float a, float b, bool up) {
-    const float own = up ? b : a, other = up ? a : b;
-    return own + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(other), CTRL, 0xf, 0xf, true));
-}
-constexpr int kXor8 = 0x128, kXor7 = 0x141, kXor3 = 0x1b, kXor1 = 0xb1;  // row_ror:8, row_half_mirror, quad_perm
 
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-constexpr int kGradWaves = 4, kGradChan = 8;                   // waves, channels of a wave at once
-constexpr int kGradStep = kGradWaves * kGradChan;              // channels of a workgroup at once
-
-// LDS of the gradient kernel: the fixed part, and per set of channels of a wave.
-template <int NT>
+// LDS of the gradient kernel; behind it, per set of 64 channels: G, gA (4 states each) and the lane's
+// own sums of gD and gbias, for every wave.
+template <int W>
 struct GradLds {
-    static constexpr int kStates = 8 * NT;
-    float bc[2][kSelTile][kStates];
-    union {
-        f32x4 rec[kGradWaves][kSelTile][kGradChan];  // d, d u, p
-        float red[kGradWaves][4 * NT][64];
-    };
+    f32x2 du[kSelTile][64];               // d, d u
+    f32x2 pu[kSelTile][64];               // p, u
+    float part[2][W][kSelTile][64];       // the waves' shares of sums over the states
 };
+constexpr int kGradOwn = 2 * kBwdNpt + 2;
 
-template <class E, int NT>
-__global__ __launch_bounds__(64 * kGradWaves) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
-                                                                       const float* __restrict__ keep,
-                                                                       SelBwdScratch W, int64_t blocks, int ntiles) {
-    constexpr int kStates = 8 * NT;
+template <class E, int W>
+__global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
+                                                                              const float* __restrict__ bc,
+                                                                              const float* __restrict__ keep,
+                                                                              SelBwdScratch S, int blocks, int ntiles) {
+    constexpr int NPT = kBwdNpt, TW = kSelTile / W, kPairs = kSelTile / 2;
     extern __shared__ __align__(16) char lds[];
-    GradLds<NT>& L = *reinterpret_cast<GradLds<NT>*>(lds);
+    GradLds<W>& L = *reinterpret_cast<GradLds<W>*>(lds);
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int d = lane & 7, nl = lane >> 3;
-    const int Cg = (int)(s.C / s.G), cut = (int)W.cut, cuts = (int)W.cuts, sets = cut / kGradStep;
-    // Per set of channels: G, gA, and the lane's own sums of gD and gbias.
-    float* const own = reinterpret_cast<float*>(lds + sizeof(GradLds<NT>)) + (int64_t)w * sets * 64 * (2 * NT + 2) + lane;
-    int64_t blk = blockIdx.x;
-    const int nt = (int)(blk % ntiles);
-    blk /= ntiles;
-    const int cu = (int)(blk % cuts);
-    blk /= cuts;
-    const int grp = (int)(blk % s.G);
-    blk /= s.G;
-    const int64_t k = blk % blocks, b = blk / blocks;
-    const int64_t len = row_length(s, b), tiles = (s.T + kSelTile - 1) / kSelTile;
-    const int n0 = nt * kStates + nl * NT, Np = (s.N + 3) / 4 * 4;
+    const int Cg = (int)(s.C / s.G), cut = (int)S.cut, cuts = (int)S.cuts;
+    unsigned blk = blockIdx.x;
+    const int cu = (int)(blk % (unsigned)cuts);
+    blk /= (unsigned)cuts;
+    const int grp = (int)(blk % (unsigned)s.G);
+    blk /= (unsigned)s.G;
+    const int nt = (int)(blk % (unsigned)ntiles);
+    blk /= (unsigned)ntiles;
+    const int k = (int)(blk % (unsigned)blocks);
+    const int64_t b = blk / (unsigned)blocks;
+    const int T = (int)s.T, tiles = (T + kSelTile - 1) / kSelTile, len = (int)row_length(s, b);
+    const int t_begin = k * kSelBlock, t_end = t_begin + kSelBlock < T ? t_begin + kSelBlock : T;
+    const int n0 = (nt * W + w) * NPT, Np = (s.N + 3) / 4 * 4;
+    const unsigned C = (unsigned)s.C;
     const bool whole = ntiles == 1;  // sums over the states are complete
+    const int c_first = cu * cut, c_end = c_first + cut < Cg ? c_first + cut : Cg;  // in the group
+    const int sets = (c_end - c_first + 63) / 64;
+    float* const own = reinterpret_cast<float*>(lds + sizeof(GradLds<W>)) + w * 64 * kGradOwn + lane;
+    constexpr int kOwnStep = W * 64 * kGradOwn;
 
-    for (int i = 0; i < sets * (2 * NT + 2); ++i) own[i * 64] = 0.f;
+    for (int j = 0; j < sets; ++j)
+        for (int i = 0; i < kGradOwn; ++i) own[j * kOwnStep + i * 64] = 0.f;
 
-    for (int q = kSelBlock / kSelTile - 1; q >= 0; --q) {
-        const int64_t t0 = k * kSelBlock + q * kSelTile;
-        if (t0 >= s.T) continue;
-        __syncthreads();  // the previous tile's bc and red have been read
-        for (int j = threadIdx.x; j < 2 * kSelTile * kStates; j += 64 * kGradWaves) {
-            const int n = nt * kStates + j % kStates, t = j / kStates % kSelTile, o = j / (kStates * kSelTile);
-            float v = 0.f;
-            if (n < s.N && t0 + t < len)
-                v = (float)reinterpret_cast<const E*>(o ? A.Cm : A.Bm)[((b * s.T + t0 + t) * s.G + grp) * s.N + n];
-            L.bc[o][t][n - nt * kStates] = v;
+    // Tiles of absent tokens alone: no gradients.
+    const int live_end = len < t_end ? (len > t_begin ? (len + kSelTile - 1) / kSelTile * kSelTile : t_begin) : t_end;
+    for (int t = live_end + w; t < t_end; t += W) {
+        if (whole) {
+            const int64_t at = (b * T + t) * s.C + grp * Cg;
+            for (int c = c_first + lane; c < c_end; c += 64) {
+                reinterpret_cast<E*>(g.gu)[at + c] = reinterpret_cast<E*>(g.gdt)[at + c] = (E)0.f;
+                if (A.z) reinterpret_cast<E*>(g.gz)[at + c] = (E)0.f;
+            }
         }
-        __syncthreads();
-        float accB[kSelTile][NT], accC[kSelTile][NT];
-#pragma unroll
-        for (int t = 0; t < kSelTile; ++t)
-#pragma unroll
-            for (int i = 0; i < NT; ++i) accB[t][i] = accC[t][i] = 0.f;
+        for (int j = lane; j < 2 * W * NPT; j += 64) {
+            const int n = nt * W * NPT + j % (W * NPT);
+            if (n < Np) S.gBC[((((int64_t)cu * s.B + b) * T + t) * s.G + grp) * 2 * Np + j / (W * NPT) * Np + n] = 0.f;
+        }
+    }
 
+    // What a lane reads of a set of channels in a tile: its wave's tokens' inputs and its states before the
+    // tile, asked for a set ahead.  Absent tokens are read as the last one that is there, lanes behind
+    // the last channel as that, inputs that were not given as others: none of that is used.
+    const bool gated = A.z != nullptr, soft = s.softplus != 0, states = n0 < s.N;
+    const void* const zp = gated ? A.z : A.u;
+    const float *const biasp = A.bias ? A.bias : A.A, *const Dp = A.D ? A.D : A.A;
+    struct Raw {
+        E u[TW], dt[TW], z[TW], gy[TW];  // as they come: a conversion would wait for the load
+        float a[NPT], bias, D;
+        f32x4 h0;
+    } next;
+    const auto fetch = [&](int q, int set) {
+        const int t0 = t_begin + q * kSelTile;
+        const int64_t base = (b * T + t0) * s.C;
+        const int in_group = c_first + set * 64 + lane;
+        const unsigned c = (unsigned)(grp * Cg + (in_group < Cg ? in_group : Cg - 1));
+#pragma unroll
+        for (int e = 0; e < TW; ++e) {
+            const int t = t0 + w * TW + e < len ? w * TW + e : len - 1 - t0;
+            const unsigned at = ((unsigned)t * C + c) * (unsigned)sizeof(E);
+            next.u[e] = load_elem<E>(elems<E>(A.u, base), at);
+            next.dt[e] = load_elem<E>(elems<E>(A.dt, base), at);
+            next.gy[e] = load_elem<E>(elems<E>(g.gy, base), at);
+            next.z[e] = load_elem<E>(elems<E>(zp, base), at);
+        }
+        const void* const hp = elems<float>(keep, (b * tiles + t0 / kSelTile) * Np * s.C);
+        next.h0 = load_elem<f32x4>(hp, ((unsigned)(states ? n0 : 0) * C + c * 4) * 4);
+#pragma unroll
+        for (int i = 0; i < NPT; ++i) next.a[i] = load_elem<float>(A.A, (c * (unsigned)s.N + (n0 + i < s.N ? n0 + i : 0)) * 4);
+        next.bias = load_elem<float>(biasp, c * 4);
+        next.D = load_elem<float>(Dp, c * 4);
+    };
+    const int q_first = (live_end - t_begin + kSelTile - 1) / kSelTile - 1;
+    if (q_first >= 0) fetch(q_first, 0);
+
+    float one[16];  // columns of ones
+#pragma unroll
+    for (int i = 0; i < 16; ++i) one[i] = (lane & 15) == i ? 1.f : 0.f;
+
+    for (int q = q_first; q >= 0; --q) {
+        const int t0 = t_begin + q * kSelTile;
+        const float* row = bc + ((((b * tiles + t0 / kSelTile) * s.G + grp) * ntiles + nt) * W + w) * (kSelTile * 2 * NPT);
+        float tot[2] = {0.f, 0.f};  // sums over channels: 64 values each
         for (int set = 0; set < sets; ++set) {
-            const int in_group = cu * cut + set * kGradStep + w * kGradChan + d;
-            if (cu * cut + set * kGradStep + w * kGradChan >= Cg) break;
-            const bool live = in_group < Cg;
-            const int64_t c = (int64_t)grp * Cg + (live ? in_group : Cg - 1);
-            float* const mine = own + set * 64 * (2 * NT + 2);
-            // This lane's two tokens.
-            const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
-            float u[2], dd[2], p[2], sig[2], gzf[2];
-            bool there[2];
+            const bool live = c_first + set * 64 + lane < c_end;
+            const unsigned c = (unsigned)(grp * Cg + c_first + set * 64 + lane);
+            float* const mine = own + set * kOwnStep;
+            const int64_t base = (b * T + t0) * s.C;
+            const float Dc = A.D ? next.D : 0.f, bias = A.bias ? next.bias : 0.f;
+            float sig[TW], gzf[TW];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int64_t t = t0 + 2 * nl + e;
-                there[e] = live && t < len;
-                u[e] = dd[e] = p[e] = gzf[e] = 0.f;
-                sig[e] = 1.f;
-                if (there[e]) {
-                    const int64_t at = (b * s.T + t) * s.C + c;
-                    u[e] = (float)reinterpret_cast<const E*>(A.u)[at];
-                    dd[e] = (float)reinterpret_cast<const E*>(A.dt)[at] + bias;
-                    p[e] = (float)reinterpret_cast<const E*>(g.gy)[at];
-                    if (A.z) {
-                        const float z = (float)reinterpret_cast<const E*>(A.z)[at];
-                        const float sg = logistic(z);
-                        gzf[e] = p[e] * sg * fmaf(z, 1.f - sg, 1.f);
-                        p[e] *= z * sg;
+            for (int e = 0; e < TW; ++e) {
+                const bool there = live && t0 + w * TW + e < len;
+                const float u = there ? (float)next.u[e] : 0.f, gy = there ? (float)next.gy[e] : 0.f;
+                const float raw = (float)next.dt[e] + bias, z = there ? (float)next.z[e] : 0.f, sg = logistic(z);
+                float d = softplus(raw, sig[e]);
+                d = there ? (soft ? d : raw) : 0.f;
+                sig[e] = there ? (soft ? sig[e] : 1.f) : 0.f;
+                gzf[e] = gy * sg * fmaf(z, 1.f - sg, 1.f);
+                const f32x2 du = {d, d * u}, pu = {gy * (gated ? z * sg : 1.f), u};
+                L.du[w * TW + e][lane] = du;
+                L.pu[w * TW + e][lane] = pu;
+            }
+            float a2[NPT], G[NPT], gA[NPT], h0[NPT];
+#pragma unroll
+            for (int i = 0; i < NPT; ++i) {
+                a2[i] = n0 + i < s.N ? next.a[i] * kLog2e : 0.f, h0[i] = n0 + i < s.N ? next.h0[i] : 0.f;
+                G[i] = mine[i * 64], gA[i] = mine[(NPT + i) * 64];
+            }
+            if (q == q_first && live && states) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(S.carry + state_at(s, b * blocks + k, n0, c));
+#pragma unroll
+                for (int i = 0; i < NPT; ++i) G[i] = n0 + i < s.N ? v[i] : 0.f;
+            }
+            {  // in one place, the last time for nothing: two places would cost their addresses twice
+                const bool same = set + 1 < sets;
+                fetch(same || q == 0 ? q : q - 1, same ? set + 1 : 0);
+            }
+            __syncthreads();
+            // The states of the tile again, and their sums q3 = sum C h.
+            float h[kSelTile][NPT], a[kSelTile][NPT];
+            {
+                typedef SelGroup<NPT, 16> Group;
+                constexpr int kGroups = Group::kGroups, kTok = Group::kTok;
+                Group of[2];
+                of[0].fetch(row, L.du, lane, 0);
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    const Group& v = of[j & 1];
+                    if (j + 1 < kGroups) of[(j + 1) & 1].fetch(row, L.du, lane, j + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int r = 0; r < kTok; ++r) {
+                        const int t = j * kTok + r;
+                        float q3 = 0.f;
+#pragma unroll
+                        for (int i = 0; i < NPT; ++i) {
+                            a[t][i] = fast_exp2(v.x[r][0] * a2[i]);
+                            h[t][i] = fmaf(a[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], v.x[r][1] * v.B(r, i));
+                            q3 = fmaf(v.C(r, i), h[t][i], q3);
+                        }
+                        L.part[0][w][t][lane] = q3;
                     }
-                    if (s.softplus) dd[e] = softplus(dd[e], sig[e]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                const f32x4 v = {dd[e], dd[e] * u[e], p[e], 0.f};
-                L.rec[w][2 * nl + e][d] = v;
             }
-            float a2[NT], G[NT], gA[NT], h0[NT];
+            __syncthreads();
+            if (gated || !whole) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const int n = n0 + i;
-                a2[i] = n < s.N ? A.A[c * s.N + n] * kLog2e : 0.f;
-                h0[i] = G[i] = 0.f;
-                if (n < s.N) {
-                    h0[i] = keep[state_at(s, b * tiles + t0 / kSelTile, n, c)];
-                    if (t0 + kSelTile >= s.T || q == kSelBlock / kSelTile - 1)
-                        G[i] = W.carry[state_at(s, b * blocks + k, n, c)];
+                for (int e = 0; e < TW; ++e) {
+                    const int t = w * TW + e;
+                    float core = 0.f;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) core += L.part[0][j][t][lane];
+                    if (!live || t0 + t >= T) continue;
+                    const unsigned at = (unsigned)t * C + c;
+                    if (!whole)
+                        store_elem<float>(S.q + ((int64_t)nt * 3 + 2) * s.B * T * s.C + base, at * 4, core);
                     else
-                        G[i] = mine[i * 64];
-                }
-                gA[i] = mine[(NT + i) * 64];
-            }
-            wave_lds_fence();
-            // The states of the tile again.
-            float h[kSelTile][NT], a[kSelTile][NT];
-#pragma unroll
-            for (int t = 0; t < kSelTile; ++t) {
-                const f32x2 x = *reinterpret_cast<const f32x2*>(&L.rec[w][t][d]);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    a[t][i] = fast_exp2(x[0] * a2[i]);
-                    h[t][i] = fmaf(a[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], x[1] * L.bc[0][t][nl * NT + i]);
+                        store_elem<E>((E*)g.gz + base, at * (unsigned)sizeof(E),
+                                      t0 + t < len ? gzf[e] * fmaf(Dc, L.pu[t][lane][1], core) : 0.f);
                 }
             }
-            // Backwards: q1 = sum A m, q2 = sum g B, q3 = sum C h (over this lane's states).
-            float q1[kSelTile], q2[kSelTile], q3[kSelTile];
+            __syncthreads();
+            // Backwards: q1 = sum A m, q2 = sum g B, and the sums over channels of g d u and p h.
+            float shares[kPairs];
+            {
+                f32x4 acc[2];
+                f32x2 x[2][2], y[2][2];
+                f32x16 v[2];
+                const auto ahead = [&](int j) {  // the pair of tokens 2 j, 2 j + 1
+                    typedef const __attribute__((address_space(4))) f32x16* P;
+                    v[j & 1] = *reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + j * 16));
 #pragma unroll
-            for (int t = kSelTile - 1; t >= 0; --t) {
-                const f32x4 x = L.rec[w][t][d];
-                q1[t] = q2[t] = q3[t] = 0.f;
+                    for (int r = 0; r < 2; ++r) x[j & 1][r] = L.du[2 * j + r][lane], y[j & 1][r] = L.pu[2 * j + r][lane];
+                };
+                ahead(kPairs - 1);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const float Bt = L.bc[0][t][nl * NT + i], Ct = L.bc[1][t][nl * NT + i];
-                    const float gt = fmaf(Ct, x[2], G[i]);
-                    G[i] = gt * a[t][i];
-                    const float m = G[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
-                    gA[i] = fmaf(x[0], m, gA[i]);
-                    q1[t] = fmaf(a2[i], m, q1[t]);
-                    q2[t] = fmaf(gt, Bt, q2[t]);
-                    q3[t] = fmaf(Ct, h[t][i], q3[t]);
-                    accB[t][i] = fmaf(gt, x[1], accB[t][i]);
-                    accC[t][i] = fmaf(x[2], h[t][i], accC[t][i]);
+                for (int j = kPairs - 1; j >= 0; --j) {
+                    if (j > 0) ahead(j - 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    f32x4& sum = acc[j & 1];
+#pragma unroll
+                    for (int r = 1; r >= 0; --r) {
+                        const int t = 2 * j + r;
+                        const float d = x[j & 1][r][0], du = x[j & 1][r][1], p = y[j & 1][r][0];
+                        float q1 = 0.f, q2 = 0.f;
+#pragma unroll
+                        for (int i = 0; i < NPT; ++i) {
+                            const float gt = fmaf(v[j & 1][r * 2 * NPT + NPT + i], p, G[i]);
+                            G[i] = gt * a[t][i];
+                            const float m = G[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
+                            gA[i] = fmaf(d, m, gA[i]);
+                            q1 = fmaf(a2[i], m, q1);
+                            q2 = fmaf(gt, v[j & 1][r * 2 * NPT + i], q2);
+                            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                            sum = __builtin_amdgcn_mfma_f32_16x16x4f32(gt * du, one[r * 8 + i], r == 1 && i == 0 ? zero : sum,
+                                                                       0, 0, 0);
+                            sum = __builtin_amdgcn_mfma_f32_16x16x4f32(p * h[t][i], one[r * 8 + 4 + i], sum, 0, 0, 0);
+                        }
+                        L.part[0][w][t][lane] = q1;
+                        L.part[1][w][t][lane] = q2;
+                    }
+                    if (j + 1 < kPairs) {  // the pair before, whose products have come out by now
+                        const f32x4& o = acc[(j + 1) & 1];
+                        shares[j + 1] = (o[0] + o[1]) + (o[2] + o[3]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+                shares[0] = (acc[0][0] + acc[0][1]) + (acc[0][2] + acc[0][3]);
             }
 #pragma unroll
-            for (int i = 0; i < NT; ++i) mine[i * 64] = G[i], mine[(NT + i) * 64] = gA[i];
-            // Over the state lanes; lane nl ends with tokens 2 nl and 2 nl + 1.
-            const bool up = lane & 8;
-            float s1[2], s2[2], s3[2];
-            const auto over_states = [&](const float* v, float* out) {
-                float r[8], r2[4];
+            for (int i = 0; i < NPT; ++i) mine[i * 64] = G[i], mine[(NPT + i) * 64] = gA[i];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) r[j] = fold32(v[j], v[j + 8]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) r2[j] = fold16(r[j], r[j + 4]);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) out[j] = fold_dpp<kXor8>(r2[j], r2[j + 2], up);
-            };
-            over_states(q1, s1);
-            over_states(q2, s2);
-            over_states(q3, s3);
-            wave_lds_fence();  // rec has been read
+            for (int j = 0; j < 2; ++j)
+                tot[j] += fold32(fold16(shares[4 * j], shares[4 * j + 1]), fold16(shares[4 * j + 2], shares[4 * j + 3]));
+            __syncthreads();
             float sD = 0.f, sb = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int64_t t = t0 + 2 * nl + e;
-                const int64_t at = (b * s.T + t) * s.C + c;
-                if (!live || t >= s.T) continue;
+            for (int e = 0; e < TW; ++e) {
+                const int t = w * TW + e;
+                float q1 = 0.f, q2 = 0.f;
+#pragma unroll
+                for (int j = 0; j < W; ++j) q1 += L.part[0][j][t][lane], q2 += L.part[1][j][t][lane];
+                if (!live || t0 + t >= T) continue;
+                const unsigned at = (unsigned)t * C + c;
                 if (whole) {
-                    const float gd = there[e] ? fmaf(u[e], s2[e], s1[e] * kLn2) * sig[e] : 0.f;
-                    const float gu = there[e] ? fmaf(Dc, p[e], dd[e] * s2[e]) : 0.f;
-                    const float gz = there[e] ? gzf[e] * fmaf(Dc, u[e], s3[e]) : 0.f;
-                    reinterpret_cast<E*>(g.gu)[at] = (E)gu;
-                    reinterpret_cast<E*>(g.gdt)[at] = (E)gd;
-                    if (A.z) reinterpret_cast<E*>(g.gz)[at] = (E)gz;
-                    sD = fmaf(p[e], u[e], sD);
+                    const bool there = t0 + t < len;
+                    const float d = L.du[t][lane][0], p = L.pu[t][lane][0], u = L.pu[t][lane][1];
+                    const float gd = there ? fmaf(u, q2, q1 * kLn2) * sig[e] : 0.f;
+                    store_elem<E>((E*)g.gu + base, at * (unsigned)sizeof(E), there ? fmaf(Dc, p, d * q2) : 0.f);
+                    store_elem<E>((E*)g.gdt + base, at * (unsigned)sizeof(E), gd);
+                    sD = fmaf(p, u, sD);
                     sb += gd;
                 } else {
-                    float* o = W.q + ((int64_t)nt * s.B * s.T * s.C + at) * 3;
-                    o[0] = s1[e] * kLn2, o[1] = s2[e], o[2] = s3[e];
+                    float* const o = S.q + (int64_t)nt * 3 * s.B * T * s.C + base;
+                    store_elem<float>(o, at * 4, q1 * kLn2);
+                    store_elem<float>(o + s.B * T * s.C, at * 4, q2);
                 }
             }
-            mine[(2 * NT) * 64] += sD;
-            mine[(2 * NT + 1) * 64] += sb;
+            mine[2 * NPT * 64] += sD;
+            mine[(2 * NPT + 1) * 64] += sb;
+            __syncthreads();
         }
-        // Over the channel lanes: bit 2 of the lane picks B or C, bits 1 and 0 the token's bits 3, 2.
-        float r[4 * NT];
-        {
-            float x[kSelTile * NT], y[8 * NT];
-            const bool up2 = lane & 4, up1 = lane & 2, up0 = lane & 1;
+        // A lane's value: the pair by its bits 5 and 4, the token of it by bit 3, B's or C's by bit 2.
 #pragma unroll
-            for (int j = 0; j < kSelTile * NT; ++j)
-                x[j] = fold_dpp<kXor7>(accB[j / NT][j % NT], accC[j / NT][j % NT], up2);
-#pragma unroll
-            for (int j = 0; j < 8 * NT; ++j) y[j] = fold_dpp<kXor3>(x[j], x[j + 8 * NT], up1);
-#pragma unroll
-            for (int j = 0; j < 4 * NT; ++j) r[j] = fold_dpp<kXor1>(y[j], y[j + 4 * NT], up0);
-        }
-        __syncthreads();  // the last set's rec has been read
-#pragma unroll
-        for (int j = 0; j < 4 * NT; ++j) L.red[w][j][lane] = r[j];
-        __syncthreads();
-        for (int j = threadIdx.x; j < 4 * NT * 64; j += 64 * kGradWaves) {
-            const int l = j & 63, v = j >> 6;
-            float x = L.red[0][v][l];
-#pragma unroll
-            for (int i = 1; i < kGradWaves; ++i) x += L.red[i][v][l];
-            const int o = l >> 2 & 1, t = (l >> 1 & 1) * 8 + (l & 1) * 4 + v / NT;
-            const int n = nt * kStates + (l >> 3) * NT + v % NT;
-            if (t0 + t < s.T && n < Np)
-                W.gBC[((((int64_t)cu * s.B + b) * s.T + t0 + t) * s.G + grp) * 2 * Np + o * Np + n] = t0 + t < len ? x : 0.f;
+        for (int j = 0; j < 2; ++j) {
+            const int t = 2 * (4 * j + (lane >> 5) * 2 + (lane >> 4 & 1)) + (lane >> 3 & 1), n = n0 + (lane & 3);
+            if (t0 + t < T && n < Np)
+                S.gBC[((((int64_t)cu * s.B + b) * T + t0 + t) * s.G + grp) * 2 * Np + (lane >> 2 & 1) * Np + n] =
+                    t0 + t < len ? tot[j] : 0.f;
         }
     }
     // What each set of channels kept.
     for (int set = 0; set < sets; ++set) {
-        const int in_group = cu * cut + set * kGradStep + w * kGradChan + d;
-        const bool live = in_group < Cg;
-        const int64_t c = (int64_t)grp * Cg + in_group;
-        const float* const mine = own + set * 64 * (2 * NT + 2);
-        if (live) {
+        const int in_group = c_first + set * 64 + lane;
+        const int64_t c = grp * Cg + in_group;
+        const float* const mine = own + set * kOwnStep;
+        if (in_group < c_end && states) {
+            float v[NPT];
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-                if (n0 + i < Np) W.gA[state_at(s, b * blocks + k, n0 + i, c)] = mine[(NT + i) * 64];
+            for (int i = 0; i < NPT; ++i) v[i] = mine[(NPT + i) * 64];
+            store16<float>(S.gA + state_at(s, b * blocks + k, n0, c), v);
         }
-        if (whole) {
-            float sD = mine[(2 * NT) * 64], sb = mine[(2 * NT + 1) * 64];
+    }
+    if (!whole) return;
+    __syncthreads();
+    for (int j = threadIdx.x; j < sets * 128; j += 64 * W) {  // D's sums, then the bias's: the waves' in order
+        const int set = j >> 7, o = j >> 6 & 1, l = j & 63, in_group = c_first + set * 64 + l;
+        const float* const all = reinterpret_cast<float*>(lds + sizeof(GradLds<W>)) + set * kOwnStep + (2 * NPT + o) * 64 + l;
+        float v = all[0];
 #pragma unroll
-            for (int o = 8; o < 64; o <<= 1) sD += __shfl_xor(sD, o), sb += __shfl_xor(sb, o);
-            if (live && nl == 0) {
-                W.gDb[((b * blocks + k) * 2) * s.C + c] = sD;
-                W.gDb[((b * blocks + k) * 2 + 1) * s.C + c] = sb;
-            }
-        }
+        for (int i = 1; i < W; ++i) v += all[i * 64 * kGradOwn];
+        if (in_group < c_end) S.gDb[((b * blocks + k) * 2 + o) * s.C + grp * Cg + in_group] = v;
     }
 }
 
 // More than 16 states: the tiles' sums over states added, and the gradients of each token and
-// channel.  A lane walks down one block's tokens of one channel.
+// channel.  A workgroup takes one block's tokens of 64 channels, 16 tokens a wave.
 template <class E>
-__global__ __launch_bounds__(64) void sel_finish_kernel(SelShape s, SelArgs A, SelBwdArgs g, SelBwdScratch W,
-                                                        int64_t blocks, int ntiles) {
+__global__ __launch_bounds__(256) void sel_finish_kernel(SelShape s, SelArgs A, SelBwdArgs g, SelBwdScratch W,
+                                                         int64_t blocks, int ntiles) {
+    __shared__ float acc[2][4][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t cols = (s.C + 63) / 64;
-    const int64_t c = (int64_t)(blockIdx.x % cols) * 64 + threadIdx.x;
+    const int64_t c = (int64_t)(blockIdx.x % cols) * 64 + lane;
     const int64_t row = blockIdx.x / cols, k = row % blocks, b = row / blocks;
-    if (c >= s.C) return;
-    const int64_t len = row_length(s, b);
-    const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
+    const bool live = c < s.C;
+    const int64_t len = row_length(s, b), plane = s.B * s.T * s.C, t0 = k * kSelBlock + w * kSelTile;
     float sD = 0.f, sb = 0.f;
-    for (int64_t t = k * kSelBlock; t < (k + 1) * kSelBlock && t < s.T; ++t) {
-        const int64_t at = (b * s.T + t) * s.C + c;
-        float gu = 0.f, gd = 0.f, gz = 0.f;
-        if (t < len) {
-            float s1 = 0.f, s2 = 0.f, s3 = 0.f;
-            for (int i = 0; i < ntiles; ++i) {
-                const float* o = W.q + ((int64_t)i * s.B * s.T * s.C + at) * 3;
-                s1 += o[0], s2 += o[1], s3 += o[2];
+    if (live) {
+        const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
+#pragma unroll 4
+        for (int64_t t = t0; t < t0 + kSelTile && t < s.T; ++t) {
+            const int64_t at = (b * s.T + t) * s.C + c;
+            float gu = 0.f, gd = 0.f, gz = 0.f;
+            if (t < len) {
+                float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+                for (int i = 0; i < ntiles; ++i) {
+                    const float* o = W.q + (int64_t)i * 3 * plane + at;
+                    s1 += o[0], s2 += o[plane], s3 += o[2 * plane];
+                }
+                const float u = (float)reinterpret_cast<const E*>(A.u)[at];
+                float d = (float)reinterpret_cast<const E*>(A.dt)[at] + bias, sig = 1.f;
+                float p = (float)reinterpret_cast<const E*>(g.gy)[at];
+                if (s.softplus) d = softplus(d, sig);
+                if (A.z) {
+                    const float z = (float)reinterpret_cast<const E*>(A.z)[at];
+                    const float sg = logistic(z);
+                    gz = p * sg * fmaf(z, 1.f - sg, 1.f) * fmaf(Dc, u, s3);
+                    p *= z * sg;
+                }
+                gd = fmaf(u, s2, s1) * sig;
+                gu = fmaf(Dc, p, d * s2);
+                sD = fmaf(p, u, sD);
+                sb += gd;
             }
-            const float u = (float)reinterpret_cast<const E*>(A.u)[at];
-            float d = (float)reinterpret_cast<const E*>(A.dt)[at] + bias, sig = 1.f;
-            float p = (float)reinterpret_cast<const E*>(g.gy)[at];
-            if (s.softplus) d = softplus(d, sig);
-            if (A.z) {
-                const float z = (float)reinterpret_cast<const E*>(A.z)[at];
-                const float sg = logistic(z);
-                gz = p * sg * fmaf(z, 1.f - sg, 1.f) * fmaf(Dc, u, s3);
-                p *= z * sg;
-            }
-            gd = fmaf(u, s2, s1) * sig;
-            gu = fmaf(Dc, p, d * s2);
-            sD = fmaf(p, u, sD);
-            sb += gd;
+            reinterpret_cast<E*>(g.gu)[at] = (E)gu;
+            reinterpret_cast<E*>(g.gdt)[at] = (E)gd;
+            if (A.z) reinterpret_cast<E*>(g.gz)[at] = (E)gz;
         }
-        reinterpret_cast<E*>(g.gu)[at] = (E)gu;
-        reinterpret_cast<E*>(g.gdt)[at] = (E)gd;
-        if (A.z) reinterpret_cast<E*>(g.gz)[at] = (E)gz;
     }
-    W.gDb[(row * 2) * s.C + c] = sD;
-    W.gDb[(row * 2 + 1) * s.C + c] = sb;
+    acc[0][w][lane] = sD, acc[1][w][lane] = sb;
+    __syncthreads();
+    if (w < 2 && live)
+        W.gDb[(row * 2 + w) * s.C + c] = acc[w][0][lane] + acc[w][1][lane] + acc[w][2][lane] + acc[w][3][lane];
 }
 
 // Column sums of (rows, cols), rows added by 16 strips at once, then the strips in order.  The
@@ -457,53 +522,34 @@ __global__ __launch_bounds__(256) void sel_fold_bc_kernel(SelShape s, const floa
     }
 }
 
-template <class E, int W, int NPT>
-hipError_t reverse(const SelShape& s, const SelArgs& A, const void* gy, const float* bc, float* out, float* sum,
-                   hipStream_t st) {
-    const int group_tiles = (int)ceil_div(s.C / s.G, 64);
+template <class E, int W>
+hipError_t by_waves(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const float* bc, const float* keep,
+                    const SelBwdScratch& S, hipStream_t st) {
     const int64_t blocks = sel_blocks(s);
-    hipLaunchKernelGGL((sel_reverse_kernel<E, W, NPT>), dim3((unsigned)(s.B * blocks * s.G * group_tiles)),
-                       dim3(64 * W), 0, st, s, A, (const E*)gy, bc, out, sum, (int)blocks, group_tiles);
-    return hipGetLastError();
-}
-
-template <class E>
-hipError_t reverse_by_states(const SelShape& s, const SelArgs& A, const SelPlan& p, const void* gy, const float* bc,
-                             float* out, float* sum, hipStream_t st) {
-    if (p.npt == 1) return reverse<E, 1, 1>(s, A, gy, bc, out, sum, st);
-    if (p.npt == 2) return reverse<E, 1, 2>(s, A, gy, bc, out, sum, st);
-    if (p.npt == 4) {
-        if (p.waves == 1) return reverse<E, 1, 4>(s, A, gy, bc, out, sum, st);
-        if (p.waves == 2) return reverse<E, 2, 4>(s, A, gy, bc, out, sum, st);
-        return reverse<E, 4, 4>(s, A, gy, bc, out, sum, st);
-    }
-    if (p.npt == 8)
-        return p.waves == 4 ? reverse<E, 4, 8>(s, A, gy, bc, out, sum, st) : reverse<E, 8, 8>(s, A, gy, bc, out, sum, st);
-    return reverse<E, 8, 16>(s, A, gy, bc, out, sum, st);
-}
-
-template <class E, int NT>
-hipError_t gradients(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const float* keep,
-                     const SelBwdScratch& W, hipStream_t st) {
-    const int64_t blocks = sel_blocks(s);
-    const int ntiles = (int)ceil_div(s.N, 8 * NT);
-    const size_t lds = sizeof(GradLds<NT>) + (size_t)(W.cut / kGradChan) * 64 * (2 * NT + 2) * sizeof(float);
-    hipLaunchKernelGGL((sel_gradient_kernel<E, NT>), dim3((unsigned)(s.B * blocks * s.G * W.cuts * ntiles)),
-                       dim3(64 * kGradWaves), lds, st, s, A, g, keep, W, blocks, ntiles);
+    const int ntiles = (int)ceil_div(s.N, kBwdNpt * W), group_tiles = (int)ceil_div(s.C / s.G, 64);
+    hipLaunchKernelGGL((sel_reverse_kernel<E, W>), dim3((unsigned)(s.B * blocks * ntiles * s.G * group_tiles)),
+                       dim3(64 * W), 0, st, s, A, (const E*)g.gy, bc, S.carry, S.sum, (int)blocks, group_tiles, ntiles);
     hipError_t e = hipGetLastError();
+    if (e == hipSuccess) e = run_sel_join(s, A.A, S.carry, S.sum, blocks, g.gs_out, g.gs_in, true, st);
+    if (e != hipSuccess) return e;
+    const size_t lds = sizeof(GradLds<W>) + (size_t)(S.cut / 64) * W * 64 * kGradOwn * sizeof(float);
+    hipLaunchKernelGGL((sel_gradient_kernel<E, W>), dim3((unsigned)(s.B * blocks * ntiles * s.G * S.cuts)), dim3(64 * W),
+                       lds, st, s, A, g, bc, keep, S, (int)blocks, ntiles);
+    e = hipGetLastError();
     if (e != hipSuccess || ntiles == 1) return e;
-    hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(s.B * blocks * ceil_div(s.C, 64))), dim3(64), 0, st, s,
-                       A, g, W, blocks, ntiles);
+    hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(s.B * blocks * ceil_div(s.C, 64))), dim3(256), 0, st, s,
+                       A, g, S, blocks, ntiles);
     return hipGetLastError();
 }
 
 template <class E>
-hipError_t backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const SelPlan& p, const float* bc,
-                    const float* keep, const SelBwdScratch& W, hipStream_t st) {
-    const int64_t blocks = sel_blocks(s), rows = s.B * blocks;
-    hipError_t e = reverse_by_states<E>(s, A, p, g.gy, bc, W.carry, W.sum, st);
-    if (e == hipSuccess) e = run_sel_join(s, A.A, W.carry, W.sum, blocks, g.gs_out, g.gs_in, true, st);
-    if (e == hipSuccess) e = s.N <= 8 ? gradients<E, 1>(s, A, g, keep, W, st) : gradients<E, 2>(s, A, g, keep, W, st);
+hipError_t backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const float* bc, const float* keep,
+                    const SelBwdScratch& W, hipStream_t st) {
+    const int64_t rows = s.B * sel_blocks(s);
+    const int waves = sel_backward_plan(s).waves;
+    hipError_t e = waves == 1   ? by_waves<E, 1>(s, A, g, bc, keep, W, st)
+                   : waves == 2 ? by_waves<E, 2>(s, A, g, bc, keep, W, st)
+                                : by_waves<E, 4>(s, A, g, bc, keep, W, st);
     if (e != hipSuccess) return e;
     const int64_t cols = (int64_t)sel_n4(s) * 4 * s.C;
     hipLaunchKernelGGL((sel_fold_kernel<true>), dim3((unsigned)ceil_div(cols, 16)), dim3(256), 0, st, s, W.gA, rows,
@@ -524,18 +570,23 @@ hipError_t backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, co
 
 }  // namespace
 
-int64_t sel_cut(const SelShape& s) {
-    // Channels of a workgroup of the gradients: up to 128, fewer where that leaves the chip empty.
-    const int64_t Cg = s.C / s.G, rows = s.B * sel_blocks(s) * s.G;
-    int64_t cut = 128;
-    while (cut > kGradStep && rows * ceil_div(Cg, cut) < 1024) cut /= 2;
-    return cut;
+SelPlan sel_backward_plan(const SelShape& s) {
+    SelPlan p{};
+    p.npt = kBwdNpt;
+    p.waves = s.N <= 4 ? 1 : s.N <= 8 ? 2 : 4;  // of a workgroup
+    p.tiles_n = (int)ceil_div(s.N, kBwdNpt * p.waves);
+    return p;
 }
 
-hipError_t run_sel_backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const SelPlan& p, const float* bc,
-                            const float* keep, const SelBwdScratch& W, hipStream_t st) {
-    return s.dtype == kBf16 ? backward<bf16_t>(s, A, g, p, bc, keep, W, st)
-                            : backward<float>(s, A, g, p, bc, keep, W, st);
+int64_t sel_cut(const SelShape& s) {
+    // Channels of a workgroup of the gradients: 128, or 64 where that leaves the chip empty.
+    const int64_t Cg = s.C / s.G, rows = s.B * sel_blocks(s) * s.G;
+    return rows * ceil_div(Cg, 128) < 1024 ? 64 : 128;
+}
+
+hipError_t run_sel_backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const float* bc, const float* keep,
+                            const SelBwdScratch& W, hipStream_t st) {
+    return s.dtype == kBf16 ? backward<bf16_t>(s, A, g, bc, keep, W, st) : backward<float>(s, A, g, bc, keep, W, st);
 }
 
 }  // namespace linrec
