@@ -1206,12 +1206,11 @@ linrec::SelShape sel_shape(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N
     return {B, T, C, (int)G, (int)N, dtype, softplus, lengths};
 }
 
-// The backward's workgroups: one a block of 64 tokens and channels, at most 8 waves.
+// The backward's workgroups: one a block of 64 tokens and channels and up to 16 states, 256 lanes.
 int check_sel_backward(const linrec::SelShape& s) {
-    const int64_t rows = s.B * linrec::sel_blocks(s) * s.G, Cg = s.C / s.G;
-    if (rows >= (1 << 23) || rows * ceil_div(Cg, 64) >= (1 << 23) ||
-        rows * ceil_div(Cg, linrec::sel_cut(s)) * ceil_div(s.N, 16) >= (1 << 24))
-        return fail(LINREC_ERR_UNSUPPORTED, "B*T*C/4096 is above 2^23 in a backward");
+    const int64_t blocks = s.B * linrec::sel_blocks(s);
+    if (blocks >= (1 << 23) || blocks * s.G * ceil_div(s.C / s.G, 64) * ceil_div(s.N, 16) >= (1 << 24))
+        return fail(LINREC_ERR_UNSUPPORTED, "B*T*C/4096 (times N/16) is above 2^24 in a backward");
     return LINREC_OK;
 }
 
@@ -1253,8 +1252,7 @@ size_t sel_backward_layout(const linrec::SelShape& s, void* ws, linrec::SelBwdSc
     w.carry = w.gA = take((size_t)(rows * s.C) * linrec::sel_n4(s) * 4);
     w.sum = take((size_t)(rows * s.C));
     w.gDb = take((size_t)(rows * 2 * s.C));
-    w.cut = linrec::sel_cut(s);
-    w.cuts = ceil_div(s.C / s.G, w.cut);
+    w.cuts = ceil_div(s.C / s.G, 64);
     w.gBC = take((size_t)(w.cuts * s.B * s.T * s.G) * 2 * linrec::sel_n4(s) * 4);
     w.q = take(s.N > 16 ? (size_t)ceil_div(s.N, 16) * (size_t)(s.B * s.T * s.C) * 3 : 0);
     if (W) *W = w;

@@ -50,10 +50,6 @@ __device__ __forceinline__ const void* elems(const void* p, int64_t first) {
     return reinterpret_cast<const E*>(p) + first;
 }
 
-// A vector of N floats; one is a float.
-template <int N> struct SelVec { typedef float type __attribute__((ext_vector_type(N))); };
-template <> struct SelVec<1> { typedef float type; };
-
 // What the states of one wave need of a few tokens: B and C by scalar loads, NF floats, and the
 // channels' own pair of floats from LDS.  Scalar loads come back in any order, so a wait for one is a
 // wait for all of them and for LDS: both are asked for together, one group ahead of their use.
@@ -77,6 +73,13 @@ struct SelGroup {
     __device__ __forceinline__ float B(int k, int i) const { return bc[(k * 2 * NPT + i) / 16][(k * 2 * NPT + i) % 16]; }
     __device__ __forceinline__ float C(int k, int i) const { return B(k, NPT + i); }
 };
+
+// LDS written by lanes of this wave is read by others of it behind this.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // Tokens of row b that are there.
 __device__ __forceinline__ int64_t row_length(const SelShape& s, int64_t b) {

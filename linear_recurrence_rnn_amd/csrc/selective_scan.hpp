@@ -70,11 +70,10 @@ struct SelBwdScratch {
     float* sum;    // (B,blocks,C) sums of d
     float* gA;     // (B*blocks) rows of states
     float* gDb;    // (B*blocks,2,C): D's gradient, bias's
-    float* gBC;    // (cuts,B,T,G,2,4*n4): B's and C's gradients by channel ranges of `cut` of a group
+    float* gBC;    // (cuts,B,T,G,2,4*n4): B's and C's gradients by ranges of 64 channels of a group
     float* q;      // (tiles of 16 states,3,B,T,C) where N > 16: sums over the states of one
-    int64_t cut, cuts;
+    int64_t cuts;
 };
-int64_t sel_cut(const SelShape& s);
 
 // keep: (B,tiles) rows of states, the state before each tile; null: not kept.
 hipError_t run_sel_prepare(const SelShape& s, const SelArgs& A, const SelPlan& p, float* bc, hipStream_t st);

@@ -17,11 +17,11 @@
 // The last kernel sums over states (for each token and channel) and over channels (for each token
 // and state).  Like the forward, a wave holds 64 channels, a lane each, and 4 states of them, with B and C by
 // scalar loads; sums over the states are added in the lane and over the waves through LDS.  Sums over the
-// lanes go through the matrix unit, which is idle otherwise: a value as one operand of the 16x16x4 product
-// and a column of ones as the other add the lanes 16 apart and put the result into that column, so
-// that 16 products into one accumulator leave 16 values side by side, with 16 shares each, four of them in a
-// lane; two folds across the lanes add the rest for 64 values at once.  In float32, and 11 cycles of
-// the vector unit a state where folds alone would take 24.
+// lanes are transposed there: 16 values (4 tokens, 4 states) are written as rows of 64 and read back as
+// quarters of rows, 16 floats a lane, that the lane adds; what the four lanes of a row have left is folded for
+// 64 values at once.  9 cycles of the vector unit a state for both sums, where folds across the
+// lanes alone would take 24.  (float32 products of the matrix unit with columns of ones were slower: on this
+// chip they keep the vector unit from its own work, 34 cycles and 35 of it taking 74.)
 // Sums over blocks, batch rows and channel ranges are partial sums in the workspace, added in
 // order by small kernels at the end: nothing depends on timing.
 #include "selective_math.hpp"
@@ -124,38 +124,36 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
     if (nt == 0 && w == 0) sum[(b * blocks + k) * s.C + c] = total;
 }
 
-// ---- sums across the lanes of a wave ---------------------------------------------------
+// ---- the gradients --------------------------------------------------------------------
 
-// Lanes below 32: a summed over lanes l and l+32; the others: b.  (xor 16: by rows of 16.)
-__device__ __forceinline__ float fold32(float a, float b) {
-    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+// The lanes with `up` false: a summed over the two lanes that the DPP permutation CTRL, an
+// involution, exchanges; the others: b.
+template <int CTRL>
+__device__ __forceinline__ float fold_dpp(float a, float b, bool up) {
+    const float own = up ? b : a, other = up ? a : b;
+    return own + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(other), CTRL, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float fold16(float a, float b) {
-    const u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
+constexpr int kXor1 = 0xb1, kXor2 = 0x4e;  // quad_perm [1,0,3,2] and [2,3,0,1]
 
-// LDS of the gradient kernel; behind it, per set of 64 channels: G, gA (4 states each) and the lane's
-// own sums of gD and gbias, for every wave.
+constexpr int kRowPad = 68;  // floats of a row of 64: a quarter starts on 16 bytes, 16 rows on 16 x 4 banks
+
 template <int W>
 struct GradLds {
-    f32x2 du[kSelTile][64];               // d, d u
-    f32x2 pu[kSelTile][64];               // p, u
-    float part[2][W][kSelTile][64];       // the waves' shares of sums over the states
+    f32x2 du[kSelTile][64];          // d, d u
+    f32x2 pu[kSelTile][64];          // p, u
+    float part[2][W][kSelTile][64];  // the waves' shares of sums over the states
+    float rows[W][16][kRowPad];      // 16 values of a wave on their way to being summed over its lanes
 };
-constexpr int kGradOwn = 2 * kBwdNpt + 2;
 
 template <class E, int W>
 __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
                                                                               const float* __restrict__ bc,
                                                                               const float* __restrict__ keep,
                                                                               SelBwdScratch S, int blocks, int ntiles) {
-    constexpr int NPT = kBwdNpt, TW = kSelTile / W, kPairs = kSelTile / 2;
-    extern __shared__ __align__(16) char lds[];
-    GradLds<W>& L = *reinterpret_cast<GradLds<W>*>(lds);
+    constexpr int NPT = kBwdNpt, TW = kSelTile / W, kPairs = kSelTile / 2, kFours = kSelTile / 4;
+    __shared__ GradLds<W> L;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int Cg = (int)(s.C / s.G), cut = (int)S.cut, cuts = (int)S.cuts;
+    const int Cg = (int)(s.C / s.G), cuts = (int)S.cuts;
     unsigned blk = blockIdx.x;
     const int cu = (int)(blk % (unsigned)cuts);
     blk /= (unsigned)cuts;
@@ -170,23 +168,17 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
     const int n0 = (nt * W + w) * NPT, Np = (s.N + 3) / 4 * 4;
     const unsigned C = (unsigned)s.C;
     const bool whole = ntiles == 1;  // sums over the states are complete
-    const int c_first = cu * cut, c_end = c_first + cut < Cg ? c_first + cut : Cg;  // in the group
-    const int sets = (c_end - c_first + 63) / 64;
-    float* const own = reinterpret_cast<float*>(lds + sizeof(GradLds<W>)) + w * 64 * kGradOwn + lane;
-    constexpr int kOwnStep = W * 64 * kGradOwn;
-
-    for (int j = 0; j < sets; ++j)
-        for (int i = 0; i < kGradOwn; ++i) own[j * kOwnStep + i * 64] = 0.f;
+    const bool gated = A.z != nullptr, soft = s.softplus != 0, states = n0 < s.N;
+    const bool live = cu * 64 + lane < Cg;
+    const unsigned c = (unsigned)(grp * Cg + (live ? cu * 64 + lane : Cg - 1));
 
     // Tiles of absent tokens alone: no gradients.
     const int live_end = len < t_end ? (len > t_begin ? (len + kSelTile - 1) / kSelTile * kSelTile : t_begin) : t_end;
     for (int t = live_end + w; t < t_end; t += W) {
-        if (whole) {
-            const int64_t at = (b * T + t) * s.C + grp * Cg;
-            for (int c = c_first + lane; c < c_end; c += 64) {
-                reinterpret_cast<E*>(g.gu)[at + c] = reinterpret_cast<E*>(g.gdt)[at + c] = (E)0.f;
-                if (A.z) reinterpret_cast<E*>(g.gz)[at + c] = (E)0.f;
-            }
+        if (whole && live) {
+            const int64_t at = (b * T + t) * s.C + c;
+            reinterpret_cast<E*>(g.gu)[at] = reinterpret_cast<E*>(g.gdt)[at] = (E)0.f;
+            if (gated) reinterpret_cast<E*>(g.gz)[at] = (E)0.f;
         }
         for (int j = lane; j < 2 * W * NPT; j += 64) {
             const int n = nt * W * NPT + j % (W * NPT);
@@ -194,22 +186,17 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
         }
     }
 
-    // What a lane reads of a set of channels in a tile: its wave's tokens' inputs and its states before the
-    // tile, asked for a set ahead.  Absent tokens are read as the last one that is there, lanes behind
-    // the last channel as that, inputs that were not given as others: none of that is used.
-    const bool gated = A.z != nullptr, soft = s.softplus != 0, states = n0 < s.N;
+    // What a lane reads of a tile: its wave's tokens' inputs and its states before the tile, asked for a
+    // tile ahead.  Absent tokens are read as the last one that is there, lanes behind the last channel
+    // as that, inputs that were not given as others: none of that is used.
     const void* const zp = gated ? A.z : A.u;
-    const float *const biasp = A.bias ? A.bias : A.A, *const Dp = A.D ? A.D : A.A;
     struct Raw {
         E u[TW], dt[TW], z[TW], gy[TW];  // as they come: a conversion would wait for the load
-        float a[NPT], bias, D;
         f32x4 h0;
     } next;
-    const auto fetch = [&](int q, int set) {
+    const auto fetch = [&](int q) {
         const int t0 = t_begin + q * kSelTile;
         const int64_t base = (b * T + t0) * s.C;
-        const int in_group = c_first + set * 64 + lane;
-        const unsigned c = (unsigned)(grp * Cg + (in_group < Cg ? in_group : Cg - 1));
 #pragma unroll
         for (int e = 0; e < TW; ++e) {
             const int t = t0 + w * TW + e < len ? w * TW + e : len - 1 - t0;
@@ -221,213 +208,202 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
         }
         const void* const hp = elems<float>(keep, (b * tiles + t0 / kSelTile) * Np * s.C);
         next.h0 = load_elem<f32x4>(hp, ((unsigned)(states ? n0 : 0) * C + c * 4) * 4);
-#pragma unroll
-        for (int i = 0; i < NPT; ++i) next.a[i] = load_elem<float>(A.A, (c * (unsigned)s.N + (n0 + i < s.N ? n0 + i : 0)) * 4);
-        next.bias = load_elem<float>(biasp, c * 4);
-        next.D = load_elem<float>(Dp, c * 4);
     };
     const int q_first = (live_end - t_begin + kSelTile - 1) / kSelTile - 1;
-    if (q_first >= 0) fetch(q_first, 0);
+    if (q_first >= 0) fetch(q_first);
 
-    float one[16];  // columns of ones
+    const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
+    float a2[NPT], G[NPT], gA[NPT], sD = 0.f, sb = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) one[i] = (lane & 15) == i ? 1.f : 0.f;
+    for (int i = 0; i < NPT; ++i) {
+        a2[i] = n0 + i < s.N ? A.A[(int64_t)c * s.N + n0 + i] * kLog2e : 0.f;
+        G[i] = n0 + i < s.N ? S.carry[state_at(s, b * blocks + k, n0 + i, c)] : 0.f;
+        gA[i] = 0.f;
+    }
+    // A lane's quarter of a row.
+    float* const rows = &L.rows[w][0][0];
+    const float* const quarter = rows + (lane >> 2) * kRowPad + (lane & 3) * 16;
 
     for (int q = q_first; q >= 0; --q) {
         const int t0 = t_begin + q * kSelTile;
+        const int64_t base = (b * T + t0) * s.C;
         const float* row = bc + ((((b * tiles + t0 / kSelTile) * s.G + grp) * ntiles + nt) * W + w) * (kSelTile * 2 * NPT);
-        float tot[2] = {0.f, 0.f};  // sums over channels: 64 values each
-        for (int set = 0; set < sets; ++set) {
-            const bool live = c_first + set * 64 + lane < c_end;
-            const unsigned c = (unsigned)(grp * Cg + c_first + set * 64 + lane);
-            float* const mine = own + set * kOwnStep;
-            const int64_t base = (b * T + t0) * s.C;
-            const float Dc = A.D ? next.D : 0.f, bias = A.bias ? next.bias : 0.f;
-            float sig[TW], gzf[TW];
+        float sig[TW], gzf[TW], h0[NPT];
 #pragma unroll
-            for (int e = 0; e < TW; ++e) {
-                const bool there = live && t0 + w * TW + e < len;
-                const float u = there ? (float)next.u[e] : 0.f, gy = there ? (float)next.gy[e] : 0.f;
-                const float raw = (float)next.dt[e] + bias, z = there ? (float)next.z[e] : 0.f, sg = logistic(z);
-                float d = softplus(raw, sig[e]);
-                d = there ? (soft ? d : raw) : 0.f;
-                sig[e] = there ? (soft ? sig[e] : 1.f) : 0.f;
-                gzf[e] = gy * sg * fmaf(z, 1.f - sg, 1.f);
-                const f32x2 du = {d, d * u}, pu = {gy * (gated ? z * sg : 1.f), u};
-                L.du[w * TW + e][lane] = du;
-                L.pu[w * TW + e][lane] = pu;
-            }
-            float a2[NPT], G[NPT], gA[NPT], h0[NPT];
+        for (int e = 0; e < TW; ++e) {
+            const bool there = live && t0 + w * TW + e < len;
+            const float u = there ? (float)next.u[e] : 0.f, gy = there ? (float)next.gy[e] : 0.f;
+            const float raw = (float)next.dt[e] + bias, z = there ? (float)next.z[e] : 0.f, sg = logistic(z);
+            float d = softplus(raw, sig[e]);
+            d = there ? (soft ? d : raw) : 0.f;
+            sig[e] = there ? (soft ? sig[e] : 1.f) : 0.f;
+            gzf[e] = gy * sg * fmaf(z, 1.f - sg, 1.f);
+            const f32x2 du = {d, d * u}, pu = {gy * (gated ? z * sg : 1.f), u};
+            L.du[w * TW + e][lane] = du;
+            L.pu[w * TW + e][lane] = pu;
+        }
 #pragma unroll
-            for (int i = 0; i < NPT; ++i) {
-                a2[i] = n0 + i < s.N ? next.a[i] * kLog2e : 0.f, h0[i] = n0 + i < s.N ? next.h0[i] : 0.f;
-                G[i] = mine[i * 64], gA[i] = mine[(NPT + i) * 64];
-            }
-            if (q == q_first && live && states) {
-                const f32x4 v = *reinterpret_cast<const f32x4*>(S.carry + state_at(s, b * blocks + k, n0, c));
+        for (int i = 0; i < NPT; ++i) h0[i] = n0 + i < s.N ? next.h0[i] : 0.f;
+        fetch(q > 0 ? q - 1 : 0);  // in one place, the last time for nothing: two places would cost their addresses twice
+        __syncthreads();
+        // The states of the tile again, their sums q3 = sum C h, and the sums over channels of p h.
+        float h[kSelTile][NPT], a[kSelTile][NPT], shares[kFours];
+        f32x4 quar[4];
+        const auto ask_sums = [&]() {
 #pragma unroll
-                for (int i = 0; i < NPT; ++i) G[i] = n0 + i < s.N ? v[i] : 0.f;
-            }
-            {  // in one place, the last time for nothing: two places would cost their addresses twice
-                const bool same = set + 1 < sets;
-                fetch(same || q == 0 ? q : q - 1, same ? set + 1 : 0);
-            }
-            __syncthreads();
-            // The states of the tile again, and their sums q3 = sum C h.
-            float h[kSelTile][NPT], a[kSelTile][NPT];
-            {
-                typedef SelGroup<NPT, 16> Group;
-                constexpr int kGroups = Group::kGroups, kTok = Group::kTok;
-                Group of[2];
-                of[0].fetch(row, L.du, lane, 0);
+            for (int i = 0; i < 4; ++i) quar[i] = *reinterpret_cast<const f32x4*>(quarter + 4 * i);
+        };
+        const auto take_sums = [&]() {
+            const f32x4 v = (quar[0] + quar[1]) + (quar[2] + quar[3]);
+            return (v[0] + v[1]) + (v[2] + v[3]);
+        };
+        const auto fold = [&]() {  // lane & 3 is the four of tokens
+            const float x = fold_dpp<kXor1>(shares[0], shares[1], lane & 1), y = fold_dpp<kXor1>(shares[2], shares[3], lane & 1);
+            return fold_dpp<kXor2>(x, y, lane & 2);
+        };
+        {
+            typedef SelGroup<NPT, 16> Group;
+            constexpr int kGroups = Group::kGroups, kTok = Group::kTok;
+            Group of[2];
+            float pt[2][2];
+            const auto ahead = [&](int j) {
+                of[j & 1].fetch(row, L.du, lane, j);
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    const Group& v = of[j & 1];
-                    if (j + 1 < kGroups) of[(j + 1) & 1].fetch(row, L.du, lane, j + 1);
-                    __builtin_amdgcn_sched_barrier(0);
+                for (int r = 0; r < kTok; ++r) pt[j & 1][r] = L.pu[j * kTok + r][lane][0];
+            };
+            ahead(0);
 #pragma unroll
-                    for (int r = 0; r < kTok; ++r) {
-                        const int t = j * kTok + r;
-                        float q3 = 0.f;
+            for (int j = 0; j < kGroups; ++j) {
+                const Group& v = of[j & 1];
+                if (j + 1 < kGroups) ahead(j + 1);
+                if (j % 2 == 0 && j > 0) ask_sums();
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                        for (int i = 0; i < NPT; ++i) {
-                            a[t][i] = fast_exp2(v.x[r][0] * a2[i]);
-                            h[t][i] = fmaf(a[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], v.x[r][1] * v.B(r, i));
-                            q3 = fmaf(v.C(r, i), h[t][i], q3);
-                        }
-                        L.part[0][w][t][lane] = q3;
+                for (int r = 0; r < kTok; ++r) {
+                    const int t = j * kTok + r;
+                    float q3 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NPT; ++i) {
+                        a[t][i] = fast_exp2(v.x[r][0] * a2[i]);
+                        h[t][i] = fmaf(a[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], v.x[r][1] * v.B(r, i));
+                        q3 = fmaf(v.C(r, i), h[t][i], q3);
+                        rows[(t % 4 * NPT + i) * kRowPad + lane] = pt[j & 1][r] * h[t][i];
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                    L.part[0][w][t][lane] = q3;
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                if (j % 2 == 1 && j > 1) shares[j / 2 - 1] = take_sums();
             }
-            __syncthreads();
-            if (gated || !whole) {
-#pragma unroll
-                for (int e = 0; e < TW; ++e) {
-                    const int t = w * TW + e;
-                    float core = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) core += L.part[0][j][t][lane];
-                    if (!live || t0 + t >= T) continue;
-                    const unsigned at = (unsigned)t * C + c;
-                    if (!whole)
-                        store_elem<float>(S.q + ((int64_t)nt * 3 + 2) * s.B * T * s.C + base, at * 4, core);
-                    else
-                        store_elem<E>((E*)g.gz + base, at * (unsigned)sizeof(E),
-                                      t0 + t < len ? gzf[e] * fmaf(Dc, L.pu[t][lane][1], core) : 0.f);
-                }
-            }
-            __syncthreads();
-            // Backwards: q1 = sum A m, q2 = sum g B, and the sums over channels of g d u and p h.
-            float shares[kPairs];
-            {
-                f32x4 acc[2];
-                f32x2 x[2][2], y[2][2];
-                f32x16 v[2];
-                const auto ahead = [&](int j) {  // the pair of tokens 2 j, 2 j + 1
-                    typedef const __attribute__((address_space(4))) f32x16* P;
-                    v[j & 1] = *reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + j * 16));
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) x[j & 1][r] = L.du[2 * j + r][lane], y[j & 1][r] = L.pu[2 * j + r][lane];
-                };
-                ahead(kPairs - 1);
-#pragma unroll
-                for (int j = kPairs - 1; j >= 0; --j) {
-                    if (j > 0) ahead(j - 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                    f32x4& sum = acc[j & 1];
-#pragma unroll
-                    for (int r = 1; r >= 0; --r) {
-                        const int t = 2 * j + r;
-                        const float d = x[j & 1][r][0], du = x[j & 1][r][1], p = y[j & 1][r][0];
-                        float q1 = 0.f, q2 = 0.f;
-#pragma unroll
-                        for (int i = 0; i < NPT; ++i) {
-                            const float gt = fmaf(v[j & 1][r * 2 * NPT + NPT + i], p, G[i]);
-                            G[i] = gt * a[t][i];
-                            const float m = G[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
-                            gA[i] = fmaf(d, m, gA[i]);
-                            q1 = fmaf(a2[i], m, q1);
-                            q2 = fmaf(gt, v[j & 1][r * 2 * NPT + i], q2);
-                            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                            sum = __builtin_amdgcn_mfma_f32_16x16x4f32(gt * du, one[r * 8 + i], r == 1 && i == 0 ? zero : sum,
-                                                                       0, 0, 0);
-                            sum = __builtin_amdgcn_mfma_f32_16x16x4f32(p * h[t][i], one[r * 8 + 4 + i], sum, 0, 0, 0);
-                        }
-                        L.part[0][w][t][lane] = q1;
-                        L.part[1][w][t][lane] = q2;
-                    }
-                    if (j + 1 < kPairs) {  // the pair before, whose products have come out by now
-                        const f32x4& o = acc[(j + 1) & 1];
-                        shares[j + 1] = (o[0] + o[1]) + (o[2] + o[3]);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                shares[0] = (acc[0][0] + acc[0][1]) + (acc[0][2] + acc[0][3]);
-            }
-#pragma unroll
-            for (int i = 0; i < NPT; ++i) mine[i * 64] = G[i], mine[(NPT + i) * 64] = gA[i];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                tot[j] += fold32(fold16(shares[4 * j], shares[4 * j + 1]), fold16(shares[4 * j + 2], shares[4 * j + 3]));
-            __syncthreads();
-            float sD = 0.f, sb = 0.f;
+            wave_lds_fence();
+            ask_sums();
+            wave_lds_fence();
+            shares[kFours - 1] = take_sums();
+        }
+        const float totC = fold();
+        __syncthreads();
+        if (gated || !whole) {
 #pragma unroll
             for (int e = 0; e < TW; ++e) {
                 const int t = w * TW + e;
-                float q1 = 0.f, q2 = 0.f;
+                float core = 0.f;
 #pragma unroll
-                for (int j = 0; j < W; ++j) q1 += L.part[0][j][t][lane], q2 += L.part[1][j][t][lane];
+                for (int j = 0; j < W; ++j) core += L.part[0][j][t][lane];
                 if (!live || t0 + t >= T) continue;
                 const unsigned at = (unsigned)t * C + c;
-                if (whole) {
-                    const bool there = t0 + t < len;
-                    const float d = L.du[t][lane][0], p = L.pu[t][lane][0], u = L.pu[t][lane][1];
-                    const float gd = there ? fmaf(u, q2, q1 * kLn2) * sig[e] : 0.f;
-                    store_elem<E>((E*)g.gu + base, at * (unsigned)sizeof(E), there ? fmaf(Dc, p, d * q2) : 0.f);
-                    store_elem<E>((E*)g.gdt + base, at * (unsigned)sizeof(E), gd);
-                    sD = fmaf(p, u, sD);
-                    sb += gd;
-                } else {
-                    float* const o = S.q + (int64_t)nt * 3 * s.B * T * s.C + base;
-                    store_elem<float>(o, at * 4, q1 * kLn2);
-                    store_elem<float>(o + s.B * T * s.C, at * 4, q2);
-                }
+                if (!whole)
+                    store_elem<float>(S.q + ((int64_t)nt * 3 + 2) * s.B * T * s.C + base, at * 4, core);
+                else
+                    store_elem<E>((E*)g.gz + base, at * (unsigned)sizeof(E),
+                                  t0 + t < len ? gzf[e] * fmaf(Dc, L.pu[t][lane][1], core) : 0.f);
             }
-            mine[2 * NPT * 64] += sD;
-            mine[(2 * NPT + 1) * 64] += sb;
-            __syncthreads();
         }
-        // A lane's value: the pair by its bits 5 and 4, the token of it by bit 3, B's or C's by bit 2.
+        __syncthreads();
+        // Backwards: q1 = sum A m, q2 = sum g B, and the sums over channels of g d u.
+        asm volatile("" : "+s"(row));  // as if it were another one: B and C of a whole tile would be kept in 128 scalar registers
+        {
+            f32x2 x[2][2], y[2][2];
+            f32x16 v[2];
+            const auto ahead = [&](int j) {  // the pair of tokens 2 j, 2 j + 1
+                typedef const __attribute__((address_space(4))) f32x16* P;
+                v[j & 1] = *reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + j * 16));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int t = 2 * (4 * j + (lane >> 5) * 2 + (lane >> 4 & 1)) + (lane >> 3 & 1), n = n0 + (lane & 3);
-            if (t0 + t < T && n < Np)
-                S.gBC[((((int64_t)cu * s.B + b) * T + t0 + t) * s.G + grp) * 2 * Np + (lane >> 2 & 1) * Np + n] =
-                    t0 + t < len ? tot[j] : 0.f;
-        }
-    }
-    // What each set of channels kept.
-    for (int set = 0; set < sets; ++set) {
-        const int in_group = c_first + set * 64 + lane;
-        const int64_t c = grp * Cg + in_group;
-        const float* const mine = own + set * kOwnStep;
-        if (in_group < c_end && states) {
-            float v[NPT];
+                for (int r = 0; r < 2; ++r) x[j & 1][r] = L.du[2 * j + r][lane], y[j & 1][r] = L.pu[2 * j + r][lane];
+            };
+            ahead(kPairs - 1);
 #pragma unroll
-            for (int i = 0; i < NPT; ++i) v[i] = mine[(NPT + i) * 64];
-            store16<float>(S.gA + state_at(s, b * blocks + k, n0, c), v);
+            for (int j = kPairs - 1; j >= 0; --j) {
+                if (j > 0) ahead(j - 1);
+                if (j % 2 == 1 && j + 1 < kPairs) ask_sums();
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int r = 1; r >= 0; --r) {
+                    const int t = 2 * j + r;
+                    const float d = x[j & 1][r][0], du = x[j & 1][r][1], p = y[j & 1][r][0];
+                    float q1 = 0.f, q2 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < NPT; ++i) {
+                        const float gt = fmaf(v[j & 1][r * 2 * NPT + NPT + i], p, G[i]);
+                        G[i] = gt * a[t][i];
+                        const float m = G[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
+                        gA[i] = fmaf(d, m, gA[i]);
+                        q1 = fmaf(a2[i], m, q1);
+                        q2 = fmaf(gt, v[j & 1][r * 2 * NPT + i], q2);
+                        rows[(t % 4 * NPT + i) * kRowPad + lane] = gt * du;
+                    }
+                    L.part[0][w][t][lane] = q1;
+                    L.part[1][w][t][lane] = q2;
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                if (j % 2 == 0 && j + 2 < kPairs) shares[j / 2 + 1] = take_sums();
+            }
+            wave_lds_fence();
+            ask_sums();
+            wave_lds_fence();
+            shares[0] = take_sums();
         }
+        const float totB = fold();
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < TW; ++e) {
+            const int t = w * TW + e;
+            float q1 = 0.f, q2 = 0.f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) q1 += L.part[0][j][t][lane], q2 += L.part[1][j][t][lane];
+            if (!live || t0 + t >= T) continue;
+            const unsigned at = (unsigned)t * C + c;
+            if (whole) {
+                const bool there = t0 + t < len;
+                const float d = L.du[t][lane][0], p = L.pu[t][lane][0], u = L.pu[t][lane][1];
+                const float gd = there ? fmaf(u, q2, q1 * kLn2) * sig[e] : 0.f;
+                store_elem<E>((E*)g.gu + base, at * (unsigned)sizeof(E), there ? fmaf(Dc, p, d * q2) : 0.f);
+                store_elem<E>((E*)g.gdt + base, at * (unsigned)sizeof(E), gd);
+                sD = fmaf(p, u, sD);
+                sb += gd;
+            } else {
+                float* const o = S.q + (int64_t)nt * 3 * s.B * T * s.C + base;
+                store_elem<float>(o, at * 4, q1 * kLn2);
+                store_elem<float>(o + s.B * T * s.C, at * 4, q2);
+            }
+        }
+        // A lane's sums over channels: of the four of tokens lane & 3, the token by bits 5 and 4 and the state
+        // by bits 3 and 2.
+        const int t = 4 * (lane & 3) + (lane >> 4), n = n0 + (lane >> 2 & 3);
+        if (t0 + t < T && n < Np) {
+            float* const o = S.gBC + ((((int64_t)cu * s.B + b) * T + t0 + t) * s.G + grp) * 2 * Np + n;
+            o[0] = t0 + t < len ? totB : 0.f;
+            o[Np] = t0 + t < len ? totC : 0.f;
+        }
+        __syncthreads();  // part, du and pu have been read
     }
+    if (live && states) store16<float>(S.gA + state_at(s, b * blocks + k, n0, c), gA);
     if (!whole) return;
+    L.part[0][w][0][lane] = sD, L.part[1][w][0][lane] = sb;
     __syncthreads();
-    for (int j = threadIdx.x; j < sets * 128; j += 64 * W) {  // D's sums, then the bias's: the waves' in order
-        const int set = j >> 7, o = j >> 6 & 1, l = j & 63, in_group = c_first + set * 64 + l;
-        const float* const all = reinterpret_cast<float*>(lds + sizeof(GradLds<W>)) + set * kOwnStep + (2 * NPT + o) * 64 + l;
-        float v = all[0];
+    for (int o = w; o < 2; o += W) {
+        float v = L.part[o][0][0][lane];
 #pragma unroll
-        for (int i = 1; i < W; ++i) v += all[i * 64 * kGradOwn];
-        if (in_group < c_end) S.gDb[((b * blocks + k) * 2 + o) * s.C + grp * Cg + in_group] = v;
+        for (int i = 1; i < W; ++i) v += L.part[o][i][0][lane];
+        if (live) S.gDb[((b * blocks + k) * 2 + o) * s.C + c] = v;
     }
 }
 
@@ -532,9 +508,8 @@ hipError_t by_waves(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, co
     hipError_t e = hipGetLastError();
     if (e == hipSuccess) e = run_sel_join(s, A.A, S.carry, S.sum, blocks, g.gs_out, g.gs_in, true, st);
     if (e != hipSuccess) return e;
-    const size_t lds = sizeof(GradLds<W>) + (size_t)(S.cut / 64) * W * 64 * kGradOwn * sizeof(float);
     hipLaunchKernelGGL((sel_gradient_kernel<E, W>), dim3((unsigned)(s.B * blocks * ntiles * s.G * S.cuts)), dim3(64 * W),
-                       lds, st, s, A, g, bc, keep, S, (int)blocks, ntiles);
+                       0, st, s, A, g, bc, keep, S, (int)blocks, ntiles);
     e = hipGetLastError();
     if (e != hipSuccess || ntiles == 1) return e;
     hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(s.B * blocks * ceil_div(s.C, 64))), dim3(256), 0, st, s,
@@ -576,12 +551,6 @@ SelPlan sel_backward_plan(const SelShape& s) {
     p.waves = s.N <= 4 ? 1 : s.N <= 8 ? 2 : 4;  // of a workgroup
     p.tiles_n = (int)ceil_div(s.N, kBwdNpt * p.waves);
     return p;
-}
-
-int64_t sel_cut(const SelShape& s) {
-    // Channels of a workgroup of the gradients: 128, or 64 where that leaves the chip empty.
-    const int64_t Cg = s.C / s.G, rows = s.B * sel_blocks(s) * s.G;
-    return rows * ceil_div(Cg, 128) < 1024 ? 64 : 128;
 }
 
 hipError_t run_sel_backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const float* bc, const float* keep,
