@@ -63,12 +63,15 @@ struct SelGroup {
     f32x2 x[kTok];
     // row: the wave's 2*NPT floats of the tile's first token, those of its other tokens behind them.
     __device__ __forceinline__ void fetch(const float* row, const f32x2 (*din)[64], int lane, int q) {
+        fetch(row, q);
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) x[k] = din[q * kTok + k][lane];
+    }
+    __device__ __forceinline__ void fetch(const float* row, int q) {
         typedef const __attribute__((address_space(4))) f32x16* P;
         const P p = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + q * NF));
 #pragma unroll
         for (int k = 0; k < NF / 16; ++k) bc[k] = p[k];
-#pragma unroll
-        for (int k = 0; k < kTok; ++k) x[k] = din[q * kTok + k][lane];
     }
     __device__ __forceinline__ float B(int k, int i) const { return bc[(k * 2 * NPT + i) / 16][(k * 2 * NPT + i) % 16]; }
     __device__ __forceinline__ float C(int k, int i) const { return B(k, NPT + i); }

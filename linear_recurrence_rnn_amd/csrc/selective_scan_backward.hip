@@ -140,12 +140,13 @@ constexpr int kRowPad = 68;  // floats of a row of 64: a quarter starts on 16 by
 template <int W>
 struct GradLds {
     f32x2 du[kSelTile][64];          // d, d u
-    f32x2 pu[kSelTile][64];          // p, u
+    float p[kSelTile][64];
     float part[2][W][kSelTile][64];  // the waves' shares of sums over the states
     float rows[W][16][kRowPad];      // 16 values of a wave on their way to being summed over its lanes
 };
 
-template <class E, int W>
+// WHOLE: one workgroup has all states of its channels, so that its sums over them are complete.
+template <class E, int W, bool WHOLE>
 __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
                                                                               const float* __restrict__ bc,
                                                                               const float* __restrict__ keep,
@@ -167,7 +168,6 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
     const int t_begin = k * kSelBlock, t_end = t_begin + kSelBlock < T ? t_begin + kSelBlock : T;
     const int n0 = (nt * W + w) * NPT, Np = (s.N + 3) / 4 * 4;
     const unsigned C = (unsigned)s.C;
-    const bool whole = ntiles == 1;  // sums over the states are complete
     const bool gated = A.z != nullptr, soft = s.softplus != 0, states = n0 < s.N;
     const bool live = cu * 64 + lane < Cg;
     const unsigned c = (unsigned)(grp * Cg + (live ? cu * 64 + lane : Cg - 1));
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
     // Tiles of absent tokens alone: no gradients.
     const int live_end = len < t_end ? (len > t_begin ? (len + kSelTile - 1) / kSelTile * kSelTile : t_begin) : t_end;
     for (int t = live_end + w; t < t_end; t += W) {
-        if (whole && live) {
+        if (WHOLE && live) {
             const int64_t at = (b * T + t) * s.C + c;
             reinterpret_cast<E*>(g.gu)[at] = reinterpret_cast<E*>(g.gdt)[at] = (E)0.f;
             if (gated) reinterpret_cast<E*>(g.gz)[at] = (E)0.f;
@@ -188,26 +188,27 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
 
     // What a lane reads of a tile: its wave's tokens' inputs and its states before the tile, asked for a
     // tile ahead.  Absent tokens are read as the last one that is there, lanes behind the last channel
-    // as that, inputs that were not given as others: none of that is used.
-    const void* const zp = gated ? A.z : A.u;
+    // as that, inputs that were not given as others: none of that is used.  Bases of the block, and a
+    // lane's byte offsets in it (below 2^32: 64 tokens of at most 2^22 channels).
+    const int64_t base = (b * T + t_begin) * s.C;
+    const void *const pu = elems<E>(A.u, base), *const pdt = elems<E>(A.dt, base), *const pgy = elems<E>(g.gy, base);
+    const void* const pz = elems<E>(gated ? A.z : A.u, base);
+    const void* const ph = elems<float>(keep, (b * tiles + t_begin / kSelTile) * Np * s.C + (int64_t)(states ? n0 : 0) * s.C);
     struct Raw {
         E u[TW], dt[TW], z[TW], gy[TW];  // as they come: a conversion would wait for the load
         f32x4 h0;
     } next;
     const auto fetch = [&](int q) {
-        const int t0 = t_begin + q * kSelTile;
-        const int64_t base = (b * T + t0) * s.C;
 #pragma unroll
         for (int e = 0; e < TW; ++e) {
-            const int t = t0 + w * TW + e < len ? w * TW + e : len - 1 - t0;
-            const unsigned at = ((unsigned)t * C + c) * (unsigned)sizeof(E);
-            next.u[e] = load_elem<E>(elems<E>(A.u, base), at);
-            next.dt[e] = load_elem<E>(elems<E>(A.dt, base), at);
-            next.gy[e] = load_elem<E>(elems<E>(g.gy, base), at);
-            next.z[e] = load_elem<E>(elems<E>(zp, base), at);
+            const int t = q * kSelTile + w * TW + e;
+            const unsigned at = ((unsigned)(t_begin + t < len ? t : len - 1 - t_begin) * C + c) * (unsigned)sizeof(E);
+            next.u[e] = load_elem<E>(pu, at);
+            next.dt[e] = load_elem<E>(pdt, at);
+            next.gy[e] = load_elem<E>(pgy, at);
+            next.z[e] = load_elem<E>(pz, at);
         }
-        const void* const hp = elems<float>(keep, (b * tiles + t0 / kSelTile) * Np * s.C);
-        next.h0 = load_elem<f32x4>(hp, ((unsigned)(states ? n0 : 0) * C + c * 4) * 4);
+        next.h0 = load_elem<f32x4>(ph, ((unsigned)(q * Np) * C + c * 4) * 4);
     };
     const int q_first = (live_end - t_begin + kSelTile - 1) / kSelTile - 1;
     if (q_first >= 0) fetch(q_first);
@@ -226,21 +227,22 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
 
     for (int q = q_first; q >= 0; --q) {
         const int t0 = t_begin + q * kSelTile;
-        const int64_t base = (b * T + t0) * s.C;
         const float* row = bc + ((((b * tiles + t0 / kSelTile) * s.G + grp) * ntiles + nt) * W + w) * (kSelTile * 2 * NPT);
-        float sig[TW], gzf[TW], h0[NPT];
+        // (Whether a token is there is the same for the whole wave.  Of an absent one, or a lane without a
+        // channel, d, u and p are zero, which leaves the states and the sums over channels alone.)
+        float sig[TW], gzf[TW], us[TW], h0[NPT];
 #pragma unroll
         for (int e = 0; e < TW; ++e) {
             const bool there = live && t0 + w * TW + e < len;
-            const float u = there ? (float)next.u[e] : 0.f, gy = there ? (float)next.gy[e] : 0.f;
-            const float raw = (float)next.dt[e] + bias, z = there ? (float)next.z[e] : 0.f, sg = logistic(z);
-            float d = softplus(raw, sig[e]);
-            d = there ? (soft ? d : raw) : 0.f;
-            sig[e] = there ? (soft ? sig[e] : 1.f) : 0.f;
+            const float raw = (float)next.dt[e] + bias, z = (float)next.z[e], gy = (float)next.gy[e], sg = logistic(z);
+            const float d = softplus(raw, sig[e]);
+            if (!soft) sig[e] = 1.f;
             gzf[e] = gy * sg * fmaf(z, 1.f - sg, 1.f);
-            const f32x2 du = {d, d * u}, pu = {gy * (gated ? z * sg : 1.f), u};
+            us[e] = there ? (float)next.u[e] : 0.f;
+            const float dd = there ? (soft ? d : raw) : 0.f;
+            const f32x2 du = {dd, dd * us[e]};
             L.du[w * TW + e][lane] = du;
-            L.pu[w * TW + e][lane] = pu;
+            L.p[w * TW + e][lane] = there ? gy * (gated ? z * sg : 1.f) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < NPT; ++i) h0[i] = n0 + i < s.N ? next.h0[i] : 0.f;
@@ -269,7 +271,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
             const auto ahead = [&](int j) {
                 of[j & 1].fetch(row, L.du, lane, j);
 #pragma unroll
-                for (int r = 0; r < kTok; ++r) pt[j & 1][r] = L.pu[j * kTok + r][lane][0];
+                for (int r = 0; r < kTok; ++r) pt[j & 1][r] = L.p[j * kTok + r][lane];
             };
             ahead(0);
 #pragma unroll
@@ -301,33 +303,34 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
         }
         const float totC = fold();
         __syncthreads();
-        if (gated || !whole) {
+        if (live && (gated || !WHOLE)) {
 #pragma unroll
             for (int e = 0; e < TW; ++e) {
                 const int t = w * TW + e;
+                if (t0 + t >= T) break;
                 float core = 0.f;
 #pragma unroll
                 for (int j = 0; j < W; ++j) core += L.part[0][j][t][lane];
-                if (!live || t0 + t >= T) continue;
-                const unsigned at = (unsigned)t * C + c;
-                if (!whole)
+                const unsigned at = (unsigned)(q * kSelTile + t) * C + c;
+                if constexpr (!WHOLE)
                     store_elem<float>(S.q + ((int64_t)nt * 3 + 2) * s.B * T * s.C + base, at * 4, core);
                 else
                     store_elem<E>((E*)g.gz + base, at * (unsigned)sizeof(E),
-                                  t0 + t < len ? gzf[e] * fmaf(Dc, L.pu[t][lane][1], core) : 0.f);
+                                  t0 + t < len ? gzf[e] * fmaf(Dc, us[e], core) : 0.f);
             }
         }
         __syncthreads();
         // Backwards: q1 = sum A m, q2 = sum g B, and the sums over channels of g d u.
         asm volatile("" : "+s"(row));  // as if it were another one: B and C of a whole tile would be kept in 128 scalar registers
         {
-            f32x2 x[2][2], y[2][2];
+            f32x2 x[2][2];
+            float y[2][2];
             f32x16 v[2];
             const auto ahead = [&](int j) {  // the pair of tokens 2 j, 2 j + 1
                 typedef const __attribute__((address_space(4))) f32x16* P;
                 v[j & 1] = *reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + j * 16));
 #pragma unroll
-                for (int r = 0; r < 2; ++r) x[j & 1][r] = L.du[2 * j + r][lane], y[j & 1][r] = L.pu[2 * j + r][lane];
+                for (int r = 0; r < 2; ++r) x[j & 1][r] = L.du[2 * j + r][lane], y[j & 1][r] = L.p[2 * j + r][lane];
             };
             ahead(kPairs - 1);
 #pragma unroll
@@ -338,7 +341,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
 #pragma unroll
                 for (int r = 1; r >= 0; --r) {
                     const int t = 2 * j + r;
-                    const float d = x[j & 1][r][0], du = x[j & 1][r][1], p = y[j & 1][r][0];
+                    const float d = x[j & 1][r][0], du = x[j & 1][r][1], p = y[j & 1][r];
                     float q1 = 0.f, q2 = 0.f;
 #pragma unroll
                     for (int i = 0; i < NPT; ++i) {
@@ -363,26 +366,28 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
         }
         const float totB = fold();
         __syncthreads();
+        if (live) {
 #pragma unroll
-        for (int e = 0; e < TW; ++e) {
-            const int t = w * TW + e;
-            float q1 = 0.f, q2 = 0.f;
+            for (int e = 0; e < TW; ++e) {
+                const int t = w * TW + e;
+                if (t0 + t >= T) break;
+                float q1 = 0.f, q2 = 0.f;
 #pragma unroll
-            for (int j = 0; j < W; ++j) q1 += L.part[0][j][t][lane], q2 += L.part[1][j][t][lane];
-            if (!live || t0 + t >= T) continue;
-            const unsigned at = (unsigned)t * C + c;
-            if (whole) {
-                const bool there = t0 + t < len;
-                const float d = L.du[t][lane][0], p = L.pu[t][lane][0], u = L.pu[t][lane][1];
-                const float gd = there ? fmaf(u, q2, q1 * kLn2) * sig[e] : 0.f;
-                store_elem<E>((E*)g.gu + base, at * (unsigned)sizeof(E), there ? fmaf(Dc, p, d * q2) : 0.f);
-                store_elem<E>((E*)g.gdt + base, at * (unsigned)sizeof(E), gd);
-                sD = fmaf(p, u, sD);
-                sb += gd;
-            } else {
-                float* const o = S.q + (int64_t)nt * 3 * s.B * T * s.C + base;
-                store_elem<float>(o, at * 4, q1 * kLn2);
-                store_elem<float>(o + s.B * T * s.C, at * 4, q2);
+                for (int j = 0; j < W; ++j) q1 += L.part[0][j][t][lane], q2 += L.part[1][j][t][lane];
+                const unsigned at = (unsigned)(q * kSelTile + t) * C + c;
+                if constexpr (WHOLE) {
+                    const float d = L.du[t][lane][0], p = L.p[t][lane];
+                    const bool there = t0 + t < len;
+                    const float gd = there ? fmaf(us[e], q2, q1 * kLn2) * sig[e] : 0.f;
+                    store_elem<E>((E*)g.gu + base, at * (unsigned)sizeof(E), there ? fmaf(Dc, p, d * q2) : 0.f);
+                    store_elem<E>((E*)g.gdt + base, at * (unsigned)sizeof(E), gd);
+                    sD = fmaf(p, us[e], sD);
+                    sb += gd;
+                } else {
+                    float* const o = S.q + (int64_t)nt * 3 * s.B * T * s.C + base;
+                    store_elem<float>(o, at * 4, q1 * kLn2);
+                    store_elem<float>(o + s.B * T * s.C, at * 4, q2);
+                }
             }
         }
         // A lane's sums over channels: of the four of tokens lane & 3, the token by bits 5 and 4 and the state
@@ -393,10 +398,10 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
             o[0] = t0 + t < len ? totB : 0.f;
             o[Np] = t0 + t < len ? totC : 0.f;
         }
-        __syncthreads();  // part, du and pu have been read
     }
     if (live && states) store16<float>(S.gA + state_at(s, b * blocks + k, n0, c), gA);
-    if (!whole) return;
+    if (!WHOLE) return;
+    __syncthreads();  // the last tile's part has been read
     L.part[0][w][0][lane] = sD, L.part[1][w][0][lane] = sb;
     __syncthreads();
     for (int o = w; o < 2; o += W) {
@@ -508,10 +513,15 @@ hipError_t by_waves(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, co
     hipError_t e = hipGetLastError();
     if (e == hipSuccess) e = run_sel_join(s, A.A, S.carry, S.sum, blocks, g.gs_out, g.gs_in, true, st);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((sel_gradient_kernel<E, W>), dim3((unsigned)(s.B * blocks * ntiles * s.G * S.cuts)), dim3(64 * W),
-                       0, st, s, A, g, bc, keep, S, (int)blocks, ntiles);
+    const dim3 grid((unsigned)(s.B * blocks * ntiles * s.G * S.cuts));
+    if (W < 4 || ntiles == 1) {
+        hipLaunchKernelGGL((sel_gradient_kernel<E, W, true>), grid, dim3(64 * W), 0, st, s, A, g, bc, keep, S, (int)blocks,
+                           ntiles);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((sel_gradient_kernel<E, 4, false>), grid, dim3(256), 0, st, s, A, g, bc, keep, S, (int)blocks, ntiles);
     e = hipGetLastError();
-    if (e != hipSuccess || ntiles == 1) return e;
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(s.B * blocks * ceil_div(s.C, 64))), dim3(256), 0, st, s,
                        A, g, S, blocks, ntiles);
     return hipGetLastError();
