@@ -27,23 +27,24 @@ namespace {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // B and C as float32, (B,tiles,G,waves,16 tokens,2,npt), zero beyond N, for absent tokens and behind T.
+// A workgroup takes 1024 floats of one tile.
 template <class E>
 __global__ __launch_bounds__(256) void sel_prepare_kernel(SelShape s, const E* __restrict__ Bm,
                                                           const E* __restrict__ Cm, float* __restrict__ bc, int npt,
-                                                          int waves, int tiles, int64_t total) {
-    const unsigned row = kSelTile * 2 * npt;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const unsigned j = (unsigned)(i % row), r = j % (2 * npt);
-        int64_t k = i / row;
-        const int w = (int)(k % waves);
-        k /= waves;
-        const int g = (int)(k % s.G);
-        k /= s.G;
-        const int64_t b = k / tiles, t = k % tiles * kSelTile + j / (2 * npt);
-        const int n = w * npt + r % npt;
-        float v = 0.f;
-        if (n < s.N && t < row_length(s, b)) v = (float)((int)r < npt ? Bm : Cm)[((b * s.T + t) * s.G + g) * s.N + n];
-        bc[i] = v;
+                                                          int waves, int64_t tiles, int64_t parts) {
+    const unsigned per = kSelTile * 2 * npt, all = per * waves * s.G;
+    for (int64_t k = blockIdx.x; k < s.B * tiles * parts; k += gridDim.x) {
+        const int64_t row = k / parts, b = row / tiles;  // row: b * tiles + tile
+        const unsigned first = (unsigned)(k % parts) * 1024, t0 = (unsigned)(row % tiles) * kSelTile;
+        const int64_t len = row_length(s, b);
+        for (unsigned i = first + threadIdx.x; i < all && i < first + 1024; i += 256) {
+            const unsigned j = i % per, w = i / per % waves, g = i / per / waves, r = j % (2 * npt);
+            const unsigned t = t0 + j / (2 * npt);
+            const int n = (int)(w * npt + r % npt);
+            float v = 0.f;
+            if (n < s.N && t < len) v = (float)((int)r < npt ? Bm : Cm)[((b * s.T + t) * s.G + g) * s.N + n];
+            bc[row * all + i] = v;
+        }
     }
 }
 
@@ -89,17 +90,19 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
     float total = 0.f;
 
     // This wave's tokens of a tile, read while the tile before is worked on.  Tokens behind the row's end
-    // are read as the last one and not used.
+    // are read as the last one, a gate that was not given as u: neither is used.
+    const bool gated = A.z != nullptr, soft = s.softplus != 0;
+    const void* const zp = gated ? A.z : A.u;
     E ur[TW], dr[TW], zr[TW];
     const auto fetch = [&](int t0) {
         const int64_t base = (b * T + t0) * s.C;
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
-            const int last = T - 1 - t0, k = w * TW + i < last ? w * TW + i : last;
-            const unsigned off = (unsigned)(k < 0 ? 0 : k) * (unsigned)s.C + c;
-            ur[i] = (reinterpret_cast<const E*>(A.u) + base)[off];
-            dr[i] = (reinterpret_cast<const E*>(A.dt) + base)[off];
-            if (!AGG && A.z) zr[i] = (reinterpret_cast<const E*>(A.z) + base)[off];
+            const int k = t0 + w * TW + i < T ? w * TW + i : T - 1 - t0;
+            const unsigned at = ((unsigned)k * (unsigned)s.C + c) * (unsigned)sizeof(E);
+            ur[i] = load_elem<E>(elems<E>(A.u, base), at);
+            dr[i] = load_elem<E>(elems<E>(A.dt, base), at);
+            if (!AGG) zr[i] = load_elem<E>(elems<E>(zp, base), at);
         }
     };
     fetch(t_begin);
@@ -113,25 +116,33 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
                         if (n0 + i < Np) store16<float>(keep + at + i * s.C, h + i);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < NPT; ++i) keep[at + i] = h[i];
+                    for (int i = 0; i < NPT; ++i)
+                        if (n0 + i < Np) keep[at + i] = h[i];
                 }
             }
         }
+        // Whether a token is there is the same for the whole wave; d and d u of an absent one, or of a
+        // lane without a channel, are zero, which leaves the states alone.
         float u[TW], z[TW];
         if (t0 < len) {
+            float d[TW];
+#pragma unroll
+            for (int i = 0; i < TW; ++i) d[i] = (float)dr[i] + bias;
+            if (soft) {  // outside of the loop: the tokens' chains of instructions then run side by side
+                float sig;
+#pragma unroll
+                for (int i = 0; i < TW; ++i) d[i] = softplus(d[i], sig);
+            }
 #pragma unroll
             for (int i = 0; i < TW; ++i) {
                 const bool there = live && t0 + w * TW + i < len;
-                u[i] = there ? (float)ur[i] : 0.f;
-                float d = (float)dr[i] + bias, sig;
-                if (s.softplus) d = softplus(d, sig);
-                d = there ? d : 0.f;
-                z[i] = !AGG && A.z && there ? (float)zr[i] : 0.f;
-                const f32x2 v = {d, d * u[i]};
+                u[i] = (float)ur[i];
+                if (!AGG) z[i] = (float)zr[i];
+                const f32x2 v = {there ? d[i] : 0.f, there ? d[i] * u[i] : 0.f};
                 din[w * TW + i][lane] = v;
             }
         }
-        if (t0 + kSelTile < t_end) fetch(t0 + kSelTile);
+        fetch(t0 + kSelTile < t_end ? t0 + kSelTile : t0);
         __syncthreads();
         if (t0 < len) {
             const float* row = bc + (((b * tiles + t0 / kSelTile) * s.G + grp) * W + w) * (kSelTile * 2 * NPT);
@@ -162,19 +173,20 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
         __syncthreads();
         if constexpr (!AGG) {
             if (A.y && live) {
-                E* const out = reinterpret_cast<E*>(A.y) + (b * T + t0) * s.C;
+                void* const out = (void*)elems<E>(A.y, (b * T + t0) * s.C);
 #pragma unroll
                 for (int i = 0; i < TW; ++i) {
                     const int t = t0 + w * TW + i;
-                    if (t >= t_end) break;
+                    if (t >= t_end) continue;
                     float y = 0.f;
                     if (t < len) {
                         y = Dc * u[i];
 #pragma unroll
                         for (int k = 0; k < W; ++k) y += part[k][w * TW + i][lane];
-                        if (A.z) y *= z[i] * logistic(z[i]);
+                        const float gate = z[i] * logistic(z[i]);
+                        y *= gated ? gate : 1.f;
                     }
-                    out[(unsigned)(w * TW + i) * (unsigned)s.C + c] = (E)y;
+                    store_elem<E>(out, ((unsigned)(w * TW + i) * (unsigned)s.C + c) * (unsigned)sizeof(E), y);
                 }
             }
         }
@@ -298,7 +310,7 @@ template <class E>
 hipError_t forward_by_states(const SelShape& s, const SelArgs& A, const SelPlan& p, const SelScratch& S, float* keep,
                              hipStream_t st) {
     if (p.npt == 1) return forward<E, 1, 1>(s, A, p, S, keep, st);
-    if (p.npt == 2) return forward<E, 1, 2>(s, A, p, S, keep, st);
+    if (p.npt == 2) return p.waves == 1 ? forward<E, 1, 2>(s, A, p, S, keep, st) : forward<E, 8, 2>(s, A, p, S, keep, st);
     if (p.npt == 4) {
         if (p.waves == 1) return forward<E, 1, 4>(s, A, p, S, keep, st);
         if (p.waves == 2) return forward<E, 2, 4>(s, A, p, S, keep, st);
@@ -315,13 +327,17 @@ SelPlan sel_plan(const SelShape& s) {
     p.tiles_n = 1;
     p.npt = s.N <= 1 ? 1 : s.N <= 2 ? 2 : s.N <= 16 ? 4 : s.N <= 64 ? 8 : 16;
     p.waves = s.N <= 4 ? 1 : s.N <= 8 ? 2 : s.N <= 32 ? 4 : 8;
-    // Segments until the chip has four waves a SIMD, of four tiles at least.
+    // Segments until the chip has six waves a SIMD, of four tiles at least: 32768 tokens of 2048 channels
+    // take 573 us, 587 with four waves a SIMD and 693 with two; 8 x 4096 tokens of 2560 635, 684 and 791.
     const int64_t wg = s.B * s.G * ceil_div(s.C / s.G, 64), tiles = sel_tiles(s);
-    int64_t segs = 4096 / (wg * p.waves);
+    int64_t segs = 6144 / (wg * p.waves);
     if (segs > tiles / 4) segs = tiles / 4;
     if (segs < 2) segs = 1;
     p.seg_tiles = ceil_div(tiles, segs);
     p.segs = ceil_div(tiles, p.seg_tiles);
+    // Rows too short for that and too few for a wave a SIMD: half the states a wave, which is as long as
+    // one tile takes then.  77 tokens of 1536 channels 12.1 us for 15.2; 8 x 1024 tokens 66.8 for 62.4.
+    if (segs == 1 && p.npt == 4 && p.waves == 4 && wg * 8 <= 1024) p.npt = 2, p.waves = 8;
     return p;
 }
 
@@ -330,16 +346,15 @@ size_t sel_bc_floats(const SelShape& s, const SelPlan& p) {
 }
 
 hipError_t run_sel_prepare(const SelShape& s, const SelArgs& A, const SelPlan& p, float* bc, hipStream_t st) {
-    const int64_t total = (int64_t)sel_bc_floats(s, p);
-    int64_t blocks = ceil_div(total, 256);
-    if (blocks > 4096) blocks = 4096;
-    const int tiles = (int)sel_tiles(s);
+    const int64_t rows = s.B * sel_tiles(s), parts = ceil_div((int64_t)sel_bc_floats(s, p) / rows, 1024);
+    const dim3 grid((unsigned)(rows * parts < (1 << 20) ? rows * parts : 1 << 20));
+    const int waves = p.tiles_n * p.waves;
     if (s.dtype == kBf16)
-        hipLaunchKernelGGL((sel_prepare_kernel<bf16_t>), dim3((unsigned)blocks), dim3(256), 0, st, s,
-                           (const bf16_t*)A.Bm, (const bf16_t*)A.Cm, bc, p.npt, p.tiles_n * p.waves, tiles, total);
+        hipLaunchKernelGGL((sel_prepare_kernel<bf16_t>), grid, dim3(256), 0, st, s, (const bf16_t*)A.Bm,
+                           (const bf16_t*)A.Cm, bc, p.npt, waves, sel_tiles(s), parts);
     else
-        hipLaunchKernelGGL((sel_prepare_kernel<float>), dim3((unsigned)blocks), dim3(256), 0, st, s,
-                           (const float*)A.Bm, (const float*)A.Cm, bc, p.npt, p.tiles_n * p.waves, tiles, total);
+        hipLaunchKernelGGL((sel_prepare_kernel<float>), grid, dim3(256), 0, st, s, (const float*)A.Bm,
+                           (const float*)A.Cm, bc, p.npt, waves, sel_tiles(s), parts);
     return hipGetLastError();
 }
 

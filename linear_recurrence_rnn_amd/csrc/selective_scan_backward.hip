@@ -86,13 +86,22 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
     int t0 = end > t_begin ? (end - 1) / kSelTile * kSelTile : t_begin - kSelTile;
     if (t0 >= t_begin) fetch(t0);
     for (; t0 >= t_begin; t0 -= kSelTile) {
+        float d[TW], p[TW];
+#pragma unroll
+        for (int i = 0; i < TW; ++i) d[i] = (float)dr[i] + bias, p[i] = (float)gr[i];
+        if (soft) {
+            float sig;
+#pragma unroll
+            for (int i = 0; i < TW; ++i) d[i] = softplus(d[i], sig);
+        }
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < TW; ++i) p[i] *= (float)zr[i] * logistic((float)zr[i]);
+        }
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
             const bool there = live && t0 + w * TW + i < len;
-            const float raw = (float)dr[i] + bias, z = there ? (float)zr[i] : 0.f, p = there ? (float)gr[i] : 0.f;
-            float sig;
-            const float d = soft ? softplus(raw, sig) : raw;
-            const f32x2 v = {there ? d : 0.f, gated ? p * (z * logistic(z)) : p};
+            const f32x2 v = {there ? d[i] : 0.f, there ? p[i] : 0.f};
             din[w * TW + i][lane] = v;
         }
         fetch(t0 > t_begin ? t0 - kSelTile : t0);
@@ -307,7 +316,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
 #pragma unroll
             for (int e = 0; e < TW; ++e) {
                 const int t = w * TW + e;
-                if (t0 + t >= T) break;
+                if (t0 + t >= T) continue;
                 float core = 0.f;
 #pragma unroll
                 for (int j = 0; j < W; ++j) core += L.part[0][j][t][lane];
@@ -370,7 +379,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
 #pragma unroll
             for (int e = 0; e < TW; ++e) {
                 const int t = w * TW + e;
-                if (t0 + t >= T) break;
+                if (t0 + t >= T) continue;
                 float q1 = 0.f, q2 = 0.f;
 #pragma unroll
                 for (int j = 0; j < W; ++j) q1 += L.part[0][j][t][lane], q2 += L.part[1][j][t][lane];
