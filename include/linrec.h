@@ -634,7 +634,7 @@ size_t group_norm_act_backward_workspace_size(int64_t N, int64_t C, int64_t G);
  *            token (s_in with T = 0).  It may be s_in itself, here and in the decode step.
  *
  * G divides C; 1 <= N <= 128.  B or C equal to 0 enqueues nothing.  The states are float32
- * throughout.  LINREC_ERR_UNSUPPORTED beyond B = 2^20, T = 2^30, C = 2^22, C*N = 2^26, B*C*N = 2^31,
+ * throughout.  LINREC_ERR_UNSUPPORTED beyond B = 2^20, T = 2^30, C = 2^22, C*N = 2^26, G*N = 2^24, B*C*N = 2^31,
  * B*C/64 = 2^22 (every group counted in whole 64s) or B*T*C, B*T*G*N = 2^44, and in the backward
  * beyond B*T/64 = 2^23 or B*T*C*N/65536 = 2^24 (in whole 64s, and whole 16s of N).
  */

@@ -1191,7 +1191,8 @@ int check_sel_shape(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int d
         return fail(LINREC_ERR_INVALID_ARG, "N=%lld outside 1..%d", (long long)N, linrec::kSelMaxN);
     if (G < 1 || C % G != 0) return fail(LINREC_ERR_INVALID_ARG, "G=%lld does not divide C=%lld", (long long)G, (long long)C);
     if (B > (1 << 20) || T > (1 << 30)) return fail(LINREC_ERR_UNSUPPORTED, "B is above 2^20, or T above 2^30");
-    if (C > (1 << 22) || C * N > (1 << 26)) return fail(LINREC_ERR_UNSUPPORTED, "C is above 2^22, or C*N above 2^26");
+    if (C > (1 << 22) || C * N > (1 << 26) || G * N > (1 << 24))
+        return fail(LINREC_ERR_UNSUPPORTED, "C is above 2^22, C*N above 2^26 or G*N above 2^24");
     if (C == 0) return LINREC_OK;
     // Here B*C*N < 2^46 and B*T*C < 2^72 / 4.
     if (B * T > ((int64_t)1 << 44) / C || B * T > ((int64_t)1 << 44) / (G * N))

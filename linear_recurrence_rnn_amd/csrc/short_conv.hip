@@ -10,10 +10,11 @@
 //   gline[i] = sum_k w[k] q_{i-k}  (+ gs_out[i - len] for len <= i < len + K - 1)
 // of which the first K-1 elements are the carried state's gradient and the others x's.
 //
-// A lane takes VEC neighbouring channels (16 bytes) and walks down a run of tokens with the last K-1
+// A lane takes VEC neighbouring channels and walks down a run of tokens with the last K-1
 // inputs, and backwards also the last K-1 of q, in registers, so a token is read once but for the K-1
-// before (and, backwards, behind) a run.  Both directions are bound by memory.  The sums over tokens
-// are kept in registers over a walker's runs, go to the workspace and are added in walker order.
+// before (and, backwards, behind) a run; the next kAhead tokens are on their way meanwhile.  Both
+// directions are bound by memory.  The sums over tokens are kept in registers over a run, go to the
+// workspace and are added in the order of the runs.
 #include "short_conv.hpp"
 #include "group_norm.hpp"  // the activations' codes
 #include "elem_types.hpp"
@@ -22,7 +23,7 @@ namespace linrec {
 
 namespace {
 
-constexpr int kRun = 16;  // tokens of a run
+constexpr int kAhead = 4;  // tokens asked for at once
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -37,25 +38,40 @@ __device__ __forceinline__ int64_t row_length(const ConvShape& s, int64_t b) {
     return n < 0 ? 0 : (n < s.T ? n : s.T);
 }
 
+// VEC elements as they come from memory, and their values.
+template <class E, int VEC> struct Raw { typedef E type __attribute__((ext_vector_type(VEC))); };
+template <class E> struct Raw<E, 1> { typedef E type; };
+
 template <class E, int VEC>
-__device__ __forceinline__ void load_vec(const E* __restrict__ p, float* __restrict__ out) {
-    if constexpr (VEC == 1) out[0] = (float)*p;
-    else load16<E>(p, out);
+__device__ __forceinline__ typename Raw<E, VEC>::type load_raw(const void* p, int64_t at) {
+    return *reinterpret_cast<const typename Raw<E, VEC>::type*>(reinterpret_cast<const E*>(p) + at);
 }
-template <class E, int VEC, bool NT>
-__device__ __forceinline__ void store_vec(E* __restrict__ p, const float* __restrict__ in) {
-    if constexpr (VEC == 1) *p = (E)in[0];
-    else store16<E, NT>(p, in);
+template <class E, int VEC>
+__device__ __forceinline__ void values(const typename Raw<E, VEC>::type& v, bool there, float (&out)[VEC]) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        if constexpr (VEC == 1) out[j] = there ? (float)v : 0.f;
+        else out[j] = there ? (float)v[j] : 0.f;
+    }
+}
+template <class E, int VEC>
+__device__ __forceinline__ void store_vec(void* p, int64_t at, const float (&in)[VEC]) {
+    typename Raw<E, VEC>::type v;
+    if constexpr (VEC == 1) v = (E)in[0];
+    else
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = (E)in[j];
+    *reinterpret_cast<typename Raw<E, VEC>::type*>(reinterpret_cast<E*>(p) + at) = v;
 }
 
 // Input at token t (which may lie in the state, t < 0) of row b, channels c..; zero where there is none.
 template <class E, int VEC>
 __device__ __forceinline__ void load_input(const ConvShape& s, const ConvArgs& A, int64_t b, int64_t t, int64_t len,
-                                           int64_t c, float* __restrict__ out) {
+                                           int64_t c, float (&out)[VEC]) {
     if (t >= 0 && t < len) {
-        load_vec<E, VEC>(reinterpret_cast<const E*>(A.x) + (b * s.T + t) * s.C + c, out);
+        values<E, VEC>(load_raw<E, VEC>(A.x, (b * s.T + t) * s.C + c), true, out);
     } else if (t < 0 && A.s_in) {
-        load_vec<E, VEC>(reinterpret_cast<const E*>(A.s_in) + (b * (s.K - 1) + t + s.K - 1) * s.C + c, out);
+        values<E, VEC>(load_raw<E, VEC>(A.s_in, (b * (s.K - 1) + t + s.K - 1) * s.C + c), true, out);
     } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) out[j] = 0.f;
@@ -72,13 +88,24 @@ __device__ __forceinline__ void load_filters(const ConvArgs& A, int64_t c, float
     }
 }
 
-// Four runs a workgroup, 64 lanes of VEC channels each.
+// One run a wave, four a workgroup, 64 lanes of VEC channels each.
 template <class E, int K, int VEC>
-__global__ __launch_bounds__(256) void short_conv_kernel(ConvShape s, ConvArgs A, int64_t runs, int64_t cols) {
-    const int64_t col = blockIdx.x % cols, run = blockIdx.x / cols * 4 + (threadIdx.x >> 6);
+__global__ __launch_bounds__(256) void short_conv_kernel(ConvShape s, ConvArgs A, int64_t runs, int64_t run_tokens,
+                                                         int64_t cols) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t col = blockIdx.x % cols, run = blockIdx.x / cols * 4 + wave;
     const int64_t c = (col * 64 + (threadIdx.x & 63)) * VEC;
     if (c >= s.C || run >= s.B * runs) return;
-    const int64_t b = run / runs, t0 = run % runs * kRun, len = row_length(s, b);
+    const int64_t b = run / runs, t0 = run % runs * run_tokens, len = row_length(s, b);
+    const int64_t t_end = t0 + run_tokens < s.T ? t0 + run_tokens : s.T;
+    // Tokens behind the run are read as its last one and not used.
+    typename Raw<E, VEC>::type next[kAhead];
+    const auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            next[u] = load_raw<E, VEC>(A.x, (b * s.T + (t + u < t_end ? t + u : t_end - 1)) * s.C + c);
+    };
+    if (t0 < t_end) fetch(t0);
     float w[K][VEC], bias[VEC];
     load_filters<K, VEC>(A, c, w, bias);
     float x[K][VEC];  // x[k] = x_{t-K+1+k}
@@ -92,40 +119,43 @@ __global__ __launch_bounds__(256) void short_conv_kernel(ConvShape s, ConvArgs A
 #pragma unroll
         for (int k = 0; k < K - 1; ++k) load_input<E, VEC>(s, A, b, len - (K - 1) + k, len, c, keep[k]);
     }
-#pragma unroll 4
-    for (int i = 0; i < kRun; ++i) {
-        const int64_t t = t0 + i;
-        if (t >= s.T) break;
+    for (int64_t t1 = t0; t1 < t_end; t1 += kAhead) {
+        typename Raw<E, VEC>::type now[kAhead];
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k)
+        for (int u = 0; u < kAhead; ++u) now[u] = next[u];
+        if (t1 + kAhead < t_end) fetch(t1 + kAhead);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) x[k][j] = x[k + 1][j];
-        load_input<E, VEC>(s, A, b, t, len, c, x[K - 1]);
-        float y[VEC];
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t t = t1 + u;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            float v = bias[j];
+            for (int k = 0; k < K - 1; ++k)
 #pragma unroll
-            for (int k = 0; k < K; ++k) v = fmaf(w[k][j], x[k][j], v);
-            if (s.act == kActSilu) v *= logistic(v);
-            y[j] = t < len ? v : 0.f;
+                for (int j = 0; j < VEC; ++j) x[k][j] = x[k + 1][j];
+            values<E, VEC>(now[u], t < len, x[K - 1]);
+            float y[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                float v = bias[j];
+#pragma unroll
+                for (int k = 0; k < K; ++k) v = fmaf(w[k][j], x[k][j], v);
+                if (s.act == kActSilu) v *= logistic(v);
+                y[j] = t < len ? v : 0.f;
+            }
+            if (t < t_end) store_vec<E, VEC>(A.y, (b * s.T + t) * s.C + c, y);
         }
-        store_vec<E, VEC, true>(reinterpret_cast<E*>(A.y) + (b * s.T + t) * s.C + c, y);
     }
     if (states) {
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k)
-            store_vec<E, VEC, false>(reinterpret_cast<E*>(A.s_out) + (b * (K - 1) + k) * s.C + c, keep[k]);
+        for (int k = 0; k < K - 1; ++k) store_vec<E, VEC>(A.s_out, (b * (K - 1) + k) * s.C + c, keep[k]);
     }
 }
 
-// Walkers of 64 lanes, four a workgroup; a walker takes every (4 * walkers)-th run.
 template <class E, int K, int VEC>
 __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvArgs A, ConvBwdArgs g, int64_t runs,
-                                                             int64_t cols, int64_t walkers) {
+                                                             int64_t run_tokens, int64_t cols) {
     __shared__ float acc[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t col = blockIdx.x % cols, walker = blockIdx.x / cols;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t col = blockIdx.x % cols, walker = blockIdx.x / cols, run = walker * 4 + wave;
     const int64_t c = (col * 64 + lane) * VEC;
     const bool live = c < s.C;
     float gw[K][VEC], gb[VEC];
@@ -135,58 +165,58 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
 #pragma unroll
         for (int k = 0; k < K; ++k) gw[k][j] = 0.f;
     }
-    if (live) {
+    if (live && run < s.B * runs) {
+        const int64_t b = run / runs, t0 = run % runs * run_tokens, len = row_length(s, b);
+        const int64_t t_end = t0 + run_tokens < s.T ? t0 + run_tokens : s.T;
+        // The line's elements up to K-1 tokens beyond the run: x's gradient at a token needs the q behind it.
+        // Absent tokens are read as the last one that is there and not used.
+        typename Raw<E, VEC>::type nx[kAhead], ny[kAhead];
+        const auto fetch = [&](int64_t t) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int64_t at = (b * s.T + (t + u < len ? t + u : len - 1)) * s.C + c;
+                nx[u] = load_raw<E, VEC>(A.x, at);
+                ny[u] = load_raw<E, VEC>(g.gy, at);
+            }
+        };
+        if (t0 < len) fetch(t0);
         float w[K][VEC], bias[VEC];
         load_filters<K, VEC>(A, c, w, bias);
-        for (int64_t run = walker * 4 + wave; run < s.B * runs; run += walkers * 4) {
-            const int64_t b = run / runs, t0 = run % runs * kRun, len = row_length(s, b);
-            float x[K][VEC], q[K][VEC];  // q[k] = q_{t-k}
+        float x[K][VEC], q[K][VEC];  // x[k] = x_{t-K+1+k}, q[k] = q_{t-k}
 #pragma unroll
-            for (int k = 0; k < K - 1; ++k) {
-                load_input<E, VEC>(s, A, b, t0 - (K - 1) + k, len, c, x[k + 1]);
+        for (int k = 0; k < K; ++k) {
+            if (k < K - 1) load_input<E, VEC>(s, A, b, t0 - (K - 1) + k, len, c, x[k + 1 < K ? k + 1 : 0]);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) q[k][j] = 0.f;
-            }
+            for (int j = 0; j < VEC; ++j) q[k][j] = 0.f;
+        }
+        for (int64_t t1 = t0; t1 < t_end + K - 1; t1 += kAhead) {
+            typename Raw<E, VEC>::type vx[kAhead], vy[kAhead];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) q[K - 1][j] = 0.f;
-            float gs[K > 1 ? K - 1 : 1][VEC];  // gs_out: it may be overwritten
-            if (g.gs_out) {
+            for (int u = 0; u < kAhead; ++u) vx[u] = nx[u], vy[u] = ny[u];
+            if (t1 + kAhead < len && t1 + kAhead < t_end + K - 1) fetch(t1 + kAhead);
 #pragma unroll
-                for (int k = 0; k < K - 1; ++k)
-                    load_vec<E, VEC>(reinterpret_cast<const E*>(g.gs_out) + (b * (K - 1) + k) * s.C + c, gs[k]);
-            }
-            // Tokens up to K-1 beyond the run: x's gradient at a token needs the q behind it.
-#pragma unroll 1
-            for (int i = 0; i < kRun + K - 1; ++i) {
-                const int64_t t = t0 + i, out = t - (K - 1);
-                const bool mine = i < kRun;
-                if (out >= s.T) break;
+            for (int u = 0; u < kAhead; ++u) {
+                const int64_t t = t1 + u, out = t - (K - 1);
 #pragma unroll
-                for (int k = 0; k < K - 1; ++k)
+                for (int j = 0; j < VEC; ++j) {
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) x[k][j] = x[k + 1][j];
+                    for (int k = 0; k < K - 1; ++k) x[k][j] = x[k + 1][j];
 #pragma unroll
-                for (int k = K - 1; k > 0; --k)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) q[k][j] = q[k - 1][j];
-                load_input<E, VEC>(s, A, b, t, len, c, x[K - 1]);
-                if (t < len) {
-                    load_vec<E, VEC>(reinterpret_cast<const E*>(g.gy) + (b * s.T + t) * s.C + c, q[0]);
-                    if (s.act == kActSilu) {
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) {
-                            float v = bias[j];
-#pragma unroll
-                            for (int k = 0; k < K; ++k) v = fmaf(w[k][j], x[k][j], v);
-                            const float sg = logistic(v);
-                            q[0][j] *= sg * fmaf(v, 1.f - sg, 1.f);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) q[0][j] = 0.f;
+                    for (int k = K - 1; k > 0; --k) q[k][j] = q[k - 1][j];
                 }
-                if (mine) {
+                values<E, VEC>(vx[u], t < len, x[K - 1]);
+                values<E, VEC>(vy[u], t < len, q[0]);
+                if (s.act == kActSilu) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        float v = bias[j];
+#pragma unroll
+                        for (int k = 0; k < K; ++k) v = fmaf(w[k][j], x[k][j], v);
+                        const float sg = logistic(v);
+                        q[0][j] = t < len ? q[0][j] * (sg * fmaf(v, 1.f - sg, 1.f)) : 0.f;
+                    }
+                }
+                if (t < t_end) {
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) {
                         gb[j] += q[0][j];
@@ -194,9 +224,8 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
                         for (int k = 0; k < K; ++k) gw[k][j] = fmaf(q[0][j], x[k][j], gw[k][j]);
                     }
                 }
-                // The line's element t, token `out`: a run's own tokens, and the state's before the first.
-                if (out < t0 && t0 > 0) continue;
-                if (out < 0 && !g.gs_in) continue;
+                // The line's element t, token `out`: the run's own tokens, and the state's before the first.
+                if (out >= t_end || (out < t0 && t0 > 0) || (out < 0 && !g.gs_in)) continue;
                 float v[VEC];
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
@@ -205,15 +234,13 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
                     for (int k = 0; k < K; ++k) v[j] = fmaf(w[k][j], q[k][j], v[j]);
                 }
                 if (g.gs_out && t >= len && t < len + K - 1) {
+                    float gs[VEC];
+                    values<E, VEC>(load_raw<E, VEC>(g.gs_out, (b * (K - 1) + t - len) * s.C + c), true, gs);
 #pragma unroll
-                    for (int k = 0; k < K - 1; ++k)
-                        if (t - len == k)
-#pragma unroll
-                            for (int j = 0; j < VEC; ++j) v[j] += gs[k][j];
+                    for (int j = 0; j < VEC; ++j) v[j] += gs[j];
                 }
-                E* p = out >= 0 ? reinterpret_cast<E*>(g.gx) + (b * s.T + out) * s.C + c
-                                : reinterpret_cast<E*>(g.gs_in) + (b * (K - 1) + t) * s.C + c;
-                store_vec<E, VEC, false>(p, v);
+                if (out >= 0) store_vec<E, VEC>(g.gx, (b * s.T + out) * s.C + c, v);
+                else store_vec<E, VEC>(g.gs_in, (b * (K - 1) + t) * s.C + c, v);
             }
         }
     }
@@ -230,7 +257,7 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
         }
 }
 
-// Sum of the walkers' partial sums, 16 strips of walkers at once, then the strips in order.
+// Sum of the workgroups' partial sums, 16 strips of them at once, then the strips in order.
 __global__ __launch_bounds__(256) void short_conv_fold_kernel(const float* __restrict__ part, int64_t rows, int64_t C,
                                                               int K, float* __restrict__ gw, float* __restrict__ gb) {
     __shared__ float lds[16][17];
@@ -250,32 +277,41 @@ __global__ __launch_bounds__(256) void short_conv_fold_kernel(const float* __res
     else if (gb) gb[c] = v;
 }
 
-// Runs of a row: one at least, for the state of a row without tokens.
-int64_t runs_of(const ConvShape& s) { return s.T ? ceil_div(s.T, kRun) : 1; }
+constexpr int kVec = 4;  // channels of a lane
 
-// Walkers: four workgroups a CU over all channels, but no more than there are runs.
-int64_t walkers_of(const ConvShape& s) {
-    const int64_t cols = ceil_div(s.C, 64 * (s.dtype == kBf16 ? 8 : 4));
-    int64_t n = ceil_div(1024, cols);
-    const int64_t most = ceil_div(s.B * runs_of(s), 4);
-    return n < most ? n : most;
+// Tokens of a run: as many as leave `waves` waves to the chip, 16 at least; a row has one run at least, for
+// its state if it has no tokens.
+struct ConvPlan {
+    int64_t run_tokens, runs, groups;  // runs of a row; workgroups a column of channels
+};
+ConvPlan plan(const ConvShape& s, int64_t waves) {
+    ConvPlan p{};
+    const int64_t cols = ceil_div(s.C, 64 * kVec);
+    int64_t n = ceil_div(s.B * s.T * cols, waves);
+    n = ceil_div(n < 16 ? 16 : n, 4) * 4;
+    p.run_tokens = n;
+    p.runs = s.T ? ceil_div(s.T, n) : 1;
+    p.groups = ceil_div(s.B * p.runs, 4);
+    return p;
 }
+constexpr int64_t kForwardWaves = 8192, kBackwardWaves = 4096;
 
 template <class E, int K, int VEC>
 hipError_t launch(const ConvShape& s, const ConvArgs& A, const ConvBwdArgs* g, hipStream_t st) {
-    const int64_t cols = ceil_div(s.C, 64 * VEC), runs = runs_of(s);
+    const int64_t cols = ceil_div(s.C, 64 * VEC);
     if (!g) {
-        hipLaunchKernelGGL((short_conv_kernel<E, K, VEC>), dim3((unsigned)(cols * ceil_div(s.B * runs, 4))), dim3(256), 0,
-                           st, s, A, runs, cols);
+        const ConvPlan p = plan(s, kForwardWaves);
+        hipLaunchKernelGGL((short_conv_kernel<E, K, VEC>), dim3((unsigned)(cols * p.groups)), dim3(256), 0, st, s, A,
+                           p.runs, p.run_tokens, cols);
         return hipGetLastError();
     }
-    const int64_t walkers = walkers_of(s);
-    hipLaunchKernelGGL((short_conv_bwd_kernel<E, K, VEC>), dim3((unsigned)(cols * walkers)), dim3(256), 0, st, s, A, *g,
-                       runs, cols, walkers);
+    const ConvPlan p = plan(s, kBackwardWaves);
+    hipLaunchKernelGGL((short_conv_bwd_kernel<E, K, VEC>), dim3((unsigned)(cols * p.groups)), dim3(256), 0, st, s, A, *g,
+                       p.runs, p.run_tokens, cols);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(short_conv_fold_kernel, dim3((unsigned)ceil_div((K + 1) * s.C, 16)), dim3(256), 0, st, g->part,
-                       walkers, s.C, K, g->gweight, g->gbias);
+                       p.groups, s.C, K, g->gweight, g->gbias);
     return hipGetLastError();
 }
 
@@ -295,11 +331,11 @@ hipError_t by_taps(const ConvShape& s, const ConvArgs& A, const ConvBwdArgs* g, 
 
 template <class E>
 hipError_t by_alignment(const ConvShape& s, const ConvArgs& A, const ConvBwdArgs* g, hipStream_t st) {
-    // 16-byte accesses where every row of every tensor starts on 16 bytes.
+    // Accesses of four elements where every row of every tensor starts on that.
     uintptr_t all = (uintptr_t)A.x | (uintptr_t)A.s_in | (uintptr_t)A.y | (uintptr_t)A.s_out;
     if (g) all |= (uintptr_t)g->gy | (uintptr_t)g->gs_out | (uintptr_t)g->gx | (uintptr_t)g->gs_in;
-    const bool wide = s.C % ElemVec<E>::n == 0 && all % 16 == 0;
-    return wide ? by_taps<E, ElemVec<E>::n>(s, A, g, st) : by_taps<E, 1>(s, A, g, st);
+    const bool wide = s.C % kVec == 0 && all % (kVec * sizeof(E)) == 0;
+    return wide ? by_taps<E, kVec>(s, A, g, st) : by_taps<E, 1>(s, A, g, st);
 }
 
 }  // namespace
@@ -309,7 +345,7 @@ hipError_t run_short_conv(const ConvShape& s, const ConvArgs& A, hipStream_t st)
 }
 
 size_t short_conv_backward_ws_bytes(const ConvShape& s) {
-    return (size_t)walkers_of(s) * (size_t)(s.K + 1) * (size_t)s.C * sizeof(float);
+    return (size_t)plan(s, kBackwardWaves).groups * (size_t)(s.K + 1) * (size_t)s.C * sizeof(float);
 }
 
 hipError_t run_short_conv_backward(const ConvShape& s, const ConvArgs& A, const ConvBwdArgs& g, hipStream_t st) {

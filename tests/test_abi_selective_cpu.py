@@ -42,7 +42,7 @@ def test_scan_sizes(lib, shape):
 
 
 @pytest.mark.parametrize("shape", [((1 << 20) + 1, 1, 1, 1, 1), (1, (1 << 30) + 1, 1, 1, 1), (1, 1, (1 << 22) + 1, 1, 1),
-                                   (1, 1, 1 << 22, 1, 17), (1 << 18, 1, 1 << 13, 1, 4), (1 << 20, 1, 8, 8, 1),
+                                   (1, 1, 1 << 22, 1, 17), (1, 1, 1 << 21, 1 << 21, 9), (1 << 18, 1, 1 << 13, 1, 4), (1 << 20, 1, 8, 8, 1),
                                    (1 << 20, 1 << 30, 1, 1, 1), (1, 1 << 30, 1 << 15, 1, 1), (1 << 62, 1 << 62, 1, 1, 1)],
                          ids=str)
 def test_scan_limits(lib, shape):
