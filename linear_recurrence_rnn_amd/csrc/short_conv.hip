@@ -12,7 +12,7 @@
 //
 // A lane takes VEC neighbouring channels and walks down a run of tokens with the last K-1
 // inputs, and backwards also the last K-1 of q, in registers, so a token is read once but for the K-1
-// before (and, backwards, behind) a run; the next kAhead tokens are on their way meanwhile.  Both
+// before (and, backwards, behind) a run; the next tokens are on their way meanwhile.  Both
 // directions are bound by memory.  The sums over tokens are kept in registers over a run, go to the
 // workspace and are added in the order of the runs.
 #include "short_conv.hpp"
@@ -23,7 +23,9 @@ namespace linrec {
 
 namespace {
 
-constexpr int kAhead = 4;  // tokens asked for at once
+// Tokens asked for at once.  Forward, 8 x 4096 tokens of 2560 bfloat16 channels take 65 us with four (5.2
+// TB/s), 67 with eight and 72 with two; backward 121 with two (4.2 TB/s), 135 with four.
+constexpr int kForwardAhead = 4, kBackwardAhead = 2;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -42,9 +44,12 @@ __device__ __forceinline__ int64_t row_length(const ConvShape& s, int64_t b) {
 template <class E, int VEC> struct Raw { typedef E type __attribute__((ext_vector_type(VEC))); };
 template <class E> struct Raw<E, 1> { typedef E type; };
 
+// Row `row` (the same for the wave) of p, a lane's channels from byte `off`: the form that takes two
+// scalar registers and one vector register for the address.
 template <class E, int VEC>
-__device__ __forceinline__ typename Raw<E, VEC>::type load_raw(const void* p, int64_t at) {
-    return *reinterpret_cast<const typename Raw<E, VEC>::type*>(reinterpret_cast<const E*>(p) + at);
+__device__ __forceinline__ typename Raw<E, VEC>::type load_raw(const void* p, int64_t row, int64_t C, unsigned off) {
+    const char* const base = reinterpret_cast<const char*>(reinterpret_cast<const E*>(p) + row * C);
+    return *reinterpret_cast<const typename Raw<E, VEC>::type*>(base + off);
 }
 template <class E, int VEC>
 __device__ __forceinline__ void values(const typename Raw<E, VEC>::type& v, bool there, float (&out)[VEC]) {
@@ -55,23 +60,24 @@ __device__ __forceinline__ void values(const typename Raw<E, VEC>::type& v, bool
     }
 }
 template <class E, int VEC>
-__device__ __forceinline__ void store_vec(void* p, int64_t at, const float (&in)[VEC]) {
+__device__ __forceinline__ void store_vec(void* p, int64_t row, int64_t C, unsigned off, const float (&in)[VEC]) {
     typename Raw<E, VEC>::type v;
     if constexpr (VEC == 1) v = (E)in[0];
     else
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[j] = (E)in[j];
-    *reinterpret_cast<typename Raw<E, VEC>::type*>(reinterpret_cast<E*>(p) + at) = v;
+    char* const base = reinterpret_cast<char*>(reinterpret_cast<E*>(p) + row * C);
+    *reinterpret_cast<typename Raw<E, VEC>::type*>(base + off) = v;
 }
 
 // Input at token t (which may lie in the state, t < 0) of row b, channels c..; zero where there is none.
 template <class E, int VEC>
 __device__ __forceinline__ void load_input(const ConvShape& s, const ConvArgs& A, int64_t b, int64_t t, int64_t len,
-                                           int64_t c, float (&out)[VEC]) {
+                                           unsigned off, float (&out)[VEC]) {
     if (t >= 0 && t < len) {
-        values<E, VEC>(load_raw<E, VEC>(A.x, (b * s.T + t) * s.C + c), true, out);
+        values<E, VEC>(load_raw<E, VEC>(A.x, b * s.T + t, s.C, off), true, out);
     } else if (t < 0 && A.s_in) {
-        values<E, VEC>(load_raw<E, VEC>(A.s_in, (b * (s.K - 1) + t + s.K - 1) * s.C + c), true, out);
+        values<E, VEC>(load_raw<E, VEC>(A.s_in, b * (s.K - 1) + t + s.K - 1, s.C, off), true, out);
     } else {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) out[j] = 0.f;
@@ -95,37 +101,40 @@ __global__ __launch_bounds__(256) void short_conv_kernel(ConvShape s, ConvArgs A
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t col = blockIdx.x % cols, run = blockIdx.x / cols * 4 + wave;
     const int64_t c = (col * 64 + (threadIdx.x & 63)) * VEC;
+    const unsigned off = (unsigned)c * (unsigned)sizeof(E);
     if (c >= s.C || run >= s.B * runs) return;
     const int64_t b = run / runs, t0 = run % runs * run_tokens, len = row_length(s, b);
     const int64_t t_end = t0 + run_tokens < s.T ? t0 + run_tokens : s.T;
-    // Tokens behind the run are read as its last one and not used.
-    typename Raw<E, VEC>::type next[kAhead];
+    // Tokens that are absent or behind the run are read as the last one that is neither, and not used.
+    const int64_t t_live = t_end < len ? t_end : len;
+    typename Raw<E, VEC>::type next[kForwardAhead];
     const auto fetch = [&](int64_t t) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            next[u] = load_raw<E, VEC>(A.x, (b * s.T + (t + u < t_end ? t + u : t_end - 1)) * s.C + c);
+        for (int u = 0; u < kForwardAhead; ++u)
+            next[u] = load_raw<E, VEC>(A.x, b * s.T + (t + u < t_live ? t + u : t_live - 1), s.C, off);
     };
-    if (t0 < t_end) fetch(t0);
+    if (t0 < t_live) fetch(t0);
     float w[K][VEC], bias[VEC];
     load_filters<K, VEC>(A, c, w, bias);
     float x[K][VEC];  // x[k] = x_{t-K+1+k}
 #pragma unroll
-    for (int k = 0; k < K - 1; ++k) load_input<E, VEC>(s, A, b, t0 - (K - 1) + k, len, c, x[k + 1]);
+    for (int k = 0; k < K - 1; ++k) load_input<E, VEC>(s, A, b, t0 - (K - 1) + k, len, off, x[k + 1]);
     // The first run of a row also writes the state, which may be the one that was read: all that
     // is needed of that is in registers before.
     float keep[K > 1 ? K - 1 : 1][VEC];
     const bool states = A.s_out && t0 == 0;
     if (states) {
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) load_input<E, VEC>(s, A, b, len - (K - 1) + k, len, c, keep[k]);
+        for (int k = 0; k < K - 1; ++k) load_input<E, VEC>(s, A, b, len - (K - 1) + k, len, off, keep[k]);
     }
-    for (int64_t t1 = t0; t1 < t_end; t1 += kAhead) {
-        typename Raw<E, VEC>::type now[kAhead];
+    int64_t t1 = t0;
+    for (; t1 < t_live; t1 += kForwardAhead) {
+        typename Raw<E, VEC>::type now[kForwardAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) now[u] = next[u];
-        if (t1 + kAhead < t_end) fetch(t1 + kAhead);
+        for (int u = 0; u < kForwardAhead; ++u) now[u] = next[u];
+        if (t1 + kForwardAhead < t_live) fetch(t1 + kForwardAhead);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
+        for (int u = 0; u < kForwardAhead; ++u) {
             const int64_t t = t1 + u;
 #pragma unroll
             for (int k = 0; k < K - 1; ++k)
@@ -141,12 +150,16 @@ __global__ __launch_bounds__(256) void short_conv_kernel(ConvShape s, ConvArgs A
                 if (s.act == kActSilu) v *= logistic(v);
                 y[j] = t < len ? v : 0.f;
             }
-            if (t < t_end) store_vec<E, VEC>(A.y, (b * s.T + t) * s.C + c, y);
+            if (t < t_end) store_vec<E, VEC>(A.y, b * s.T + t, s.C, off, y);
         }
     }
+    float none[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) none[j] = 0.f;
+    for (; t1 < t_end; ++t1) store_vec<E, VEC>(A.y, b * s.T + t1, s.C, off, none);
     if (states) {
 #pragma unroll
-        for (int k = 0; k < K - 1; ++k) store_vec<E, VEC>(A.s_out, (b * (K - 1) + k) * s.C + c, keep[k]);
+        for (int k = 0; k < K - 1; ++k) store_vec<E, VEC>(A.s_out, b * (K - 1) + k, s.C, off, keep[k]);
     }
 }
 
@@ -157,6 +170,7 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t col = blockIdx.x % cols, walker = blockIdx.x / cols, run = walker * 4 + wave;
     const int64_t c = (col * 64 + lane) * VEC;
+    const unsigned off = (unsigned)c * (unsigned)sizeof(E);
     const bool live = c < s.C;
     float gw[K][VEC], gb[VEC];
 #pragma unroll
@@ -170,13 +184,13 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
         const int64_t t_end = t0 + run_tokens < s.T ? t0 + run_tokens : s.T;
         // The line's elements up to K-1 tokens beyond the run: x's gradient at a token needs the q behind it.
         // Absent tokens are read as the last one that is there and not used.
-        typename Raw<E, VEC>::type nx[kAhead], ny[kAhead];
+        typename Raw<E, VEC>::type nx[kBackwardAhead], ny[kBackwardAhead];
         const auto fetch = [&](int64_t t) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int64_t at = (b * s.T + (t + u < len ? t + u : len - 1)) * s.C + c;
-                nx[u] = load_raw<E, VEC>(A.x, at);
-                ny[u] = load_raw<E, VEC>(g.gy, at);
+            for (int u = 0; u < kBackwardAhead; ++u) {
+                const int64_t row = b * s.T + (t + u < len ? t + u : len - 1);
+                nx[u] = load_raw<E, VEC>(A.x, row, s.C, off);
+                ny[u] = load_raw<E, VEC>(g.gy, row, s.C, off);
             }
         };
         if (t0 < len) fetch(t0);
@@ -185,17 +199,17 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
         float x[K][VEC], q[K][VEC];  // x[k] = x_{t-K+1+k}, q[k] = q_{t-k}
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (k < K - 1) load_input<E, VEC>(s, A, b, t0 - (K - 1) + k, len, c, x[k + 1 < K ? k + 1 : 0]);
+            if (k < K - 1) load_input<E, VEC>(s, A, b, t0 - (K - 1) + k, len, off, x[k + 1 < K ? k + 1 : 0]);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) q[k][j] = 0.f;
         }
-        for (int64_t t1 = t0; t1 < t_end + K - 1; t1 += kAhead) {
-            typename Raw<E, VEC>::type vx[kAhead], vy[kAhead];
+        for (int64_t t1 = t0; t1 < t_end + K - 1; t1 += kBackwardAhead) {
+            typename Raw<E, VEC>::type vx[kBackwardAhead], vy[kBackwardAhead];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) vx[u] = nx[u], vy[u] = ny[u];
-            if (t1 + kAhead < len && t1 + kAhead < t_end + K - 1) fetch(t1 + kAhead);
+            for (int u = 0; u < kBackwardAhead; ++u) vx[u] = nx[u], vy[u] = ny[u];
+            if (t1 + kBackwardAhead < len && t1 + kBackwardAhead < t_end + K - 1) fetch(t1 + kBackwardAhead);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
+            for (int u = 0; u < kBackwardAhead; ++u) {
                 const int64_t t = t1 + u, out = t - (K - 1);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
@@ -235,12 +249,12 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
                 }
                 if (g.gs_out && t >= len && t < len + K - 1) {
                     float gs[VEC];
-                    values<E, VEC>(load_raw<E, VEC>(g.gs_out, (b * (K - 1) + t - len) * s.C + c), true, gs);
+                    values<E, VEC>(load_raw<E, VEC>(g.gs_out, b * (K - 1) + t - len, s.C, off), true, gs);
 #pragma unroll
                     for (int j = 0; j < VEC; ++j) v[j] += gs[j];
                 }
-                if (out >= 0) store_vec<E, VEC>(g.gx, (b * s.T + out) * s.C + c, v);
-                else store_vec<E, VEC>(g.gs_in, (b * (K - 1) + t) * s.C + c, v);
+                if (out >= 0) store_vec<E, VEC>(g.gx, b * s.T + out, s.C, off, v);
+                else store_vec<E, VEC>(g.gs_in, b * (K - 1) + t, s.C, off, v);
             }
         }
     }
@@ -287,14 +301,19 @@ struct ConvPlan {
 ConvPlan plan(const ConvShape& s, int64_t waves) {
     ConvPlan p{};
     const int64_t cols = ceil_div(s.C, 64 * kVec);
-    int64_t n = ceil_div(s.B * s.T * cols, waves);
+    int64_t runs = waves / cols / s.B;  // of a row, so that all of them fit
+    if (runs < 1) runs = 1;
+    int64_t n = ceil_div(s.T, runs);
     n = ceil_div(n < 16 ? 16 : n, 4) * 4;
     p.run_tokens = n;
     p.runs = s.T ? ceil_div(s.T, n) : 1;
     p.groups = ceil_div(s.B * p.runs, 4);
     return p;
 }
-constexpr int64_t kForwardWaves = 8192, kBackwardWaves = 4096;
+// Forward four times what the chip holds at once, so that ragged rows even out: a batch of 16 ragged
+// rows of up to 2000 tokens takes 43 us, 47 with half as many waves; full rows care little.  Backward what
+// it holds: 16 workgroups more than that cost a second round (174 us for 135).
+constexpr int64_t kForwardWaves = 16384, kBackwardWaves = 4096;
 
 template <class E, int K, int VEC>
 hipError_t launch(const ConvShape& s, const ConvArgs& A, const ConvBwdArgs* g, hipStream_t st) {
