@@ -18,6 +18,8 @@
 // Where the rows and channels are too few to fill the chip, the rows are cut into segments: each
 // segment's state from a zero state, and the sum of its steps (the decay over a segment is e^{A sum}),
 // then the states that enter the segments one after the other, then the segments again from those.
+#include <type_traits>
+
 #include "selective_math.hpp"
 
 namespace linrec {
@@ -231,61 +233,145 @@ __global__ __launch_bounds__(256) void sel_join_kernel(SelShape s, const float* 
     if (out && n < s.N) out[at] = x;
 }
 
-// One token: LN lanes a channel, four states each.
-template <class E, bool VEC>
-__global__ __launch_bounds__(256) void sel_step_kernel(SelShape s, SelArgs A, int ln) {
-    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = j / ln;  // b * C + c
-    const int n0 = (int)(j % ln) * 4;
-    const bool live = row < s.B * s.C;
-    const int64_t b = live ? row / s.C : 0, c = live ? row % s.C : 0;
-    float y = 0.f, u = 0.f;
-    if (live) {
-        u = (float)reinterpret_cast<const E*>(A.u)[row];
-        float d = (float)reinterpret_cast<const E*>(A.dt)[row] + (A.bias ? A.bias[c] : 0.f), sig;
-        if (s.softplus) d = softplus(d, sig);
-        const int64_t bg = (b * s.G + c / (s.C / s.G)) * s.N;
-        const E* Bm = reinterpret_cast<const E*>(A.Bm) + bg;
-        const E* Cm = reinterpret_cast<const E*>(A.Cm) + bg;
-        float h[4], a[4];
+// v of lane `I` of each LN lanes (of each four, where they are more).
+template <int LN, int I>
+__device__ __forceinline__ float of_lane(float v) {
+    if constexpr (LN == 1) return v;
+    constexpr int ctrl = LN == 2 ? (I | I << 2 | (2 + I) << 4 | (2 + I) << 6) : I * 0x55;  // quad_perm
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
+}
+
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// v summed over LN lanes, in every one of them.
+template <int LN>
+__device__ __forceinline__ float over_lanes(float v) {
+    if constexpr (LN > 1) v = add_dpp<0xb1>(v);   // quad_perm [1,0,3,2]
+    if constexpr (LN > 2) v = add_dpp<0x4e>(v);   // quad_perm [2,3,0,1]
+    if constexpr (LN > 4) v = add_dpp<0x141>(v);  // row_half_mirror
+    if constexpr (LN > 8) v = add_dpp<0x140>(v);  // row_mirror
+    if constexpr (LN > 16) {
+        const u32x2 r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return v;
+}
+
+// One token.  LN lanes hold a channel's states, four each, and M neighbouring channels of them; what
+// depends on the channel alone is formed once, channel i's by lane i.  Bound by memory, the state read and
+// written; VEC: 16 bytes of it at once.
+template <class E, int LN, bool VEC>
+__global__ __launch_bounds__(256) void sel_step_kernel(SelShape s, SelArgs A, unsigned col_blocks) {
+    constexpr int M = LN < 4 ? LN : 4, kChan = 256 / LN * M;  // channels of a workgroup
+    const unsigned b = blockIdx.x / col_blocks, col = blockIdx.x % col_blocks;
+    const unsigned l = threadIdx.x % LN, c0 = col * kChan + threadIdx.x / LN * M;
+    const int n0 = (int)l * 4;
+    const unsigned C = (unsigned)s.C, Cg = C / (unsigned)s.G;
+    const int64_t rows = (int64_t)b * s.C;  // b * C: of the state's rows, and of u
+    float h[M][4], a[M][4], Bv[M][4], Cv[M][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = a[i] = 0.f;
+    for (int i = 0; i < M; ++i) {
+        const bool live = c0 + i < C;
+        const int64_t at = (live ? c0 + i : 0u) * (int64_t)s.N + n0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i][j] = a[i][j] = 0.f;
         if constexpr (VEC) {
-            if (n0 < s.N) {
-                load16<float>(A.A + c * s.N + n0, a);
-                if (A.s_in) load16<float>(A.s_in + row * s.N + n0, h);
+            if (live && n0 < s.N) {
+                load16<float>(A.A + at, a[i]);
+                if (A.s_in) load16<float>(A.s_in + rows * s.N + at, h[i]);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n0 + i < s.N) {
-                    a[i] = A.A[c * s.N + n0 + i];
-                    if (A.s_in) h[i] = A.s_in[row * s.N + n0 + i];
+            for (int j = 0; j < 4; ++j)
+                if (live && n0 + j < s.N) {
+                    a[i][j] = A.A[at + j];
+                    if (A.s_in) h[i][j] = A.s_in[rows * s.N + at + j];
                 }
         }
+    }
+    // B and C: the same for all channels of one group.
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (n0 + i >= s.N) continue;
-            h[i] = fmaf(fast_exp2(d * (a[i] * kLog2e)), h[i], d * u * (float)Bm[n0 + i]);
-            y = fmaf((float)Cm[n0 + i], h[i], y);
+    for (int i = 0; i < M; ++i) {
+        if (i > 0 && s.G == 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) Bv[i][j] = Bv[0][j], Cv[i][j] = Cv[0][j];
+            continue;
         }
-        if constexpr (VEC) {
-            if (n0 < s.N) store16<float>(A.s_out + row * s.N + n0, h);
-        } else {
+        const unsigned c = c0 + i < C ? c0 + i : C - 1, g = s.G == 1 ? 0u : c / Cg;
+        const int64_t at = ((int64_t)b * s.G + g) * s.N;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n0 + i < s.N) A.s_out[row * s.N + n0 + i] = h[i];
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + j < s.N ? n0 + j : 0;
+            Bv[i][j] = n0 + j < s.N ? (float)reinterpret_cast<const E*>(A.Bm)[at + n] : 0.f;
+            Cv[i][j] = n0 + j < s.N ? (float)reinterpret_cast<const E*>(A.Cm)[at + n] : 0.f;
         }
     }
-    for (int o = 1; o < ln; o <<= 1) y += __shfl_xor(y, o);
-    if (live && n0 == 0) {
-        if (A.D) y = fmaf(A.D[c], u, y);
-        if (A.z) {
-            const float z = (float)reinterpret_cast<const E*>(A.z)[row];
-            y *= z * logistic(z);
-        }
-        reinterpret_cast<E*>(A.y)[row] = (E)y;
+    // This lane's own channel, the same for every fourth lane.
+    const unsigned own = l % M;
+    const bool mine = l < (unsigned)M && c0 + own < C;
+    const unsigned c = c0 + own < C ? c0 + own : C - 1;
+    const float u = (float)reinterpret_cast<const E*>(A.u)[rows + c];
+    float d = (float)reinterpret_cast<const E*>(A.dt)[rows + c] + (A.bias ? A.bias[c] : 0.f), sig, gate = 1.f;
+    const float Dc = A.D ? A.D[c] : 0.f;
+    if (A.z) {
+        const float z = (float)reinterpret_cast<const E*>(A.z)[rows + c];
+        gate = z * logistic(z);
     }
+    if (s.softplus) d = softplus(d, sig);
+    const float du = d * u;
+    float out = 0.f;
+    const auto channel = [&](auto index) {
+        constexpr int i = decltype(index)::value;
+        if constexpr (i < M) {
+            const float di = of_lane<LN, i>(d), xi = of_lane<LN, i>(du);
+            float y = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[i][j] = fmaf(fast_exp2(di * (a[i][j] * kLog2e)), h[i][j], xi * Bv[i][j]);
+                y = fmaf(Cv[i][j], h[i][j], y);
+            }
+            y = over_lanes<LN>(y);
+            out = own == (unsigned)i ? y : out;
+            if (c0 + i < C && n0 < s.N) {
+                float* const o = A.s_out + (rows + c0 + i) * s.N + n0;
+                if constexpr (VEC) {
+                    store16<float>(o, h[i]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (n0 + j < s.N) o[j] = h[i][j];
+                }
+            }
+        }
+    };
+    channel(std::integral_constant<int, 0>());
+    channel(std::integral_constant<int, 1>());
+    channel(std::integral_constant<int, 2>());
+    channel(std::integral_constant<int, 3>());
+    if (mine) reinterpret_cast<E*>(A.y)[rows + c] = (E)(fmaf(Dc, u, out) * gate);
+}
+
+template <class E, int LN>
+hipError_t step(const SelShape& s, const SelArgs& A, hipStream_t st) {
+    const int64_t col_blocks = ceil_div(s.C, 256 / LN * (LN < 4 ? LN : 4));
+    const dim3 grid((unsigned)(s.B * col_blocks));
+    const bool vec = s.N % 4 == 0 && ((uintptr_t)A.A | (uintptr_t)A.s_in | (uintptr_t)A.s_out) % 16 == 0;
+    if (vec) hipLaunchKernelGGL((sel_step_kernel<E, LN, true>), grid, dim3(256), 0, st, s, A, (unsigned)col_blocks);
+    else hipLaunchKernelGGL((sel_step_kernel<E, LN, false>), grid, dim3(256), 0, st, s, A, (unsigned)col_blocks);
+    return hipGetLastError();
+}
+
+template <class E>
+hipError_t step_by_states(const SelShape& s, const SelArgs& A, hipStream_t st) {
+    if (s.N <= 4) return step<E, 1>(s, A, st);
+    if (s.N <= 8) return step<E, 2>(s, A, st);
+    if (s.N <= 16) return step<E, 4>(s, A, st);
+    if (s.N <= 32) return step<E, 8>(s, A, st);
+    if (s.N <= 64) return step<E, 16>(s, A, st);
+    return step<E, 32>(s, A, st);
 }
 
 template <class E, int W, int NPT>
@@ -373,18 +459,7 @@ hipError_t run_sel_join(const SelShape& s, const float* A, float* v, const float
 }
 
 hipError_t run_sel_step(const SelShape& s, const SelArgs& A, hipStream_t st) {
-    int ln = 1;
-    while (4 * ln < s.N) ln *= 2;
-    const dim3 grid((unsigned)ceil_div(s.B * s.C * ln, 256));
-    const bool vec = s.N % 4 == 0 && ((uintptr_t)A.A | (uintptr_t)A.s_in | (uintptr_t)A.s_out) % 16 == 0;
-    if (s.dtype == kBf16) {
-        if (vec) hipLaunchKernelGGL((sel_step_kernel<bf16_t, true>), grid, dim3(256), 0, st, s, A, ln);
-        else hipLaunchKernelGGL((sel_step_kernel<bf16_t, false>), grid, dim3(256), 0, st, s, A, ln);
-    } else {
-        if (vec) hipLaunchKernelGGL((sel_step_kernel<float, true>), grid, dim3(256), 0, st, s, A, ln);
-        else hipLaunchKernelGGL((sel_step_kernel<float, false>), grid, dim3(256), 0, st, s, A, ln);
-    }
-    return hipGetLastError();
+    return s.dtype == kBf16 ? step_by_states<bf16_t>(s, A, st) : step_by_states<float>(s, A, st);
 }
 
 }  // namespace linrec
