@@ -422,30 +422,38 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
 }
 
 // More than 16 states: the tiles' sums over states added, and the gradients of each token and
-// channel.  A workgroup takes one block's tokens of 64 channels, 16 tokens a wave.
+// channel.  A workgroup takes one block's tokens of 64 channels, 4 tokens a wave.
 template <class E>
-__global__ __launch_bounds__(256) void sel_finish_kernel(SelShape s, SelArgs A, SelBwdArgs g, SelBwdScratch W,
-                                                         int64_t blocks, int ntiles) {
-    __shared__ float acc[2][4][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+__global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A, SelBwdArgs g, SelBwdScratch S,
+                                                          int64_t blocks, int ntiles) {
+    constexpr int kWaves = 16, kTok = kSelBlock / kWaves;
+    __shared__ float acc[2][kWaves][64];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t cols = (s.C + 63) / 64;
     const int64_t c = (int64_t)(blockIdx.x % cols) * 64 + lane;
     const int64_t row = blockIdx.x / cols, k = row % blocks, b = row / blocks;
     const bool live = c < s.C;
-    const int64_t len = row_length(s, b), plane = s.B * s.T * s.C, t0 = k * kSelBlock + w * kSelTile;
+    const int64_t len = row_length(s, b), plane = s.B * s.T * s.C, t0 = k * kSelBlock + w * kTok;
     float sD = 0.f, sb = 0.f;
     if (live) {
         const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
-#pragma unroll 4
-        for (int64_t t = t0; t < t0 + kSelTile && t < s.T; ++t) {
-            const int64_t at = (b * s.T + t) * s.C + c;
+        float q[kTok][3];
+#pragma unroll
+        for (int e = 0; e < kTok; ++e) {
+            q[e][0] = q[e][1] = q[e][2] = 0.f;
+            const int64_t t = t0 + e < s.T ? t0 + e : s.T - 1;
+            for (int i = 0; i < ntiles; ++i) {
+                const float* o = S.q + (int64_t)i * 3 * plane + (b * s.T + t) * s.C + c;
+#pragma unroll
+                for (int j = 0; j < 3; ++j) q[e][j] += o[j * plane];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kTok; ++e) {
+            const int64_t t = t0 + e, at = (b * s.T + t) * s.C + c;
+            if (t >= s.T) continue;
             float gu = 0.f, gd = 0.f, gz = 0.f;
             if (t < len) {
-                float s1 = 0.f, s2 = 0.f, s3 = 0.f;
-                for (int i = 0; i < ntiles; ++i) {
-                    const float* o = W.q + (int64_t)i * 3 * plane + at;
-                    s1 += o[0], s2 += o[plane], s3 += o[2 * plane];
-                }
                 const float u = (float)reinterpret_cast<const E*>(A.u)[at];
                 float d = (float)reinterpret_cast<const E*>(A.dt)[at] + bias, sig = 1.f;
                 float p = (float)reinterpret_cast<const E*>(g.gy)[at];
@@ -453,11 +461,11 @@ __global__ __launch_bounds__(256) void sel_finish_kernel(SelShape s, SelArgs A, 
                 if (A.z) {
                     const float z = (float)reinterpret_cast<const E*>(A.z)[at];
                     const float sg = logistic(z);
-                    gz = p * sg * fmaf(z, 1.f - sg, 1.f) * fmaf(Dc, u, s3);
+                    gz = p * sg * fmaf(z, 1.f - sg, 1.f) * fmaf(Dc, u, q[e][2]);
                     p *= z * sg;
                 }
-                gd = fmaf(u, s2, s1) * sig;
-                gu = fmaf(Dc, p, d * s2);
+                gd = fmaf(u, q[e][1], q[e][0]) * sig;
+                gu = fmaf(Dc, p, d * q[e][1]);
                 sD = fmaf(p, u, sD);
                 sb += gd;
             }
@@ -468,47 +476,66 @@ __global__ __launch_bounds__(256) void sel_finish_kernel(SelShape s, SelArgs A, 
     }
     acc[0][w][lane] = sD, acc[1][w][lane] = sb;
     __syncthreads();
-    if (w < 2 && live)
-        W.gDb[(row * 2 + w) * s.C + c] = acc[w][0][lane] + acc[w][1][lane] + acc[w][2][lane] + acc[w][3][lane];
+    if (w < 2 && live) {
+        float v = acc[w][0][lane];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) v += acc[w][i][lane];
+        S.gDb[(row * 2 + w) * s.C + c] = v;
+    }
 }
 
-// Column sums of (rows, cols), rows added by 16 strips at once, then the strips in order.  The
-// column's place in the results: a state's (STATES), or D's and the bias's.
-template <bool STATES>
-__global__ __launch_bounds__(256) void sel_fold_kernel(SelShape s, const float* __restrict__ part, int64_t rows,
-                                                       int64_t cols, float* __restrict__ x, float* __restrict__ y) {
-    __shared__ float lds[16][17];
+// The partial sums: A's gradients over the rows of blocks, those of D and the bias, B's and C's over
+// the channel ranges.  Columns of (rows, cols) are added by 16 strips of rows at once, then the
+// strips in order; one launch does all three, in as many workgroups each as `wg` says.
+struct SelFold {
+    unsigned wg[3];
+    int64_t rows;
+};
+
+// The sum of column j, in the lanes of strip 0.
+__device__ __forceinline__ float fold_column(const float* __restrict__ part, int64_t rows, int64_t cols, int64_t j,
+                                             float (&lds)[16][17]) {
     const int cx = threadIdx.x & 15, strip = threadIdx.x >> 4;
-    const int64_t j = (int64_t)blockIdx.x * 16 + cx;
     float v = 0.f;
     if (j < cols)
 #pragma unroll 4
         for (int64_t r = strip; r < rows; r += 16) v += part[r * cols + j];
     lds[strip][cx] = v;
     __syncthreads();
-    if (strip != 0 || j >= cols) return;
+    if (strip == 0) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) v += lds[i][cx];
-    if constexpr (STATES) {
-        const int n = (int)(j / (4 * s.C)) * 4 + (int)(j & 3);
-        if (n < s.N) x[j / 4 % s.C * s.N + n] = v;
-    } else if (j < s.C) {
-        if (x) x[j] = v;
-    } else if (y) {
-        y[j - s.C] = v;
+        for (int i = 1; i < 16; ++i) v += lds[i][cx];
     }
+    return v;
 }
 
-// B's and C's gradients: the channel ranges' shares added.
 template <class E>
-__global__ __launch_bounds__(256) void sel_fold_bc_kernel(SelShape s, const float* __restrict__ part, int64_t cuts,
-                                                          E* __restrict__ gB, E* __restrict__ gC, int64_t total) {
+__global__ __launch_bounds__(256) void sel_fold_kernel(SelShape s, SelBwdArgs g, SelBwdScratch S, SelFold f) {
+    __shared__ float lds[16][17];
     const int Np = (s.N + 3) / 4 * 4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    unsigned blk = blockIdx.x;
+    if (blk < f.wg[0]) {
+        const int64_t cols = (int64_t)Np * s.C, j = (int64_t)blk * 16 + (threadIdx.x & 15);
+        const float v = fold_column(S.gA, f.rows, cols, j, lds);
+        const int n = (int)(j / (4 * s.C)) * 4 + (int)(j & 3);
+        if (threadIdx.x < 16 && j < cols && n < s.N) g.gA[j / 4 % s.C * s.N + n] = v;
+        return;
+    }
+    blk -= f.wg[0];
+    if (blk < f.wg[1]) {
+        const int64_t cols = 2 * s.C, j = (int64_t)blk * 16 + (threadIdx.x & 15);
+        const float v = fold_column(S.gDb, f.rows, cols, j, lds);
+        float* const out = j < s.C ? g.gD : g.gbias;
+        if (threadIdx.x < 16 && j < cols && out) out[j < s.C ? j : j - s.C] = v;
+        return;
+    }
+    blk -= f.wg[1];
+    const int64_t total = s.B * s.T * s.G * 2 * Np;
+    for (int64_t i = (int64_t)blk * 256 + threadIdx.x; i < total; i += (int64_t)f.wg[2] * 256) {
         float v = 0.f;
-        for (int64_t k = 0; k < cuts; ++k) v += part[k * total + i];
+        for (int64_t k = 0; k < S.cuts; ++k) v += S.gBC[k * total + i];
         const int j = (int)(i % (2 * Np)), n = j % Np;
-        if (n < s.N) (j < Np ? gB : gC)[i / (2 * Np) * s.N + n] = (E)v;
+        if (n < s.N) reinterpret_cast<E*>(j < Np ? g.gB : g.gC)[i / (2 * Np) * s.N + n] = (E)v;
     }
 }
 
@@ -531,7 +558,7 @@ hipError_t by_waves(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, co
     hipLaunchKernelGGL((sel_gradient_kernel<E, 4, false>), grid, dim3(256), 0, st, s, A, g, bc, keep, S, (int)blocks, ntiles);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(s.B * blocks * ceil_div(s.C, 64))), dim3(256), 0, st, s,
+    hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(s.B * blocks * ceil_div(s.C, 64))), dim3(1024), 0, st, s,
                        A, g, S, blocks, ntiles);
     return hipGetLastError();
 }
@@ -539,26 +566,18 @@ hipError_t by_waves(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, co
 template <class E>
 hipError_t backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const float* bc, const float* keep,
                     const SelBwdScratch& W, hipStream_t st) {
-    const int64_t rows = s.B * sel_blocks(s);
     const int waves = sel_backward_plan(s).waves;
     hipError_t e = waves == 1   ? by_waves<E, 1>(s, A, g, bc, keep, W, st)
                    : waves == 2 ? by_waves<E, 2>(s, A, g, bc, keep, W, st)
                                 : by_waves<E, 4>(s, A, g, bc, keep, W, st);
     if (e != hipSuccess) return e;
-    const int64_t cols = (int64_t)sel_n4(s) * 4 * s.C;
-    hipLaunchKernelGGL((sel_fold_kernel<true>), dim3((unsigned)ceil_div(cols, 16)), dim3(256), 0, st, s, W.gA, rows,
-                       cols, g.gA, (float*)nullptr);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (g.gD || g.gbias) {
-        hipLaunchKernelGGL((sel_fold_kernel<false>), dim3((unsigned)ceil_div(2 * s.C, 16)), dim3(256), 0, st, s, W.gDb,
-                           rows, 2 * s.C, g.gD, g.gbias);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    const int64_t total = s.B * s.T * s.G * 2 * sel_n4(s) * 4;
-    int64_t wg = ceil_div(total, 256);
-    if (wg > 8192) wg = 8192;
-    hipLaunchKernelGGL((sel_fold_bc_kernel<E>), dim3((unsigned)wg), dim3(256), 0, st, s, W.gBC, W.cuts, (E*)g.gB,
-                       (E*)g.gC, total);
+    SelFold f{};
+    f.rows = s.B * sel_blocks(s);
+    f.wg[0] = (unsigned)ceil_div((int64_t)sel_n4(s) * 4 * s.C, 16);
+    f.wg[1] = g.gD || g.gbias ? (unsigned)ceil_div(2 * s.C, 16) : 0;
+    const int64_t wg = ceil_div(s.B * s.T * s.G * 2 * sel_n4(s) * 4, 256);
+    f.wg[2] = (unsigned)(wg < 8192 ? wg : 8192);
+    hipLaunchKernelGGL((sel_fold_kernel<E>), dim3(f.wg[0] + f.wg[1] + f.wg[2]), dim3(256), 0, st, s, g, W, f);
     return hipGetLastError();
 }
 
