@@ -17,9 +17,9 @@
 // The last kernel sums over states (for each token and channel) and over channels (for each token
 // and state).  Like the forward, a wave holds 64 channels, a lane each, and 4 states of them, with B and C by
 // scalar loads; sums over the states are added in the lane and over the waves through LDS.  Sums over the
-// lanes are transposed there: 16 values (4 tokens, 4 states) are written as rows of 64 and read back as
-// quarters of rows, 16 floats a lane, that the lane adds; what the four lanes of a row have left is folded for
-// 64 values at once.  9 cycles of the vector unit a state for both sums, where folds across the
+// lanes are transposed there: 8 values (2 tokens, 4 states) are written as rows of 64 and read back as
+// eighths of rows, 8 floats a lane, that the lane adds; what the eight lanes of a row have left is folded for
+// 64 values at once.  10 cycles of the vector unit a state for both sums, where folds across the
 // lanes alone would take 24.  (float32 products of the matrix unit with columns of ones were slower: on this
 // chip they keep the vector unit from its own work, 34 cycles and 35 of it taking 74.)
 // Sums over blocks, batch rows and channel ranges are partial sums in the workspace, added in
@@ -142,25 +142,36 @@ __device__ __forceinline__ float fold_dpp(float a, float b, bool up) {
     const float own = up ? b : a, other = up ? a : b;
     return own + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(other), CTRL, 0xf, 0xf, true));
 }
-constexpr int kXor1 = 0xb1, kXor2 = 0x4e;  // quad_perm [1,0,3,2] and [2,3,0,1]
+constexpr int kMirror8 = 0x141, kXor1 = 0xb1, kXor2 = 0x4e;  // quad_perm [1,0,3,2] and [2,3,0,1]
 
-constexpr int kRowPad = 68;  // floats of a row of 64: a quarter starts on 16 bytes, 16 rows on 16 x 4 banks
+// Tokens of a tile whose decays are kept from the pass over the states to the one back over their gradients.
+// The others are formed again, 12 cycles of the vector unit each, so that the registers are enough for three waves
+// a SIMD: 1045 us for 8 x 4096 tokens of 2560 channels, 1061 with none kept, 1245 with all and two waves.
+constexpr int kKept = 4;
+
+constexpr int kRowPad = 68;  // floats of a row of 64: an eighth starts on 16 bytes, two rows on other banks
 
 template <int W>
 struct GradLds {
     f32x2 du[kSelTile][64];          // d, d u
     float p[kSelTile][64];
     float part[2][W][kSelTile][64];  // the waves' shares of sums over the states
-    float rows[W][16][kRowPad];      // 16 values of a wave on their way to being summed over its lanes
+    float rows[W][8][kRowPad];       // 8 values of a wave on their way to being summed over its lanes
 };
+
+// v, or zero: formed in any case, as a branch around it would part it from its neighbours.
+__device__ __forceinline__ float where(bool there, float v) {
+    asm volatile("" : "+v"(v));
+    return there ? v : 0.f;
+}
 
 // WHOLE: one workgroup has all states of its channels, so that its sums over them are complete.
 template <class E, int W, bool WHOLE>
-__global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
+__global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
                                                                               const float* __restrict__ bc,
                                                                               const float* __restrict__ keep,
                                                                               SelBwdScratch S, int blocks, int ntiles) {
-    constexpr int NPT = kBwdNpt, TW = kSelTile / W, kPairs = kSelTile / 2, kFours = kSelTile / 4;
+    constexpr int NPT = kBwdNpt, TW = kSelTile / W, kPairs = kSelTile / 2;
     __shared__ GradLds<W> L;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int Cg = (int)(s.C / s.G), cuts = (int)S.cuts;
@@ -230,16 +241,24 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
         G[i] = n0 + i < s.N ? S.carry[state_at(s, b * blocks + k, n0 + i, c)] : 0.f;
         gA[i] = 0.f;
     }
-    // A lane's quarter of a row.
+    // A lane's eighth of a row.
     float* const rows = &L.rows[w][0][0];
-    const float* const quarter = rows + (lane >> 2) * kRowPad + (lane & 3) * 16;
+    const float* const eighth = rows + (lane >> 3) * kRowPad + (lane & 7) * 8;
 
+    // The block's first tile of B and C and of their gradients, and steps from one tile to the next.
+    const float* const bc0 =
+        bc + ((((b * tiles + t_begin / kSelTile) * s.G + grp) * ntiles + nt) * W + w) * (kSelTile * 2 * NPT);
+    float* const gbc0 = S.gBC + ((((int64_t)cu * s.B + b) * T + t_begin) * s.G + grp) * 2 * Np;
+    const int bc_step = s.G * ntiles * W * (kSelTile * 2 * NPT), gbc_step = kSelTile * s.G * 2 * Np;
     for (int q = q_first; q >= 0; --q) {
         const int t0 = t_begin + q * kSelTile;
-        const float* row = bc + ((((b * tiles + t0 / kSelTile) * s.G + grp) * ntiles + nt) * W + w) * (kSelTile * 2 * NPT);
+        const float* row = bc0 + q * bc_step;
         // (Whether a token is there is the same for the whole wave.  Of an absent one, or a lane without a
         // channel, d, u and p are zero, which leaves the states and the sums over channels alone.)
         float sig[TW], gzf[TW], us[TW], h0[NPT];
+        int own = s.N - n0;
+        asm volatile("" : "+s"(own));  // four masks of the wave would be kept
+
 #pragma unroll
         for (int e = 0; e < TW; ++e) {
             const bool there = live && t0 + w * TW + e < len;
@@ -254,26 +273,29 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
             L.p[w * TW + e][lane] = there ? gy * (gated ? z * sg : 1.f) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < NPT; ++i) h0[i] = n0 + i < s.N ? next.h0[i] : 0.f;
-        fetch(q > 0 ? q - 1 : 0);  // in one place, the last time for nothing: two places would cost their addresses twice
+        for (int i = 0; i < NPT; ++i) h0[i] = i < own ? next.h0[i] : 0.f;
         __syncthreads();
         // The states of the tile again, their sums q3 = sum C h, and the sums over channels of p h.
-        float h[kSelTile][NPT], a[kSelTile][NPT], shares[kFours];
-        f32x4 quar[4];
+        float h[kSelTile][NPT], a[kKept][NPT], shares[kPairs];
+        f32x4 eight[2];
         const auto ask_sums = [&]() {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) quar[i] = *reinterpret_cast<const f32x4*>(quarter + 4 * i);
+            for (int i = 0; i < 2; ++i) eight[i] = *reinterpret_cast<const f32x4*>(eighth + 4 * i);
         };
         const auto take_sums = [&]() {
-            const f32x4 v = (quar[0] + quar[1]) + (quar[2] + quar[3]);
+            const f32x4 v = eight[0] + eight[1];
             return (v[0] + v[1]) + (v[2] + v[3]);
         };
-        const auto fold = [&]() {  // lane & 3 is the four of tokens
-            const float x = fold_dpp<kXor1>(shares[0], shares[1], lane & 1), y = fold_dpp<kXor1>(shares[2], shares[3], lane & 1);
-            return fold_dpp<kXor2>(x, y, lane & 2);
+        // A share of a pair of tokens joins the others: the pair's bits 0, 1 and 2 are the lane's bits 2, 1 and 0.
+        float xs[2], ys[2];
+        const auto join = [&](int j, bool up) {  // up: the pairs come in order, otherwise from the last
+            if (j % 2 != (up ? 1 : 0)) return;
+            xs[j / 2 % 2] = fold_dpp<kMirror8>(shares[j & ~1], shares[j | 1], lane & 4);
+            if (j / 2 % 2 == (up ? 1 : 0)) ys[j / 4] = fold_dpp<kXor2>(xs[0], xs[1], lane & 2);
         };
+        const auto fold = [&]() { return fold_dpp<kXor1>(ys[0], ys[1], lane & 1); };
         {
-            typedef SelGroup<NPT, 16> Group;
+            typedef SelGroup<NPT, 16> Group;  // pairs of tokens
             constexpr int kGroups = Group::kGroups, kTok = Group::kTok;
             Group of[2];
             float pt[2][2];
@@ -287,7 +309,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
             for (int j = 0; j < kGroups; ++j) {
                 const Group& v = of[j & 1];
                 if (j + 1 < kGroups) ahead(j + 1);
-                if (j % 2 == 0 && j > 0) ask_sums();
+                if (j > 0) ask_sums();
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int r = 0; r < kTok; ++r) {
@@ -295,37 +317,43 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
                     float q3 = 0.f;
 #pragma unroll
                     for (int i = 0; i < NPT; ++i) {
-                        a[t][i] = fast_exp2(v.x[r][0] * a2[i]);
-                        h[t][i] = fmaf(a[t][i], t ? h[t ? t - 1 : 0][i] : h0[i], v.x[r][1] * v.B(r, i));
+                        const float f = fast_exp2(v.x[r][0] * a2[i]);
+                        if (t >= kSelTile - kKept) a[t - (kSelTile - kKept)][i] = f;
+                        h[t][i] = fmaf(f, t ? h[t ? t - 1 : 0][i] : h0[i], v.x[r][1] * v.B(r, i));
                         q3 = fmaf(v.C(r, i), h[t][i], q3);
-                        rows[(t % 4 * NPT + i) * kRowPad + lane] = pt[j & 1][r] * h[t][i];
+                        rows[(r * NPT + i) * kRowPad + lane] = pt[j & 1][r] * h[t][i];
                     }
                     L.part[0][w][t][lane] = q3;
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                if (j % 2 == 1 && j > 1) shares[j / 2 - 1] = take_sums();
+                if (j > 0) shares[j - 1] = take_sums(), join(j - 1, true);
             }
             wave_lds_fence();
             ask_sums();
             wave_lds_fence();
-            shares[kFours - 1] = take_sums();
+            shares[kPairs - 1] = take_sums(), join(kPairs - 1, true);
         }
         const float totC = fold();
         __syncthreads();
-        if (live && (gated || !WHOLE)) {
+        if (gated || !WHOLE) {
+            float core[TW];
 #pragma unroll
             for (int e = 0; e < TW; ++e) {
-                const int t = w * TW + e;
-                if (t0 + t >= T) continue;
-                float core = 0.f;
+                core[e] = L.part[0][0][w * TW + e][lane];
 #pragma unroll
-                for (int j = 0; j < W; ++j) core += L.part[0][j][t][lane];
-                const unsigned at = (unsigned)(q * kSelTile + t) * C + c;
-                if constexpr (!WHOLE)
-                    store_elem<float>(S.q + ((int64_t)nt * 3 + 2) * s.B * T * s.C + base, at * 4, core);
-                else
-                    store_elem<E>((E*)g.gz + base, at * (unsigned)sizeof(E),
-                                  t0 + t < len ? gzf[e] * fmaf(Dc, us[e], core) : 0.f);
+                for (int j = 1; j < W; ++j) core[e] += L.part[0][j][w * TW + e][lane];
+                if (WHOLE) core[e] = where(t0 + w * TW + e < len, gzf[e] * fmaf(Dc, us[e], core[e]));
+            }
+            if (live) {
+#pragma unroll
+                for (int e = 0; e < TW; ++e) {
+                    const unsigned at = (unsigned)(q * kSelTile + w * TW + e) * C + c;
+                    if (t0 + w * TW + e >= T) break;
+                    if constexpr (!WHOLE)
+                        store_elem<float>(S.q + ((int64_t)nt * 3 + 2) * s.B * T * s.C + base, at * 4, core[e]);
+                    else
+                        store_elem<E>((E*)g.gz + base, at * (unsigned)sizeof(E), core[e]);
+                }
             }
         }
         __syncthreads();
@@ -345,7 +373,8 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
 #pragma unroll
             for (int j = kPairs - 1; j >= 0; --j) {
                 if (j > 0) ahead(j - 1);
-                if (j % 2 == 1 && j + 1 < kPairs) ask_sums();
+                if (j == kPairs / 2) fetch(q > 0 ? q - 1 : 0);  // the last time for nothing
+                if (j + 1 < kPairs) ask_sums();
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int r = 1; r >= 0; --r) {
@@ -355,57 +384,69 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 2 : 1) void sel_gradient_kernel(Se
 #pragma unroll
                     for (int i = 0; i < NPT; ++i) {
                         const float gt = fmaf(v[j & 1][r * 2 * NPT + NPT + i], p, G[i]);
-                        G[i] = gt * a[t][i];
+                        G[i] = gt * (t >= kSelTile - kKept ? a[t - (kSelTile - kKept)][i] : fast_exp2(d * a2[i]));
                         const float m = G[i] * (t ? h[t ? t - 1 : 0][i] : h0[i]);
                         gA[i] = fmaf(d, m, gA[i]);
                         q1 = fmaf(a2[i], m, q1);
                         q2 = fmaf(gt, v[j & 1][r * 2 * NPT + i], q2);
-                        rows[(t % 4 * NPT + i) * kRowPad + lane] = gt * du;
+                        rows[(r * NPT + i) * kRowPad + lane] = gt * du;
                     }
                     L.part[0][w][t][lane] = q1;
                     L.part[1][w][t][lane] = q2;
                 }
+#pragma unroll
+                for (int i = 0; i < NPT; ++i) asm volatile("" : "+v"(gA[i]));  // now: behind the loop it would keep all m
                 __builtin_amdgcn_sched_barrier(0);
-                if (j % 2 == 0 && j + 2 < kPairs) shares[j / 2 + 1] = take_sums();
+                if (j + 1 < kPairs) shares[j + 1] = take_sums(), join(j + 1, false);
             }
             wave_lds_fence();
             ask_sums();
             wave_lds_fence();
-            shares[0] = take_sums();
+            shares[0] = take_sums(), join(0, false);
         }
         const float totB = fold();
         __syncthreads();
-        if (live) {
+        {
+            float q1[TW], q2[TW];
 #pragma unroll
             for (int e = 0; e < TW; ++e) {
                 const int t = w * TW + e;
-                if (t0 + t >= T) continue;
-                float q1 = 0.f, q2 = 0.f;
+                q1[e] = L.part[0][0][t][lane], q2[e] = L.part[1][0][t][lane];
 #pragma unroll
-                for (int j = 0; j < W; ++j) q1 += L.part[0][j][t][lane], q2 += L.part[1][j][t][lane];
-                const unsigned at = (unsigned)(q * kSelTile + t) * C + c;
+                for (int j = 1; j < W; ++j) q1[e] += L.part[0][j][t][lane], q2[e] += L.part[1][j][t][lane];
                 if constexpr (WHOLE) {
                     const float d = L.du[t][lane][0], p = L.p[t][lane];
                     const bool there = t0 + t < len;
-                    const float gd = there ? fmaf(us[e], q2, q1 * kLn2) * sig[e] : 0.f;
-                    store_elem<E>((E*)g.gu + base, at * (unsigned)sizeof(E), there ? fmaf(Dc, p, d * q2) : 0.f);
-                    store_elem<E>((E*)g.gdt + base, at * (unsigned)sizeof(E), gd);
+                    q1[e] = where(there, fmaf(us[e], q2[e], q1[e] * kLn2) * sig[e]);
+                    q2[e] = where(there, fmaf(Dc, p, d * q2[e]));
                     sD = fmaf(p, us[e], sD);
-                    sb += gd;
-                } else {
-                    float* const o = S.q + (int64_t)nt * 3 * s.B * T * s.C + base;
-                    store_elem<float>(o, at * 4, q1 * kLn2);
-                    store_elem<float>(o + s.B * T * s.C, at * 4, q2);
+                    sb += q1[e];
+                }
+            }
+            if (live) {
+#pragma unroll
+                for (int e = 0; e < TW; ++e) {
+                    const unsigned at = (unsigned)(q * kSelTile + w * TW + e) * C + c;
+                    if (t0 + w * TW + e >= T) break;
+                    if constexpr (WHOLE) {
+                        store_elem<E>((E*)g.gu + base, at * (unsigned)sizeof(E), q2[e]);
+                        store_elem<E>((E*)g.gdt + base, at * (unsigned)sizeof(E), q1[e]);
+                    } else {
+                        float* const o = S.q + (int64_t)nt * 3 * s.B * T * s.C + base;
+                        store_elem<float>(o, at * 4, q1[e] * kLn2);
+                        store_elem<float>(o + s.B * T * s.C, at * 4, q2[e]);
+                    }
                 }
             }
         }
-        // A lane's sums over channels: of the four of tokens lane & 3, the token by bits 5 and 4 and the state
-        // by bits 3 and 2.
-        const int t = 4 * (lane & 3) + (lane >> 4), n = n0 + (lane >> 2 & 3);
+        // A lane's sums over channels: of a pair of tokens by bits 0 to 2, the token by bit 5 and the state
+        // by bits 4 and 3.
+        const int t = 8 * (lane & 1) + 2 * (lane & 2) + (lane >> 1 & 2) + (lane >> 5), n = n0 + (lane >> 3 & 3);
         if (t0 + t < T && n < Np) {
-            float* const o = S.gBC + ((((int64_t)cu * s.B + b) * T + t0 + t) * s.G + grp) * 2 * Np + n;
-            o[0] = t0 + t < len ? totB : 0.f;
-            o[Np] = t0 + t < len ? totC : 0.f;
+            float* const o = gbc0 + q * gbc_step;
+            const unsigned at = (unsigned)(t * s.G * 2 * Np + n) * 4;
+            store_elem<float>(o, at, t0 + t < len ? totB : 0.f);
+            store_elem<float>(o + Np, at, t0 + t < len ? totC : 0.f);
         }
     }
     if (live && states) store16<float>(S.gA + state_at(s, b * blocks + k, n0, c), gA);
