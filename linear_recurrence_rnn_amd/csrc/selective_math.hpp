@@ -41,9 +41,13 @@ template <class E>
 __device__ __forceinline__ E load_elem(const void* base, unsigned at) {
     return *reinterpret_cast<const E*>(reinterpret_cast<const char*>(base) + at);
 }
+template <class V>
+__device__ __forceinline__ void store_as(void* base, unsigned at, V x) {
+    *reinterpret_cast<V*>(reinterpret_cast<char*>(base) + at) = x;
+}
 template <class E>
 __device__ __forceinline__ void store_elem(void* base, unsigned at, float x) {
-    *reinterpret_cast<E*>(reinterpret_cast<char*>(base) + at) = (E)x;
+    store_as<E>(base, at, (E)x);
 }
 template <class E>
 __device__ __forceinline__ const void* elems(const void* p, int64_t first) {
@@ -82,6 +86,12 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// v, or zero: formed in any case, as a branch around it would part it from its neighbours.
+__device__ __forceinline__ float where(bool there, float v) {
+    asm volatile("" : "+v"(v));
+    return there ? v : 0.f;
 }
 
 // Tokens of row b that are there.

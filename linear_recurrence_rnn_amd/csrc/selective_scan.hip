@@ -96,32 +96,39 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
     const bool gated = A.z != nullptr, soft = s.softplus != 0;
     const void* const zp = gated ? A.z : A.u;
     E ur[TW], dr[TW], zr[TW];
-    const auto fetch = [&](int t0) {
-        const int64_t base = (b * T + t0) * s.C;
+    const unsigned C = (unsigned)s.C;
+    const auto fetch = [&](int t0, int64_t at0) {  // at0: the tile's first element
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
             const int k = t0 + w * TW + i < T ? w * TW + i : T - 1 - t0;
-            const unsigned at = ((unsigned)k * (unsigned)s.C + c) * (unsigned)sizeof(E);
-            ur[i] = load_elem<E>(elems<E>(A.u, base), at);
-            dr[i] = load_elem<E>(elems<E>(A.dt, base), at);
-            if (!AGG) zr[i] = load_elem<E>(elems<E>(zp, base), at);
+            const unsigned at = ((unsigned)k * C + c) * (unsigned)sizeof(E);
+            ur[i] = load_elem<E>(elems<E>(A.u, at0), at);
+            dr[i] = load_elem<E>(elems<E>(A.dt, at0), at);
+            if (!AGG) zr[i] = load_elem<E>(elems<E>(zp, at0), at);
         }
     };
-    fetch(t_begin);
+    // Where this tile's elements, B and C, and kept states are.
+    int64_t base = (b * T + t_begin) * s.C;
+    const int64_t first = b * tiles + t_begin / kSelTile;
+    const float* row = bc + ((first * s.G + grp) * W + w) * (kSelTile * 2 * NPT);
+    float* kept = keep + (first * Np + n0 / 4 * 4) * s.C + (n0 & 3);
+    fetch(t_begin, base);
     for (int t0 = t_begin; t0 < t_end; t0 += kSelTile) {
         if constexpr (!AGG) {
             if (keep && live) {
-                const int64_t at = state_at(s, b * tiles + t0 / kSelTile, n0, c);
                 if constexpr (NPT % 4 == 0) {
 #pragma unroll
-                    for (int i = 0; i < NPT; i += 4)
-                        if (n0 + i < Np) store16<float>(keep + at + i * s.C, h + i);
+                    for (int i = 0; i < NPT; i += 4) {
+                        const f32x4 v = {h[i], h[i + 1], h[i + 2], h[i + 3]};
+                        if (n0 + i < Np) store_as<f32x4>(kept + i * s.C, c * 16, v);
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < NPT; ++i)
-                        if (n0 + i < Np) keep[at + i] = h[i];
+                        if (n0 + i < Np) store_as<float>(kept + i, c * 16, h[i]);
                 }
             }
+            kept += Np * s.C;
         }
         // Whether a token is there is the same for the whole wave; d and d u of an absent one, or of a
         // lane without a channel, are zero, which leaves the states alone.
@@ -144,10 +151,10 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
                 din[w * TW + i][lane] = v;
             }
         }
-        fetch(t0 + kSelTile < t_end ? t0 + kSelTile : t0);
+        const bool more = t0 + kSelTile < t_end;
+        fetch(more ? t0 + kSelTile : t0, more ? base + kSelTile * s.C : base);
         __syncthreads();
         if (t0 < len) {
-            const float* row = bc + (((b * tiles + t0 / kSelTile) * s.G + grp) * W + w) * (kSelTile * 2 * NPT);
             float subtotal = 0.f;
             SelGroup<NPT> grp_of[2];
             grp_of[0].fetch(row, din, lane, 0);
@@ -174,24 +181,28 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
         }
         __syncthreads();
         if constexpr (!AGG) {
-            if (A.y && live) {
-                void* const out = (void*)elems<E>(A.y, (b * T + t0) * s.C);
+            if (A.y) {
+                float y[TW];
 #pragma unroll
                 for (int i = 0; i < TW; ++i) {
-                    const int t = t0 + w * TW + i;
-                    if (t >= t_end) continue;
-                    float y = 0.f;
-                    if (t < len) {
-                        y = Dc * u[i];
+                    y[i] = Dc * u[i];
 #pragma unroll
-                        for (int k = 0; k < W; ++k) y += part[k][w * TW + i][lane];
-                        const float gate = z[i] * logistic(z[i]);
-                        y *= gated ? gate : 1.f;
+                    for (int k = 0; k < W; ++k) y[i] += part[k][w * TW + i][lane];
+                    const float gate = z[i] * logistic(z[i]);
+                    y[i] = where(t0 + w * TW + i < len, y[i] * (gated ? gate : 1.f));
+                }
+                if (live) {
+                    void* const out = (void*)elems<E>(A.y, base);
+#pragma unroll
+                    for (int i = 0; i < TW; ++i) {
+                        if (t0 + w * TW + i >= t_end) break;
+                        store_elem<E>(out, ((unsigned)(w * TW + i) * C + c) * (unsigned)sizeof(E), y[i]);
                     }
-                    store_elem<E>(out, ((unsigned)(w * TW + i) * (unsigned)s.C + c) * (unsigned)sizeof(E), y);
                 }
             }
         }
+        base += kSelTile * s.C;
+        row += s.G * W * (kSelTile * 2 * NPT);
     }
     if (!live) return;
     if constexpr (AGG) {

@@ -53,7 +53,7 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
     const int grp = tile / group_tiles, Cg = (int)(s.C / s.G);
     const int in_group = (tile % group_tiles) * 64 + lane;
     const bool live = in_group < Cg;
-    const unsigned c = (unsigned)(grp * Cg + (live ? in_group : Cg - 1));
+    const unsigned C = (unsigned)s.C, c = (unsigned)(grp * Cg + (live ? in_group : Cg - 1));
     const int T = (int)s.T, tiles = (T + kSelTile - 1) / kSelTile;
     const int t_begin = k * kSelBlock, len = (int)row_length(s, b);
     const int n0 = (nt * W + w) * NPT;
@@ -70,12 +70,11 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
     // This wave's tokens of a tile, read while the tile behind it is worked on.  Absent ones are read as
     // the last that is there and not used.
     E dr[TW], zr[TW], gr[TW];
-    const auto fetch = [&](int t0) {
-        const int64_t base = (b * T + t0) * s.C;
+    const auto fetch = [&](int t0, int64_t base) {  // base: the tile's first element
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
             const int j = t0 + w * TW + i < len ? w * TW + i : len - 1 - t0;
-            const unsigned at = ((unsigned)j * (unsigned)s.C + c) * (unsigned)sizeof(E);
+            const unsigned at = ((unsigned)j * C + c) * (unsigned)sizeof(E);
             dr[i] = load_elem<E>(elems<E>(A.dt, base), at);
             gr[i] = load_elem<E>(elems<E>(gy, base), at);
             zr[i] = load_elem<E>(elems<E>(zp, base), at);
@@ -84,7 +83,12 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
     // Tiles of absent tokens alone change nothing.
     const int end = t_begin + kSelBlock < len ? t_begin + kSelBlock : len;
     int t0 = end > t_begin ? (end - 1) / kSelTile * kSelTile : t_begin - kSelTile;
-    if (t0 >= t_begin) fetch(t0);
+    int64_t base = (b * T + t0) * s.C;
+    const int step = s.G * ntiles * W * (kSelTile * 2 * NPT);  // of B and C, from tile to tile
+    const float* row =
+        bc + ((((b * tiles + t_begin / kSelTile) * s.G + grp) * ntiles + nt) * W + w) * (kSelTile * 2 * NPT) +
+        (int64_t)((t0 - t_begin) / kSelTile) * step;
+    if (t0 >= t_begin) fetch(t0, base);
     for (; t0 >= t_begin; t0 -= kSelTile) {
         float d[TW], p[TW];
 #pragma unroll
@@ -104,9 +108,9 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
             const f32x2 v = {there ? d[i] : 0.f, there ? p[i] : 0.f};
             din[w * TW + i][lane] = v;
         }
-        fetch(t0 > t_begin ? t0 - kSelTile : t0);
+        if (t0 > t_begin) base -= kSelTile * s.C;
+        fetch(t0 > t_begin ? t0 - kSelTile : t0, base);
         __syncthreads();
-        const float* row = bc + ((((b * tiles + t0 / kSelTile) * s.G + grp) * ntiles + nt) * W + w) * (kSelTile * 2 * NPT);
         constexpr int kGroups = SelGroup<NPT>::kGroups, kTok = SelGroup<NPT>::kTok;
         float subtotal = 0.f;
         SelGroup<NPT> grp_of[2];
@@ -126,6 +130,7 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
             __builtin_amdgcn_sched_barrier(0);
         }
         total += subtotal;
+        row -= step;
         __syncthreads();
     }
     if (!live) return;
@@ -158,12 +163,6 @@ struct GradLds {
     float part[2][W][kSelTile][64];  // the waves' shares of sums over the states
     float rows[W][8][kRowPad];       // 8 values of a wave on their way to being summed over its lanes
 };
-
-// v, or zero: formed in any case, as a branch around it would part it from its neighbours.
-__device__ __forceinline__ float where(bool there, float v) {
-    asm volatile("" : "+v"(v));
-    return there ? v : 0.f;
-}
 
 // WHOLE: one workgroup has all states of its channels, so that its sums over them are complete.
 template <class E, int W, bool WHOLE>
