@@ -218,6 +218,8 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
 }
 
 // One element of every state and row: the blocks' shares become the states that enter them.
+constexpr int kAhead = 8;
+
 template <bool REV>
 __global__ __launch_bounds__(256) void sel_join_kernel(SelShape s, const float* __restrict__ A, float* __restrict__ v,
                                                        const float* __restrict__ sum, int64_t blocks,
@@ -231,16 +233,35 @@ __global__ __launch_bounds__(256) void sel_join_kernel(SelShape s, const float* 
     const int64_t at = (b * s.C + c) * s.N + n;
     const float a2 = n < s.N ? A[c * s.N + n] * kLog2e : 0.f;
     float x = in && n < s.N ? in[at] : 0.f;
-    for (int64_t i = 0; i < blocks; ++i) {
-        const int64_t k = b * blocks + (REV ? blocks - 1 - i : i);
-        if (!REV && i == blocks - 1) {  // what leaves the last one is not asked for, and was not formed
-            v[k * per + e] = x;
-            break;
+    // What leaves the last block forwards is not asked for, and its share was not formed.
+    const int64_t known = REV ? blocks : blocks - 1;
+    const auto place = [&](int64_t i) { return b * blocks + (REV ? blocks - 1 - i : i); };
+    // Loads of kAhead blocks at once, and ahead of the stores of those before: not one by one, where they are used.
+    float own[2][kAhead], d[2][kAhead];
+    const auto load = [&](int64_t i, float (&o)[kAhead], float (&f)[kAhead]) {
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) {
+            const int64_t k = place(i + r < known ? i + r : known - 1);
+            o[r] = v[k * per + e], f[r] = sum[k * s.C + c];
         }
-        const float own = v[k * per + e];
-        v[k * per + e] = x;
-        x = fmaf(fast_exp2(a2 * sum[k * s.C + c]), x, own);
+    };
+    if (known > 0) load(0, own[0], d[0]);
+    const auto group = [&](int64_t i, float (&o)[kAhead], float (&f)[kAhead], float (&o1)[kAhead], float (&f1)[kAhead]) {
+        load(i + kAhead, o1, f1);
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) asm volatile("" : "+v"(o[r]), "+v"(f[r]));
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) {
+            if (i + r >= known) break;
+            v[place(i + r) * per + e] = x;
+            x = fmaf(fast_exp2(a2 * f[r]), x, o[r]);
+        }
+    };
+    for (int64_t i = 0; i < known; i += 2 * kAhead) {
+        group(i, own[0], d[0], own[1], d[1]);
+        if (i + kAhead < known) group(i + kAhead, own[1], d[1], own[0], d[0]);
     }
+    if (!REV) v[place(blocks - 1) * per + e] = x;
     if (out && n < s.N) out[at] = x;
 }
 
@@ -424,17 +445,21 @@ SelPlan sel_plan(const SelShape& s) {
     p.tiles_n = 1;
     p.npt = s.N <= 1 ? 1 : s.N <= 2 ? 2 : s.N <= 16 ? 4 : s.N <= 64 ? 8 : 16;
     p.waves = s.N <= 4 ? 1 : s.N <= 8 ? 2 : s.N <= 32 ? 4 : 8;
-    // Segments until the chip has six waves a SIMD, of four tiles at least: 32768 tokens of 2048 channels
-    // take 573 us, 587 with four waves a SIMD and 693 with two; 8 x 4096 tokens of 2560 635, 684 and 791.
+    // Segments until the chip has six waves a SIMD: 32768 tokens of 2048 channels took 573 us, 587 with four waves a
+    // SIMD and 693 with two; 8 x 4096 tokens of 2560 635, 684 and 791.  Of two tiles at least, of four in rows of more
+    // than 128 tiles, where the states that enter the segments would cost more: 512 tokens of 1536 channels take 26.0 us
+    // with two, 28.7 with four, 4096 of 256 with kept fours 32.1, 36.5 with twos.  Fewer than four segments form too
+    // much twice: 12 x 1024 tokens of 2560 take 182 us whole, 227 with three; 8 x 1024 180 whole, 158 with four.
     const int64_t wg = s.B * s.G * ceil_div(s.C / s.G, 64), tiles = sel_tiles(s);
     int64_t segs = 6144 / (wg * p.waves);
-    if (segs > tiles / 4) segs = tiles / 4;
-    if (segs < 2) segs = 1;
+    const int64_t most = tiles <= 128 ? tiles / 2 : tiles / 4;
+    if (segs > most) segs = most;
+    if (segs < 4) segs = 1;
     p.seg_tiles = ceil_div(tiles, segs);
     p.segs = ceil_div(tiles, p.seg_tiles);
-    // Rows too short for that and too few for a wave a SIMD: half the states a wave, which is as long as
-    // one tile takes then.  77 tokens of 1536 channels 12.1 us for 15.2; 8 x 1024 tokens 66.8 for 62.4.
-    if (segs == 1 && p.npt == 4 && p.waves == 4 && wg * 8 <= 1024) p.npt = 2, p.waves = 8;
+    // Whole rows too few for four waves a SIMD: half the states a wave.  77 tokens of 1536 channels take 12.1 us for
+    // 15.2, 12 x 1024 of 2560 173 for 182, but 24 x 1024 302 for 291.
+    if (p.segs == 1 && p.npt == 4 && p.waves == 4 && wg * 8 <= 4096) p.npt = 2, p.waves = 8;
     return p;
 }
 
