@@ -41,6 +41,8 @@ class LinrecError(RuntimeError):
 def load(path: str | None = None):
     """Load the library once (raises if it has not been built)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -770,6 +772,11 @@ def _need(t, name, dtype, shape, device):
         _expect(t, name, dtype, shape, device)
 
 
+def _dense(t, name):
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -1020,7 +1027,7 @@ _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_d
 def _on_device(call):
     @functools.wraps(call)
     def checked(x, *args, **kw):
-        if isinstance(x, torch.Tensor) and x.is_cuda and x.device.index != _get_device():
+        if isinstance(x, torch.Tensor) and x.get_device() not in (-1, _get_device()):  # -1: no GPU's, refused below
             with torch.cuda.device(x.device):
                 return call(x, *args, **kw)
         return call(x, *args, **kw)
@@ -1038,7 +1045,7 @@ def _selective_shape(u, dt, A, B, C, D, z, dt_bias, lead):
         raise ValueError("B and C must have %d axes" % (lead + 2))
     shape, ty, dev = u.shape, u.dtype, u.device
     ch, (G, N) = shape[lead], B.shape[lead:]
-    _need(u, "u", ty, shape, dev)
+    _dense(u, "u")
     _need(dt, "dt", ty, shape, dev)
     _need(A, "A", torch.float32, (ch, N), dev)
     _need(B, "B", ty, shape[:lead] + (G, N), dev)
@@ -1191,7 +1198,7 @@ def _conv_shape(x, weight, bias, act, lead):
     if x.dim() != lead + 1 or not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("x must have %d axes and weight two" % (lead + 1))
     C, K, dev = x.shape[lead], weight.shape[1], x.device
-    _need(x, "x", x.dtype, x.shape, dev)
+    _dense(x, "x")
     _need(weight, "weight", torch.float32, (C, K), dev)
     if bias is not None:
         _need(bias, "bias", torch.float32, (C,), dev)
@@ -1296,7 +1303,7 @@ def _rms_shape(x, weight, other, name):
     if x.dim() < 1:
         raise ValueError("x must have a channel axis")
     shape, C, dev = x.shape, x.shape[-1], x.device
-    _need(x, "x" if name == "residual" else "gy", x.dtype, shape, dev)
+    _dense(x, "x" if name == "residual" else "gy")
     _need(weight, "weight", torch.float32, (C,), dev)
     rcode = code
     if other is not None:
