@@ -462,7 +462,10 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
 }
 
 // More than 16 states: the tiles' sums over states added, and the gradients of each token and
-// channel.  A workgroup takes one block's tokens of 64 channels, 4 tokens a wave.
+// channel.  A workgroup takes blocks' tokens of 64 channels, 4 tokens a wave; 32 of those a CU keep the chip
+// busy, and 2^22 would be more threads than one launch may have.
+constexpr int kFinishGroups = 8192;
+
 template <class E>
 __global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A, SelBwdArgs g, SelBwdScratch S,
                                                           int64_t blocks, int ntiles) {
@@ -470,57 +473,59 @@ __global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A,
     __shared__ float acc[2][kWaves][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t cols = (s.C + 63) / 64;
-    const int64_t c = (int64_t)(blockIdx.x % cols) * 64 + lane;
-    const int64_t row = blockIdx.x / cols, k = row % blocks, b = row / blocks;
-    const bool live = c < s.C;
-    const int64_t len = row_length(s, b), plane = s.B * s.T * s.C, t0 = k * kSelBlock + w * kTok;
-    float sD = 0.f, sb = 0.f;
-    if (live) {
-        const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
-        float q[kTok][3];
+    for (int64_t blk = blockIdx.x; blk < s.B * blocks * cols; blk += gridDim.x) {
+        const int64_t c = blk % cols * 64 + lane, row = blk / cols, k = row % blocks, b = row / blocks;
+        const bool live = c < s.C;
+        const int64_t len = row_length(s, b), plane = s.B * s.T * s.C, t0 = k * kSelBlock + w * kTok;
+        float sD = 0.f, sb = 0.f;
+        if (live) {
+            const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
+            float q[kTok][3];
 #pragma unroll
-        for (int e = 0; e < kTok; ++e) {
-            q[e][0] = q[e][1] = q[e][2] = 0.f;
-            const int64_t t = t0 + e < s.T ? t0 + e : s.T - 1;
-            for (int i = 0; i < ntiles; ++i) {
-                const float* o = S.q + (int64_t)i * 3 * plane + (b * s.T + t) * s.C + c;
+            for (int e = 0; e < kTok; ++e) {
+                q[e][0] = q[e][1] = q[e][2] = 0.f;
+                const int64_t t = t0 + e < s.T ? t0 + e : s.T - 1;
+                for (int i = 0; i < ntiles; ++i) {
+                    const float* o = S.q + (int64_t)i * 3 * plane + (b * s.T + t) * s.C + c;
 #pragma unroll
-                for (int j = 0; j < 3; ++j) q[e][j] += o[j * plane];
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < kTok; ++e) {
-            const int64_t t = t0 + e, at = (b * s.T + t) * s.C + c;
-            if (t >= s.T) continue;
-            float gu = 0.f, gd = 0.f, gz = 0.f;
-            if (t < len) {
-                const float u = (float)reinterpret_cast<const E*>(A.u)[at];
-                float d = (float)reinterpret_cast<const E*>(A.dt)[at] + bias, sig = 1.f;
-                float p = (float)reinterpret_cast<const E*>(g.gy)[at];
-                if (s.softplus) d = softplus(d, sig);
-                if (A.z) {
-                    const float z = (float)reinterpret_cast<const E*>(A.z)[at];
-                    const float sg = logistic(z);
-                    gz = p * sg * fmaf(z, 1.f - sg, 1.f) * fmaf(Dc, u, q[e][2]);
-                    p *= z * sg;
+                    for (int j = 0; j < 3; ++j) q[e][j] += o[j * plane];
                 }
-                gd = fmaf(u, q[e][1], q[e][0]) * sig;
-                gu = fmaf(Dc, p, d * q[e][1]);
-                sD = fmaf(p, u, sD);
-                sb += gd;
             }
-            reinterpret_cast<E*>(g.gu)[at] = (E)gu;
-            reinterpret_cast<E*>(g.gdt)[at] = (E)gd;
-            if (A.z) reinterpret_cast<E*>(g.gz)[at] = (E)gz;
-        }
-    }
-    acc[0][w][lane] = sD, acc[1][w][lane] = sb;
-    __syncthreads();
-    if (w < 2 && live) {
-        float v = acc[w][0][lane];
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) v += acc[w][i][lane];
-        S.gDb[(row * 2 + w) * s.C + c] = v;
+            for (int e = 0; e < kTok; ++e) {
+                const int64_t t = t0 + e, at = (b * s.T + t) * s.C + c;
+                if (t >= s.T) continue;
+                float gu = 0.f, gd = 0.f, gz = 0.f;
+                if (t < len) {
+                    const float u = (float)reinterpret_cast<const E*>(A.u)[at];
+                    float d = (float)reinterpret_cast<const E*>(A.dt)[at] + bias, sig = 1.f;
+                    float p = (float)reinterpret_cast<const E*>(g.gy)[at];
+                    if (s.softplus) d = softplus(d, sig);
+                    if (A.z) {
+                        const float z = (float)reinterpret_cast<const E*>(A.z)[at];
+                        const float sg = logistic(z);
+                        gz = p * sg * fmaf(z, 1.f - sg, 1.f) * fmaf(Dc, u, q[e][2]);
+                        p *= z * sg;
+                    }
+                    gd = fmaf(u, q[e][1], q[e][0]) * sig;
+                    gu = fmaf(Dc, p, d * q[e][1]);
+                    sD = fmaf(p, u, sD);
+                    sb += gd;
+                }
+                reinterpret_cast<E*>(g.gu)[at] = (E)gu;
+                reinterpret_cast<E*>(g.gdt)[at] = (E)gd;
+                if (A.z) reinterpret_cast<E*>(g.gz)[at] = (E)gz;
+            }
+        }
+        acc[0][w][lane] = sD, acc[1][w][lane] = sb;
+        __syncthreads();
+        if (w < 2 && live) {
+            float v = acc[w][0][lane];
+#pragma unroll
+            for (int i = 1; i < kWaves; ++i) v += acc[w][i][lane];
+            S.gDb[(row * 2 + w) * s.C + c] = v;
+        }
+        __syncthreads();  // acc has been read
     }
 }
 
@@ -598,8 +603,9 @@ hipError_t by_waves(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, co
     hipLaunchKernelGGL((sel_gradient_kernel<E, 4, false>), grid, dim3(256), 0, st, s, A, g, bc, keep, S, (int)blocks, ntiles);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(s.B * blocks * ceil_div(s.C, 64))), dim3(1024), 0, st, s,
-                       A, g, S, blocks, ntiles);
+    const int64_t all = s.B * blocks * ceil_div(s.C, 64);
+    hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(all < kFinishGroups ? all : kFinishGroups)), dim3(1024), 0,
+                       st, s, A, g, S, blocks, ntiles);
     return hipGetLastError();
 }
 
