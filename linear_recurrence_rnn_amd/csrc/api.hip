@@ -1207,10 +1207,10 @@ linrec::SelShape sel_shape(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N
     return {B, T, C, (int)G, (int)N, dtype, softplus, lengths};
 }
 
-// The backward's workgroups: one a block of 64 tokens and channels and up to 16 states, 256 lanes.
+// The backward's workgroups: one a block of 64 tokens or more, 64 channels and up to 16 states, 256 lanes.
 int check_sel_backward(const linrec::SelShape& s) {
-    const int64_t blocks = s.B * linrec::sel_blocks(s);
-    if (blocks >= (1 << 23) || blocks * s.G * ceil_div(s.C / s.G, 64) * ceil_div(s.N, 16) >= (1 << 24))
+    const int64_t blocks = s.B * ceil_div(s.T, linrec::kSelBlock);
+    if (blocks >= (1 << 23) || linrec::sel_block_groups(s, linrec::kSelBlock) >= (1 << 24))
         return fail(LINREC_ERR_UNSUPPORTED, "B*T*C/4096 (times N/16) is above 2^24 in a backward");
     return LINREC_OK;
 }
@@ -1252,7 +1252,7 @@ size_t sel_backward_layout(const linrec::SelShape& s, void* ws, linrec::SelBwdSc
     linrec::SelBwdScratch w{};
     w.carry = w.gA = take((size_t)(rows * s.C) * linrec::sel_n4(s) * 4);
     w.sum = take((size_t)(rows * s.C));
-    w.gDb = take((size_t)(rows * 2 * s.C));
+    w.gDb = take((size_t)(linrec::sel_share_rows(s) * 2 * s.C));
     w.cuts = ceil_div(s.C / s.G, 64);
     w.gBC = take((size_t)(w.cuts * s.B * s.T * s.G) * 2 * linrec::sel_n4(s) * 4);
     w.q = take(s.N > 16 ? (size_t)ceil_div(s.N, 16) * (size_t)(s.B * s.T * s.C) * 3 : 0);

@@ -14,7 +14,7 @@ namespace linrec {
 
 constexpr int kSelMaxN = 128;  // states of a channel: 16 a lane, 8 waves
 constexpr int kSelTile = 16;   // tokens between two kept states, and staged at once
-constexpr int kSelBlock = 64;  // tokens of a workgroup of the backward
+constexpr int kSelBlock = 64;  // tokens of a workgroup of the backward, or 2 or 4 times as many
 
 struct SelShape {
     int64_t B, T, C;
@@ -46,7 +46,23 @@ struct SelBwdArgs {
 // States between kernels are laid out (rows, N/4 rounded up, C, 4).
 inline int sel_n4(const SelShape& s) { return (s.N + 3) / 4; }
 inline int64_t sel_tiles(const SelShape& s) { return (s.T + kSelTile - 1) / kSelTile; }
-inline int64_t sel_blocks(const SelShape& s) { return (s.T + kSelBlock - 1) / kSelBlock; }
+
+// Tokens of the backward's workgroups.  Longer ones write fewer partial sums and states: a training step of 8 x 4096
+// tokens of 2560 channels takes 1922 us with 64, 1867 with 128 and 1852 with 256.  They are for many of them, six times
+// the 768 that the chip holds, so that the last ones, and ragged rows, do not leave it idle; and for offsets of 32 bits.
+inline int64_t sel_block_groups(const SelShape& s, int64_t tokens) {  // workgroups
+    return s.B * ((s.T + tokens - 1) / tokens) * s.G * ((s.C / s.G + 63) / 64) * ((s.N + 15) / 16);
+}
+inline int sel_block(const SelShape& s) {
+    int tokens = kSelBlock;
+    while (tokens < 4 * kSelBlock && sel_block_groups(s, 2 * tokens) >= 4608 && s.C * sel_n4(s) < (1 << 22)) tokens *= 2;
+    return tokens;
+}
+inline int64_t sel_blocks(const SelShape& s) { return (s.T + sel_block(s) - 1) / sel_block(s); }
+// Rows of the shares of D's gradient and the bias's: with more than 16 states another kernel forms them.
+inline int64_t sel_share_rows(const SelShape& s) {
+    return s.B * (s.N > 16 ? (s.T + kSelBlock - 1) / kSelBlock : sel_blocks(s));
+}
 
 // How the forward is split: states of a lane, waves of a workgroup, segments of the rows.
 struct SelPlan {
@@ -69,7 +85,7 @@ struct SelBwdScratch {
     float* carry;  // (B,blocks) rows of states: the gradient that enters each block from its right
     float* sum;    // (B,blocks,C) sums of d
     float* gA;     // (B*blocks) rows of states
-    float* gDb;    // (B*blocks,2,C): D's gradient, bias's
+    float* gDb;    // (share rows,2,C): D's gradient, bias's
     float* gBC;    // (cuts,B,T,G,2,4*n4): B's and C's gradients by ranges of 64 channels of a group
     float* q;      // (tiles of 16 states,3,B,T,C) where N > 16: sums over the states of one
     int64_t cuts;

@@ -9,7 +9,7 @@
 //   gu_t = D p_t + d_t sum_n g_t[n] B_t[n],   gD = sum_t p_t u_t
 //   gdt_t = gd_t softplus'(dt_t + bias),  gbias = sum_t gdt_t,  gz_t = gy_t core_t silu'(z_t)
 //
-// The rows are cut into blocks of 64 tokens.  First each block's share of the G that leaves it on
+// The rows are cut into blocks of 64 to 256 tokens.  First each block's share of the G that leaves it on
 // the left, from zero on its right (all blocks at once, as the forward's segments); then the G that
 // enters each block, one block after the other (the decay over a block is e^{A sum d}); then all gradients,
 // all blocks at once, the states formed again from those the forward kept every 16 tokens.
@@ -38,7 +38,7 @@ constexpr int kBwdNpt = 4;  // states of a lane in the kernels below; a workgrou
 template <class E, int W>
 __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs A, const E* __restrict__ gy,
                                                              const float* __restrict__ bc, float* __restrict__ out,
-                                                             float* __restrict__ sum, int blocks, int group_tiles,
+                                                             float* __restrict__ sum, int blocks, int block, int group_tiles,
                                                              int ntiles) {
     constexpr int TW = kSelTile / W, NPT = kBwdNpt;
     __shared__ f32x2 din[kSelTile][64];  // d, p
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
     const bool live = in_group < Cg;
     const unsigned C = (unsigned)s.C, c = (unsigned)(grp * Cg + (live ? in_group : Cg - 1));
     const int T = (int)s.T, tiles = (T + kSelTile - 1) / kSelTile;
-    const int t_begin = k * kSelBlock, len = (int)row_length(s, b);
+    const int t_begin = k * block, len = (int)row_length(s, b);
     const int n0 = (nt * W + w) * NPT;
     float g[NPT], a2[NPT];
 #pragma unroll
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
         }
     };
     // Tiles of absent tokens alone change nothing.
-    const int end = t_begin + kSelBlock < len ? t_begin + kSelBlock : len;
+    const int end = t_begin + block < len ? t_begin + block : len;
     int t0 = end > t_begin ? (end - 1) / kSelTile * kSelTile : t_begin - kSelTile;
     int64_t base = (b * T + t0) * s.C;
     const int step = s.G * ntiles * W * (kSelTile * 2 * NPT);  // of B and C, from tile to tile
@@ -169,7 +169,7 @@ template <class E, int W, bool WHOLE>
 __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
                                                                               const float* __restrict__ bc,
                                                                               const float* __restrict__ keep,
-                                                                              SelBwdScratch S, int blocks, int ntiles) {
+                                                                              SelBwdScratch S, int blocks, int block, int ntiles) {
     constexpr int NPT = kBwdNpt, TW = kSelTile / W, kPairs = kSelTile / 2;
     __shared__ GradLds<W> L;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
     const int k = (int)(blk % (unsigned)blocks);
     const int64_t b = blk / (unsigned)blocks;
     const int T = (int)s.T, tiles = (T + kSelTile - 1) / kSelTile, len = (int)row_length(s, b);
-    const int t_begin = k * kSelBlock, t_end = t_begin + kSelBlock < T ? t_begin + kSelBlock : T;
+    const int t_begin = k * block, t_end = t_begin + block < T ? t_begin + block : T;
     const int n0 = (nt * W + w) * NPT, Np = (s.N + 3) / 4 * 4;
     const unsigned C = (unsigned)s.C;
     const bool gated = A.z != nullptr, soft = s.softplus != 0, states = n0 < s.N;
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
     // What a lane reads of a tile: its wave's tokens' inputs and its states before the tile, asked for a
     // tile ahead.  Absent tokens are read as the last one that is there, lanes behind the last channel
     // as that, inputs that were not given as others: none of that is used.  Bases of the block, and a
-    // lane's byte offsets in it (below 2^32: 64 tokens of at most 2^22 channels).
+    // lane's byte offsets in it (below 2^32: 64 tokens of at most 2^22 channels, more of fewer).
     const int64_t base = (b * T + t_begin) * s.C;
     const void *const pu = elems<E>(A.u, base), *const pdt = elems<E>(A.dt, base), *const pgy = elems<E>(g.gy, base);
     const void* const pz = elems<E>(gated ? A.z : A.u, base);
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
     const int bc_step = s.G * ntiles * W * (kSelTile * 2 * NPT), gbc_step = kSelTile * s.G * 2 * Np;
     for (int q = q_first; q >= 0; --q) {
         const int t0 = t_begin + q * kSelTile;
-        const float* row = bc0 + q * bc_step;
+        const float* row = bc0 + (int64_t)q * bc_step;
         // (Whether a token is there is the same for the whole wave.  Of an absent one, or a lane without a
         // channel, d, u and p are zero, which leaves the states and the sums over channels alone.)
         float sig[TW], gzf[TW], us[TW], h0[NPT];
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
         // by bits 4 and 3.
         const int t = 8 * (lane & 1) + 2 * (lane & 2) + (lane >> 1 & 2) + (lane >> 5), n = n0 + (lane >> 3 & 3);
         if (t0 + t < T && n < Np) {
-            float* const o = gbc0 + q * gbc_step;
+            float* const o = gbc0 + (int64_t)q * gbc_step;
             const unsigned at = (unsigned)(t * s.G * 2 * Np + n) * 4;
             store_elem<float>(o, at, t0 + t < len ? totB : 0.f);
             store_elem<float>(o + Np, at, t0 + t < len ? totC : 0.f);
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
 }
 
 // More than 16 states: the tiles' sums over states added, and the gradients of each token and
-// channel.  A workgroup takes blocks' tokens of 64 channels, 4 tokens a wave; 32 of those a CU keep the chip
+// channel.  A workgroup takes 64 tokens of 64 channels at a time, 4 tokens a wave; 32 of those a CU keep the chip
 // busy, and 2^22 would be more threads than one launch may have.
 constexpr int kFinishGroups = 8192;
 
@@ -534,7 +534,7 @@ __global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A,
 // strips in order; one launch does all three, in as many workgroups each as `wg` says.
 struct SelFold {
     unsigned wg[3];
-    int64_t rows;
+    int64_t rows, share_rows;
 };
 
 // The sum of column j, in the lanes of strip 0.
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(256) void sel_fold_kernel(SelShape s, SelBwdArgs g,
     blk -= f.wg[0];
     if (blk < f.wg[1]) {
         const int64_t cols = 2 * s.C, j = (int64_t)blk * 16 + (threadIdx.x & 15);
-        const float v = fold_column(S.gDb, f.rows, cols, j, lds);
+        const float v = fold_column(S.gDb, f.share_rows, cols, j, lds);
         float* const out = j < s.C ? g.gD : g.gbias;
         if (threadIdx.x < 16 && j < cols && out) out[j < s.C ? j : j - s.C] = v;
         return;
@@ -588,24 +588,26 @@ template <class E, int W>
 hipError_t by_waves(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, const float* bc, const float* keep,
                     const SelBwdScratch& S, hipStream_t st) {
     const int64_t blocks = sel_blocks(s);
+    const int block = sel_block(s);
     const int ntiles = (int)ceil_div(s.N, kBwdNpt * W), group_tiles = (int)ceil_div(s.C / s.G, 64);
     hipLaunchKernelGGL((sel_reverse_kernel<E, W>), dim3((unsigned)(s.B * blocks * ntiles * s.G * group_tiles)),
-                       dim3(64 * W), 0, st, s, A, (const E*)g.gy, bc, S.carry, S.sum, (int)blocks, group_tiles, ntiles);
+                       dim3(64 * W), 0, st, s, A, (const E*)g.gy, bc, S.carry, S.sum, (int)blocks, block, group_tiles, ntiles);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess) e = run_sel_join(s, A.A, S.carry, S.sum, blocks, g.gs_out, g.gs_in, true, st);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)(s.B * blocks * ntiles * s.G * S.cuts));
     if (W < 4 || ntiles == 1) {
         hipLaunchKernelGGL((sel_gradient_kernel<E, W, true>), grid, dim3(64 * W), 0, st, s, A, g, bc, keep, S, (int)blocks,
-                           ntiles);
+                           block, ntiles);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((sel_gradient_kernel<E, 4, false>), grid, dim3(256), 0, st, s, A, g, bc, keep, S, (int)blocks, ntiles);
+    hipLaunchKernelGGL((sel_gradient_kernel<E, 4, false>), grid, dim3(256), 0, st, s, A, g, bc, keep, S, (int)blocks, block,
+                       ntiles);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t all = s.B * blocks * ceil_div(s.C, 64);
+    const int64_t shares = sel_share_rows(s) / s.B, all = s.B * shares * ceil_div(s.C, 64);
     hipLaunchKernelGGL((sel_finish_kernel<E>), dim3((unsigned)(all < kFinishGroups ? all : kFinishGroups)), dim3(1024), 0,
-                       st, s, A, g, S, blocks, ntiles);
+                       st, s, A, g, S, shares, ntiles);
     return hipGetLastError();
 }
 
@@ -619,6 +621,7 @@ hipError_t backward(const SelShape& s, const SelArgs& A, const SelBwdArgs& g, co
     if (e != hipSuccess) return e;
     SelFold f{};
     f.rows = s.B * sel_blocks(s);
+    f.share_rows = sel_share_rows(s);
     f.wg[0] = (unsigned)ceil_div((int64_t)sel_n4(s) * 4 * s.C, 16);
     f.wg[1] = g.gD || g.gbias ? (unsigned)ceil_div(2 * s.C, 16) : 0;
     const int64_t wg = ceil_div(s.B * s.T * s.G * 2 * sel_n4(s) * 4, 256);

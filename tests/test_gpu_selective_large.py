@@ -26,6 +26,10 @@ def announce(msg):
     ((3, 1100, 64, 1, 100), "bf16", None),
     ((700, 20, 64, 1, 16), "f32", None),           # too many rows for eight waves each
     ((90, 130, 300, 3, 5), "bf16", None),
+    # so many workgroups that a backward's take 128 and 256 tokens
+    ((320, 300, 5, 5, 16), "f32", [300, 129, 128, 127, 0] * 64),
+    ((480, 310, 5, 5, 3), "f32", [310, 257, 256, 255, 64, 1] * 80),
+    ((480, 310, 5, 5, 17), "bf16", [310, 300, 288, 0, 65, 200] * 80),
     ((260, 260, 70, 1, 16), "f32", [260] * 130 + [0] * 65 + [1] * 65),
 ], ids=lambda x: str(x)[:24])
 def test_many_segments_and_rows(L, shape, dtype, lengths):  # noqa: F811
