@@ -1,6 +1,6 @@
 // selective_scan.hip -- the selective state space scan, forward and for one token.
 //
-//   d_t = softplus(dt_t + bias),  h_t[n] = e^{d_t A[n]} h_{t-1}[n] + d_t u_t B_t[n],
+//   d_t = softplus<E>(dt_t + bias),  h_t[n] = e^{d_t A[n]} h_{t-1}[n] + d_t u_t B_t[n],
 //   y_t = (sum_n C_t[n] h_t[n] + D u_t) silu(z_t)
 //
 // Nothing is shared between channels but B_t and C_t, so there is no matrix product in it: each
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
             if (soft) {  // outside of the loop: the tokens' chains of instructions then run side by side
                 float sig;
 #pragma unroll
-                for (int i = 0; i < TW; ++i) d[i] = softplus(d[i], sig);
+                for (int i = 0; i < TW; ++i) d[i] = softplus<E>(d[i], sig);
             }
 #pragma unroll
             for (int i = 0; i < TW; ++i) {
@@ -352,7 +352,7 @@ __global__ __launch_bounds__(256) void sel_step_kernel(SelShape s, SelArgs A, un
         const float z = (float)reinterpret_cast<const E*>(A.z)[rows + c];
         gate = z * logistic(z);
     }
-    if (s.softplus) d = softplus(d, sig);
+    if (s.softplus) d = softplus<E>(d, sig);
     const float du = d * u;
     float out = 0.f;
     const auto channel = [&](auto index) {
@@ -412,12 +412,14 @@ hipError_t forward(const SelShape& s, const SelArgs& A, const SelPlan& p, const 
     const int group_tiles = (int)ceil_div(s.C / s.G, 64);
     const int64_t wg = s.B * s.G * group_tiles;
     const int segs = (int)p.segs, seg_tiles = (int)p.seg_tiles;
-    if (segs > 1) {
-        hipLaunchKernelGGL((sel_forward_kernel<E, W, NPT, true>), dim3((unsigned)(wg * (segs - 1))), dim3(64 * W), 0, st,
-                           s, A, S.bc, S.agg, S.sum, (float*)nullptr, segs, seg_tiles, group_tiles);
-        hipError_t e = hipGetLastError();
-        if (e == hipSuccess) e = run_sel_join(s, A.A, S.agg, S.sum, p.segs, A.s_in, nullptr, false, st);
-        if (e != hipSuccess) return e;
+    if constexpr (!(W == 8 && NPT == 2)) {  // whole rows alone are split like that
+        if (segs > 1) {
+            hipLaunchKernelGGL((sel_forward_kernel<E, W, NPT, true>), dim3((unsigned)(wg * (segs - 1))), dim3(64 * W), 0, st,
+                               s, A, S.bc, S.agg, S.sum, (float*)nullptr, segs, seg_tiles, group_tiles);
+            hipError_t e = hipGetLastError();
+            if (e == hipSuccess) e = run_sel_join(s, A.A, S.agg, S.sum, p.segs, A.s_in, nullptr, false, st);
+            if (e != hipSuccess) return e;
+        }
     }
     hipLaunchKernelGGL((sel_forward_kernel<E, W, NPT, false>), dim3((unsigned)(wg * segs)), dim3(64 * W), 0, st, s, A,
                        S.bc, S.agg, S.sum, keep, segs, seg_tiles, group_tiles);

@@ -96,7 +96,7 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
         if (soft) {
             float sig;
 #pragma unroll
-            for (int i = 0; i < TW; ++i) d[i] = softplus(d[i], sig);
+            for (int i = 0; i < TW; ++i) d[i] = softplus<E>(d[i], sig);
         }
         if (gated) {
 #pragma unroll
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
         for (int e = 0; e < TW; ++e) {
             const bool there = live && t0 + w * TW + e < len;
             const float raw = (float)next.dt[e] + bias, z = (float)next.z[e], gy = (float)next.gy[e], sg = logistic(z);
-            const float d = softplus(raw, sig[e]);
+            const float d = softplus<E>(raw, sig[e]);
             if (!soft) sig[e] = 1.f;
             gzf[e] = gy * sg * fmaf(z, 1.f - sg, 1.f);
             us[e] = there ? (float)next.u[e] : 0.f;
@@ -500,7 +500,7 @@ __global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A,
                     const float u = (float)reinterpret_cast<const E*>(A.u)[at];
                     float d = (float)reinterpret_cast<const E*>(A.dt)[at] + bias, sig = 1.f;
                     float p = (float)reinterpret_cast<const E*>(g.gy)[at];
-                    if (s.softplus) d = softplus(d, sig);
+                    if (s.softplus) d = softplus<E>(d, sig);
                     if (A.z) {
                         const float z = (float)reinterpret_cast<const E*>(A.z)[at];
                         const float sg = logistic(z);
