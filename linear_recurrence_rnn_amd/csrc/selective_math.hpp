@@ -98,6 +98,13 @@ __device__ __forceinline__ float where(bool there, float v) {
     return there ? v : 0.f;
 }
 
+// The workgroup's place among n, such that `together` neighbours, which read the same tokens' lines, run on one of
+// the eight chiplets that workgroups go round, and share its cache.
+__device__ __forceinline__ unsigned place_of(unsigned i, unsigned n, unsigned together) {
+    if (i >= n / (8 * together) * (8 * together)) return i;
+    return (i / 8 / together * 8 + i % 8) * together + i / 8 % together;
+}
+
 // Tokens of row b that are there.
 __device__ __forceinline__ int64_t row_length(const SelShape& s, int64_t b) {
     if (!s.lengths) return s.T;

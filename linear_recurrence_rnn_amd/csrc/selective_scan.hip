@@ -61,7 +61,7 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
     __shared__ float part[AGG ? 1 : W][AGG ? 1 : kSelTile][64];  // the waves' shares of y
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int runs = AGG ? segs - 1 : segs;  // nothing needs the last segment's share
-    unsigned blk = blockIdx.x;
+    unsigned blk = place_of(blockIdx.x, gridDim.x, (unsigned)(s.G * group_tiles));
     const int tile = (int)(blk % (unsigned)(s.G * group_tiles));
     blk /= (unsigned)(s.G * group_tiles);
     const int seg = (int)(blk % (unsigned)runs);
@@ -91,16 +91,17 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
     const float Dc = A.D ? A.D[c] : 0.f;
     float total = 0.f;
 
-    // This wave's tokens of a tile, read while the tile before is worked on.  Tokens behind the row's end
-    // are read as the last one, a gate that was not given as u: neither is used.
+    // This wave's tokens of a tile, read while the tile before is worked on.  Absent tokens are read as the last
+    // that is there (or the segment's first), a gate that was not given as u: neither is used.
     const bool gated = A.z != nullptr, soft = s.softplus != 0;
     const void* const zp = gated ? A.z : A.u;
     E ur[TW], dr[TW], zr[TW];
     const unsigned C = (unsigned)s.C;
+    const int t_stop = len < t_end ? (len > t_begin ? len : t_begin + 1) : t_end;
     const auto fetch = [&](int t0, int64_t at0) {  // at0: the tile's first element
 #pragma unroll
         for (int i = 0; i < TW; ++i) {
-            const int k = t0 + w * TW + i < T ? w * TW + i : T - 1 - t0;
+            const int k = t0 + w * TW + i < t_stop ? w * TW + i : t_stop - 1 - t0;
             const unsigned at = ((unsigned)k * C + c) * (unsigned)sizeof(E);
             ur[i] = load_elem<E>(elems<E>(A.u, at0), at);
             dr[i] = load_elem<E>(elems<E>(A.dt, at0), at);
@@ -112,7 +113,9 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
     const int64_t first = b * tiles + t_begin / kSelTile;
     const float* row = bc + ((first * s.G + grp) * W + w) * (kSelTile * 2 * NPT);
     float* kept = keep + (first * Np + n0 / 4 * 4) * s.C + (n0 & 3);
-    fetch(t_begin, base);
+    int next = t_begin;  // the tile on its way
+    int64_t next_base = base;
+    fetch(next, next_base);
     for (int t0 = t_begin; t0 < t_end; t0 += kSelTile) {
         if constexpr (!AGG) {
             if (keep && live) {
@@ -151,8 +154,8 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
                 din[w * TW + i][lane] = v;
             }
         }
-        const bool more = t0 + kSelTile < t_end;
-        fetch(more ? t0 + kSelTile : t0, more ? base + kSelTile * s.C : base);
+        if (next + kSelTile < t_stop) next += kSelTile, next_base += kSelTile * s.C;
+        fetch(next, next_base);
         __syncthreads();
         if (t0 < len) {
             float subtotal = 0.f;

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
     constexpr int TW = kSelTile / W, NPT = kBwdNpt;
     __shared__ f32x2 din[kSelTile][64];  // d, p
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    unsigned blk = blockIdx.x;
+    unsigned blk = place_of(blockIdx.x, gridDim.x, (unsigned)(s.G * group_tiles * ntiles));
     const int tile = (int)(blk % (unsigned)(s.G * group_tiles));
     blk /= (unsigned)(s.G * group_tiles);
     const int nt = (int)(blk % (unsigned)ntiles);
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
     __shared__ GradLds<W> L;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int Cg = (int)(s.C / s.G), cuts = (int)S.cuts;
-    unsigned blk = blockIdx.x;
+    unsigned blk = place_of(blockIdx.x, gridDim.x, (unsigned)(cuts * s.G * ntiles));
     const int cu = (int)(blk % (unsigned)cuts);
     blk /= (unsigned)cuts;
     const int grp = (int)(blk % (unsigned)s.G);
