@@ -1,7 +1,7 @@
 /*
  * linrec.h -- C ABI of the MI355X (gfx950) per-channel linear-recurrence library.
  *
- * Four operations, all over activations laid out (B, T, C) row-major with the channel
+ * Recurrences of language models and what stands next to them, all over activations laid out (B, T, C) row-major with the channel
  * index fastest (batch B, sequence length T, channels C: the layout the RWKV-LLM page
  * "RWKV：基于RNN的LLM" uses in its section on parallel training):
  *
@@ -36,8 +36,8 @@
  * Conventions shared by every entry point:
  *  - Pointers are DEVICE pointers (hipMalloc / torch CUDA-on-ROCm memory) unless a
  *    comment says otherwise; the caller owns every buffer for the whole call.  Outputs
- *    must not alias inputs or each other (the one exception: the state of
- *    wkv4_decode_step, updated in place).
+ *    must not alias inputs or each other (the exceptions are named with their calls: the
+ *    state of a decode step, for one, is updated in place).
  *  - Calls are asynchronous: they validate arguments on the host, then enqueue kernels on
  *    `stream` (a hipStream_t; NULL means the default stream) and return.  The library never
  *    synchronises, allocates or frees device memory; scratch memory comes from the
@@ -67,8 +67,9 @@
  *    while kernels run surface on the stream, as for any HIP work.
  *  - Input values are not inspected (that would need a device read): non-finite inputs
  *    propagate to the outputs.
- *  - The gated delta rule and the group norm take float32 or bfloat16 tensors (their own rules
- *    of sizes stand with them); what follows here and above on types is of the other calls.
+ *  - The gated delta rule, the group norm, the selective scan, the short convolution and the
+ *    root-mean-square norm take float32 or bfloat16 tensors (their own rules of sizes stand with
+ *    them); what follows here and above on types is of the other calls.
  *  - Arithmetic is float32 (complex64 as float32 pairs); results match an fp64 evaluation
  *    of the same definition to a relative error of about 1e-5 of the per-sequence RMS.
  */

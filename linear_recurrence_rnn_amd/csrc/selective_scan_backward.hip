@@ -24,6 +24,9 @@
 // chip they keep the vector unit from its own work, 34 cycles and 35 of it taking 74.)
 // Sums over blocks, batch rows and channel ranges are partial sums in the workspace, added in
 // order by small kernels at the end: nothing depends on timing.
+//
+// 8 x 4096 tokens of 2560 channels, 16 states, bfloat16: reverse 268-290 us, gradients 943-1021 (the lower ones
+// before the clock falls), partial sums 57.  The vector unit is busy 98% and 97% of the first two.
 #include "selective_math.hpp"
 
 namespace linrec {
