@@ -9,7 +9,7 @@
 //   gu_t = D p_t + d_t sum_n g_t[n] B_t[n],   gD = sum_t p_t u_t
 //   gdt_t = gd_t softplus'(dt_t + bias),  gbias = sum_t gdt_t,  gz_t = gy_t core_t silu'(z_t)
 //
-// The rows are cut into blocks of 64 to 256 tokens.  First each block's share of the G that leaves it on
+// The rows are cut into blocks of 16 to 256 tokens.  First each block's share of the G that leaves it on
 // the left, from zero on its right (all blocks at once, as the forward's segments); then the G that
 // enters each block, one block after the other (the decay over a block is e^{A sum d}); then all gradients,
 // all blocks at once, the states formed again from those the forward kept every 16 tokens.
@@ -483,13 +483,19 @@ __global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A,
         float sD = 0.f, sb = 0.f;
         if (live) {
             const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
+            // Everything of the four tokens is asked for before any is used; absent ones are read as the row's last.
             float q[kTok][3];
+            E ur[kTok], dr[kTok], pr[kTok], zr[kTok];
 #pragma unroll
             for (int e = 0; e < kTok; ++e) {
                 q[e][0] = q[e][1] = q[e][2] = 0.f;
-                const int64_t t = t0 + e < s.T ? t0 + e : s.T - 1;
+                const int64_t t = t0 + e < s.T ? t0 + e : s.T - 1, at = (b * s.T + t) * s.C + c;
+                ur[e] = reinterpret_cast<const E*>(A.u)[at];
+                dr[e] = reinterpret_cast<const E*>(A.dt)[at];
+                pr[e] = reinterpret_cast<const E*>(g.gy)[at];
+                zr[e] = reinterpret_cast<const E*>(A.z ? A.z : A.u)[at];
                 for (int i = 0; i < ntiles; ++i) {
-                    const float* o = S.q + (int64_t)i * 3 * plane + (b * s.T + t) * s.C + c;
+                    const float* o = S.q + (int64_t)i * 3 * plane + at;
 #pragma unroll
                     for (int j = 0; j < 3; ++j) q[e][j] += o[j * plane];
                 }
@@ -500,13 +506,11 @@ __global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A,
                 if (t >= s.T) continue;
                 float gu = 0.f, gd = 0.f, gz = 0.f;
                 if (t < len) {
-                    const float u = (float)reinterpret_cast<const E*>(A.u)[at];
-                    float d = (float)reinterpret_cast<const E*>(A.dt)[at] + bias, sig = 1.f;
-                    float p = (float)reinterpret_cast<const E*>(g.gy)[at];
+                    const float u = (float)ur[e];
+                    float d = (float)dr[e] + bias, p = (float)pr[e], sig = 1.f;
                     if (s.softplus) d = softplus<E>(d, sig);
                     if (A.z) {
-                        const float z = (float)reinterpret_cast<const E*>(A.z)[at];
-                        const float sg = logistic(z);
+                        const float z = (float)zr[e], sg = logistic(z);
                         gz = p * sg * fmaf(z, 1.f - sg, 1.f) * fmaf(Dc, u, q[e][2]);
                         p *= z * sg;
                     }
