@@ -458,18 +458,22 @@ SelPlan sel_plan(const SelShape& s) {
     // Segments until the chip has six waves a SIMD: 32768 tokens of 2048 channels took 573 us, 587 with four waves a
     // SIMD and 693 with two; 8 x 4096 tokens of 2560 635, 684 and 791.  Of two tiles at least, of four in rows of more
     // than 128 tiles, where the states that enter the segments would cost more: 512 tokens of 1536 channels take 26.0 us
-    // with twos, 28.7 with fours, 4096 of 256 36.5 and 32.1.  Fewer than four segments form too
-    // much twice: 12 x 1024 tokens of 2560 take 182 us whole, 227 with three; 8 x 1024 180 whole, 158 with four.
+    // with twos, 28.7 with fours, 4096 of 256 36.5 and 32.1.  Of one where that leaves SIMDs with two waves, in up to 64
+    // tiles: 500 tokens of 256 take 18.1 us, 20.1 with twos, but 1024 of 1536, with six waves a SIMD, 36.3 and 30.9.
+    // Fewer than four segments form too much twice: 12 x 1024 tokens of 2560 take 182 us whole, 227 with three; 8 x 1024
+    // 180 whole, 158 with four.  Nor are up to seven of the quicker tiles of half the states a wave cut: 77 tokens of
+    // 1536 take 14.4 us whole, 18 in five; but 112 of 256 with 128 states 67 whole, 41 in seven, with 2 states 24 and 15.
     const int64_t wg = s.B * s.G * ceil_div(s.C / s.G, 64), tiles = sel_tiles(s);
     int64_t segs = 6144 / (wg * p.waves);
-    const int64_t most = tiles <= 128 ? tiles / 2 : tiles / 4;
+    const int64_t most = tiles <= 64 && wg * p.waves * tiles <= 2048 ? tiles : tiles <= 128 ? tiles / 2 : tiles / 4;
     if (segs > most) segs = most;
-    if (segs < 4) segs = 1;
+    const bool halved = p.npt == 4 && p.waves == 4;  // may be, below
+    if (segs < 4 || (halved && tiles < 8)) segs = 1;
     p.seg_tiles = ceil_div(tiles, segs);
     p.segs = ceil_div(tiles, p.seg_tiles);
     // Whole rows too few for four waves a SIMD: half the states a wave.  77 tokens of 1536 channels take 12.1 us for
     // 15.2, 12 x 1024 of 2560 173 for 182, but 24 x 1024 302 for 291.
-    if (p.segs == 1 && p.npt == 4 && p.waves == 4 && wg * 8 <= 4096) p.npt = 2, p.waves = 8;
+    if (p.segs == 1 && halved && wg * 8 <= 4096) p.npt = 2, p.waves = 8;
     return p;
 }
 
