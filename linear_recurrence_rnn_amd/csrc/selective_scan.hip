@@ -455,18 +455,22 @@ SelPlan sel_plan(const SelShape& s) {
     p.tiles_n = 1;
     p.npt = s.N <= 1 ? 1 : s.N <= 2 ? 2 : s.N <= 16 ? 4 : s.N <= 64 ? 8 : 16;
     p.waves = s.N <= 4 ? 1 : s.N <= 8 ? 2 : s.N <= 32 ? 4 : 8;
-    // Segments until the chip has six waves a SIMD: 32768 tokens of 2048 channels took 573 us, 587 with four waves a
-    // SIMD and 693 with two; 8 x 4096 tokens of 2560 635, 684 and 791.  Of two tiles at least, of four in rows of more
-    // than 128 tiles, where the states that enter the segments would cost more: 512 tokens of 1536 channels take 26.0 us
-    // with twos, 28.7 with fours, 4096 of 256 36.5 and 32.1.  Of one where that leaves SIMDs with two waves, in up to 64
-    // tiles: 500 tokens of 256 take 18.1 us, 20.1 with twos, but 1024 of 1536, with six waves a SIMD, 36.3 and 30.9.
-    // Fewer than four segments form too much twice: 12 x 1024 tokens of 2560 take 182 us whole, 227 with three; 8 x 1024
-    // 180 whole, 158 with four.  Nor are up to seven of the quicker tiles of half the states a wave cut: 77 tokens of
-    // 1536 take 14.4 us whole, 18 in five; but 112 of 256 with 128 states 67 whole, 41 in seven, with 2 states 24 and 15.
+    // Segments until there are ten waves a SIMD, of which it holds three (one wave a workgroup) to eight at once: 8 x 4096
+    // tokens of 2560 channels take 515 us, 536 with six; with 8 states 370 and 410; 32768 of 2048 449 and 471; more gain
+    // nothing.  Each but the last is walked twice, so that a few segments cost more than they give: whole from
+    // fewer than eight on, or six where a workgroup has one wave or two.  12 x 4096 tokens of 2560, five segments, 643 us
+    // whole and 792 cut; with 32 states 10 x 2048, six, 564 and 620; with 8 20 x 2048, six, 533 and 456.
     const int64_t wg = s.B * s.G * ceil_div(s.C / s.G, 64), tiles = sel_tiles(s);
-    int64_t segs = 6144 / (wg * p.waves);
+    int64_t segs = 10240 / (wg * p.waves);
+    if (segs < (p.waves <= 2 ? 6 : 8)) segs = 1;
+    // Of two tiles at least, of four in rows of more than 128 tiles, where the states that enter the segments would cost
+    // more: 512 tokens of 1536 channels take 26.0 us with twos, 28.7 with fours, 4096 of 256 36.5 and 32.1.  Of one where
+    // that leaves SIMDs with two waves, in up to 64 tiles: 500 tokens of 256 take 18.1 us, 20.1 with twos, but 1024 of
+    // 1536, with six waves a SIMD, 36.3 and 30.9.
     const int64_t most = tiles <= 64 && wg * p.waves * tiles <= 2048 ? tiles : tiles <= 128 ? tiles / 2 : tiles / 4;
     if (segs > most) segs = most;
+    // Nor are rows cut into fewer than four, or up to seven of the quicker tiles of half the states a wave: 77 tokens of
+    // 1536 take 14.4 us whole, 18 in five; but 112 of 256 with 128 states 67 whole, 41 in seven, with 2 states 24 and 15.
     const bool halved = p.npt == 4 && p.waves == 4;  // may be, below
     if (segs < 4 || (halved && tiles < 8)) segs = 1;
     p.seg_tiles = ceil_div(tiles, segs);
