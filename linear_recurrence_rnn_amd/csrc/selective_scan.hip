@@ -19,8 +19,8 @@
 // segment's state from a zero state, and the sum of its steps (the decay over a segment is e^{A sum}),
 // then the states that enter the segments one after the other, then the segments again from those.
 //
-// 8 x 1024 tokens of 1536 channels, 16 states, bfloat16: 103 us, of which the segments' states take 44 and
-// the outputs 60; the vector unit is busy 88% and 90% of that.  A state and token costs it 24 cycles for 64
+// 8 x 1024 tokens of 1536 channels, 16 states, bfloat16: 102 us, of which the segments' states take 42 and
+// the outputs 58; the vector unit is busy 88% and 90% of that.  A state and token costs it 24 cycles for 64
 // of them; what a token and channel costs, once per pass, is a quarter to a third of all instructions.
 #include <type_traits>
 
