@@ -25,7 +25,7 @@
 // Sums over blocks, batch rows and channel ranges are partial sums in the workspace, added in
 // order by small kernels at the end: nothing depends on timing.
 //
-// 8 x 4096 tokens of 2560 channels, 16 states, bfloat16: reverse 274-289 us, gradients 949-1006 (the lower ones
+// 8 x 4096 tokens of 2560 channels, 16 states, bfloat16: reverse 274-289 us, gradients 934-1000 (the lower ones
 // before the clock falls), partial sums 56.  The vector unit is busy 98% and 97% of the first two.
 #include "selective_math.hpp"
 
@@ -154,8 +154,9 @@ constexpr int kMirror8 = 0x141, kXor1 = 0xb1, kXor2 = 0x4e;  // quad_perm [1,0,3
 
 // Tokens of a tile whose decays are kept from the pass over the states to the one back over their gradients.
 // The others are formed again, 12 cycles of the vector unit each, so that the registers are enough for three waves
-// a SIMD: 1045 us for 8 x 4096 tokens of 2560 channels, 1061 with none kept, 1245 with all and two waves.
-constexpr int kKept = 4;
+// a SIMD: 1045 us for 8 x 4096 tokens of 2560 channels with four, 1061 with none, 1245 with all and two waves; later
+// 980 to 1000 with six, which is as many as the registers hold, for 1005 with four.
+constexpr int kKept = 6;
 
 constexpr int kRowPad = 68;  // floats of a row of 64: an eighth starts on 16 bytes, two rows on other banks
 
