@@ -1025,12 +1025,16 @@ _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_d
 
 
 def _on_device(call):
+    first = call.__code__.co_varnames[0]  # the tensor whose device counts, by position or by name
+
     @functools.wraps(call)
-    def checked(x, *args, **kw):
-        if isinstance(x, torch.Tensor) and x.get_device() not in (-1, _get_device()):  # -1: no GPU's, refused below
-            with torch.cuda.device(x.device):
-                return call(x, *args, **kw)
-        return call(x, *args, **kw)
+    def checked(*args, **kw):
+        x = args[0] if args else kw.get(first)
+        device = x.get_device() if isinstance(x, torch.Tensor) else -1  # -1: no GPU's, refused below
+        if device >= 0 and device != _get_device():
+            with torch.cuda.device(device):
+                return call(*args, **kw)
+        return call(*args, **kw)
 
     return checked
 
