@@ -193,6 +193,13 @@ def _workspace(nbytes: int, device, workspace):
     if nbytes == 0:
         return None, 0
     if workspace is not None:
+        if not isinstance(workspace, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        # The kernels write there: memory of another device, or between a view's elements, is not theirs.
+        if workspace.device != device:
+            raise ValueError("workspace is on %s, expected %s" % (workspace.device, device))
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         if workspace.numel() * workspace.element_size() < nbytes:
             raise ValueError("workspace too small: %d < %d bytes" % (
                 workspace.numel() * workspace.element_size(), nbytes))
