@@ -9,25 +9,22 @@ namespace linrec {
 
 constexpr float kLn2 = 0.69314718055994531f;
 
-// e^x for x <= 0.  The product with log2(e) is taken to twice float32's digits: rounded once, it
-// would cost x * 2^-24 of the result, up to four bits of a step of 1e-7.  Where steps come in bfloat16
-// that is far below their own rounding, x * 2^-9: once will do, for six of the twenty instructions.
-template <class E>
+// e^x for x <= 0: 2^p for p = x log2(e) as rounded, and what that rounding left of x, x - p ln 2, to first order.
+// kLn2 is 2.7e-9 of ln 2 away from it, which costs x * 2^-28 of the result; without the second term the product's
+// rounding would cost x * 2^-24, up to four bits of a step of 1e-7.  With bfloat16 tensors too: where steps are
+// small, most of x is the bias, which is float32, and so are the states and sums that a step reaches.
 __device__ __forceinline__ float exp_neg(float x) {
-    if constexpr (sizeof(E) == 2) return fast_exp2(x * kLog2e);
-    x = x < -104.f ? -104.f : x;  // 0 there; a NaN stays one
+    x = __builtin_elementwise_maximum(x, -104.f);  // 0 there; a NaN stays one
     const float p = x * kLog2e;
-    const float r = fmaf(x, 1.925963033500e-8f, fmaf(x, kLog2e, -p));
     const float e = fast_exp2(p);
-    return fmaf(e * kLn2, r, e);
+    return fmaf(e, fmaf(-p, kLn2, x), e);
 }
 
 // softplus(x) = max(x, 0) + log(1 + e^{-|x|}).  The logarithm of w = 1 + e as rounded, and what
 // that rounding lost, e - (w - 1), which is all there is left of a small e.
 // sig: the logistic function of x, softplus's derivative.
-template <class E>
 __device__ __forceinline__ float softplus(float x, float& sig) {
-    const float e = exp_neg<E>(-fabsf(x));
+    const float e = exp_neg(-fabsf(x));
     const float w = 1.f + e;
     const float r = __builtin_amdgcn_rcpf(w);
     sig = x >= 0.f ? r : e * r;

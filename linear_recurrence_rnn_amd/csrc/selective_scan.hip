@@ -147,7 +147,7 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
             if (soft) {  // outside of the loop: the tokens' chains of instructions then run side by side
                 float sig;
 #pragma unroll
-                for (int i = 0; i < TW; ++i) d[i] = softplus<E>(d[i], sig);
+                for (int i = 0; i < TW; ++i) d[i] = softplus(d[i], sig);
             }
 #pragma unroll
             for (int i = 0; i < TW; ++i) {
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(256) void sel_step_kernel(SelShape s, SelArgs A, un
         const float z = (float)reinterpret_cast<const E*>(A.z)[rows + c];
         gate = z * logistic(z);
     }
-    if (s.softplus) d = softplus<E>(d, sig);
+    if (s.softplus) d = softplus(d, sig);
     const float du = d * u;
     float out = 0.f;
     const auto channel = [&](auto index) {

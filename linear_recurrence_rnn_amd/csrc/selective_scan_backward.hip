@@ -99,7 +99,7 @@ __global__ __launch_bounds__(64 * W) void sel_reverse_kernel(SelShape s, SelArgs
         if (soft) {
             float sig;
 #pragma unroll
-            for (int i = 0; i < TW; ++i) d[i] = softplus<E>(d[i], sig);
+            for (int i = 0; i < TW; ++i) d[i] = softplus(d[i], sig);
         }
         if (gated) {
 #pragma unroll
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
         for (int e = 0; e < TW; ++e) {
             const bool there = live && t0 + w * TW + e < len;
             const float raw = (float)next.dt[e] + bias, z = (float)next.z[e], gy = (float)next.gy[e], sg = logistic(z);
-            const float d = softplus<E>(raw, sig[e]);
+            const float d = softplus(raw, sig[e]);
             if (!soft) sig[e] = 1.f;
             gzf[e] = gy * sg * fmaf(z, 1.f - sg, 1.f);
             us[e] = there ? (float)next.u[e] : 0.f;
@@ -509,7 +509,7 @@ __global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A,
                 if (t < len) {
                     const float u = (float)ur[e];
                     float d = (float)dr[e] + bias, p = (float)pr[e], sig = 1.f;
-                    if (s.softplus) d = softplus<E>(d, sig);
+                    if (s.softplus) d = softplus(d, sig);
                     if (A.z) {
                         const float z = (float)zr[e], sg = logistic(z);
                         gz = p * sg * fmaf(z, 1.f - sg, 1.f) * fmaf(Dc, u, q[e][2]);
