@@ -82,7 +82,8 @@ struct SelGroup {
     __device__ __forceinline__ float C(int k, int i) const { return B(k, NPT + i); }
 };
 
-// LDS written by lanes of this wave is read by others of it behind this.
+// LDS written by lanes of this wave is read by others of it behind this, and what was read may be written.  The wave's
+// LDS accesses are carried out in their order anyway: this keeps the compiler to it, and costs no instruction.
 __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();

@@ -312,7 +312,11 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
             for (int j = 0; j < kGroups; ++j) {
                 const Group& v = of[j & 1];
                 if (j + 1 < kGroups) ahead(j + 1);
-                if (j > 0) ask_sums();
+                if (j > 0) {
+                    wave_lds_fence();  // the pair before has been written, and is read before the next is
+                    ask_sums();
+                    wave_lds_fence();
+                }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int r = 0; r < kTok; ++r) {
@@ -377,7 +381,11 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(Se
             for (int j = kPairs - 1; j >= 0; --j) {
                 if (j > 0) ahead(j - 1);
                 if (j == kPairs / 2) fetch(q > 0 ? q - 1 : 0);  // the last time for nothing
-                if (j + 1 < kPairs) ask_sums();
+                if (j + 1 < kPairs) {
+                    wave_lds_fence();
+                    ask_sums();
+                    wave_lds_fence();
+                }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int r = 1; r >= 0; --r) {
