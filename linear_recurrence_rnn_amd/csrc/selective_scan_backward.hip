@@ -154,9 +154,12 @@ constexpr int kMirror8 = 0x141, kXor1 = 0xb1, kXor2 = 0x4e;  // quad_perm [1,0,3
 
 // Tokens of a tile whose decays are kept from the pass over the states to the one back over their gradients.
 // The others are formed again, 12 cycles of the vector unit each, so that the registers are enough for three waves
-// a SIMD: 1045 us for 8 x 4096 tokens of 2560 channels with four, 1061 with none, 1245 with all and two waves; later
-// 980 to 1000 with six, which is as many as the registers hold, for 1005 with four.
-constexpr int kKept = 6;
+// a SIMD with four waves a workgroup (all kept: two waves, 1245 us for 1045 at the time) and for two with one wave or two.
+// Whole training steps of 8 x 4096 tokens of 2560 channels, bfloat16 / float32: 16 states 1770 / 1872 us with six, 1789 / 1894
+// with four; 4 states, one wave a workgroup, 1286 / 1592 with six, which leave it one wave a SIMD, 1017 / 1330
+// with four; 8 states, two waves, 1325 / 1567 with either.
+template <int W>
+constexpr int kKeptBy = W == 1 ? 4 : 6;
 
 constexpr int kRowPad = 68;  // floats of a row of 64: an eighth starts on 16 bytes, two rows on other banks
 
@@ -170,11 +173,11 @@ struct GradLds {
 
 // WHOLE: one workgroup has all states of its channels, so that its sums over them are complete.
 template <class E, int W, bool WHOLE>
-__global__ __launch_bounds__(64 * W, W == 4 ? 3 : 1) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
+__global__ __launch_bounds__(64 * W, W == 4 ? 3 : 2) void sel_gradient_kernel(SelShape s, SelArgs A, SelBwdArgs g,
                                                                               const float* __restrict__ bc,
                                                                               const float* __restrict__ keep,
                                                                               SelBwdScratch S, int blocks, int block, int ntiles) {
-    constexpr int NPT = kBwdNpt, TW = kSelTile / W, kPairs = kSelTile / 2;
+    constexpr int NPT = kBwdNpt, TW = kSelTile / W, kPairs = kSelTile / 2, kKept = kKeptBy<W>;
     __shared__ GradLds<W> L;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int Cg = (int)(s.C / s.G), cuts = (int)S.cuts;
