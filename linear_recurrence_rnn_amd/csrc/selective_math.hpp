@@ -59,6 +59,8 @@ __device__ __forceinline__ const void* elems(const void* p, int64_t first) {
 // channels' own pair of floats from LDS.  Scalar loads come back in any order, so a wait for one is a
 // wait for all of them and for LDS: both are asked for together, one group ahead of their use.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef f32x16 f32x16_at16 __attribute__((aligned(16)));  // at 16 bytes, which is what a workspace is sure to start on
+static_assert(alignof(f32x16_at16) == 16 && sizeof(f32x16_at16) == 64);
 
 template <int NPT, int NF = 32>
 struct SelGroup {
@@ -73,7 +75,7 @@ struct SelGroup {
         for (int k = 0; k < kTok; ++k) x[k] = din[q * kTok + k][lane];
     }
     __device__ __forceinline__ void fetch(const float* row, int q) {
-        typedef const __attribute__((address_space(4))) f32x16* P;
+        typedef const __attribute__((address_space(4))) f32x16_at16* P;
         const P p = reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + q * NF));
 #pragma unroll
         for (int k = 0; k < NF / 16; ++k) bc[k] = p[k];

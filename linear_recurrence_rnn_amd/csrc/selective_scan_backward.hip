@@ -374,7 +374,7 @@ __global__ __launch_bounds__(64 * W, W == 4 ? 3 : 2) void sel_gradient_kernel(Se
             float y[2][2];
             f32x16 v[2];
             const auto ahead = [&](int j) {  // the pair of tokens 2 j, 2 j + 1
-                typedef const __attribute__((address_space(4))) f32x16* P;
+                typedef const __attribute__((address_space(4))) f32x16_at16* P;
                 v[j & 1] = *reinterpret_cast<P>(reinterpret_cast<uintptr_t>(row + j * 16));
 #pragma unroll
                 for (int r = 0; r < 2; ++r) x[j & 1][r] = L.du[2 * j + r][lane], y[j & 1][r] = L.p[2 * j + r][lane];
