@@ -228,6 +228,14 @@ __global__ __launch_bounds__(64 * W) void sel_forward_kernel(SelShape s, SelArgs
 // latency, one block after the other, hence eight at once: 16384 tokens of 256 channels 128 -> 72 us.
 constexpr int kAhead = 8;
 
+// x 2^p.  States that grow (A above zero, or steps below) may grow over a block by more than a float32 holds and be none
+// the less one, or zero: the whole part of p goes to the exponent.  A p beyond 1000 either way leaves nothing or infinity.
+__device__ __forceinline__ float grown(float x, float p) {
+    p = fminf(fmaxf(p, -1000.f), 1000.f);
+    const float whole = floorf(p);
+    return __builtin_amdgcn_ldexpf(x * fast_exp2(p - whole), (int)whole);
+}
+
 template <bool REV>
 __global__ __launch_bounds__(256) void sel_join_kernel(SelShape s, const float* __restrict__ A, float* __restrict__ v,
                                                        const float* __restrict__ sum, int64_t blocks,
@@ -262,7 +270,7 @@ __global__ __launch_bounds__(256) void sel_join_kernel(SelShape s, const float* 
         for (int r = 0; r < kAhead; ++r) {
             if (i + r >= known) break;
             v[place(i + r) * per + e] = x;
-            x = fmaf(fast_exp2(a2 * f[r]), x, o[r]);
+            x = grown(x, a2 * f[r]) + o[r];
         }
     };
     for (int64_t i = 0; i < known; i += 2 * kAhead) {
