@@ -628,7 +628,8 @@ size_t group_norm_act_backward_workspace_size(int64_t N, int64_t C, int64_t G);
  *   y_t    = (sum_n C_t[g,n] h_t[n] + D u_t) * silu(z_t)
  *
  *   u, dt, z, y (B,T,C), Bm, Cm (B,T,G,N)  of type dtype; z may be NULL (no gate)
- *   A (C,N) float32, finite, usually negative;  D, dt_bias (C) float32 or NULL (zero)
+ *   A (C,N) float32, finite, usually negative (states may grow, with e^{d_t A[n]} a float32 for every
+ *            token);  D, dt_bias (C) float32 or NULL (zero)
  *   lengths  (B) int32 or NULL: tokens t >= lengths[b] (clamped to 0..T) of row b are absent:
  *            they leave the state alone, y is 0 there, and nothing of them is used
  *   s_in     (B,C,N) float32 or NULL (zero);  s_out (B,C,N) float32 or NULL: the state after the last
@@ -663,6 +664,8 @@ size_t linrec_scan_selective_workspace_size(int64_t B, int64_t T, int64_t C, int
  *   gD, gz, gdt_bias are NULL exactly when D, z, dt_bias are
  *
  * With B or T = 0 the sums gA, gD, gdt_bias are zero-filled and gs_in is gs_out.
+ * With C = 0 nothing is enqueued: gB and gC, sums over no channels, are left as they were (the
+ * Python binding fills them with zeros).
  */
 size_t linrec_scan_selective_checkpoint_size(int64_t B, int64_t T, int64_t C, int64_t G, int64_t N, int dtype);
 

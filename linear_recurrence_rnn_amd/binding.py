@@ -1169,6 +1169,8 @@ def scan_selective_backward(u, dt, A, B, C, gy, D=None, z=None, dt_bias=None, so
                 raise ValueError("out[%d] must be given exactly when its input is" % i)
             if o is not None:
                 _need(o, "out[%d]" % i, f32 if t is None else t.dtype, (Bn, ch, N) if t is None else t.shape, dev)
+    if ch == 0:  # B's and C's gradients have elements all the same: sums over no channels
+        out[3].zero_(), out[4].zero_()
     nws = lib.linrec_scan_selective_workspace_size(Bn, T, ch, G, N, code, 1 if ckpt is None else 2)
     ws = _scratch(nws, dev, workspace)
     _check(lib.linrec_scan_selective_backward(Bn, T, ch, G, N, code, u.data_ptr(), dt.data_ptr(), A.data_ptr(),
