@@ -495,21 +495,24 @@ __global__ __launch_bounds__(1024) void sel_finish_kernel(SelShape s, SelArgs A,
         float sD = 0.f, sb = 0.f;
         if (live) {
             const float bias = A.bias ? A.bias[c] : 0.f, Dc = A.D ? A.D[c] : 0.f;
-            // Everything of the four tokens is asked for before any is used; absent ones are read as the row's last.
+            // Everything of the four tokens is asked for before any is used; absent ones are read as the row's last one
+            // that is there, and nothing where all four are.
             float q[kTok][3];
             E ur[kTok], dr[kTok], pr[kTok], zr[kTok];
+            if (t0 < len) {
 #pragma unroll
-            for (int e = 0; e < kTok; ++e) {
-                q[e][0] = q[e][1] = q[e][2] = 0.f;
-                const int64_t t = t0 + e < s.T ? t0 + e : s.T - 1, at = (b * s.T + t) * s.C + c;
-                ur[e] = reinterpret_cast<const E*>(A.u)[at];
-                dr[e] = reinterpret_cast<const E*>(A.dt)[at];
-                pr[e] = reinterpret_cast<const E*>(g.gy)[at];
-                zr[e] = reinterpret_cast<const E*>(A.z ? A.z : A.u)[at];
-                for (int i = 0; i < ntiles; ++i) {
-                    const float* o = S.q + (int64_t)i * 3 * plane + at;
+                for (int e = 0; e < kTok; ++e) {
+                    q[e][0] = q[e][1] = q[e][2] = 0.f;
+                    const int64_t t = t0 + e < len ? t0 + e : len - 1, at = (b * s.T + t) * s.C + c;
+                    ur[e] = reinterpret_cast<const E*>(A.u)[at];
+                    dr[e] = reinterpret_cast<const E*>(A.dt)[at];
+                    pr[e] = reinterpret_cast<const E*>(g.gy)[at];
+                    zr[e] = reinterpret_cast<const E*>(A.z ? A.z : A.u)[at];
+                    for (int i = 0; i < ntiles; ++i) {
+                        const float* o = S.q + (int64_t)i * 3 * plane + at;
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) q[e][j] += o[j * plane];
+                        for (int j = 0; j < 3; ++j) q[e][j] += o[j * plane];
+                    }
                 }
             }
 #pragma unroll
