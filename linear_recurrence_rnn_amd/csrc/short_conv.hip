@@ -13,8 +13,10 @@
 // A lane takes VEC neighbouring channels and walks down a run of tokens with the last K-1
 // inputs, and backwards also the last K-1 of q, in registers, so a token is read once but for the K-1
 // before (and, backwards, behind) a run; the next tokens are on their way meanwhile.  Both
-// directions are bound by memory.  The sums over tokens are kept in registers over a run, go to the
-// workspace and are added in the order of the runs.
+// directions are bound by memory.  The sums over tokens are kept in registers over a wave's runs, go to the
+// workspace and are added in the order of the waves.
+#include <algorithm>
+
 #include "short_conv.hpp"
 #include "group_norm.hpp"  // the activations' codes
 #include "elem_types.hpp"
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
                                                              int64_t run_tokens, int64_t cols) {
     __shared__ float acc[4][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t col = blockIdx.x % cols, walker = blockIdx.x / cols, run = walker * 4 + wave;
+    const int64_t col = blockIdx.x % cols, walker = blockIdx.x / cols, walkers = gridDim.x / cols;
     const int64_t c = (col * 64 + lane) * VEC;
     const unsigned off = (unsigned)c * (unsigned)sizeof(E);
     const bool live = c < s.C;
@@ -179,7 +181,9 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
 #pragma unroll
         for (int k = 0; k < K; ++k) gw[k][j] = 0.f;
     }
-    if (live && run < s.B * runs) {
+    float w[K][VEC], bias[VEC];
+    if (live) load_filters<K, VEC>(A, c, w, bias);
+    for (int64_t run = walker * 4 + wave; live && run < s.B * runs; run += walkers * 4) {
         const int64_t b = run / runs, t0 = run % runs * run_tokens, len = row_length(s, b);
         const int64_t t_end = t0 + run_tokens < s.T ? t0 + run_tokens : s.T;
         // The line's elements up to K-1 tokens beyond the run: x's gradient at a token needs the q behind it.
@@ -194,8 +198,6 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
             }
         };
         if (t0 < len) fetch(t0);
-        float w[K][VEC], bias[VEC];
-        load_filters<K, VEC>(A, c, w, bias);
         float x[K][VEC], q[K][VEC];  // x[k] = x_{t-K+1+k}, q[k] = q_{t-k}
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -293,14 +295,15 @@ __global__ __launch_bounds__(256) void short_conv_fold_kernel(const float* __res
 
 constexpr int kVec = 4;  // channels of a lane
 
-// Tokens of a run: as many as leave `waves` waves to the chip, 16 at least; a row has one run at least, for
-// its state if it has no tokens.
+// Tokens of a run: as many as leave `waves` waves of 64 lanes with `vec` channels each to the chip, 16 at least; a row has
+// one run at least, for its state if it has no tokens.  A wave takes one run or, `bounded`, as many as leave no more
+// than that many waves.
 struct ConvPlan {
     int64_t run_tokens, runs, groups;  // runs of a row; workgroups a column of channels
 };
-ConvPlan plan(const ConvShape& s, int64_t waves) {
+ConvPlan plan(const ConvShape& s, int64_t waves, int vec, bool bounded) {
     ConvPlan p{};
-    const int64_t cols = ceil_div(s.C, 64 * kVec);
+    const int64_t cols = ceil_div(s.C, 64 * vec);
     int64_t runs = waves / cols / s.B;  // of a row, so that all of them fit
     if (runs < 1) runs = 1;
     int64_t n = ceil_div(s.T, runs);
@@ -308,23 +311,28 @@ ConvPlan plan(const ConvShape& s, int64_t waves) {
     p.run_tokens = n;
     p.runs = s.T ? ceil_div(s.T, n) : 1;
     p.groups = ceil_div(s.B * p.runs, 4);
+    if (bounded) p.groups = std::min(p.groups, std::max<int64_t>(waves / cols / 4, 1));
     return p;
 }
 // Forward four times what the chip holds at once, so that ragged rows even out: a batch of 16 ragged
-// rows of up to 2000 tokens takes 43 us, 47 with half as many waves; full rows care little.  Backward what
-// it holds: 16 workgroups more than that cost a second round (174 us for 135).
+// rows of up to 2000 tokens takes 43 us, 47 with half as many waves; full rows care little.  With one channel a lane runs
+// as long as with four, and so four times the waves: 8 x 4096 tokens of 2562 channels take 151 us, 164 with as many.
+// Backward what it holds, and no more: 16 workgroups more than that cost a second round (174 us for 135), and
+// each leaves K + 1 rows of partial sums.  Many short rows are taken by the same waves: a training step of 65536 rows of 4
+// tokens, 256 channels, takes 211 us, 359 with a wave a row (and 84 MB of partial sums for 5).  One channel a lane: 8 x 4096
+// tokens of 250 channels 40.4 us, 44.4 with four times the waves, of 2562 in float32 481 and 489.
 constexpr int64_t kForwardWaves = 16384, kBackwardWaves = 4096;
 
 template <class E, int K, int VEC>
 hipError_t launch(const ConvShape& s, const ConvArgs& A, const ConvBwdArgs* g, hipStream_t st) {
     const int64_t cols = ceil_div(s.C, 64 * VEC);
     if (!g) {
-        const ConvPlan p = plan(s, kForwardWaves);
+        const ConvPlan p = plan(s, kForwardWaves, kVec, false);
         hipLaunchKernelGGL((short_conv_kernel<E, K, VEC>), dim3((unsigned)(cols * p.groups)), dim3(256), 0, st, s, A,
                            p.runs, p.run_tokens, cols);
         return hipGetLastError();
     }
-    const ConvPlan p = plan(s, kBackwardWaves);
+    const ConvPlan p = plan(s, kBackwardWaves, VEC, true);
     hipLaunchKernelGGL((short_conv_bwd_kernel<E, K, VEC>), dim3((unsigned)(cols * p.groups)), dim3(256), 0, st, s, A, *g,
                        p.runs, p.run_tokens, cols);
     hipError_t e = hipGetLastError();
@@ -364,7 +372,8 @@ hipError_t run_short_conv(const ConvShape& s, const ConvArgs& A, hipStream_t st)
 }
 
 size_t short_conv_backward_ws_bytes(const ConvShape& s) {
-    return (size_t)plan(s, kBackwardWaves).groups * (size_t)(s.K + 1) * (size_t)s.C * sizeof(float);
+    const int64_t groups = std::max(plan(s, kBackwardWaves, kVec, true).groups, plan(s, kBackwardWaves, 1, true).groups);
+    return (size_t)groups * (size_t)(s.K + 1) * (size_t)s.C * sizeof(float);
 }
 
 hipError_t run_short_conv_backward(const ConvShape& s, const ConvArgs& A, const ConvBwdArgs& g, hipStream_t st) {
