@@ -465,22 +465,30 @@ SelPlan sel_plan(const SelShape& s) {
     p.waves = s.N <= 4 ? 1 : s.N <= 8 ? 2 : s.N <= 32 ? 4 : 8;
     // Segments until there are ten waves a SIMD, of which it holds three (one wave a workgroup) to eight at once: 8 x 4096
     // tokens of 2560 channels take 515 us, 536 with six; with 8 states 370 and 410; 32768 of 2048 449 and 471; more gain
-    // nothing.  Each but the last is walked twice, so that a few segments cost more than they give: whole from
-    // fewer than eight on, or six where a workgroup has one wave or two.  12 x 4096 tokens of 2560, five segments, 643 us
-    // whole and 792 cut; with 32 states 10 x 2048, six, 564 and 620; with 8 20 x 2048, six, 533 and 456.
+    // nothing.
     const int64_t wg = s.B * s.G * ceil_div(s.C / s.G, 64), tiles = sel_tiles(s);
     int64_t segs = 10240 / (wg * p.waves);
-    if (segs < (p.waves <= 2 ? 6 : 8)) segs = 1;
     // Of two tiles at least, of four in rows of more than 128 tiles, where the states that enter the segments would cost
     // more: 512 tokens of 1536 channels take 26.0 us with twos, 28.7 with fours, 4096 of 256 36.5 and 32.1.  Of one where
     // that leaves SIMDs with two waves, in up to 64 tiles: 500 tokens of 256 take 18.1 us, 20.1 with twos, but 1024 of
     // 1536, with six waves a SIMD, 36.3 and 30.9.
     const int64_t most = tiles <= 64 && wg * p.waves * tiles <= 2048 ? tiles : tiles <= 128 ? tiles / 2 : tiles / 4;
     if (segs > most) segs = most;
-    // Nor are rows cut into fewer than four, or up to seven of the quicker tiles of half the states a wave: 77 tokens of
-    // 1536 take 14.4 us whole, 18 in five; but 112 of 256 with 128 states 67 whole, 41 in seven, with 2 states 24 and 15.
-    const bool halved = p.npt == 4 && p.waves == 4;  // may be, below
-    if (segs < 4 || (halved && tiles < 8)) segs = 1;
+    // Each segment but the last is walked twice, so that cut rows keep the chip busy for a time that grows with the
+    // workgroups, where whole ones take what one of them takes, alone on its CU or with others, however few they are.
+    // Microseconds a tile of 16 tokens: one whole row's workgroup alone, with others, and a workgroup's part of cut ones'.
+    const bool halved = p.npt == 4 && p.waves == 4;  // whole rows may be, below
+    const double us[6][3] = {{3.3, 4.4, 0.0033}, {2.45, 3.8, 0.0046}, {1.7, 2.5, 0.0065},
+                             {3.27, 4.4, 0.0116}, {4.25, 6.95, 0.0235}, {7.75, 13.3, 0.046}};
+    const double* const tile_us = us[s.N <= 4 ? 0 : s.N <= 8 ? 1 : s.N <= 16 ? 2 : s.N <= 32 ? 3 : s.N <= 64 ? 4 : 5];
+    const double saved = (double)tiles * (tile_us[wg > 256] - tile_us[2] * (double)wg);
+    // Cutting costs two launches and the segments' states written and read.  That model and the measured times of both
+    // sides, 1536 or 2560 channels in bfloat16, whole / cut: of 16 states 8 x 128 tokens 20.6 / 31.5 us, 8 x 256 33.7 /
+    // 44.3, 4 x 256 33.5 / 31.9, 8 x 512 60 / 68, 8 x 1024 113 / 105, 9 x 4096 651 / 635 (seven segments), 10 x 4096 654 /
+    // 692 (six), 8 x 4096 631 / 532 (eight); of 8 24 x 256 57 / 66, 20 x 4096 1114 / 945, 24 x 4096 1124 / 1128; of 4
+    // 12 x 128 33.4 / 29.6, 32 x 128 34.4 / 39.1, 32 x 4096 1226 / 1060, 42 x 512 157 / 210; of 32 4 x 128 35 / 38, 2 x 128
+    // 34 / 30, 9 x 4096 1152 / 1100, 10 x 4096 1159 / 1216; of 64 4 x 128 44 / 59, 4 x 512 144 / 117, 8 x 1024 281 / 317.
+    if (segs < 4 || saved < 16. + 2.5e-4 * (double)(wg * segs) * s.N) segs = 1;
     p.seg_tiles = ceil_div(tiles, segs);
     p.segs = ceil_div(tiles, p.seg_tiles);
     // Whole rows too few for four waves a SIMD: half the states a wave.  77 tokens of 1536 channels take 12.1 us for
