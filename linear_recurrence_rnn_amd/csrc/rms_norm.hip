@@ -14,19 +14,13 @@
 // memory: the next row is on its way while one is worked on, without which the backward took 277 us
 // for 113 (32768 tokens of 2560 bfloat16 channels), four barriers a row between its loads.
 #include "rms_norm.hpp"
-#include "elem_types.hpp"
+#include "row_ops.hpp"
 
 namespace linrec {
 
 namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// v summed over this lane and the one that the DPP permutation CTRL exchanges it with.
-template <int CTRL>
-__device__ __forceinline__ float add_dpp(float v) {
-    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
-}
 
 // Sum over the LPR lanes of a row, the same bits in every lane.  In a workgroup of several waves two
 // sums in a row use `lds` of their own, so that one barrier each is enough.
@@ -248,18 +242,9 @@ __global__ __launch_bounds__(256) void rms_norm_bwd_kernel(RmsArgs A) {
 __global__ __launch_bounds__(256) void rms_norm_fold_kernel(const float* __restrict__ part, int64_t rows, int64_t C,
                                                             float* __restrict__ gw) {
     __shared__ float lds[16][17];
-    const int cx = threadIdx.x & 15, strip = threadIdx.x >> 4;
-    const int64_t j = (int64_t)blockIdx.x * 16 + cx;
-    float v = 0.f;
-    if (j < C)
-#pragma unroll 4
-        for (int64_t r = strip; r < rows; r += 16) v += part[r * C + j];
-    lds[strip][cx] = v;
-    __syncthreads();
-    if (strip != 0 || j >= C) return;
-#pragma unroll
-    for (int i = 1; i < 16; ++i) v += lds[i][cx];
-    gw[j] = v;
+    const int64_t j = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
+    const float v = fold_column(part, rows, C, j, lds);
+    if (threadIdx.x < 16 && j < C) gw[j] = v;
 }
 
 struct RmsPlan {

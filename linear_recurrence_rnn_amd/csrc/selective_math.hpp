@@ -3,7 +3,7 @@
 #pragma once
 
 #include "selective_scan.hpp"
-#include "elem_types.hpp"
+#include "row_ops.hpp"
 
 namespace linrec {
 
@@ -29,11 +29,6 @@ __device__ __forceinline__ float softplus(float x, float& sig) {
     const float r = __builtin_amdgcn_rcpf(w);
     sig = x >= 0.f ? r : e * r;
     return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(w), kLn2, e - (w - 1.f));
-}
-
-__device__ __forceinline__ float logistic(float t) {
-    // e^{-t} may be infinite: the reciprocal is then 0.
-    return __builtin_amdgcn_rcpf(1.f + fast_exp2(-t * kLog2e));
 }
 
 // One element at a wave-uniform base and a lane's byte offset: the form that takes two scalar registers
@@ -106,11 +101,7 @@ __device__ __forceinline__ unsigned place_of(unsigned i, unsigned n, unsigned to
 }
 
 // Tokens of row b that are there.
-__device__ __forceinline__ int64_t row_length(const SelShape& s, int64_t b) {
-    if (!s.lengths) return s.T;
-    const int64_t n = s.lengths[b];
-    return n < 0 ? 0 : (n < s.T ? n : s.T);
-}
+__device__ __forceinline__ int64_t row_length(const SelShape& s, int64_t b) { return tokens_of(s.lengths, s.T, b); }
 
 // Element (row, n, c) of an array of states between kernels.
 __device__ __forceinline__ int64_t state_at(const SelShape& s, int64_t row, int n, int64_t c) {

@@ -289,11 +289,6 @@ __device__ __forceinline__ float of_lane(float v) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xf, 0xf, true));
 }
 
-template <int CTRL>
-__device__ __forceinline__ float add_dpp(float v) {
-    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-
 // v summed over LN lanes, in every one of them.
 template <int LN>
 __device__ __forceinline__ float over_lanes(float v) {

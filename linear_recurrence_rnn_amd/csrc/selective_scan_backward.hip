@@ -559,23 +559,6 @@ struct SelFold {
     int64_t rows, share_rows;
 };
 
-// The sum of column j, in the lanes of strip 0.
-__device__ __forceinline__ float fold_column(const float* __restrict__ part, int64_t rows, int64_t cols, int64_t j,
-                                             float (&lds)[16][17]) {
-    const int cx = threadIdx.x & 15, strip = threadIdx.x >> 4;
-    float v = 0.f;
-    if (j < cols)
-#pragma unroll 4
-        for (int64_t r = strip; r < rows; r += 16) v += part[r * cols + j];
-    lds[strip][cx] = v;
-    __syncthreads();
-    if (strip == 0) {
-#pragma unroll
-        for (int i = 1; i < 16; ++i) v += lds[i][cx];
-    }
-    return v;
-}
-
 template <class E>
 __global__ __launch_bounds__(256) void sel_fold_kernel(SelShape s, SelBwdArgs g, SelBwdScratch S, SelFold f) {
     __shared__ float lds[16][17];

@@ -19,7 +19,7 @@
 
 #include "short_conv.hpp"
 #include "group_norm.hpp"  // the activations' codes
-#include "elem_types.hpp"
+#include "row_ops.hpp"
 
 namespace linrec {
 
@@ -31,16 +31,7 @@ constexpr int kForwardAhead = 4, kBackwardAhead = 2;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-__device__ __forceinline__ float logistic(float t) {
-    // e^{-t} may be infinite: the reciprocal is then 0.
-    return __builtin_amdgcn_rcpf(1.f + fast_exp2(-t * kLog2e));
-}
-
-__device__ __forceinline__ int64_t row_length(const ConvShape& s, int64_t b) {
-    if (!s.lengths) return s.T;
-    const int64_t n = s.lengths[b];
-    return n < 0 ? 0 : (n < s.T ? n : s.T);
-}
+__device__ __forceinline__ int64_t row_length(const ConvShape& s, int64_t b) { return tokens_of(s.lengths, s.T, b); }
 
 // VEC elements as they come from memory, and their values.
 template <class E, int VEC> struct Raw { typedef E type __attribute__((ext_vector_type(VEC))); };
@@ -277,17 +268,9 @@ __global__ __launch_bounds__(256) void short_conv_bwd_kernel(ConvShape s, ConvAr
 __global__ __launch_bounds__(256) void short_conv_fold_kernel(const float* __restrict__ part, int64_t rows, int64_t C,
                                                               int K, float* __restrict__ gw, float* __restrict__ gb) {
     __shared__ float lds[16][17];
-    const int cx = threadIdx.x & 15, strip = threadIdx.x >> 4;
-    const int64_t cols = (K + 1) * C, j = (int64_t)blockIdx.x * 16 + cx;
-    float v = 0.f;
-    if (j < cols)
-#pragma unroll 4
-        for (int64_t r = strip; r < rows; r += 16) v += part[r * cols + j];
-    lds[strip][cx] = v;
-    __syncthreads();
-    if (strip != 0 || j >= cols) return;
-#pragma unroll
-    for (int i = 1; i < 16; ++i) v += lds[i][cx];
+    const int64_t cols = (K + 1) * C, j = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
+    const float v = fold_column(part, rows, cols, j, lds);
+    if (threadIdx.x >= 16 || j >= cols) return;
     const int64_t k = j / C, c = j % C;
     if (k < K) gw[c * K + k] = v;
     else if (gb) gb[c] = v;
