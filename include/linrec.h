@@ -621,7 +621,7 @@ size_t group_norm_act_backward_workspace_size(int64_t N, int64_t C, int64_t G);
 
 /*
  * Selective state space scan.  Per batch row, channel c and state n (of N), with the channels in G
- * groups of C/G and g = c / (C/G):
+ * groups of C/G and g = c / (C/G) (a group's channels are taken in whole 64s: smaller ones cost as much):
  *
  *   d_t    = softplus(dt_t + dt_bias)   (softplus nonzero), or dt_t + dt_bias itself
  *   h_t[n] = e^{d_t A[n]} h_{t-1}[n] + d_t u_t B_t[g,n]
@@ -705,7 +705,7 @@ int linrec_scan_selective_decode_step(int64_t B, int64_t C, int64_t G, int64_t N
  *            there, and nothing of them is used
  *
  * No workspace.  With K = 1 the states have no elements and are ignored.  LINREC_ERR_UNSUPPORTED beyond
- * B = 2^20, T = 2^30, C = 2^24 or about B*T*C/16 = 2^31.
+ * B = 2^20, T = 2^30, C = 2^24 or B * (T/16 rounded up, plus 1) * (C + 256) = 2^31.
  */
 int short_conv_act(int64_t B, int64_t T, int64_t C, int64_t K, int dtype, const void *x, const float *weight,
                    const float *bias, int act, const int32_t *lengths, const void *s_in, void *y, void *s_out,
@@ -735,6 +735,7 @@ size_t short_conv_act_backward_workspace_size(int64_t B, int64_t T, int64_t C, i
  *   x, y (N,C) of type dtype; residual, sum (N,C) of type rtype (dtype, or LINREC_F32), both or neither:
  *   sum is s, rounded to rtype, and the norm is that of s as stored there.  Without them s is x.
  *   weight (C) float32;  eps >= 0;  C <= 8192 (else LINREC_ERR_UNSUPPORTED)
+ *   The squares are summed in float32: |s| below 1e19 / sqrt(C) (above, the sum is infinite and y zero).
  *   sum may be residual itself.
  */
 int rms_norm_add(int64_t N, int64_t C, int dtype, int rtype, const void *x, const void *residual,

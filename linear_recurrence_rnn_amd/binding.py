@@ -1334,7 +1334,7 @@ def _rms_shape(x, weight, other, name):
 def rms_norm_add(x, weight, residual=None, eps=1e-5, out=None):
     """(y, s): s = x + residual in the residual's type (x itself without one) and y the
     root-mean-square norm of s over the channels times ``weight``, in x's type.  x (..., C) float32
-    or bfloat16; residual of x's shape, its type or float32; weight (C,) float32.  ``out`` = (y, s)
+    or bfloat16, C up to 8192; residual of x's shape, its type or float32; weight (C,) float32.  ``out`` = (y, s)
     buffers, s of which may be the residual."""
     lib = load()
     code, rcode, N, C, dev = _rms_shape(x, weight, residual, "residual")

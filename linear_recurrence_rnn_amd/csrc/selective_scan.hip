@@ -19,9 +19,10 @@
 // segment's state from a zero state, and the sum of its steps (the decay over a segment is e^{A sum}),
 // then the states that enter the segments one after the other, then the segments again from those.
 //
-// 8 x 1024 tokens of 1536 channels, 16 states, bfloat16: 102 us, of which the segments' states take 42 and
-// the outputs 58; the vector unit is busy 88% and 90% of that.  A state and token costs it 24 cycles for 64
+// 8 x 1024 tokens of 1536 channels, 16 states, bfloat16: 105 us, of which the segments' states take 38% and
+// the outputs 51%; the vector unit is busy 87% and 94% of those.  A state and token costs it 24 cycles for 64
 // of them; what a token and channel costs, once per pass, is a quarter to a third of all instructions.
+// Channels of one group alone share B and C: groups that are not of whole 64s leave lanes idle.
 #include <type_traits>
 
 #include "selective_math.hpp"
@@ -459,8 +460,8 @@ SelPlan sel_plan(const SelShape& s) {
     p.npt = s.N <= 1 ? 1 : s.N <= 2 ? 2 : s.N <= 16 ? 4 : s.N <= 64 ? 8 : 16;
     p.waves = s.N <= 4 ? 1 : s.N <= 8 ? 2 : s.N <= 32 ? 4 : 8;
     // Segments until there are ten waves a SIMD, of which it holds three (one wave a workgroup) to eight at once: 8 x 4096
-    // tokens of 2560 channels take 515 us, 536 with six; with 8 states 370 and 410; 32768 of 2048 449 and 471; more gain
-    // nothing.
+    // tokens of 2560 channels take 537 us, 558 with six waves, 549 with sixteen; with 8 states 390, 427 and 391; 32768 of 2048
+    // 471, 493 and 462.
     const int64_t wg = s.B * s.G * ceil_div(s.C / s.G, 64), tiles = sel_tiles(s);
     int64_t segs = 10240 / (wg * p.waves);
     // Of two tiles at least, of four in rows of more than 128 tiles, where the states that enter the segments would cost

@@ -25,8 +25,8 @@
 // Sums over blocks, batch rows and channel ranges are partial sums in the workspace, added in
 // order by small kernels at the end: nothing depends on timing.
 //
-// 8 x 4096 tokens of 2560 channels, 16 states, bfloat16: reverse 274-289 us, gradients 934-1000 (the lower ones
-// before the clock falls), partial sums 56.  The vector unit is busy 98% and 97% of the first two.
+// 8 x 4096 tokens of 2560 channels, 16 states, bfloat16, by trace: reverse 275-295 us, gradients 921-994 (the lower ones
+// before the clock falls), partial sums 56.  The vector unit is busy 98% and 96% of the first two.
 #include "selective_math.hpp"
 
 namespace linrec {
