@@ -472,7 +472,8 @@ SelPlan sel_plan(const SelShape& s) {
     if (segs > most) segs = most;
     // Each segment but the last is walked twice, so that cut rows keep the chip busy for a time that grows with the
     // workgroups, where whole ones take what one of them takes, alone on its CU or with others, however few they are.
-    // Microseconds a tile of 16 tokens: one whole row's workgroup alone, with others, and a workgroup's part of cut ones'.
+    // Microseconds a tile of 16 tokens, by the number of states: a whole row's workgroup alone on its CU (of 256), one with
+    // others, and a workgroup's part of cut rows' time.
     const bool halved = p.npt == 4 && p.waves == 4;  // whole rows may be, below
     const double us[6][3] = {{3.3, 4.4, 0.0033}, {2.45, 3.8, 0.0046}, {1.7, 2.5, 0.0065},
                              {3.27, 4.4, 0.0116}, {4.25, 6.95, 0.0235}, {7.75, 13.3, 0.046}};
